@@ -1,6 +1,7 @@
 /*
  * fa.h -- C ABI of fused exact attention for GB300 (sm_103a): the forward (with masks and a
- * split-K/V form), its backward, and host-buffer forms of both.
+ * split-K/V form), its backward, host-buffer forms of both, and a paged key-value cache
+ * (fa_key_weights, fa_paged_append, fa_paged_decode, fa_paged_evict).
  *
  * The operation ("FlashAttention 优化原理与实现要点解析" §1, §2, §4.3, §5, §7):
  *
@@ -61,7 +62,9 @@ enum fa_status {
     FA_ERR_SCALE = -9,    /* scale is not finite */
     FA_ERR_CUDA = -10,    /* a CUDA runtime or driver query failed */
     FA_ERR_WORKSPACE = -11, /* workspace smaller than fa_fwd_splitkv_workspace_size() */
-    FA_ERR_POINTER = -12    /* a device-side argument is not device memory of the current device */
+    FA_ERR_POINTER = -12,   /* a device-side argument is not device memory of the current device */
+    FA_ERR_PAGE = -13       /* a block table or length named a token outside the cache (found on the
+                               device, read with fa_get_device_error) */
 };
 
 /*
@@ -296,13 +299,135 @@ int fa_bwd_host_masked(const void* q_h, const void* k_h, const void* v_h, const 
                        int window_left, int window_right, const int* seqlens_k, float scale,
                        int dtype, fa_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The paged key-value cache
+ *
+ * A cache is a pool of pages shared by many sequences. k_pages and v_pages are
+ * [num_pages, page_size, Hkv, d]: a page holds page_size tokens in the [N, H, d] layout of k and
+ * v above (dense keys [B, N, H, d] with N a multiple of page_size are pages as they stand).
+ * weights, where a cache keeps them, is [num_pages, Hkv, page_size] fp32: the attention weight
+ * that each token has received from the queries so far, for each key head.
+ *
+ *   block_table  device int32 [B, max_pages]: token t of sequence b is row t % page_size of page
+ *                block_table[b, t / page_size]. Entries behind the sequence's last page are not
+ *                read for their value (-1 or anything else).
+ *   seqlens      device int32 [B]: tokens of each sequence (0 .. max_pages * page_size)
+ *   page_size    16, 32, 64, 128 or 256
+ *   Hq, Hkv      query heads and key heads, Hq a multiple of Hkv: query head h reads key head
+ *                h / (Hq / Hkv)
+ *   d, dtype, stream, return codes, pointer checks: as in fa_fwd (block_table, seqlens, weights
+ *                and the other int32 / fp32 arrays 4-byte aligned, pages and q, k, v, o 16-byte)
+ *
+ * The block table and the lengths live on the device and are checked there. A page number
+ * outside [0, num_pages), where a token needs it, or a length outside the table is never
+ * followed: the kernel records FA_ERR_PAGE in the device error word and leaves those tokens out
+ * (each entry point says how). Pages may be shared between sequences where they are only read;
+ * a page that a call writes must belong to one sequence of that call (otherwise its contents
+ * are those of any of the writers).
+ */
+
+/*
+ * fa_key_weights -- the attention weight that every key of a prompt received, from the LSE that
+ * the forward left:
+ *   w[b, hk, j] = sum over the query heads h of key head hk, and over the queries i that see
+ *                 key j, of exp(scale * <q[b, i, h], k[b, j, hk]> - lse[b, h, i])
+ * with the masks of fa_fwd_masked (queries and keys share N). Queries at or past seqlens_k[b]
+ * are padding and add nothing; a masked key gets 0; a query whose LSE is -inf adds nothing.
+ *
+ *   q            [B, N, Hq, d] dtype;  k  [B, N, Hkv, d] dtype
+ *   lse          [B, Hq, N] fp32: the forward's LSE for the same q, k, masks and scale
+ *   w            [B, Hkv, N] fp32, written (every element)
+ *   workspace    device memory of at least fa_key_weights_workspace_size(B, Hq, Hkv, N) bytes,
+ *                16-byte aligned, not overlapping any other argument; NULL where that is 0.
+ *                Calls sharing a workspace must not overlap.
+ * The sums run in fp32 in a fixed order: the same call gives the same bits.
+ */
+int fa_key_weights(const void* q, const void* k, const float* lse, float* w, int B, int Hq,
+                   int Hkv, int N, int d, int causal, int window_left, int window_right,
+                   const int* seqlens_k, float scale, int dtype, void* workspace,
+                   size_t workspace_bytes, fa_stream_t stream);
+
+/* Bytes of workspace fa_key_weights needs: B*Hq*N*4 when heads share a key head, else 0. */
+size_t fa_key_weights_workspace_size(int B, int Hq, int Hkv, int N);
+
+/*
+ * fa_paged_append -- new tokens written into the cache's pages. seqlens counts them already, as
+ * it will for the fa_paged_decode that follows: new token i of sequence b (0 <= i < n_b) becomes
+ * token seqlens[b] - n_b + i.
+ *
+ *   k, v         [B, N, Hkv, d] dtype: the new tokens, padded to the longest
+ *   w            [B, Hkv, N] fp32: their weights (of fa_key_weights), or NULL for zeros
+ *   new_lens     device int32 [B]: n_b, clamped to [0, N]; NULL: N for every sequence
+ *   weights      the cache's weights, or NULL when it keeps none (then w must be NULL)
+ * Everything else in the pages is left as it was. Tokens whose place is outside the table, or
+ * in a page outside the pool, are dropped (FA_ERR_PAGE in the device error word).
+ */
+int fa_paged_append(const void* k, const void* v, const float* w, void* k_pages, void* v_pages,
+                    float* weights, const int* block_table, const int* seqlens,
+                    const int* new_lens, int B, int N, int Hkv, int d, int page_size,
+                    int num_pages, int max_pages, int dtype, fa_stream_t stream);
+
+/*
+ * fa_paged_decode -- attention of one new token of every sequence over the pages:
+ *   O = softmax(scale * Q K^T) V over the tokens of the sequence, and LSE; the new token's own
+ *   key and value are in the cache already (fa_paged_append). With weights, every visible token
+ *   adds to weights[page, hk, row] the sum over the query heads of hk of its probability.
+ *
+ *   q, o         [B, Hq, d] dtype;  lse  [B, Hq] fp32
+ *   window_left  >= 0: only the last window_left + 1 tokens are visible; negative: all are
+ *   weights      updated in place, or NULL
+ *   workspace    device memory of at least fa_paged_decode_workspace_size(...) bytes, 16-byte
+ *                aligned, not overlapping any other argument. Calls sharing a workspace must
+ *                not overlap. Its contents need no initialisation.
+ * A sequence with no visible token gets O = 0 and LSE = -inf. What the pages hold behind a
+ * sequence's last token (NaN included) does not matter. A length beyond the table is taken as
+ * the table's, and tokens in pages outside the pool are left out (FA_ERR_PAGE in the device
+ * error word). The same call gives the same bits.
+ */
+int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, float* weights,
+                    const int* block_table, const int* seqlens, void* o, float* lse, int B,
+                    int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                    int window_left, float scale, int dtype, void* workspace,
+                    size_t workspace_bytes, fa_stream_t stream);
+
+/* Bytes of workspace fa_paged_decode needs (with_weights: whether weights is passed). */
+size_t fa_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size,
+                                      int max_pages, int with_weights);
+
+/*
+ * fa_paged_evict -- every sequence cut to `budget` tokens for each key head: its `recent` newest
+ * tokens, and of the others the ones with the largest weights (of equal ones the oldest; a NaN
+ * counts as the smallest). The kept tokens move, in their order, to the first tokens of the
+ * pages in out_table: keys, values and weights. Heads keep different tokens, so a row of a page
+ * holds different tokens for different heads from then on; attention does not mind. A sequence
+ * of at most `budget` tokens keeps them all (and is copied to out_table's pages as it is).
+ *
+ *   out_table    device int32 [B, out_pages], out_pages * page_size >= budget: free pages, or
+ *                the sequence's own (block_table's first entries again: eviction in place).
+ *                A page of out_table may stand in the sequence's own block table at the same
+ *                place or an earlier one, and must not stand in another sequence's tables.
+ *   kept         device int32 [B, Hkv, budget], written: the tokens kept, ascending; -1 behind
+ *                the last
+ *   new_seqlens  device int32 [B], written: min(seqlens, budget)
+ *   budget       >= 1;  0 <= recent <= budget
+ * Rows at or behind the new length are left as they were. Where a length or a page number is
+ * bad, or a page of out_table stands in the sequence's block table at a later place, nothing of
+ * that sequence moves: its kept is all -1, its new length the old one, and the device error
+ * word gets FA_ERR_PAGE.
+ */
+int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* block_table,
+                   const int* seqlens, const int* out_table, int* kept, int* new_seqlens, int B,
+                   int Hkv, int d, int page_size, int num_pages, int max_pages, int out_pages,
+                   int budget, int recent, int dtype, fa_stream_t stream);
+
 /* Static English text for a status code (never NULL). */
 const char* fa_error_string(int code);
 
 /*
  * fa_get_device_error -- synchronise `stream`, then return and clear the current device's
  * error word: FA_OK when no kernel wait has run out since the last call, FA_ERR_TIMEOUT
- * otherwise, FA_ERR_CUDA when the synchronisation or the read failed.
+ * otherwise, FA_ERR_CUDA when the synchronisation or the read failed. FA_ERR_PAGE when no wait
+ * has run out but a paged-cache kernel met a bad block-table entry or length (see below).
  */
 int fa_get_device_error(fa_stream_t stream);
 

@@ -16,6 +16,7 @@ LIB_NAME = "libfa_gb300.so"
 FA_BF16, FA_FP16 = 0, 1
 FA_OK = 0
 FA_ERR_TIMEOUT = -8
+FA_ERR_PAGE = -13
 
 _lock = threading.Lock()
 _lib = None
@@ -77,6 +78,19 @@ def load_library() -> ctypes.CDLL:
             lib.fa_bwd_host_masked.restype = i32
             lib.fa_bwd_workspace_size.argtypes = [i32, i32, i32, i32]
             lib.fa_bwd_workspace_size.restype = ctypes.c_size_t
+            szt = ctypes.c_size_t
+            lib.fa_key_weights.argtypes = [vp] * 4 + [i32] * 8 + [vp, f32, i32, vp, szt, vp]
+            lib.fa_key_weights.restype = i32
+            lib.fa_key_weights_workspace_size.argtypes = [i32] * 4
+            lib.fa_key_weights_workspace_size.restype = szt
+            lib.fa_paged_append.argtypes = [vp] * 9 + [i32] * 8 + [vp]
+            lib.fa_paged_append.restype = i32
+            lib.fa_paged_decode.argtypes = [vp] * 8 + [i32] * 8 + [f32, i32, vp, szt, vp]
+            lib.fa_paged_decode.restype = i32
+            lib.fa_paged_decode_workspace_size.argtypes = [i32] * 7
+            lib.fa_paged_decode_workspace_size.restype = szt
+            lib.fa_paged_evict.argtypes = [vp] * 8 + [i32] * 10 + [vp]
+            lib.fa_paged_evict.restype = i32
             lib.fa_error_string.argtypes = [i32]
             lib.fa_error_string.restype = ctypes.c_char_p
             lib.fa_get_device_error.argtypes = [vp]

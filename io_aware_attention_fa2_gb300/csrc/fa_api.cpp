@@ -39,6 +39,10 @@ EncodeTiledFn encode_tiled_fn() {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_arch_ok[kMaxDevices];   // 0 unknown, 1 sm_103, -1 other
 
+}  // namespace
+
+namespace fa {
+
 int check_arch(int* device) {
   if (cudaGetDevice(device) != cudaSuccess) return FA_ERR_CUDA;
   if (*device < 0 || *device >= kMaxDevices) return FA_ERR_CUDA;
@@ -93,7 +97,12 @@ bool encode_bnhd(CUtensorMap* map, const void* base, int B, int H, int N, int d,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
+}  // namespace fa
+
+using fa::check_arch;
+using fa::check_device_ptrs;
+using fa::encode_bnhd;
+using fa::overlaps;
 
 extern "C" {
 
@@ -118,6 +127,7 @@ const char* fa_error_string(int code) {
     case FA_ERR_WORKSPACE: return "workspace smaller than fa_fwd_splitkv_workspace_size()";
     case FA_ERR_POINTER:
       return "a device-side argument is not device memory of the current device";
+    case FA_ERR_PAGE: return "a block table or length named a token outside the paged cache";
     default: return "unknown status";
   }
 }
@@ -590,12 +600,15 @@ int fa_selftest_wait_timeout(int limit_us, fa_stream_t stream) {
 }
 
 int fa_get_device_error(fa_stream_t stream) {
-  int value = 0, bwd_value = 0;
+  int value = 0, bwd_value = 0, kw_value = 0, paged_value = 0;
   if (fa::read_and_clear_device_error(reinterpret_cast<cudaStream_t>(stream), &value) !=
           cudaSuccess ||
-      fa::read_and_clear_bwd_error(&bwd_value) != cudaSuccess)
+      fa::read_and_clear_bwd_error(&bwd_value) != cudaSuccess ||
+      fa::read_and_clear_key_weights_error(&kw_value) != cudaSuccess ||
+      fa::read_and_clear_paged_error(&paged_value) != cudaSuccess)
     return FA_ERR_CUDA;
-  return (value == 0 && bwd_value == 0) ? FA_OK : FA_ERR_TIMEOUT;
+  if (value != 0 || bwd_value != 0 || kw_value != 0) return FA_ERR_TIMEOUT;
+  return paged_value;
 }
 
 size_t fa_bwd_workspace_size(int B, int H, int N, int d) {
