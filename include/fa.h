@@ -311,12 +311,13 @@ int fa_bwd_host_masked(const void* q_h, const void* k_h, const void* v_h, const 
  *   block_table  device int32 [B, max_pages]: token t of sequence b is row t % page_size of page
  *                block_table[b, t / page_size]. Entries behind the sequence's last page are not
  *                read for their value (-1 or anything else).
- *   seqlens      device int32 [B]: tokens of each sequence (0 .. max_pages * page_size)
+ *   seqlens      device int32 [B]: tokens of each sequence (0 .. max_pages * page_size, which is
+ *                at most 2^30)
  *   page_size    16, 32, 64, 128 or 256
  *   Hq, Hkv      query heads and key heads, Hq a multiple of Hkv: query head h reads key head
  *                h / (Hq / Hkv)
- *   d, dtype, stream, return codes, pointer checks: as in fa_fwd (block_table, seqlens, weights
- *                and the other int32 / fp32 arrays 4-byte aligned, pages and q, k, v, o 16-byte)
+ *   d, dtype, stream, return codes, pointer checks: as in fa_fwd (pages, weights and q, k, v, o
+ *                16-byte aligned, block_table, seqlens and the other int32 / fp32 arrays 4-byte)
  *
  * The block table and the lengths live on the device and are checked there. A page number
  * outside [0, num_pages), where a token needs it, or a length outside the table is never

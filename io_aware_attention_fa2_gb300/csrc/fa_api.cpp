@@ -43,6 +43,8 @@ std::atomic<int> g_arch_ok[kMaxDevices];   // 0 unknown, 1 sm_103, -1 other
 
 namespace fa {
 
+void* encode_tiled_entry() { return reinterpret_cast<void*>(encode_tiled_fn()); }
+
 int check_arch(int* device) {
   if (cudaGetDevice(device) != cudaSuccess) return FA_ERR_CUDA;
   if (*device < 0 || *device >= kMaxDevices) return FA_ERR_CUDA;

@@ -87,6 +87,8 @@ int check_arch(int* device);
 // FA_OK when every non-null pointer is device memory usable by `device`, else FA_ERR_POINTER.
 int check_device_ptrs(int device, std::initializer_list<const void*> ptrs);
 bool overlaps(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes);
+// The driver's cuTensorMapEncodeTiled, or null.
+void* encode_tiled_entry();
 // [B, N, H, d] 16-bit tensor as a 4-D TMA map (d, H, N, B) with box (64, 1, 128, 1).
 bool encode_bnhd(CUtensorMap* map, const void* base, int B, int H, int N, int d, bool fp16);
 
@@ -150,5 +152,6 @@ cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream);
 // The error words of these kernels on the current device: read and clear (no synchronisation).
 cudaError_t read_and_clear_key_weights_error(int* value);
 cudaError_t read_and_clear_paged_error(int* value);   // FA_ERR_TIMEOUT before FA_ERR_PAGE
+cudaError_t read_and_clear_decode_error(int* bits);   // or-ed in: 1 timeout, 2 bad page
 
 }  // namespace fa

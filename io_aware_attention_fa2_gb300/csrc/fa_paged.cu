@@ -1,43 +1,14 @@
-// fa_paged.cu -- the paged key-value cache: append, decode, evict (include/fa.h has the layouts
-// and the rules for bad block-table entries and lengths).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "fa_internal.h"
-#include "ptx_sm103.cuh"
+// fa_paged.cu -- the paged key-value cache: append and evict (include/fa.h has the layouts and
+// the rules for bad block-table entries and lengths).
+#include "fa_paged.cuh"
 
 namespace fa {
 
-// Device error word of the paged kernels: bit 0 a wait ran past its limit, bit 1 a block-table
-// entry or a length named a token outside the cache.
-__device__ int g_paged_error = 0;
-
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kPageError = 2;
+using namespace paged;
+
 constexpr int kErrTimeout = -8, kErrPage = -13;   // FA_ERR_TIMEOUT, FA_ERR_PAGE
-
-__device__ __forceinline__ void record_page_error() { atomicOr(&g_paged_error, kPageError); }
-
-template <bool FP16>
-__device__ __forceinline__ float to_float(uint16_t x) {
-  if constexpr (FP16) {
-    return __half2float(__ushort_as_half(x));
-  } else {
-    return __uint_as_float(static_cast<uint32_t>(x) << 16);
-  }
-}
-
-template <bool FP16>
-__device__ __forceinline__ uint16_t from_float(float x) {
-  if constexpr (FP16) {
-    return __half_as_ushort(__float2half_rn(x));
-  } else {
-    return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-  }
-}
 
 // Page of the table entry at `at`, or -1 (recorded) when it is outside the pool.
 __device__ __forceinline__ int page_at(const int* __restrict__ table, int64_t at, int num_pages) {
@@ -79,132 +50,6 @@ __global__ void __launch_bounds__(128)
     for (int h = threadIdx.x; h < Hkv; h += blockDim.x)
       weights[(static_cast<int64_t>(page) * Hkv + h) * page_size + row] =
           w ? w[(static_cast<int64_t>(b) * Hkv + h) * N + i] : 0.f;
-}
-
-// ---------------------------------------------------------------------------------------------
-// Decode. One block per (b, query head); each warp takes every fourth visible token with the
-// running maximum and sum of an online softmax, and the four are merged at the end.
-struct Visible {
-  int lo, hi;
-};
-__device__ __forceinline__ Visible visible_tokens(const int* __restrict__ seqlens, int b,
-                                                  int capacity, int window_left) {
-  int len = seqlens[b];
-  if (len > capacity || len < 0) {
-    record_page_error();
-    len = min(max(len, 0), capacity);
-  }
-  const int lo = window_left >= 0 ? max(0, len - 1 - window_left) : 0;
-  return {lo, len};
-}
-
-template <int D, bool FP16>
-__global__ void __launch_bounds__(128)
-    fa_paged_decode_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ k_pages,
-                           const uint16_t* __restrict__ v_pages, const int* __restrict__ table,
-                           const int* __restrict__ seqlens, uint16_t* __restrict__ o,
-                           float* __restrict__ lse, int Hq, int Hkv, int page_size, int num_pages,
-                           int max_pages, int window_left, float scale_log2) {
-  constexpr int E = D / 32;
-  const int b = blockIdx.x / Hq, h = blockIdx.x % Hq, hk = h / (Hq / Hkv);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const Visible vis = visible_tokens(seqlens, b, max_pages * page_size, window_left);
-  float qr[E], acc[E];
-  for (int e = 0; e < E; ++e) {
-    qr[e] = to_float<FP16>(q[static_cast<int64_t>(blockIdx.x) * D + lane + 32 * e]);
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int t = vis.lo + warp; t < vis.hi; t += 4) {
-    const int page =
-        page_at(table, static_cast<int64_t>(b) * max_pages + t / page_size, num_pages);
-    if (page < 0) continue;
-    const int64_t at =
-        ((static_cast<int64_t>(page) * page_size + t % page_size) * Hkv + hk) * D + lane;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = fmaf(qr[e], to_float<FP16>(k_pages[at + 32 * e]), s);
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= scale_log2;
-    const float m_new = fmaxf(m, s), m_use = m_new == -INFINITY ? 0.f : m_new;
-    const float alpha = exp2f(m - m_use), p = exp2f(s - m_use);
-    m = m_new;
-    l = l * alpha + p;
-    for (int e = 0; e < E; ++e)
-      acc[e] = acc[e] * alpha + p * to_float<FP16>(v_pages[at + 32 * e]);
-  }
-  __shared__ float sm[4], sl[4], so[4][D];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = acc[e];
-  __syncthreads();
-  const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float sum = 0.f, f[4];
-  for (int x = 0; x < 4; ++x) {
-    f[x] = mx == -INFINITY ? 0.f : exp2f(sm[x] - mx);
-    sum += sl[x] * f[x];
-  }
-  for (int c = threadIdx.x; c < D; c += 128) {
-    float a = 0.f;
-    for (int x = 0; x < 4; ++x) a += so[x][c] * f[x];
-    o[static_cast<int64_t>(blockIdx.x) * D + c] = from_float<FP16>(sum > 0.f ? a / sum : 0.f);
-  }
-  if (threadIdx.x == 0)
-    lse[blockIdx.x] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
-}
-
-// weights[page, hk, row] += sum over the group's heads of exp(s - LSE): one warp per token.
-template <int D, bool FP16>
-__global__ void __launch_bounds__(256)
-    fa_paged_weights_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ k_pages,
-                            float* __restrict__ weights, const int* __restrict__ table,
-                            const int* __restrict__ seqlens, const float* __restrict__ lse, int Hq,
-                            int Hkv, int page_size, int num_pages, int max_pages,
-                            int window_left, float scale_log2) {
-  constexpr int E = D / 32;
-  const int b = blockIdx.y / Hkv, hk = blockIdx.y % Hkv, G = Hq / Hkv;
-  const int lane = threadIdx.x % 32;
-  const Visible vis = visible_tokens(seqlens, b, max_pages * page_size, window_left);
-  for (int t = vis.lo + blockIdx.x * 8 + threadIdx.x / 32; t < vis.hi; t += gridDim.x * 8) {
-    const int page =
-        page_at(table, static_cast<int64_t>(b) * max_pages + t / page_size, num_pages);
-    if (page < 0) continue;
-    const int row = t % page_size;
-    const int64_t at = ((static_cast<int64_t>(page) * page_size + row) * Hkv + hk) * D + lane;
-    float kr[E], sum = 0.f;
-    for (int e = 0; e < E; ++e) kr[e] = to_float<FP16>(k_pages[at + 32 * e]);
-    for (int g = 0; g < G; ++g) {
-      const int64_t hrow = static_cast<int64_t>(b) * Hq + hk * G + g;
-      float s = 0.f;
-      for (int e = 0; e < E; ++e) s = fmaf(kr[e], to_float<FP16>(q[hrow * D + lane + 32 * e]), s);
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      const float l = lse[hrow];
-      if (l != -INFINITY) sum += exp2f(s * scale_log2 - l * kLog2e);
-    }
-    if (lane == 0)
-      atomicAdd(&weights[(static_cast<int64_t>(page) * Hkv + hk) * page_size + row], sum);
-  }
-}
-
-template <int D, bool FP16>
-cudaError_t decode_impl(const DecodeParams& p, cudaStream_t stream) {
-  const PagedCache& c = p.c;
-  const uint16_t* q = static_cast<const uint16_t*>(p.q);
-  const uint16_t* k = static_cast<const uint16_t*>(c.k_pages);
-  fa_paged_decode_kernel<D, FP16><<<c.B * p.Hq, 128, 0, stream>>>(
-      q, k, static_cast<const uint16_t*>(c.v_pages), c.block_table, c.seqlens,
-      static_cast<uint16_t*>(p.o), p.lse, p.Hq, c.Hkv, c.page_size, c.num_pages, c.max_pages,
-      p.window_left, p.scale_log2);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || !c.weights) return err;
-  // (b, hk) on the grid's second axis: at most 65535 rows there
-  if (static_cast<int64_t>(c.B) * c.Hkv > 65535) return cudaErrorInvalidConfiguration;
-  const dim3 grid(64, c.B * c.Hkv);
-  fa_paged_weights_kernel<D, FP16><<<grid, 256, 0, stream>>>(
-      q, k, c.weights, c.block_table, c.seqlens, p.lse, p.Hq, c.Hkv, c.page_size, c.num_pages,
-      c.max_pages, p.window_left, p.scale_log2);
-  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -373,14 +218,6 @@ cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-size_t paged_decode_workspace(int, int, int, int, int, int, bool) { return 16; }
-
-cudaError_t launch_paged_decode(const DecodeParams& p, cudaStream_t stream) {
-  if (p.c.d == 64)
-    return p.fp16 ? decode_impl<64, true>(p, stream) : decode_impl<64, false>(p, stream);
-  return p.fp16 ? decode_impl<128, true>(p, stream) : decode_impl<128, false>(p, stream);
-}
-
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream) {
   const PagedCache& c = p.c;
   fa_paged_evict_kernel<<<c.B * c.Hkv, kEvictThreads, 0, stream>>>(
@@ -392,11 +229,10 @@ cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream) {
 
 cudaError_t read_and_clear_paged_error(int* value) {
   int bits = 0;
-  cudaError_t err = cudaMemcpyFromSymbol(&bits, g_paged_error, sizeof(int));
-  if (err != cudaSuccess) return err;
-  *value = bits & 1 ? kErrTimeout : bits & kPageError ? kErrPage : 0;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_paged_error, &zero, sizeof(int));
+  cudaError_t err = read_and_clear_error(&bits);
+  if (err == cudaSuccess) err = read_and_clear_decode_error(&bits);
+  *value = bits & kTimeoutBit ? kErrTimeout : bits & kPageBit ? kErrPage : 0;
+  return err;
 }
 
 }  // namespace fa

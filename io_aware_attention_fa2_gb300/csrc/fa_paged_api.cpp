@@ -43,14 +43,13 @@ int check_device(std::initializer_list<const void*> ptrs) {
   return rc != FA_OK ? rc : fa::check_device_ptrs(device, ptrs);
 }
 
-// Shape of a cache. Lengths are int32 (max_pages * page_size < 2^31) and the pool's bytes and
-// the kernels' grids stay far inside 64 and 31 bits.
+// Shape of a cache. Lengths are int32 with room for the tiles behind the last one (at most 2^30
+// tokens a sequence), and the pool's bytes and the kernels' grids stay far inside 64 and 31 bits.
 bool cache_shape_ok(int B, int Hkv, int d, int page_size, int num_pages, int max_pages) {
   if (B < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1) return false;
   if (d != 64 && d != 128) return false;
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return false;
-  if ((int64_t)max_pages * page_size >= (1ll << 31)) return false;
-  if ((int64_t)B * max_pages >= (1ll << 40)) return false;
+  if ((int64_t)max_pages * page_size > (1ll << 30)) return false;
   // a page within 2^31 bytes, the pool within 2^62
   const uint64_t page_bytes = (uint64_t)page_size * (uint64_t)Hkv * (uint64_t)d * 2;
   if (page_bytes >= (1ull << 31)) return false;
@@ -153,8 +152,8 @@ int fa_paged_append(const void* k, const void* v, const float* w, void* k_pages,
   if (N < 1 || !cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages)) return FA_ERR_SHAPE;
   if ((uint64_t)B * (uint64_t)N >= (1ull << 31)) return FA_ERR_SHAPE;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
-  if (!aligned({k, v, k_pages, v_pages}, 16) ||
-      !aligned({w, weights, block_table, seqlens, new_lens}, 4))
+  if (!aligned({k, v, k_pages, v_pages, weights}, 16) ||
+      !aligned({w, block_table, seqlens, new_lens}, 4))
     return FA_ERR_ALIGN;
   const uint64_t pool = pool_bytes(Hkv, d, page_size, num_pages);
   const uint64_t in = (uint64_t)B * N * Hkv * d * 2, lens = (uint64_t)B * 4;
@@ -179,7 +178,9 @@ int fa_paged_append(const void* k, const void* v, const float* w, void* k_pages,
 
 size_t fa_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size,
                                       int max_pages, int with_weights) {
-  if (Hq < Hkv || !cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) || Hq % Hkv) return 0;
+  if (!cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) || Hq < Hkv || Hq % Hkv ||
+      (uint64_t)B * (uint64_t)Hq * (uint64_t)max_pages * page_size >= (1ull << 48))
+    return 0;
   return fa::paged_decode_workspace(B, Hq, Hkv, d, page_size, max_pages, with_weights != 0);
 }
 
@@ -191,15 +192,17 @@ int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, flo
   if (!q || !k_pages || !v_pages || !block_table || !seqlens || !o || !lse || !workspace)
     return FA_ERR_NULL;
   if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages) || Hq < Hkv || Hq % Hkv ||
-      (uint64_t)B * (uint64_t)Hq >= (1ull << 31))
+      (uint64_t)B * (uint64_t)Hq >= (1ull << 31) ||
+      // tiles of all units stay far inside 64 bits
+      (uint64_t)B * (uint64_t)Hq * (uint64_t)max_pages * page_size >= (1ull << 48))
     return FA_ERR_SHAPE;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
   if (!isfinite(scale)) return FA_ERR_SCALE;
   const uint64_t ws_need =
       fa::paged_decode_workspace(B, Hq, Hkv, d, page_size, max_pages, weights != nullptr);
   if (workspace_bytes < ws_need) return FA_ERR_WORKSPACE;
-  if (!aligned({q, k_pages, v_pages, o, workspace}, 16) ||
-      !aligned({weights, block_table, seqlens, lse}, 4))
+  if (!aligned({q, k_pages, v_pages, o, weights, workspace}, 16) ||
+      !aligned({block_table, seqlens, lse}, 4))
     return FA_ERR_ALIGN;
   const uint64_t pool = pool_bytes(Hkv, d, page_size, num_pages);
   const uint64_t rows = (uint64_t)B * Hq, lens = (uint64_t)B * 4;
@@ -236,11 +239,11 @@ int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* bloc
   if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages)) return FA_ERR_SHAPE;
   if (out_pages < 1 || budget < 1 || recent < 0 || recent > budget ||
       (int64_t)out_pages * page_size < budget ||
-      (int64_t)out_pages * page_size >= (1ll << 31))
+      (int64_t)out_pages * page_size > (1ll << 30))
     return FA_ERR_SHAPE;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
-  if (!aligned({k_pages, v_pages}, 16) ||
-      !aligned({weights, block_table, seqlens, out_table, kept, new_seqlens}, 4))
+  if (!aligned({k_pages, v_pages, weights}, 16) ||
+      !aligned({block_table, seqlens, out_table, kept, new_seqlens}, 4))
     return FA_ERR_ALIGN;
   const uint64_t pool = pool_bytes(Hkv, d, page_size, num_pages), lens = (uint64_t)B * 4;
   int rc = check_spans({{block_table, lens * max_pages}, {seqlens, lens},
