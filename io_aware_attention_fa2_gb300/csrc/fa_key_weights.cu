@@ -1,71 +1,357 @@
 // fa_key_weights.cu -- the attention weight that every key of a prompt received:
 //   w[b, hk, j] = sum_{h of hk} sum_{i sees j} exp(scale <q_i, k_j> - LSE[b, h, i]).
+//
+// The forward's S and its softmax statistics again, without P V: 2 d operations and one
+// exponential for every visible (query, key) pair, and no tensor larger than the inputs. It is
+// bound by the tensor pipe and the exponentials (at d = 128 a 128 x 128 tile is 4.2 MFLOP and
+// 16384 exponentials).
+//
+// Keys are the rows: S^T = K Q^T puts one key in each TMEM lane, so that the sum over queries is
+// a sum inside a thread, and the query's LSE is a value that all lanes share (a broadcast read
+// from shared memory). One CTA takes 256 keys (two tiles, A and B) of one (batch, query head),
+// keeps them in shared memory and walks the query tiles that see them:
+//   warp 0       TMA producer: K_A, K_B once, then the Q tiles through a ring
+//   warp 1       TMEM allocator and MMA issuer (one thread)
+//   warps 2..5   keys of tile A, warps 6..9 keys of tile B: p = 2^(scale_log2 S - LSE log2 e),
+//                summed per key
+// Each tile has two S buffers of 128 TMEM columns, so that S(j+1) is computed while S(j) is
+// summed. Two key tiles share every Q tile that is loaded, which halves the reads of Q from L2.
+//
+// Sums: 32 bits, a query tile at a time in four chains, the tiles' sums added with Kahan's
+// compensation: a key of a long prompt is the sum of many thousand terms. With shared key heads
+// each query head writes its own sums (fp32 workspace) and a second kernel adds them in the order
+// of the heads, so that the result does not depend on which CTA ends first.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "fa_internal.h"
 #include "ptx_sm103.cuh"
 
 namespace fa {
 
+// Device error word: nonzero after a kernel wait ran past its limit.
 __device__ int g_key_weights_error = 0;
 
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kStages = 4;                                  // depth of the Q ring
+constexpr int kThreads = 64 + 256;
+constexpr uint32_t kBoxBytes = BOX_ROWS * BOX_COLS * 2;     // 16 KiB
+constexpr uint64_t kWaitLimitNs = 1000000000ull;            // 1 s per wait
+constexpr int kErrTimeout = -8;                             // FA_ERR_TIMEOUT
+constexpr uint32_t kTmemCols = 512;
 
-template <bool FP16>
-__device__ __forceinline__ float to_float(uint16_t x) {
-  if constexpr (FP16) {
-    return __half2float(__ushort_as_half(x));
+template <int D>
+struct Smem {
+  static constexpr uint32_t kTile = (D / BOX_COLS) * kBoxBytes;
+  static constexpr uint32_t kK = 0;
+  static constexpr uint32_t kQ = 2 * kTile;
+  static constexpr uint32_t kLse = kQ + kStages * kTile;    // [tile][buffer][128] floats
+  static constexpr uint32_t kBars = kLse + 2 * 2 * 128 * 4;
+  static constexpr uint32_t kDynamic = kBars + 24 * 8 + 1024;
+};
+
+enum : int {
+  BAR_K_FULL = 0,
+  BAR_Q_FULL = 1,                         // + stage
+  BAR_Q_EMPTY = BAR_Q_FULL + kStages,     // + stage
+  BAR_S_FULL = BAR_Q_EMPTY + kStages,     // + 2 * tile + buffer
+  BAR_S_EMPTY = BAR_S_FULL + 4,           // + 2 * tile + buffer (128 arrivals)
+  BAR_MMA_DONE = BAR_S_EMPTY + 4,
+  BAR_COUNT = BAR_MMA_DONE + 1
+};
+static_assert(BAR_COUNT <= 24, "barrier slots");
+
+__device__ __forceinline__ void record_timeout(volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicCAS(&g_key_weights_error, 0, kErrTimeout);
+}
+
+// The queries that see key j: [lo(j), hi(j)), both nondecreasing in j.
+struct QueryMask {
+  int len, causal, left, right;
+  __device__ __forceinline__ int lo(int j) const {
+    int a = causal ? j : 0;
+    if (right >= 0) a = max(a, j - right);
+    return a;
+  }
+  __device__ __forceinline__ int hi(int j) const {
+    return left >= 0 ? min(len, j + left + 1) : len;
+  }
+  // Query tiles [t0, t1) that see a key of the tile starting at k0; t1 <= t0 when none does.
+  __device__ __forceinline__ void tile_range(int k0, int& t0, int& t1) const {
+    const int a = lo(k0), z = k0 < len ? hi(min(k0 + BLOCK_N, len) - 1) : 0;
+    t0 = z <= a ? 0 : a / BLOCK_M;
+    t1 = z <= a ? 0 : (z + BLOCK_M - 1) / BLOCK_M;
+  }
+};
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const float* __restrict__ lse, float* __restrict__ out, int Hq, int G,
+                          int N, int causal, int left, int right,
+                          const int* __restrict__ seqlens, float scale_log2,
+                          int heads_per_group) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t tmem_base_slot;
+  __shared__ int abort_flag;
+  const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sK = base + L::kK, sQ = base + L::kQ;
+  float* const s_lse =
+      reinterpret_cast<float*>(smem_raw + (base - ptx::smem_addr(smem_raw)) + L::kLse);
+  auto bar = [&](int i) { return base + L::kBars + 8u * static_cast<uint32_t>(i); };
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  // Unit from a 1-D grid: heads in groups whose Q stays in L2, in a group key block by key
+  // block, the first (seen by the most queries when causal) first.
+  const int num_kblk = (N + 2 * BLOCK_N - 1) / (2 * BLOCK_N);
+  const int num_bh = gridDim.x / num_kblk;
+  const int group_units = heads_per_group * num_kblk;
+  const int grp = static_cast<int>(blockIdx.x) / group_units;
+  const int rem = static_cast<int>(blockIdx.x) % group_units;
+  const int g_size = min(heads_per_group, num_bh - grp * heads_per_group);
+  const int bh = grp * heads_per_group + rem % g_size;
+  const int kblk = rem / g_size;
+  const int b = bh / Hq, h = bh % Hq;
+  QueryMask mask;
+  mask.len = seqlens ? min(max(seqlens[b], 0), N) : N;
+  mask.causal = causal;
+  mask.left = left;
+  mask.right = right;
+  // query tiles of key tiles A and B, and their union [u0, u1), which the producer streams
+  int a0, a1, b0, b1;
+  mask.tile_range(2 * kblk * BLOCK_N, a0, a1);
+  mask.tile_range((2 * kblk + 1) * BLOCK_N, b0, b1);
+  const bool a_any = a1 > a0, b_any = b1 > b0, any_work = a_any || b_any;
+  const int u0 = a_any ? (b_any ? min(a0, b0) : a0) : b0;
+  const int u1 = max(a1, b1);
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    ptx::mbar_init(bar(BAR_K_FULL), 1);
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bar(BAR_Q_FULL + s), 1);
+      ptx::mbar_init(bar(BAR_Q_EMPTY + s), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(bar(BAR_S_FULL + i), 1);
+      ptx::mbar_init(bar(BAR_S_EMPTY + i), 128);
+    }
+    ptx::mbar_init(bar(BAR_MMA_DONE), 1);
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(&tmem_base_slot), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem = tmem_base_slot;
+  volatile int* abort_p = &abort_flag;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0 && any_work) {
+      ptx::prefetch_tensormap(&tm_q);
+      ptx::prefetch_tensormap(&tm_k);
+      ptx::mbar_arrive_expect_tx(bar(BAR_K_FULL), 2 * L::kTile);
+      for (int x = 0; x < 2; ++x)
+        for (int c = 0; c < D / BOX_COLS; ++c)
+          ptx::tma_load_4d(sK + x * L::kTile + c * kBoxBytes, &tm_k, bar(BAR_K_FULL),
+                           c * BOX_COLS, h / G, (2 * kblk + x) * BLOCK_N, b);
+      int issued = 0;
+      for (int n = 0; n < u1 - u0; ++n) {
+        const int s = n % kStages;
+        if (!ptx::wait_bounded(bar(BAR_Q_EMPTY + s), ((n / kStages) & 1) ^ 1, abort_p,
+                               kWaitLimitNs)) {
+          record_timeout(abort_p);
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(bar(BAR_Q_FULL + s), L::kTile);
+        for (int c = 0; c < D / BOX_COLS; ++c)
+          ptx::tma_load_4d(sQ + s * L::kTile + c * kBoxBytes, &tm_q, bar(BAR_Q_FULL + s),
+                           c * BOX_COLS, h, (u0 + n) * BLOCK_M, b);
+        issued = n + 1;
+      }
+      // Leave no copy in flight (on the normal path these phases completed long ago).
+      ptx::wait_bounded(bar(BAR_K_FULL), 0, abort_p, kWaitLimitNs);
+      for (int n = max(0, issued - kStages); n < issued; ++n)
+        ptx::wait_bounded(bar(BAR_Q_FULL + n % kStages), (n / kStages) & 1, abort_p,
+                          kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = ptx::idesc_f16(FP16, BLOCK_N, BLOCK_M, false);
+      auto wait = [&](int slot, uint32_t parity) {
+        return ptx::wait_bounded(bar(slot), parity, abort_p, kWaitLimitNs);
+      };
+      bool ok = !any_work || wait(BAR_K_FULL, 0);
+      for (int i = u0; ok && i < u1; ++i) {
+        const int n = i - u0, s = n % kStages;
+        if (!wait(BAR_Q_FULL + s, (n / kStages) & 1)) { ok = false; break; }
+        const ptx::SmemDesc q_desc = ptx::smem_desc_sw128_split(sQ + s * L::kTile, 16, 1024);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int x0 = x ? b0 : a0, x1 = x ? b1 : a1;
+          if (i < x0 || i >= x1) continue;
+          const int p = (i - x0) & 1;
+          if (!wait(BAR_S_EMPTY + 2 * x + p, (((i - x0) / 2) & 1) ^ 1)) { ok = false; break; }
+          ptx::tc_fence_after_sync();
+          const ptx::SmemDesc k_desc = ptx::smem_desc_sw128_split(sK + x * L::kTile, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * kBoxBytes + (kk % 4) * 32;
+            ptx::mma_f16_ss(tmem + x * 256 + p * 128, k_desc.at(off), q_desc.at(off), idesc,
+                            kk > 0);
+          }
+          ptx::mma_commit(bar(BAR_S_FULL + 2 * x + p));
+        }
+        ptx::mma_commit(bar(BAR_Q_EMPTY + s));
+      }
+      if (!ok) record_timeout(abort_p);
+      // Every MMA this thread issued has completed before TMEM can be released.
+      ptx::mma_commit(bar(BAR_MMA_DONE));
+      wait(BAR_MMA_DONE, 0);
+    }
+    __syncwarp();
   } else {
-    return __uint_as_float(static_cast<uint32_t>(x) << 16);
+    // ------------------------------------------------------------------ sums over queries
+    const int x = (warp - 2) / 4;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;               // TMEM lane = key of the tile
+    const int k0 = (2 * kblk + x) * BLOCK_N, key = k0 + row;
+    const int x0 = x ? b0 : a0, x1 = x ? b1 : a1;
+    const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + x * 256;
+    float* const my_lse = s_lse + x * 256;
+    const float* lse_row = lse + static_cast<int64_t>(bh) * N;
+    // Queries [q_lo, q_hi) see this key; a query tile inside [full_lo, full_hi) is seen by every
+    // key of the tile. (Keys at or past len are left out at the end.)
+    const int q_lo = mask.lo(key), q_hi = mask.hi(key);
+    const int full_lo = mask.lo(k0 + BLOCK_N - 1), full_hi = mask.hi(k0);
+    // -LSE in log2 units of the query this thread stages; -inf where the query adds nothing
+    auto minus_lse = [&](int i) {
+      const int q = i * BLOCK_M + row;
+      if (i >= x1 || q >= mask.len) return -INFINITY;
+      const float v = lse_row[q];
+      return v == -INFINITY ? -INFINITY : -v * kLog2e;
+    };
+    float total = 0.f, comp = 0.f, staged = x1 > x0 ? minus_lse(x0) : 0.f;
+    bool ok = true;
+    for (int i = x0; i < x1; ++i) {
+      const int p = (i - x0) & 1;
+      // two buffers: the one written here was last read two tiles ago, before the barrier of
+      // the tile in between
+      my_lse[p * 128 + row] = staged;
+      ptx::named_barrier_sync(1 + x, 128);
+      staged = minus_lse(i + 1);
+      // after a wait has run out the loop goes on without data: every warp meets the barriers
+      if (ok && !ptx::wait_bounded_warp(bar(BAR_S_FULL + 2 * x + p), ((i - x0) / 2) & 1, abort_p,
+                                        kWaitLimitNs)) {
+        ok = false;
+        record_timeout(abort_p);
+      }
+      if (!ok) continue;
+      ptx::tc_fence_after_sync();
+      uint32_t sr[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(tS + p * 128 + c * 32, sr[c]);
+      ptx::tmem_wait_ld();
+      ptx::tc_fence_before_sync();
+      ptx::mbar_arrive(bar(BAR_S_EMPTY + 2 * x + p));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ptx::reg_fence(sr[c]);
+      const int q0 = i * BLOCK_M;
+      const bool full = q0 >= full_lo && q0 + BLOCK_M <= full_hi;
+      const int lo = q_lo - q0, hi = q_hi - q0;
+      float t0 = 0.f, t1 = 0.f, t2 = 0.f, t3 = 0.f;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float4 nl = *reinterpret_cast<const float4*>(my_lse + p * 128 + 4 * c);
+        const uint32_t(&s)[32] = sr[c / 8];
+        const int o = 4 * (c % 8);
+        float e0, e1, e2, e3;
+        ptx::fma2(e0, e1, __uint_as_float(s[o]), __uint_as_float(s[o + 1]), scale_log2,
+                  scale_log2, nl.x, nl.y);
+        ptx::fma2(e2, e3, __uint_as_float(s[o + 2]), __uint_as_float(s[o + 3]), scale_log2,
+                  scale_log2, nl.z, nl.w);
+        if (!full) {
+          if (4 * c + 0 < lo || 4 * c + 0 >= hi) e0 = -INFINITY;
+          if (4 * c + 1 < lo || 4 * c + 1 >= hi) e1 = -INFINITY;
+          if (4 * c + 2 < lo || 4 * c + 2 >= hi) e2 = -INFINITY;
+          if (4 * c + 3 < lo || 4 * c + 3 >= hi) e3 = -INFINITY;
+        }
+        ptx::add2(t0, t1, t0, t1, ptx::exp2_approx(e0), ptx::exp2_approx(e1));
+        ptx::add2(t2, t3, t2, t3, ptx::exp2_approx(e2), ptx::exp2_approx(e3));
+      }
+      const float y = ((t0 + t1) + (t2 + t3)) - comp;
+      const float sum = total + y;
+      comp = (sum - total) - y;
+      total = sum;
+    }
+    if (key < N) out[static_cast<int64_t>(bh) * N + key] = key < mask.len ? total : 0.f;
+  }
+
+  // ------------------------------------------------------------------ teardown
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after_sync();
+    ptx::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-// One warp per key: lane t holds components t, t + 32, ... of the key; the queries that see it
-// are walked in order.
-template <int D, bool FP16>
+// w[b, hk, j] = sum over the G query heads, in their order, of part[b, hk * G + g, j].
 __global__ void __launch_bounds__(256)
-    fa_key_weights_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
-                          const float* __restrict__ lse, float* __restrict__ w, int B, int Hq,
-                          int Hkv, int N, int causal, int left, int right,
-                          const int* __restrict__ seqlens, float scale_log2) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (row >= static_cast<int64_t>(B) * Hkv * N) return;
-  const int lane = threadIdx.x % 32;
-  const int j = static_cast<int>(row % N);
-  const int hk = static_cast<int>(row / N % Hkv), b = static_cast<int>(row / N / Hkv);
-  const int len = seqlens ? min(max(seqlens[b], 0), N) : N;
-  float kr[D / 32];
-  for (int e = 0; e < D / 32; ++e)
-    kr[e] = to_float<FP16>(k[((static_cast<int64_t>(b) * N + j) * Hkv + hk) * D + lane + 32 * e]);
-  int lo = 0, hi = j < len ? len : 0;   // queries that see key j
-  if (causal) lo = max(lo, j);
-  if (left >= 0) hi = min(hi, j + left + 1);
-  if (right >= 0) lo = max(lo, j - right);
+    fa_key_weights_sum_kernel(const float* __restrict__ part, float* __restrict__ w, int G, int N,
+                              int64_t count) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= count) return;
+  const int64_t head = at / N, j = at % N;
   float sum = 0.f;
-  for (int g = 0; g < Hq / Hkv; ++g) {
-    const int h = hk * (Hq / Hkv) + g;
-    for (int i = lo; i < hi; ++i) {
-      const uint16_t* qr = q + ((static_cast<int64_t>(b) * N + i) * Hq + h) * D;
-      float s = 0.f;
-      for (int e = 0; e < D / 32; ++e) s = fmaf(kr[e], to_float<FP16>(qr[lane + 32 * e]), s);
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      const float l = lse[(static_cast<int64_t>(b) * Hq + h) * N + i];
-      if (l != -INFINITY) sum += exp2f(s * scale_log2 - l * kLog2e);
-    }
-  }
-  if (lane == 0) w[row] = sum;
+  for (int g = 0; g < G; ++g) sum += part[(head * G + g) * N + j];
+  w[at] = sum;
 }
 
 template <int D, bool FP16>
 cudaError_t launch_impl(const KeyWeightsParams& p, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv * p.N;
-  fa_key_weights_kernel<D, FP16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(
-      static_cast<const uint16_t*>(p.q), static_cast<const uint16_t*>(p.k), p.lse, p.w, p.B,
-      p.Hq, p.Hkv, p.N, p.causal, p.window_left, p.window_right, p.seqlens_k, p.scale_log2);
-  return cudaGetLastError();
+  auto kernel = fa_key_weights_kernel<D, FP16>;
+  const int smem = static_cast<int>(Smem<D>::kDynamic);
+  cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  const int64_t bh = static_cast<int64_t>(p.B) * p.Hq;
+  const int64_t num_kblk = (p.N + 2 * BLOCK_N - 1) / (2 * BLOCK_N);
+  const int G = p.Hq / p.Hkv;
+  // Heads per dispatch group: their Q within 32 MiB, a quarter of L2, as in the forward.
+  const int64_t q_bytes = 2ll * p.N * D;
+  const int heads_per_group =
+      static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(bh, (32ll << 20) / q_bytes)));
+  kernel<<<static_cast<unsigned>(bh * num_kblk), kThreads, smem, stream>>>(
+      p.tm_q, p.tm_k, p.lse, G > 1 ? p.part : p.w, p.Hq, G, p.N, p.causal, p.window_left,
+      p.window_right, p.seqlens_k, p.scale_log2, heads_per_group);
+  err = cudaGetLastError();
+  if (err != cudaSuccess || G == 1) return err;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t count = static_cast<int64_t>(p.B) * p.Hkv * p.N;
+  cfg.gridDim = dim3(static_cast<unsigned>((count + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_key_weights_sum_kernel, static_cast<const float*>(p.part),
+                            p.w, G, p.N, count);
 }
 
 }  // namespace

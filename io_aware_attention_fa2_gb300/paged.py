@@ -22,13 +22,16 @@ outside the cache is found on the device: ``device_error()`` then returns ``FA_E
 from __future__ import annotations
 
 import contextlib
+import ctypes
+import math
 
-from .binding import FA_OK, FaError, _dtype_code, _stream_handle, load_library
+from .binding import FA_OK, FaError, _dtype_code, load_library
+
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _check(name, t, shape, dtype, device):
-    if (not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != shape
-            or not t.is_contiguous()):
+    if (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
         raise ValueError("%s must be a contiguous %s tensor %s on %s" % (
             name, str(dtype).replace("torch.", ""), list(shape), device))
 
@@ -44,7 +47,7 @@ def _on(device):
     """The library works on the current device: make it the tensors'."""
     import torch
     if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
+        return _NO_CONTEXT
     return torch.cuda.device(device)
 
 
@@ -52,22 +55,30 @@ def _stream_of(stream, device):
     """Allocations inside belong to the call's stream."""
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _NO_CONTEXT
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
 
 
+def _handle(stream, device):
+    """The stream's handle; None: the current stream of the tensors' device."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device.index) or None
+    return getattr(stream, "cuda_stream", stream) or None
+
+
 def _workspace(need, workspace, device, stream):
     """(tensor, address, bytes) of a workspace: the caller's, or one of `need` bytes that PyTorch
     allocates for the call's stream, so that it is reused only by later work there."""
-    import torch
     if workspace is not None:
-        if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on %s" % device)
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
         return None, None, 0
+    import torch
     with _stream_of(stream, device):
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     return workspace, workspace.data_ptr(), need
@@ -94,10 +105,7 @@ def _ptr(t):
 
 
 def _default_scale(d):
-    import math
-
-    import torch
-    return float(torch.tensor(1.0 / math.sqrt(d), dtype=torch.float32))
+    return ctypes.c_float(1.0 / math.sqrt(d)).value
 
 
 def key_weights_workspace_size(B: int, Hq: int, Hkv: int, N: int) -> int:
@@ -129,7 +137,7 @@ def fa_key_weights(q, k, lse, w, causal: bool, scale: float, workspace=None, str
         rc = lib.fa_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), w.data_ptr(), B, Hq,
                                 Hkv, N, d, int(bool(causal)), left, right, _ptr(seqlens_k),
                                 float(scale), _dtype_code(q), ws, ws_bytes,
-                                _stream_handle(stream))
+                                _handle(stream, device))
     if rc != FA_OK:
         raise FaError(rc, "fa_key_weights")
 
@@ -174,7 +182,7 @@ def fa_paged_append(k, v, k_pages, v_pages, block_table, seqlens, new_lens=None,
         rc = load_library().fa_paged_append(
             k.data_ptr(), v.data_ptr(), _ptr(w), k_pages.data_ptr(), v_pages.data_ptr(),
             _ptr(weights), block_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens), B, N, Hkv,
-            d, page_size, num_pages, max_pages, _dtype_code(k), _stream_handle(stream))
+            d, page_size, num_pages, max_pages, _dtype_code(k), _handle(stream, device))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_append")
 
@@ -211,7 +219,7 @@ def fa_paged_decode(q, k_pages, v_pages, block_table, seqlens, o, lse, scale: fl
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(weights),
             block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
             d, page_size, num_pages, max_pages, int(window_left), float(scale), _dtype_code(q),
-            ws, ws_bytes, _stream_handle(stream))
+            ws, ws_bytes, _handle(stream, device))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_decode")
 
@@ -258,7 +266,7 @@ def fa_paged_evict(k_pages, v_pages, weights, block_table, seqlens, out_table, k
             k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), block_table.data_ptr(),
             seqlens.data_ptr(), out_table.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr(), B,
             Hkv, d, page_size, num_pages, max_pages, out_pages, budget, int(recent),
-            _dtype_code(k_pages), _stream_handle(stream))
+            _dtype_code(k_pages), _handle(stream, device))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_evict")
 
