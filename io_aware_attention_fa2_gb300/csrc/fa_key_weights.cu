@@ -12,8 +12,9 @@
 // keeps them in shared memory and walks the query tiles that see them:
 //   warp 0       TMA producer: K_A, K_B once, then the Q tiles through a ring
 //   warp 1       TMEM allocator and MMA issuer (one thread)
-//   warps 2..5   keys of tile A, warps 6..9 keys of tile B: p = 2^(scale_log2 S - LSE log2 e),
-//                summed per key
+//   warps 2..17  p = 2^(scale_log2 S - LSE log2 e), summed per key: four warps for each 64 queries
+//                of each key tile. Nothing synchronises them but the S buffers: every warp keeps
+//                its own copy of the LSEs that it needs.
 // Each tile has two S buffers of 128 TMEM columns, so that S(j+1) is computed while S(j) is
 // summed. Two key tiles share every Q tile that is loaded, which halves the reads of Q from L2.
 //
@@ -38,7 +39,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kStages = 4;                                  // depth of the Q ring
-constexpr int kThreads = 64 + 256;
+constexpr int kThreads = 64 + 512;
+constexpr int kCols = 64;                                   // queries of a tile for one warp
 constexpr uint32_t kBoxBytes = BOX_ROWS * BOX_COLS * 2;     // 16 KiB
 constexpr uint64_t kWaitLimitNs = 1000000000ull;            // 1 s per wait
 constexpr int kErrTimeout = -8;                             // FA_ERR_TIMEOUT
@@ -49,8 +51,9 @@ struct Smem {
   static constexpr uint32_t kTile = (D / BOX_COLS) * kBoxBytes;
   static constexpr uint32_t kK = 0;
   static constexpr uint32_t kQ = 2 * kTile;
-  static constexpr uint32_t kLse = kQ + kStages * kTile;    // [tile][buffer][128] floats
-  static constexpr uint32_t kBars = kLse + 2 * 2 * 128 * 4;
+  static constexpr uint32_t kLse = kQ + kStages * kTile;    // [warp][buffer][64] floats
+  static constexpr uint32_t kSums = kLse + 16 * 2 * kCols * 4;   // [tile][128] floats
+  static constexpr uint32_t kBars = kSums + 2 * 128 * 4;
   static constexpr uint32_t kDynamic = kBars + 24 * 8 + 1024;
 };
 
@@ -59,7 +62,7 @@ enum : int {
   BAR_Q_FULL = 1,                         // + stage
   BAR_Q_EMPTY = BAR_Q_FULL + kStages,     // + stage
   BAR_S_FULL = BAR_Q_EMPTY + kStages,     // + 2 * tile + buffer
-  BAR_S_EMPTY = BAR_S_FULL + 4,           // + 2 * tile + buffer (128 arrivals)
+  BAR_S_EMPTY = BAR_S_FULL + 4,           // + 2 * tile + buffer (one arrival a warp)
   BAR_MMA_DONE = BAR_S_EMPTY + 4,
   BAR_COUNT = BAR_MMA_DONE + 1
 };
@@ -89,6 +92,32 @@ struct QueryMask {
   }
 };
 
+// Sum over 64 queries of 2^(scale_log2 s + nl), of the queries [lo, hi) alone when MASKED.
+template <bool MASKED>
+__device__ __forceinline__ float tile_sum(const uint32_t (&sr)[2][32], const float* nl,
+                                          float scale_log2, int lo, int hi) {
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < kCols / 4; ++c) {
+    const float4 n4 = *reinterpret_cast<const float4*>(nl + 4 * c);
+    const uint32_t(&s)[32] = sr[c / 8];
+    const int o = 4 * (c % 8);
+    float e[4];
+    ptx::fma2(e[0], e[1], __uint_as_float(s[o]), __uint_as_float(s[o + 1]), scale_log2,
+              scale_log2, n4.x, n4.y);
+    ptx::fma2(e[2], e[3], __uint_as_float(s[o + 2]), __uint_as_float(s[o + 3]), scale_log2,
+              scale_log2, n4.z, n4.w);
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (4 * c + k < lo || 4 * c + k >= hi) e[k] = -INFINITY;
+    }
+    ptx::add2(t[0], t[1], t[0], t[1], ptx::exp2_approx(e[0]), ptx::exp2_approx(e[1]));
+    ptx::add2(t[2], t[3], t[2], t[3], ptx::exp2_approx(e[2]), ptx::exp2_approx(e[3]));
+  }
+  return (t[0] + t[1]) + (t[2] + t[3]);
+}
+
 template <int D, bool FP16>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -103,8 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_flag;
   const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t sK = base + L::kK, sQ = base + L::kQ;
-  float* const s_lse =
-      reinterpret_cast<float*>(smem_raw + (base - ptx::smem_addr(smem_raw)) + L::kLse);
+  uint8_t* const gen = smem_raw + (base - ptx::smem_addr(smem_raw));
   auto bar = [&](int i) { return base + L::kBars + 8u * static_cast<uint32_t>(i); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
@@ -141,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(bar(BAR_S_FULL + i), 1);
-      ptx::mbar_init(bar(BAR_S_EMPTY + i), 128);
+      ptx::mbar_init(bar(BAR_S_EMPTY + i), 8);
     }
     ptx::mbar_init(bar(BAR_MMA_DONE), 1);
     ptx::fence_barrier_init();
@@ -224,79 +252,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ sums over queries
-    const int x = (warp - 2) / 4;
+    const int cw = warp - 2, x = cw / 8, half = cw / 4 % 2;   // key tile, 64-query half
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;               // TMEM lane = key of the tile
     const int k0 = (2 * kblk + x) * BLOCK_N, key = k0 + row;
     const int x0 = x ? b0 : a0, x1 = x ? b1 : a1;
-    const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + x * 256;
-    float* const my_lse = s_lse + x * 256;
+    const uint32_t tS =
+        tmem + (static_cast<uint32_t>(quarter * 32) << 16) + x * 256 + half * kCols;
+    float* const my_lse = reinterpret_cast<float*>(gen + L::kLse) + cw * 2 * kCols;
     const float* lse_row = lse + static_cast<int64_t>(bh) * N;
-    // Queries [q_lo, q_hi) see this key; a query tile inside [full_lo, full_hi) is seen by every
-    // key of the tile. (Keys at or past len are left out at the end.)
+    // Queries [q_lo, q_hi) see this key; queries inside [full_lo, full_hi) are seen by every key
+    // of the tile. (Keys at or past len are left out at the end.)
     const int q_lo = mask.lo(key), q_hi = mask.hi(key);
     const int full_lo = mask.lo(k0 + BLOCK_N - 1), full_hi = mask.hi(k0);
-    // -LSE in log2 units of the query this thread stages; -inf where the query adds nothing
-    auto minus_lse = [&](int i) {
-      const int q = i * BLOCK_M + row;
-      if (i >= x1 || q >= mask.len) return -INFINITY;
-      const float v = lse_row[q];
-      return v == -INFINITY ? -INFINITY : -v * kLog2e;
-    };
-    float total = 0.f, comp = 0.f, staged = x1 > x0 ? minus_lse(x0) : 0.f;
-    bool ok = true;
-    for (int i = x0; i < x1; ++i) {
+    // LSE of query q as it is loaded (one tile ahead), and as it is used: negated, in log2 units,
+    // -inf where the query adds nothing
+    auto load_lse = [&](int q) { return q < mask.len ? lse_row[q] : -INFINITY; };
+    auto minus_log2 = [](float v) { return v == -INFINITY ? v : -v * kLog2e; };
+    float total = 0.f, comp = 0.f;
+    int q0 = x0 * BLOCK_M + half * kCols;              // first of the warp's queries of tile i
+    float next0 = x1 > x0 ? load_lse(q0 + lane) : 0.f;
+    float next1 = x1 > x0 ? load_lse(q0 + 32 + lane) : 0.f;
+    for (int i = x0; i < x1; ++i, q0 += BLOCK_M) {
       const int p = (i - x0) & 1;
-      // two buffers: the one written here was last read two tiles ago, before the barrier of
-      // the tile in between
-      my_lse[p * 128 + row] = staged;
-      ptx::named_barrier_sync(1 + x, 128);
-      staged = minus_lse(i + 1);
-      // after a wait has run out the loop goes on without data: every warp meets the barriers
-      if (ok && !ptx::wait_bounded_warp(bar(BAR_S_FULL + 2 * x + p), ((i - x0) / 2) & 1, abort_p,
-                                        kWaitLimitNs)) {
-        ok = false;
-        record_timeout(abort_p);
+      float* const nl = my_lse + p * kCols;
+      nl[lane] = minus_log2(next0);
+      nl[32 + lane] = minus_log2(next1);
+      if (i + 1 < x1) {
+        next0 = load_lse(q0 + BLOCK_M + lane);
+        next1 = load_lse(q0 + BLOCK_M + 32 + lane);
       }
-      if (!ok) continue;
+      __syncwarp();
+      if (!ptx::wait_bounded_warp(bar(BAR_S_FULL + 2 * x + p), ((i - x0) / 2) & 1, abort_p,
+                                  kWaitLimitNs)) {
+        record_timeout(abort_p);
+        break;
+      }
       ptx::tc_fence_after_sync();
-      uint32_t sr[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(tS + p * 128 + c * 32, sr[c]);
+      uint32_t sr[2][32];
+      ptx::tmem_ld_32x32b_x32(tS + p * 128, sr[0]);
+      ptx::tmem_ld_32x32b_x32(tS + p * 128 + 32, sr[1]);
       ptx::tmem_wait_ld();
       ptx::tc_fence_before_sync();
-      ptx::mbar_arrive(bar(BAR_S_EMPTY + 2 * x + p));
-#pragma unroll
-      for (int c = 0; c < 4; ++c) ptx::reg_fence(sr[c]);
-      const int q0 = i * BLOCK_M;
-      const bool full = q0 >= full_lo && q0 + BLOCK_M <= full_hi;
-      const int lo = q_lo - q0, hi = q_hi - q0;
-      float t0 = 0.f, t1 = 0.f, t2 = 0.f, t3 = 0.f;
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float4 nl = *reinterpret_cast<const float4*>(my_lse + p * 128 + 4 * c);
-        const uint32_t(&s)[32] = sr[c / 8];
-        const int o = 4 * (c % 8);
-        float e0, e1, e2, e3;
-        ptx::fma2(e0, e1, __uint_as_float(s[o]), __uint_as_float(s[o + 1]), scale_log2,
-                  scale_log2, nl.x, nl.y);
-        ptx::fma2(e2, e3, __uint_as_float(s[o + 2]), __uint_as_float(s[o + 3]), scale_log2,
-                  scale_log2, nl.z, nl.w);
-        if (!full) {
-          if (4 * c + 0 < lo || 4 * c + 0 >= hi) e0 = -INFINITY;
-          if (4 * c + 1 < lo || 4 * c + 1 >= hi) e1 = -INFINITY;
-          if (4 * c + 2 < lo || 4 * c + 2 >= hi) e2 = -INFINITY;
-          if (4 * c + 3 < lo || 4 * c + 3 >= hi) e3 = -INFINITY;
-        }
-        ptx::add2(t0, t1, t0, t1, ptx::exp2_approx(e0), ptx::exp2_approx(e1));
-        ptx::add2(t2, t3, t2, t3, ptx::exp2_approx(e2), ptx::exp2_approx(e3));
-      }
-      const float y = ((t0 + t1) + (t2 + t3)) - comp;
+      if (lane == 0) ptx::mbar_arrive(bar(BAR_S_EMPTY + 2 * x + p));
+      ptx::reg_fence(sr[0]);
+      ptx::reg_fence(sr[1]);
+      const bool full = q0 >= full_lo && q0 + kCols <= full_hi;
+      const float tile = full ? tile_sum<false>(sr, nl, scale_log2, 0, 0)
+                              : tile_sum<true>(sr, nl, scale_log2, q_lo - q0, q_hi - q0);
+      const float y = tile - comp;
       const float sum = total + y;
       comp = (sum - total) - y;
       total = sum;
     }
-    if (key < N) out[static_cast<int64_t>(bh) * N + key] = key < mask.len ? total : 0.f;
+    // the second half's sums to the first half's threads, of the same key
+    float* const sums = reinterpret_cast<float*>(gen + L::kSums) + x * 128;
+    if (half == 1) sums[row] = total;
+    ptx::named_barrier_sync(1 + x, 256);
+    if (half == 0 && key < N)
+      out[static_cast<int64_t>(bh) * N + key] = key < mask.len ? total + sums[row] : 0.f;
   }
 
   // ------------------------------------------------------------------ teardown
