@@ -9,14 +9,17 @@
 // Keys are the rows: S^T = K Q^T puts one key in each TMEM lane, so that the sum over queries is
 // a sum inside a thread, and the query's LSE is a value that all lanes share (a broadcast read
 // from shared memory). One CTA takes 256 keys (two tiles, A and B) of one (batch, query head),
-// keeps them in shared memory and walks the query tiles that see them:
+// keeps them in shared memory and walks the tiles of 256 queries that see them:
 //   warp 0       TMA producer: K_A, K_B once, then the Q tiles through a ring
-//   warp 1       TMEM allocator and MMA issuer (one thread)
-//   warps 2..17  p = 2^(scale_log2 S - LSE log2 e), summed per key: four warps for each 64 queries
-//                of each key tile. Nothing synchronises them but the S buffers: every warp keeps
-//                its own copy of the LSEs that it needs.
-// Each tile has two S buffers of 128 TMEM columns, so that S(j+1) is computed while S(j) is
-// summed. Two key tiles share every Q tile that is loaded, which halves the reads of Q from L2.
+//   warp 1       TMEM allocator and MMA issuer (one thread): S_A and S_B in turn, 256 columns
+//                each
+//   warps 2..17  p = 2^(scale_log2 S - LSE log2 e), summed per key: four warps for each 64
+//                queries of a tile. Nothing synchronises them but the S buffers: every warp
+//                keeps its own copy of the LSEs that it needs.
+// The warps take S_A into registers while S_B is computed, and sum it while S_A of the next
+// queries is. 256 queries a product: with 128 the tensor pipe was fed with two operands of 4 KB
+// of shared memory for 64 cycles of work, and the products alone took 455 us of the 494 us of
+// B=1 H=16 N=16384 d=128 causal.
 //
 // Sums: 32 bits, a query tile at a time in four chains, the tiles' sums added with Kahan's
 // compensation: a key of a long prompt is the sum of many thousand terms. With shared key heads
@@ -38,7 +41,7 @@ __device__ int g_key_weights_error = 0;
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kStages = 4;                                  // depth of the Q ring
+constexpr int kQueries = 256;                               // queries of a tile
 constexpr int kThreads = 64 + 512;
 constexpr int kCols = 64;                                   // queries of a tile for one warp
 constexpr uint32_t kBoxBytes = BOX_ROWS * BOX_COLS * 2;     // 16 KiB
@@ -48,25 +51,27 @@ constexpr uint32_t kTmemCols = 512;
 
 template <int D>
 struct Smem {
-  static constexpr uint32_t kTile = (D / BOX_COLS) * kBoxBytes;
+  static constexpr int kStages = D == 128 ? 2 : 4;          // depth of the Q ring
+  static constexpr uint32_t kKTile = (D / BOX_COLS) * kBoxBytes;
+  static constexpr uint32_t kQTile = 2 * kKTile;            // 64 columns of 256 queries, twice
   static constexpr uint32_t kK = 0;
-  static constexpr uint32_t kQ = 2 * kTile;
-  static constexpr uint32_t kLse = kQ + kStages * kTile;    // [warp][buffer][64] floats
-  static constexpr uint32_t kSums = kLse + 16 * 2 * kCols * 4;   // [tile][128] floats
-  static constexpr uint32_t kBars = kSums + 2 * 128 * 4;
-  static constexpr uint32_t kDynamic = kBars + 24 * 8 + 1024;
+  static constexpr uint32_t kQ = 2 * kKTile;
+  static constexpr uint32_t kLse = kQ + kStages * kQTile;   // [warp][buffer][64] floats
+  static constexpr uint32_t kSums = kLse + 16 * 2 * kCols * 4;   // [column group][256] floats
+  static constexpr uint32_t kBars = kSums + 4 * 256 * 4;
+  static constexpr uint32_t kDynamic = kBars + 16 * 8 + 1024;
 };
 
 enum : int {
   BAR_K_FULL = 0,
-  BAR_Q_FULL = 1,                         // + stage
-  BAR_Q_EMPTY = BAR_Q_FULL + kStages,     // + stage
-  BAR_S_FULL = BAR_Q_EMPTY + kStages,     // + 2 * tile + buffer
-  BAR_S_EMPTY = BAR_S_FULL + 4,           // + 2 * tile + buffer (one arrival a warp)
-  BAR_MMA_DONE = BAR_S_EMPTY + 4,
-  BAR_COUNT = BAR_MMA_DONE + 1
+  BAR_S_FULL = 1,                         // + tile
+  BAR_S_EMPTY = BAR_S_FULL + 2,           // + tile (one arrival a warp)
+  BAR_MMA_DONE = BAR_S_EMPTY + 2,
+  BAR_Q_FULL = BAR_MMA_DONE + 1,          // + stage
+  BAR_Q_EMPTY = BAR_Q_FULL + 4,           // + stage
+  BAR_COUNT = BAR_Q_EMPTY + 4
 };
-static_assert(BAR_COUNT <= 24, "barrier slots");
+static_assert(BAR_COUNT <= 16, "barrier slots");
 
 __device__ __forceinline__ void record_timeout(volatile int* abort_flag) {
   *abort_flag = 1;
@@ -87,8 +92,8 @@ struct QueryMask {
   // Query tiles [t0, t1) that see a key of the tile starting at k0; t1 <= t0 when none does.
   __device__ __forceinline__ void tile_range(int k0, int& t0, int& t1) const {
     const int a = lo(k0), z = k0 < len ? hi(min(k0 + BLOCK_N, len) - 1) : 0;
-    t0 = z <= a ? 0 : a / BLOCK_M;
-    t1 = z <= a ? 0 : (z + BLOCK_M - 1) / BLOCK_M;
+    t0 = z <= a ? 0 : a / kQueries;
+    t1 = z <= a ? 0 : (z + kQueries - 1) / kQueries;
   }
 };
 
@@ -127,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const int* __restrict__ seqlens, float scale_log2,
                           int heads_per_group) {
   using L = Smem<D>;
+  constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
@@ -167,9 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(BAR_Q_FULL + s), 1);
       ptx::mbar_init(bar(BAR_Q_EMPTY + s), 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      ptx::mbar_init(bar(BAR_S_FULL + i), 1);
-      ptx::mbar_init(bar(BAR_S_EMPTY + i), 8);
+    for (int x = 0; x < 2; ++x) {
+      ptx::mbar_init(bar(BAR_S_FULL + x), 1);
+      ptx::mbar_init(bar(BAR_S_EMPTY + x), 16);
     }
     ptx::mbar_init(bar(BAR_MMA_DONE), 1);
     ptx::fence_barrier_init();
@@ -189,10 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && any_work) {
       ptx::prefetch_tensormap(&tm_q);
       ptx::prefetch_tensormap(&tm_k);
-      ptx::mbar_arrive_expect_tx(bar(BAR_K_FULL), 2 * L::kTile);
+      ptx::mbar_arrive_expect_tx(bar(BAR_K_FULL), 2 * L::kKTile);
       for (int x = 0; x < 2; ++x)
         for (int c = 0; c < D / BOX_COLS; ++c)
-          ptx::tma_load_4d(sK + x * L::kTile + c * kBoxBytes, &tm_k, bar(BAR_K_FULL),
+          ptx::tma_load_4d(sK + x * L::kKTile + c * kBoxBytes, &tm_k, bar(BAR_K_FULL),
                            c * BOX_COLS, h / G, (2 * kblk + x) * BLOCK_N, b);
       int issued = 0;
       for (int n = 0; n < u1 - u0; ++n) {
@@ -202,10 +208,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           record_timeout(abort_p);
           break;
         }
-        ptx::mbar_arrive_expect_tx(bar(BAR_Q_FULL + s), L::kTile);
+        ptx::mbar_arrive_expect_tx(bar(BAR_Q_FULL + s), L::kQTile);
         for (int c = 0; c < D / BOX_COLS; ++c)
-          ptx::tma_load_4d(sQ + s * L::kTile + c * kBoxBytes, &tm_q, bar(BAR_Q_FULL + s),
-                           c * BOX_COLS, h, (u0 + n) * BLOCK_M, b);
+          for (int r = 0; r < 2; ++r)
+            ptx::tma_load_4d(sQ + s * L::kQTile + (2 * c + r) * kBoxBytes, &tm_q,
+                             bar(BAR_Q_FULL + s), c * BOX_COLS, h,
+                             (u0 + n) * kQueries + r * BOX_ROWS, b);
         issued = n + 1;
       }
       // Leave no copy in flight (on the normal path these phases completed long ago).
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = ptx::idesc_f16(FP16, BLOCK_N, BLOCK_M, false);
+      constexpr uint32_t idesc = ptx::idesc_f16(FP16, BLOCK_N, kQueries, false);
       auto wait = [&](int slot, uint32_t parity) {
         return ptx::wait_bounded(bar(slot), parity, abort_p, kWaitLimitNs);
       };
@@ -225,22 +233,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = u0; ok && i < u1; ++i) {
         const int n = i - u0, s = n % kStages;
         if (!wait(BAR_Q_FULL + s, (n / kStages) & 1)) { ok = false; break; }
-        const ptx::SmemDesc q_desc = ptx::smem_desc_sw128_split(sQ + s * L::kTile, 16, 1024);
+        const ptx::SmemDesc q_desc = ptx::smem_desc_sw128_split(sQ + s * L::kQTile, 16, 1024);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int x0 = x ? b0 : a0, x1 = x ? b1 : a1;
           if (i < x0 || i >= x1) continue;
-          const int p = (i - x0) & 1;
-          if (!wait(BAR_S_EMPTY + 2 * x + p, (((i - x0) / 2) & 1) ^ 1)) { ok = false; break; }
+          if (!wait(BAR_S_EMPTY + x, ((i - x0) & 1) ^ 1)) { ok = false; break; }
           ptx::tc_fence_after_sync();
-          const ptx::SmemDesc k_desc = ptx::smem_desc_sw128_split(sK + x * L::kTile, 16, 1024);
+          const ptx::SmemDesc k_desc = ptx::smem_desc_sw128_split(sK + x * L::kKTile, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * kBoxBytes + (kk % 4) * 32;
-            ptx::mma_f16_ss(tmem + x * 256 + p * 128, k_desc.at(off), q_desc.at(off), idesc,
-                            kk > 0);
-          }
-          ptx::mma_commit(bar(BAR_S_FULL + 2 * x + p));
+          for (int kk = 0; kk < D / 16; ++kk)
+            ptx::mma_f16_ss(tmem + x * kQueries, k_desc.at((kk / 4) * kBoxBytes + (kk % 4) * 32),
+                            q_desc.at((kk / 4) * 2 * kBoxBytes + (kk % 4) * 32), idesc, kk > 0);
+          ptx::mma_commit(bar(BAR_S_FULL + x));
         }
         ptx::mma_commit(bar(BAR_Q_EMPTY + s));
       }
@@ -252,65 +257,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ sums over queries
-    const int cw = warp - 2, x = cw / 8, half = cw / 4 % 2;   // key tile, 64-query half
+    const int cw = warp - 2, group = cw / 4;           // 64 of the tile's queries
     const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;               // TMEM lane = key of the tile
-    const int k0 = (2 * kblk + x) * BLOCK_N, key = k0 + row;
-    const int x0 = x ? b0 : a0, x1 = x ? b1 : a1;
-    const uint32_t tS =
-        tmem + (static_cast<uint32_t>(quarter * 32) << 16) + x * 256 + half * kCols;
+    const int row = quarter * 32 + lane;               // TMEM lane = key of a tile
+    const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * kCols;
     float* const my_lse = reinterpret_cast<float*>(gen + L::kLse) + cw * 2 * kCols;
     const float* lse_row = lse + static_cast<int64_t>(bh) * N;
-    // Queries [q_lo, q_hi) see this key; queries inside [full_lo, full_hi) are seen by every key
-    // of the tile. (Keys at or past len are left out at the end.)
-    const int q_lo = mask.lo(key), q_hi = mask.hi(key);
-    const int full_lo = mask.lo(k0 + BLOCK_N - 1), full_hi = mask.hi(k0);
     // LSE of query q as it is loaded (one tile ahead), and as it is used: negated, in log2 units,
     // -inf where the query adds nothing
     auto load_lse = [&](int q) { return q < mask.len ? lse_row[q] : -INFINITY; };
     auto minus_log2 = [](float v) { return v == -INFINITY ? v : -v * kLog2e; };
-    float total = 0.f, comp = 0.f;
-    int q0 = x0 * BLOCK_M + half * kCols;              // first of the warp's queries of tile i
-    float next0 = x1 > x0 ? load_lse(q0 + lane) : 0.f;
-    float next1 = x1 > x0 ? load_lse(q0 + 32 + lane) : 0.f;
-    for (int i = x0; i < x1; ++i, q0 += BLOCK_M) {
-      const int p = (i - x0) & 1;
-      float* const nl = my_lse + p * kCols;
+    float total[2] = {0.f, 0.f}, comp[2] = {0.f, 0.f};
+    int q0 = u0 * kQueries + group * kCols;            // first of the warp's queries of tile i
+    float next0 = any_work ? load_lse(q0 + lane) : 0.f;
+    float next1 = any_work ? load_lse(q0 + 32 + lane) : 0.f;
+    bool ok = true;
+    for (int i = u0; ok && i < u1; ++i, q0 += kQueries) {
+      float* const nl = my_lse + (i & 1) * kCols;
       nl[lane] = minus_log2(next0);
       nl[32 + lane] = minus_log2(next1);
-      if (i + 1 < x1) {
-        next0 = load_lse(q0 + BLOCK_M + lane);
-        next1 = load_lse(q0 + BLOCK_M + 32 + lane);
+      if (i + 1 < u1) {
+        next0 = load_lse(q0 + kQueries + lane);
+        next1 = load_lse(q0 + kQueries + 32 + lane);
       }
       __syncwarp();
-      if (!ptx::wait_bounded_warp(bar(BAR_S_FULL + 2 * x + p), ((i - x0) / 2) & 1, abort_p,
-                                  kWaitLimitNs)) {
-        record_timeout(abort_p);
-        break;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int x0 = x ? b0 : a0, x1 = x ? b1 : a1;
+        if (i < x0 || i >= x1) continue;
+        if (!ptx::wait_bounded_warp(bar(BAR_S_FULL + x), (i - x0) & 1, abort_p, kWaitLimitNs)) {
+          record_timeout(abort_p);
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after_sync();
+        uint32_t sr[2][32];
+        ptx::tmem_ld_32x32b_x32(tS + x * kQueries, sr[0]);
+        ptx::tmem_ld_32x32b_x32(tS + x * kQueries + 32, sr[1]);
+        ptx::tmem_wait_ld();
+        ptx::tc_fence_before_sync();
+        if (lane == 0) ptx::mbar_arrive(bar(BAR_S_EMPTY + x));
+        ptx::reg_fence(sr[0]);
+        ptx::reg_fence(sr[1]);
+        // Queries [q_lo, q_hi) see this key; 64 queries inside [lo(last key), hi(first key)) are
+        // seen by every key of the tile. (Keys at or past len are left out at the end.)
+        const int k0 = (2 * kblk + x) * BLOCK_N;
+        const bool full = q0 >= mask.lo(k0 + BLOCK_N - 1) && q0 + kCols <= mask.hi(k0);
+        const float tile = full ? tile_sum<false>(sr, nl, scale_log2, 0, 0)
+                                : tile_sum<true>(sr, nl, scale_log2, mask.lo(k0 + row) - q0,
+                                                 mask.hi(k0 + row) - q0);
+        const float y = tile - comp[x];
+        const float sum = total[x] + y;
+        comp[x] = (sum - total[x]) - y;
+        total[x] = sum;
       }
-      ptx::tc_fence_after_sync();
-      uint32_t sr[2][32];
-      ptx::tmem_ld_32x32b_x32(tS + p * 128, sr[0]);
-      ptx::tmem_ld_32x32b_x32(tS + p * 128 + 32, sr[1]);
-      ptx::tmem_wait_ld();
-      ptx::tc_fence_before_sync();
-      if (lane == 0) ptx::mbar_arrive(bar(BAR_S_EMPTY + 2 * x + p));
-      ptx::reg_fence(sr[0]);
-      ptx::reg_fence(sr[1]);
-      const bool full = q0 >= full_lo && q0 + kCols <= full_hi;
-      const float tile = full ? tile_sum<false>(sr, nl, scale_log2, 0, 0)
-                              : tile_sum<true>(sr, nl, scale_log2, q_lo - q0, q_hi - q0);
-      const float y = tile - comp;
-      const float sum = total + y;
-      comp = (sum - total) - y;
-      total = sum;
     }
-    // the second half's sums to the first half's threads, of the same key
-    float* const sums = reinterpret_cast<float*>(gen + L::kSums) + x * 128;
-    if (half == 1) sums[row] = total;
-    ptx::named_barrier_sync(1 + x, 256);
-    if (half == 0 && key < N)
-      out[static_cast<int64_t>(bh) * N + key] = key < mask.len ? total + sums[row] : 0.f;
+    // the four column groups' sums of each key, added in their order
+    float* const sums = reinterpret_cast<float*>(gen + L::kSums);
+    sums[group * 256 + row] = total[0];
+    sums[group * 256 + 128 + row] = total[1];
+    ptx::named_barrier_sync(1, 512);
+    const int at = threadIdx.x - 64, key = 2 * kblk * BLOCK_N + at;
+    if (at < 256 && key < N) {
+      const float sum = (sums[at] + sums[256 + at]) + (sums[512 + at] + sums[768 + at]);
+      out[static_cast<int64_t>(bh) * N + key] = key < mask.len ? sum : 0.f;
+    }
   }
 
   // ------------------------------------------------------------------ teardown
