@@ -13,13 +13,15 @@
 //   warp 0       TMA producer: K_A, K_B once, then the Q tiles through a ring
 //   warp 1       TMEM allocator and MMA issuer (one thread): S_A and S_B in turn, 256 columns
 //                each
-//   warps 2..17  p = 2^(scale_log2 S - LSE log2 e), summed per key: four warps for each 64
-//                queries of a tile. Nothing synchronises them but the S buffers: every warp
-//                keeps its own copy of the LSEs that it needs.
-// The warps take S_A into registers while S_B is computed, and sum it while S_A of the next
-// queries is. 256 queries a product: with 128 the tensor pipe was fed with two operands of 4 KB
-// of shared memory for 64 cycles of work, and the products alone took 455 us of the 494 us of
-// B=1 H=16 N=16384 d=128 causal.
+//   warps 2..9   S_A: p = 2^(scale_log2 S - LSE log2 e), summed per key, four warps for each 128
+//                queries of the tile; warps 10..17 the same for S_B. Nothing synchronises them
+//                but the S buffers: every warp keeps its own copy of the LSEs that it needs.
+// One half of the warps sums S_A while S_B is computed, and the other way round. Measured on B=1
+// H=16 N=16384 d=128 causal: 400 us (1374 TFLOP/s), of which the products alone take 309 and the
+// sums alone 375: the exponentials (32 a cycle and SM) and the instructions around them are
+// what is left. Slower: all sixteen warps on S_A, then on S_B (421 us); eight warps with twice
+// the columns (427); 32-column loads of S one ahead of the sums (439); products with 128
+// queries, whose operands are 8 KB of shared memory for 64 cycles of work (494).
 //
 // Sums: 32 bits, a query tile at a time in four chains, the tiles' sums added with Kahan's
 // compensation: a key of a long prompt is the sum of many thousand terms. With shared key heads
@@ -43,7 +45,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kQueries = 256;                               // queries of a tile
 constexpr int kThreads = 64 + 512;
-constexpr int kCols = 64;                                   // queries of a tile for one warp
+constexpr int kCols = 64;                                   // columns of S in registers
 constexpr uint32_t kBoxBytes = BOX_ROWS * BOX_COLS * 2;     // 16 KiB
 constexpr uint64_t kWaitLimitNs = 1000000000ull;            // 1 s per wait
 constexpr int kErrTimeout = -8;                             // FA_ERR_TIMEOUT
@@ -56,9 +58,9 @@ struct Smem {
   static constexpr uint32_t kQTile = 2 * kKTile;            // 64 columns of 256 queries, twice
   static constexpr uint32_t kK = 0;
   static constexpr uint32_t kQ = 2 * kKTile;
-  static constexpr uint32_t kLse = kQ + kStages * kQTile;   // [warp][buffer][64] floats
-  static constexpr uint32_t kSums = kLse + 16 * 2 * kCols * 4;   // [column group][256] floats
-  static constexpr uint32_t kBars = kSums + 4 * 256 * 4;
+  static constexpr uint32_t kLse = kQ + kStages * kQTile;   // [warp][buffer][128] floats
+  static constexpr uint32_t kSums = kLse + 16 * 2 * 128 * 4;   // [half][256] floats
+  static constexpr uint32_t kBars = kSums + 2 * 256 * 4;
   static constexpr uint32_t kDynamic = kBars + 16 * 8 + 1024;
 };
 
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       ptx::mbar_init(bar(BAR_S_FULL + x), 1);
-      ptx::mbar_init(bar(BAR_S_EMPTY + x), 16);
+      ptx::mbar_init(bar(BAR_S_EMPTY + x), 8);
     }
     ptx::mbar_init(bar(BAR_MMA_DONE), 1);
     ptx::fence_barrier_init();
@@ -257,71 +259,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ sums over queries
-    const int cw = warp - 2, group = cw / 4;           // 64 of the tile's queries
+    const int cw = warp - 2, x = cw / 8, half = cw / 4 % 2;   // key tile; 128 of the queries
     const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;               // TMEM lane = key of a tile
-    const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * kCols;
-    float* const my_lse = reinterpret_cast<float*>(gen + L::kLse) + cw * 2 * kCols;
+    const int row = quarter * 32 + lane;               // TMEM lane = key of the tile
+    const int k0 = (2 * kblk + x) * BLOCK_N, key = k0 + row;
+    const int x0 = x ? b0 : a0, x1 = x ? b1 : a1;
+    const uint32_t tS =
+        tmem + (static_cast<uint32_t>(quarter * 32) << 16) + x * kQueries + half * 128;
+    float* const my_lse = reinterpret_cast<float*>(gen + L::kLse) + cw * 2 * 128;
     const float* lse_row = lse + static_cast<int64_t>(bh) * N;
     // LSE of query q as it is loaded (one tile ahead), and as it is used: negated, in log2 units,
     // -inf where the query adds nothing
     auto load_lse = [&](int q) { return q < mask.len ? lse_row[q] : -INFINITY; };
     auto minus_log2 = [](float v) { return v == -INFINITY ? v : -v * kLog2e; };
-    float total[2] = {0.f, 0.f}, comp[2] = {0.f, 0.f};
-    int q0 = u0 * kQueries + group * kCols;            // first of the warp's queries of tile i
-    float next0 = any_work ? load_lse(q0 + lane) : 0.f;
-    float next1 = any_work ? load_lse(q0 + 32 + lane) : 0.f;
+    float total = 0.f, comp = 0.f;
+    int q0 = x0 * kQueries + half * 128;               // first of the warp's queries of tile i
+    // Queries [q_lo, q_hi) see this key; queries inside [full_lo, full_hi) are seen by every key
+    // of the tile. (Keys at or past len are left out at the end.)
+    const int q_lo = mask.lo(key), q_hi = mask.hi(key);
+    const int full_lo = mask.lo(k0 + BLOCK_N - 1), full_hi = mask.hi(k0);
+    float next[4] = {0.f, 0.f, 0.f, 0.f};
+    if (x1 > x0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) next[e] = load_lse(q0 + 32 * e + lane);
+    }
     bool ok = true;
-    for (int i = u0; ok && i < u1; ++i, q0 += kQueries) {
-      float* const nl = my_lse + (i & 1) * kCols;
-      nl[lane] = minus_log2(next0);
-      nl[32 + lane] = minus_log2(next1);
-      if (i + 1 < u1) {
-        next0 = load_lse(q0 + kQueries + lane);
-        next1 = load_lse(q0 + kQueries + 32 + lane);
+    for (int i = x0; i < x1; ++i, q0 += kQueries) {
+      float* const nl = my_lse + (i & 1) * 128;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) nl[32 * e + lane] = minus_log2(next[e]);
+      if (i + 1 < x1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) next[e] = load_lse(q0 + kQueries + 32 * e + lane);
       }
       __syncwarp();
+      if (!ptx::wait_bounded_warp(bar(BAR_S_FULL + x), (i - x0) & 1, abort_p, kWaitLimitNs)) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after_sync();
+      float tile = 0.f;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int x0 = x ? b0 : a0, x1 = x ? b1 : a1;
-        if (i < x0 || i >= x1) continue;
-        if (!ptx::wait_bounded_warp(bar(BAR_S_FULL + x), (i - x0) & 1, abort_p, kWaitLimitNs)) {
-          record_timeout(abort_p);
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after_sync();
+      for (int hf = 0; hf < 2; ++hf) {
         uint32_t sr[2][32];
-        ptx::tmem_ld_32x32b_x32(tS + x * kQueries, sr[0]);
-        ptx::tmem_ld_32x32b_x32(tS + x * kQueries + 32, sr[1]);
+        ptx::tmem_ld_32x32b_x32(tS + 64 * hf, sr[0]);
+        ptx::tmem_ld_32x32b_x32(tS + 64 * hf + 32, sr[1]);
         ptx::tmem_wait_ld();
-        ptx::tc_fence_before_sync();
-        if (lane == 0) ptx::mbar_arrive(bar(BAR_S_EMPTY + x));
+        if (hf == 1) {
+          ptx::tc_fence_before_sync();
+          if (lane == 0) ptx::mbar_arrive(bar(BAR_S_EMPTY + x));
+        }
         ptx::reg_fence(sr[0]);
         ptx::reg_fence(sr[1]);
-        // Queries [q_lo, q_hi) see this key; 64 queries inside [lo(last key), hi(first key)) are
-        // seen by every key of the tile. (Keys at or past len are left out at the end.)
-        const int k0 = (2 * kblk + x) * BLOCK_N;
-        const bool full = q0 >= mask.lo(k0 + BLOCK_N - 1) && q0 + kCols <= mask.hi(k0);
-        const float tile = full ? tile_sum<false>(sr, nl, scale_log2, 0, 0)
-                                : tile_sum<true>(sr, nl, scale_log2, mask.lo(k0 + row) - q0,
-                                                 mask.hi(k0 + row) - q0);
-        const float y = tile - comp[x];
-        const float sum = total[x] + y;
-        comp[x] = (sum - total[x]) - y;
-        total[x] = sum;
+        const int q = q0 + 64 * hf;
+        const bool full = q >= full_lo && q + 64 <= full_hi;
+        tile += full ? tile_sum<false>(sr, nl + 64 * hf, scale_log2, 0, 0)
+                     : tile_sum<true>(sr, nl + 64 * hf, scale_log2, q_lo - q, q_hi - q);
       }
+      const float y = tile - comp;
+      const float sum = total + y;
+      comp = (sum - total) - y;
+      total = sum;
     }
-    // the four column groups' sums of each key, added in their order
+    if (!ok) record_timeout(abort_p);
+    // the two halves' sums of each key
     float* const sums = reinterpret_cast<float*>(gen + L::kSums);
-    sums[group * 256 + row] = total[0];
-    sums[group * 256 + 128 + row] = total[1];
+    sums[half * 256 + x * 128 + row] = total;
     ptx::named_barrier_sync(1, 512);
-    const int at = threadIdx.x - 64, key = 2 * kblk * BLOCK_N + at;
-    if (at < 256 && key < N) {
-      const float sum = (sums[at] + sums[256 + at]) + (sums[512 + at] + sums[768 + at]);
-      out[static_cast<int64_t>(bh) * N + key] = key < mask.len ? sum : 0.f;
-    }
+    const int at = threadIdx.x - 64, okey = 2 * kblk * BLOCK_N + at;
+    if (at < 256 && okey < N)
+      out[static_cast<int64_t>(bh) * N + okey] = okey < mask.len ? sums[at] + sums[256 + at] : 0.f;
   }
 
   // ------------------------------------------------------------------ teardown
