@@ -17,8 +17,8 @@
 // CTAs on each SM), whatever the lengths are: a long sequence alone fills the GPU and a batch of
 // unequal ones is balanced without the host knowing the lengths. A run that covers a whole unit
 // writes O and LSE; one that covers a part leaves the part's running maximum, sum and
-// unnormalised O (fp32) in the workspace, and a second kernel joins the parts of a unit in
-// their order. Each CTA recomputes where its run starts from seqlens.
+// unnormalised O (fp32) in the workspace, and a second kernel joins the parts of a unit in a
+// fixed order. Each CTA recomputes where its run starts from seqlens.
 //
 // One CTA: warp 4 loads (TMA boxes of up to 64 rows of a page, all d columns of one head, into a
 // ring of three tiles of K and V, 128-byte swizzle); warps 0..3 each take 16 tokens of every tile
@@ -29,7 +29,7 @@
 // into one fp32 accumulator: O then carries the rounding of the output alone.
 //
 // Weights need the final LSE: the scaled scores are kept (fp32, 4 G bytes a token against the
-// 4 d of K and V) and a last kernel adds exp2(score - maximum) / sum over the group's heads.
+// 4 d of K and V) and the second kernel adds exp2(score - maximum) / sum over the group's heads.
 #include <algorithm>
 
 #include "fa_paged.cuh"
@@ -72,7 +72,10 @@ struct Args {
   float* weights;
   float* part_o;      // [2 * CTAs][16][D]: CTA c's first run at slot 2c, its last at 2c + 1
   float2* part_ml;    // [2 * CTAs][16]: maximum (log2 units) and sum of the part
-  float2* stats;      // [B * Hq]: maximum and 1 / sum, when the cache keeps weights
+  int2* units;        // [B * Hkv * blocks]: slot of the unit's first part, number of parts (0: the
+                      // unit was one run's, and is written)
+  float2* stats;      // [B * Hq]: maximum and 1 / sum of a head that one run covered, when the
+                      // cache keeps weights
   float* scores;      // [B * Hq][capacity], log2 units, when the cache keeps weights
   int B, Hq, Hkv, G, blocks;   // blocks of 16 query heads for each key head
   int page_size, num_pages, max_pages, capacity, box_rows;
@@ -92,22 +95,13 @@ __device__ __forceinline__ Tiles tiles_of(const Args& a, int b) {
   return {v.lo, v.hi, first, max(1, (v.hi - 1) / kTile + 1 - first)};
 }
 
-// Tiles of a unit summed over the sequences before `until` and over all of them, by one warp.
-__device__ __forceinline__ void count_tiles(const Args& a, int until, int64_t* before,
-                                            int64_t* all) {
-  int64_t x = 0, y = 0;
-  for (int b = threadIdx.x % 32; b < a.B; b += 32) {
-    const int n = tiles_of<false>(a, b).count;
-    x += n;
-    if (b < until) y += n;
-  }
+// Tiles of a unit summed over all sequences, by one warp.
+__device__ __forceinline__ int64_t count_tiles(const Args& a) {
+  int64_t x = 0;
+  for (int b = threadIdx.x % 32; b < a.B; b += 32) x += tiles_of<false>(a, b).count;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, off);
-    y += __shfl_xor_sync(0xffffffffu, y, off);
-  }
-  *all = x;
-  *before = y;
+  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
 }
 
 // CTAs that get a run: every one of them at least a tile, so that no part of a unit is empty.
@@ -230,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   using L = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag, s_seq;
-  __shared__ int64_t s_at, s_left;
+  __shared__ int64_t s_at, s_left, s_start, s_total;
   const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* const gen = smem_raw + (base - ptx::smem_addr(smem_raw));
   auto full = [&](int s) { return base + L::kBars + 8u * s; };
@@ -249,9 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   // where this CTA's run starts: the sequence, and the tile within it
   if (warp == 0) {
-    int64_t unused, per_unit;
-    count_tiles(a, 0, &unused, &per_unit);
-    const int64_t total = per_unit * a.Hkv * a.blocks;
+    const int64_t total = count_tiles(a) * a.Hkv * a.blocks;
     const int ctas = running(total, gridDim.x);
     const int64_t start = run_start(total, cta, ctas);
     // the last sequence whose first tile is at or before `start`
@@ -282,6 +274,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       s_seq = seq;
       s_at = at;
       s_left = cta < ctas ? run_start(total, cta + 1, ctas) - start : 0;
+      s_start = start;
+      s_total = total;
     }
   }
   __syncthreads();
@@ -547,6 +541,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         l += sm_l[w * kRows + r] * ptx::exp2_approx(sm_m[w * kRows + r] - u);
     };
     const int64_t slot = 2ll * cta + (runs > 0);
+    if (sg.tile == 0 && threadIdx.x == 0) {
+      // this run holds the unit's first tile; its last is in the last run that starts before
+      // the unit's end: the largest c with floor(total * c / ctas) < end
+      const int ctas = running(s_total, gridDim.x);
+      const int64_t end = s_start + n - sg.count + t.count;
+      const int last = static_cast<int>((end * ctas - 1) / s_total);
+      a.units[static_cast<int64_t>(sg.b) * a.Hkv * a.blocks + sg.unit] =
+          make_int2(static_cast<int>(slot), sg.whole ? 0 : last - cta + 1);
+    }
     if (threadIdx.x < kRows) {
       float m, l;
       row_stats(threadIdx.x, m, l);
@@ -601,104 +604,124 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins the parts of every unit that more than one run covers: one block per (b, h).
-template <int D, bool FP16, bool WEIGHTS>
-__global__ void __launch_bounds__(128)
-    fa_paged_join_kernel(const __grid_constant__ Args a, int grid) {
-  constexpr int kLanes = D / 4, kSets = 128 / kLanes;   // threads of a part's row; parts at once
-  launch_dependents();
-  wait_prerequisites();
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  __shared__ int64_t s_before, s_all;
-  __shared__ float4 s_acc[kSets][kLanes];
-  __shared__ float s_l[kSets];
-  if (threadIdx.x < 32) {
-    int64_t before, all;
-    count_tiles(a, b, &before, &all);
-    if (threadIdx.x == 0) {
-      s_before = before;
-      s_all = all;
-    }
-  }
-  __syncthreads();
-  const int64_t units = static_cast<int64_t>(a.Hkv) * a.blocks;
-  const int64_t total = s_all * units;
-  const int ctas = running(total, grid);
-  const int nt = tiles_of<false>(a, b).count;
-  const int unit = h / a.G * a.blocks + h % a.G / kRows, row = h % a.G % kRows;
-  const int64_t start = s_before * units + static_cast<int64_t>(unit) * nt;
-  // the run that holds tile x: the largest c with floor(total * c / ctas) <= x
-  const int first = static_cast<int>(((start + 1) * ctas - 1) / total);
-  const int last = static_cast<int>(((start + nt) * ctas - 1) / total);
-  if (first == last) return;   // one run covers the unit: written already
-  const int skip = run_start(total, first, ctas) < start;   // the first part is its CTA's last
-  auto slot = [&](int c) { return 2ll * c + (c == first ? skip : 0); };
-  float m = -INFINITY;
-  for (int c = first; c <= last; ++c) m = fmaxf(m, a.part_ml[slot(c) * kRows + row].x);
+// After the runs, in one launch: blocks [0, B * Hq) join the parts of a query head whose unit
+// more than one run covers; with weights, the blocks behind them add the probabilities to the
+// weights, 1024 tokens of a (sequence, key head) each. These need every head's final maximum and
+// sum, and join those (not O) themselves instead of waiting for the others.
+constexpr int kFinishThreads = 256;
+
+// Maximum (log2 units) and sum of row `row` of a unit of `info` parts, by one warp (every lane
+// gets them). The part in the first run's slot is followed by those of the next CTAs, each in
+// its CTA's first slot.
+__device__ __forceinline__ int part_slot(int2 info, int p) {
+  return p == 0 ? info.x : 2 * (info.x / 2 + p);
+}
+__device__ __forceinline__ float2 join_stats(const Args& a, int2 info, int row) {
+  const int lane = threadIdx.x % 32;
+  float m = -INFINITY, l = 0.f;
+  for (int p = lane; p < info.y; p += 32)
+    m = fmaxf(m, a.part_ml[part_slot(info, p) * kRows + row].x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   const float u = m == -INFINITY ? 0.f : m;
+  for (int p = lane; p < info.y; p += 32) {
+    const float2 ml = a.part_ml[part_slot(info, p) * kRows + row];
+    l += ml.y * ptx::exp2_approx(ml.x - u);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  return make_float2(m, l);
+}
+__device__ __forceinline__ int2 unit_info(const Args& a, int b, int h) {
+  const int unit = h / a.G * a.blocks + h % a.G / kRows;
+  return a.units[static_cast<int64_t>(b) * a.Hkv * a.blocks + unit];
+}
+
+template <int D, bool FP16>
+__device__ __forceinline__ void join_head(const Args& a, int64_t head) {
+  constexpr int kLanes = D / 4, kSets = kFinishThreads / kLanes;   // threads of a row; parts at once
+  __shared__ float4 s_acc[kSets][kLanes];
+  const int b = static_cast<int>(head / a.Hq), h = static_cast<int>(head % a.Hq);
+  const int row = h % a.G % kRows;
+  const int2 info = unit_info(a, b, h);
+  if (info.y == 0) return;   // one run covered the unit: written already
+  const float2 ml = join_stats(a, info, row);
+  const float u = ml.x == -INFINITY ? 0.f : ml.x;
   const int set = threadIdx.x / kLanes, x = threadIdx.x % kLanes;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int c = first + set; c <= last; c += kSets) {
-    const float2 ml = a.part_ml[slot(c) * kRows + row];
-    const float f = ptx::exp2_approx(ml.x - u);
-    const float4 v =
-        *reinterpret_cast<const float4*>(a.part_o + (slot(c) * kRows + row) * D + 4 * x);
-    l += ml.y * f;
+#pragma unroll 4
+  for (int p = set; p < info.y; p += kSets) {
+    const int64_t at = static_cast<int64_t>(part_slot(info, p)) * kRows + row;
+    const float f = ptx::exp2_approx(a.part_ml[at].x - u);
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + 4 * x);
     acc.x += v.x * f;
     acc.y += v.y * f;
     acc.z += v.z * f;
     acc.w += v.w * f;
   }
   s_acc[set][x] = acc;
-  if (x == 0) s_l[set] = l;
   __syncthreads();
   if (threadIdx.x >= kLanes) return;
-  l = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int y = 0; y < kSets; ++y) {
-    l += s_l[y];
+  acc = s_acc[0][x];
+  for (int y = 1; y < kSets; ++y) {
     acc.x += s_acc[y][x].x;
     acc.y += s_acc[y][x].y;
     acc.z += s_acc[y][x].z;
     acc.w += s_acc[y][x].w;
   }
-  const float inv = inverse(l);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + static_cast<int64_t>(blockIdx.x) * D +
-                            4 * x) = make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv),
-                                                pack2<FP16>(acc.z * inv, acc.w * inv));
-  if (x == 0) {
-    a.lse[blockIdx.x] = lse_of(m, l);
-    if constexpr (WEIGHTS) a.stats[blockIdx.x] = make_float2(m, inverse(l));
-  }
+  const float inv = inverse(ml.y);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + head * D + 4 * x) = make_uint2(
+      pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
+  if (x == 0) a.lse[head] = lse_of(ml.x, ml.y);
 }
 
 // weights[page, hk, row] += sum over the group's heads of 2^(score - maximum) / sum. Four
-// tokens a thread (one 16-byte load of each head's scores), 1024 a block. Every weight gets one
-// addition from each sequence that holds its page, as an atomic so that sequences may share
-// pages; where none does the result has one order only.
-__global__ void __launch_bounds__(256)
-    fa_paged_add_weights_kernel(const __grid_constant__ Args a, int chunks) {
-  wait_prerequisites();
-  const int64_t unit = blockIdx.x / chunks;
-  const int chunk = blockIdx.x % chunks;
+// tokens a thread (one 16-byte load of each head's scores). Every weight gets one addition from
+// each sequence that holds its page, as an atomic so that sequences may share pages; where none
+// does the result has one order only.
+__device__ __forceinline__ void add_weights(const Args& a, int64_t unit, int chunk) {
+  constexpr int kHeads = 64;
+  __shared__ float2 s_stat[kHeads];   // maximum and 1 / sum
   const int b = static_cast<int>(unit / a.Hkv), hk = static_cast<int>(unit % a.Hkv);
   const Visible v = visible_tokens<false>(a.seqlens, b, a.capacity, a.window_left);
-  const int t0 = (v.lo / 4 + chunk * 256 + static_cast<int>(threadIdx.x)) * 4;
-  if (t0 >= v.hi) return;
-  const int page = a.table[static_cast<int64_t>(b) * a.max_pages + t0 / a.page_size];
-  if (page < 0 || page >= a.num_pages) return;   // recorded by the main kernel
+  const int first = (v.lo / 4 + chunk * kFinishThreads) * 4;
+  if (first >= v.hi) return;
+  const int t0 = first + static_cast<int>(threadIdx.x) * 4;
+  const int page = t0 < v.hi ? a.table[static_cast<int64_t>(b) * a.max_pages + t0 / a.page_size]
+                             : -1;
+  const bool in = page >= 0 && page < a.num_pages;   // a bad page was recorded by the runs
   const int64_t head0 = static_cast<int64_t>(b) * a.Hq + hk * a.G;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int g = 0; g < a.G; ++g) {
-    const float4 s = *reinterpret_cast<const float4*>(a.scores + (head0 + g) * a.capacity + t0);
-    const float2 st = a.stats[head0 + g];
-    const float u = st.x == -INFINITY ? 0.f : st.x;
-    sum.x += ptx::exp2_approx(s.x - u) * st.y;
-    sum.y += ptx::exp2_approx(s.y - u) * st.y;
-    sum.z += ptx::exp2_approx(s.z - u) * st.y;
-    sum.w += ptx::exp2_approx(s.w - u) * st.y;
+  for (int g0 = 0; g0 < a.G; g0 += kHeads) {
+    const int heads = min(kHeads, a.G - g0);
+    for (int g = threadIdx.x / 32; g < heads; g += kFinishThreads / 32) {
+      const int h = hk * a.G + g0 + g;
+      const int2 info = unit_info(a, b, h);
+      float2 st;
+      if (info.y == 0) {
+        st = a.stats[static_cast<int64_t>(b) * a.Hq + h];
+      } else {
+        st = join_stats(a, info, (g0 + g) % kRows);
+        st.y = inverse(st.y);
+      }
+      if (threadIdx.x % 32 == 0) s_stat[g] = make_float2(st.x == -INFINITY ? 0.f : st.x, st.y);
+    }
+    __syncthreads();
+    if (in) {
+#pragma unroll 4
+      for (int g = 0; g < heads; ++g) {
+        const float4 s =
+            *reinterpret_cast<const float4*>(a.scores + (head0 + g0 + g) * a.capacity + t0);
+        const float2 st = s_stat[g];
+        sum.x += ptx::exp2_approx(s.x - st.x) * st.y;
+        sum.y += ptx::exp2_approx(s.y - st.x) * st.y;
+        sum.z += ptx::exp2_approx(s.z - st.x) * st.y;
+        sum.w += ptx::exp2_approx(s.w - st.x) * st.y;
+      }
+    }
+    __syncthreads();
   }
+  if (!in) return;
   float* w = a.weights + (static_cast<int64_t>(page) * a.Hkv + hk) * a.page_size +
              t0 % a.page_size;
   if (t0 >= v.lo && t0 + 4 <= v.hi) {
@@ -709,6 +732,17 @@ __global__ void __launch_bounds__(256)
     for (int i = 0; i < 4; ++i)
       if (t0 + i >= v.lo && t0 + i < v.hi) ptx::red_add_f32(w + i, each[i]);
   }
+}
+
+template <int D, bool FP16, bool WEIGHTS>
+__global__ void __launch_bounds__(kFinishThreads)
+    fa_paged_finish_kernel(const __grid_constant__ Args a, int64_t heads, int chunks) {
+  wait_prerequisites();
+  const int64_t at = blockIdx.x;
+  if (at < heads)
+    join_head<D, FP16>(a, at);
+  else if constexpr (WEIGHTS)
+    add_weights(a, (at - heads) / chunks, static_cast<int>((at - heads) % chunks));
 }
 
 // k_pages or v_pages as a 5-D TMA map: 64 columns, head, row of the page, 64-column half, page.
@@ -743,15 +777,18 @@ int64_t grid_size(int B, int Hq, int Hkv, int64_t capacity) {
   return std::min<int64_t>(kMaxCtas, tiles);
 }
 
-// Workspace: the parts' O, their maxima and sums, then (with weights) statistics and scores.
+// Workspace: the parts' O, their maxima and sums, the units' parts, then (with weights)
+// statistics and scores.
 struct Layout {
-  size_t part_ml, stats, scores, end;
+  size_t part_ml, units, stats, scores, end;
 };
 Layout layout(int B, int Hq, int Hkv, int d, int64_t capacity, bool with_weights) {
   const size_t slots = 2 * static_cast<size_t>(grid_size(B, Hq, Hkv, capacity));
   Layout l;
   l.part_ml = slots * kRows * d * 4;
-  l.stats = l.part_ml + slots * kRows * 8;
+  l.units = l.part_ml + slots * kRows * 8;
+  const size_t blocks = (Hq / Hkv + kRows - 1) / kRows;
+  l.stats = l.units + static_cast<size_t>(B) * Hkv * blocks * 8;
   const size_t heads = static_cast<size_t>(B) * Hq;
   l.scores = (l.stats + (with_weights ? heads * 8 : 0) + 15) / 16 * 16;
   l.end = l.scores + (with_weights ? heads * capacity * 4 : 0);
@@ -773,6 +810,7 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
   char* ws = static_cast<char*>(p.workspace);
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+  a.units = reinterpret_cast<int2*>(ws + l.units);
   a.stats = reinterpret_cast<float2*>(ws + l.stats);
   a.scores = reinterpret_cast<float*>(ws + l.scores);
   a.B = c.B;
@@ -806,22 +844,21 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  if (a.capacity > kTile) {   // units of one tile are never split
-    cfg.gridDim = dim3(static_cast<unsigned>(c.B * p.Hq));
-    cfg.blockDim = dim3(128);
-    err = cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, FP16, WEIGHTS>, a, ctas);
-    if (err != cudaSuccess) return err;
-  }
-  if constexpr (WEIGHTS) {
+  // units of one tile are never split: no head to join
+  const int64_t heads = a.capacity > kTile ? static_cast<int64_t>(c.B) * p.Hq : 0;
+  int64_t blocks = heads;
+  int chunks = 1;
+  if (WEIGHTS) {
     // a window's tokens span at most window_left + 1, from a multiple of 4
     int64_t span = a.capacity;
     if (a.window_left >= 0) span = std::min<int64_t>(span, static_cast<int64_t>(a.window_left) + 4);
-    const int chunks = static_cast<int>((span + 1023) / 1024);
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(c.B) * c.Hkv * chunks));
-    cfg.blockDim = dim3(256);
-    err = cudaLaunchKernelEx(&cfg, fa_paged_add_weights_kernel, a, chunks);
+    chunks = static_cast<int>((span + 4 * kFinishThreads - 1) / (4 * kFinishThreads));
+    blocks += static_cast<int64_t>(c.B) * c.Hkv * chunks;
   }
-  return err;
+  if (blocks == 0) return cudaSuccess;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kFinishThreads);
+  return cudaLaunchKernelEx(&cfg, fa_paged_finish_kernel<D, FP16, WEIGHTS>, a, heads, chunks);
 }
 
 template <int D, bool FP16>
