@@ -239,7 +239,8 @@ int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* bloc
   if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages)) return FA_ERR_SHAPE;
   if (out_pages < 1 || budget < 1 || recent < 0 || recent > budget ||
       (int64_t)out_pages * page_size < budget ||
-      (int64_t)out_pages * page_size > (1ll << 30))
+      (int64_t)out_pages * page_size > (1ll << 30) ||
+      (uint64_t)B * (uint64_t)Hkv >= (1ull << 28))   // eight CTAs for each
     return FA_ERR_SHAPE;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
   if (!aligned({k_pages, v_pages, weights}, 16) ||
