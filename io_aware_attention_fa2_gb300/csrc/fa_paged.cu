@@ -2,6 +2,8 @@
 // the rules for bad block-table entries and lengths).
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -55,36 +57,14 @@ __global__ void __launch_bounds__(128)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Evict. A cluster of eight CTAs for each (sequence, key head): each CTA has an eighth of the
-// candidates, and the histograms, counts and flags are exchanged through distributed shared
-// memory. What has to be read and written is the weights (4 bytes a token) and the kept rows
-// twice (4 d bytes a token each way).
+// Evict, in two kernels: which tokens stay (kept), then their move. What has to be read and
+// written is the weights (4 bytes a token) and the kept rows once each way (4 d bytes a token).
 //
-// Which ones stay: the want-th largest weight among the tokens before the recent ones, found by
-// radix selection on the weights as ordered 32-bit keys (digits of 11, 11 and 10 bits, one
-// histogram over the cluster each), then the equal ones from the oldest until there are enough.
-// The keys are read once and kept in shared memory.
-//
-// The move: kept token i goes to row i of out_table's pages, in rounds of the cluster's width. When
-// out_table names pages of the sequence itself, a cluster barrier between a round's reads and
-// its writes keeps the order: a token's new place is never behind its old one, so a later round's
-// sources lie behind every earlier destination.
+// Selection, for each (sequence, key head): the want-th largest weight among the tokens before
+// the recent ones, by radix selection on the weights as ordered 32-bit keys (digits of 11, 11
+// and 10 bits), then the equal ones from the oldest until there are enough. The keys are read
+// once and kept in shared memory.
 namespace cg = cooperative_groups;
-
-constexpr int kEvictThreads = 512, kEvictCluster = 8;
-constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictBins = 2048;
-constexpr int kEvictCache = 12288;   // keys of a CTA's eighth in shared memory; further ones are
-                                     // read from the pages in every pass
-constexpr int kMoveTokens = 4;       // tokens in flight for each 32 lanes
-constexpr size_t kEvictSmem = (2 * kEvictBins + kEvictCache) * 4;
-
-// Weights as unsigned numbers in the same order: NaN lowest, -0 equal to +0.
-__device__ __forceinline__ uint32_t order_key(float w) {
-  if (!(w == w)) return 0u;
-  const uint32_t u = __float_as_uint(w + 0.f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
 
 struct EvictArgs {
   uint4* k_pages;
@@ -98,36 +78,61 @@ struct EvictArgs {
   int Hkv, page_size, num_pages, max_pages, out_pages, budget, recent;
 };
 
-template <int D>
-__global__ void __cluster_dims__(kEvictCluster, 1, 1) __launch_bounds__(kEvictThreads, 3)
-    fa_paged_evict_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ uint4 smem_raw[];
-  uint32_t* const hist = reinterpret_cast<uint32_t*>(smem_raw);   // [2][kEvictBins]
-  uint32_t* const cache = hist + 2 * kEvictBins;
-  __shared__ uint32_t s_warp[kEvictWarps], s_found[2];
-  __shared__ int2 s_count, s_warp_count[kEvictWarps];   // candidates above and at the threshold
-  __shared__ int s_bad, s_own_pages;   // flags of this CTA's share of the checks
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank());
+constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048, kBinsPerThread = kBins / kSelectThreads;
+constexpr int kMaxCache = 49152;   // keys a CTA keeps in shared memory; further ones are read from
+                                   // the pages in every pass
+
+// Weights as unsigned numbers in the same order: NaN lowest, -0 equal to +0.
+__device__ __forceinline__ uint32_t order_key(float w) {
+  if (!(w == w)) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// CTAS CTAs (a cluster) for each (sequence, key head), each with its share of the candidates:
+// the flags, histograms and counts are exchanged through distributed shared memory. One CTA
+// needs no exchange, which costs 3 us a digit. `cache` keys fit in the dynamic shared memory.
+template <int CTAS>
+__global__ void __launch_bounds__(kSelectThreads, 1)
+    fa_paged_select_kernel(const __grid_constant__ EvictArgs a, int cache_keys) {
+  extern __shared__ uint32_t smem[];
+  uint32_t* const hist = smem;                            // [kBins] (two of them with a cluster)
+  uint32_t* const cache = smem + (CTAS > 1 ? 2 : 1) * kBins;
+  __shared__ uint32_t s_warp[kSelectWarps], s_found[2];
+  __shared__ int2 s_count, s_warp_count[kSelectWarps];   // candidates above and at the threshold
+  __shared__ int s_bad;                                  // flag of this CTA's share of the checks
+  const int rank = CTAS > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int wide = rank * kEvictThreads + tid, width = kEvictCluster * kEvictThreads;
-  const int64_t unit = blockIdx.x / kEvictCluster;
+  const int wide = rank * kSelectThreads + tid, width = CTAS * kSelectThreads;
+  // all CTAs of the unit: shared memory written before is readable in the others after
+  auto sync_all = [&] {
+    if constexpr (CTAS > 1)
+      cg::this_cluster().sync();
+    else
+      __syncthreads();
+  };
+  auto of_rank = [&](auto* p, int r) {
+    if constexpr (CTAS > 1)
+      return cg::this_cluster().map_shared_rank(p, r);
+    else
+      return p;
+  };
+  const int64_t unit = blockIdx.x / CTAS;
   const int b = static_cast<int>(unit / a.Hkv), hk = static_cast<int>(unit % a.Hkv);
   const int ps = a.page_size;
   const int* const src_table = a.table + static_cast<int64_t>(b) * a.max_pages;
   const int* const dst_table = a.out_table + static_cast<int64_t>(b) * a.out_pages;
   int* const kept = a.kept + unit * a.budget;
+  launch_dependents();
 
   const int raw_len = a.seqlens[b];
   const bool bad_len = raw_len < 0 || raw_len > a.max_pages * ps;
   const int len = bad_len ? 0 : raw_len, new_len = min(len, a.budget);
   const int src_used = (len + ps - 1) / ps, dst_used = (new_len + ps - 1) / ps;
   auto in_pool = [&](int page) { return page >= 0 && page < a.num_pages; };
-  if (tid == 0) {
-    s_bad = bad_len;
-    s_own_pages = 0;
-  }
-  for (int i = tid; i < 2 * kEvictBins; i += kEvictThreads) hist[i] = 0;
+  if (tid == 0) s_bad = bad_len;
+  for (int i = tid; i < (CTAS > 1 ? 2 : 1) * kBins; i += kSelectThreads) hist[i] = 0;
   __syncthreads();
   // the pages are in the pool, and no destination stands in the sequence at a later place
   for (int i = wide; i < src_used; i += width)
@@ -136,77 +141,64 @@ __global__ void __cluster_dims__(kEvictCluster, 1, 1) __launch_bounds__(kEvictTh
     if (!in_pool(dst_table[i])) s_bad = 1;
   for (int64_t x = wide; x < static_cast<int64_t>(dst_used) * src_used; x += width) {
     const int i = static_cast<int>(x / src_used), j = static_cast<int>(x % src_used);
-    if (dst_table[i] == src_table[j]) {
-      s_own_pages = 1;
-      if (j > i) s_bad = 1;
-    }
+    if (j > i && dst_table[i] == src_table[j]) s_bad = 1;
   }
 
-  // ---- selection
   const bool select = len > a.budget;
   const int n = select ? len - a.recent : 0;         // candidates: tokens [0, n)
   uint32_t want = select ? a.budget - a.recent : 0;  // of them stay
-  const int share = (n + kEvictCluster - 1) / kEvictCluster;
+  const int share = (n + CTAS - 1) / CTAS;
   const int t0 = min(rank * share, n), mine = min(share, n - t0);   // this CTA's: [t0, t0 + mine)
   auto load_key = [&](int t) {
     const int page = src_table[t / ps];
     // (a bad page: the sequence is given up below)
-    return in_pool(page) ? order_key(__ldcg(
-                               a.weights + (static_cast<int64_t>(page) * a.Hkv + hk) * ps + t % ps))
-                         : 0u;
+    return in_pool(page)
+               ? order_key(a.weights[(static_cast<int64_t>(page) * a.Hkv + hk) * ps + t % ps])
+               : 0u;
   };
-  const int cached = min(mine, kEvictCache);
-#pragma unroll 4
-  for (int i = tid; i < cached; i += kEvictThreads) cache[i] = load_key(t0 + i);
-  __syncthreads();
+  const int cached = min(mine, cache_keys);
+#pragma unroll 8
+  for (int i = tid; i < cached; i += kSelectThreads) cache[i] = load_key(t0 + i);
+  sync_all();
+  int bad = 0;
+#pragma unroll
+  for (int r = 0; r < CTAS; ++r) bad |= *of_rank(&s_bad, r);
+  if (bad) {
+    for (int i = wide; i < a.budget; i += width) kept[i] = -1;
+    if (wide == 0) {
+      record_page_error();
+      if (hk == 0) a.new_seqlens[b] = raw_len;
+    }
+    if constexpr (CTAS > 1) sync_all();   // no CTA leaves while another reads its flag
+    return;
+  }
+  if (wide == 0 && hk == 0) a.new_seqlens[b] = new_len;
   auto key_at = [&](int i) { return i < cached ? cache[i] : load_key(t0 + i); };
 
-  bool own_pages = false;
   uint32_t prefix = 0;   // digits found so far
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     constexpr int kShift[3] = {21, 10, 0};
     const int shift = kShift[pass], bits = pass == 2 ? 10 : 11;
-    uint32_t* const h = hist + (pass & 1) * kEvictBins;
-    if (want) {
-      for (int i = tid; i < mine; i += kEvictThreads) {
+    uint32_t* const h = hist + (CTAS > 1 ? (pass & 1) * kBins : 0);
+    if (want)
+      for (int i = tid; i < mine; i += kSelectThreads) {
         const uint32_t key = key_at(i);
         if (pass == 0 || (key >> (shift + bits)) == prefix)
           atomicAdd(&h[(key >> shift) & ((1u << bits) - 1)], 1u);
       }
-    }
-    cluster.sync();
-    if (pass == 0) {
-      // the first exchange carries the flags, too
-      int bad = 0, own = 0;
-      for (int r = 0; r < kEvictCluster; ++r) {
-        bad |= *cluster.map_shared_rank(&s_bad, r);
-        own |= *cluster.map_shared_rank(&s_own_pages, r);
-      }
-      if (bad) {
-        for (int i = wide; i < a.budget; i += width) kept[i] = -1;
-        if (wide == 0) {
-          record_page_error();
-          if (hk == 0) a.new_seqlens[b] = raw_len;
-        }
-        cluster.sync();   // no CTA leaves while another reads its flags
-        return;
-      }
-      own_pages = own;
-    }
+    sync_all();
     if (want) {
-      // four bins a thread, from the top: bins below thread tid's are those of later threads
-      uint32_t bin[4] = {0, 0, 0, 0};
-      const int top = kEvictBins - 4 - 4 * tid;
-      for (int r = 0; r < kEvictCluster; ++r) {
-        const uint4 x = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(h + top, r));
-        bin[0] += x.w;
-        bin[1] += x.z;
-        bin[2] += x.y;
-        bin[3] += x.x;
+      // two bins a thread, from the top; `before`: the keys in the bins of earlier threads
+      const int top = kBins - kBinsPerThread * (tid + 1);
+      uint32_t high = 0, low = 0;
+#pragma unroll
+      for (int r = 0; r < CTAS; ++r) {
+        const uint2 x = *reinterpret_cast<const uint2*>(of_rank(h + top, r));
+        low += x.x;
+        high += x.y;
       }
-      const uint32_t sum = bin[0] + bin[1] + bin[2] + bin[3];
-      uint32_t inc = sum;
+      uint32_t inc = high + low;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, inc, off);
@@ -214,87 +206,131 @@ __global__ void __cluster_dims__(kEvictCluster, 1, 1) __launch_bounds__(kEvictTh
       }
       if (lane == 31) s_warp[warp] = inc;
       __syncthreads();
-      uint32_t before = inc - sum;
-      for (int w = 0; w < warp; ++w) before += s_warp[w];
-      if (before < want && want <= before + sum) {
-        int e = 0;
-        while (before + bin[e] < want) before += bin[e++];
-        s_found[0] = top + 3 - e;
-        s_found[1] = before;
+      uint32_t before = lane < warp ? s_warp[lane] : 0u;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+      before += inc - high - low;
+      if (before < want && want <= before + high + low) {
+        const bool is_high = want <= before + high;
+        s_found[0] = top + (is_high ? 1 : 0);
+        s_found[1] = is_high ? before : before + high;
       }
-      __syncthreads();
+    }
+    // a cluster's third pass takes the first histogram again, which every CTA has read by now
+    if (pass < 2 && (CTAS == 1 || pass == 1))
+      for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+    __syncthreads();
+    if (want) {
       prefix = prefix << bits | s_found[0];
       want -= s_found[1];   // of the keys that start with prefix
     }
-    if (pass == 1) {
-      // every CTA has read the first histogram: it serves the third pass
-      for (int i = tid; i < kEvictBins; i += kEvictThreads) hist[i] = 0;
-      __syncthreads();
-    }
   }
 
-  // ---- kept: the tokens above the threshold and the oldest `want` at it, in order
-  if (select) {
-    const bool any = a.budget > a.recent;
-    const int per_warp = (mine + 32 * kEvictWarps - 1) / (32 * kEvictWarps) * 32;
-    const int w0 = min(warp * per_warp, mine), w1 = min(w0 + per_warp, mine);
-    int2 count = make_int2(0, 0);
-    for (int i = w0; i < w1; i += 32) {
-      const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
-      const bool in = any && i + lane < w1;
-      count.x += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
-      count.y += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
-    }
-    if (lane == 0) s_warp_count[warp] = count;
-    __syncthreads();
-    if (tid == 0) {
-      int2 sum = make_int2(0, 0);
-      for (int w = 0; w < kEvictWarps; ++w) {
-        sum.x += s_warp_count[w].x;
-        sum.y += s_warp_count[w].y;
-      }
-      s_count = sum;
-    }
-    cluster.sync();
-    int above = 0, equal = 0;   // before this warp's candidates
+  if (!select) {
+    for (int i = wide; i < a.budget; i += width) kept[i] = i < len ? i : -1;
+    if constexpr (CTAS > 1) sync_all();
+    return;
+  }
+  // The tokens above the threshold and the oldest `want` at it, in order: every warp counts a
+  // run of its own, then places it behind the runs before.
+  const bool any = a.budget > a.recent;
+  const int per_warp = (mine + kSelectThreads - 1) / kSelectThreads * 32;
+  const int w0 = min(warp * per_warp, mine), w1 = min(w0 + per_warp, mine);
+  int2 count = make_int2(0, 0);
+#pragma unroll 4
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
+    const bool in = any && i + lane < w1;
+    count.x += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
+    count.y += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
+  }
+  if (lane == 0) s_warp_count[warp] = count;
+  __syncthreads();
+  const int2 mine_of = s_warp_count[lane];
+  int above = lane < warp ? mine_of.x : 0, equal = lane < warp ? mine_of.y : 0;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    above += __shfl_xor_sync(0xffffffffu, above, off);
+    equal += __shfl_xor_sync(0xffffffffu, equal, off);
+  }
+  if constexpr (CTAS > 1) {
+    if (tid == kSelectThreads - 1) s_count = make_int2(above + count.x, equal + count.y);
+    sync_all();
     for (int r = 0; r < rank; ++r) {
-      const int2 c = *cluster.map_shared_rank(&s_count, r);
+      const int2 c = *of_rank(&s_count, r);
       above += c.x;
       equal += c.y;
     }
-    for (int w = 0; w < warp; ++w) {
-      above += s_warp_count[w].x;
-      equal += s_warp_count[w].y;
-    }
-    const unsigned below = (1u << lane) - 1;
-    for (int i = w0; i < w1; i += 32) {
-      const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
-      const bool in = any && i + lane < w1;
-      const unsigned up = __ballot_sync(0xffffffffu, in && key > prefix);
-      const unsigned at = __ballot_sync(0xffffffffu, in && key == prefix);
-      const int rank_at = equal + __popc(at & below);
-      const bool keep = (up >> lane & 1) || ((at >> lane & 1) && rank_at < static_cast<int>(want));
-      if (keep)
-        kept[above + __popc(up & below) + min(rank_at, static_cast<int>(want))] = t0 + i + lane;
-      above += __popc(up);
-      equal += __popc(at);
-    }
-    for (int i = wide; i < a.recent; i += width) kept[a.budget - a.recent + i] = n + i;
-  } else {
-    for (int i = wide; i < a.budget; i += width) kept[i] = i < len ? i : -1;
   }
-  if (wide == 0 && hk == 0) a.new_seqlens[b] = new_len;
-  cluster.sync();   // kept is complete; and no shared memory is read from another CTA after this
+  const unsigned below = (1u << lane) - 1;
+  const int limit = static_cast<int>(want);
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
+    const bool in = any && i + lane < w1;
+    const unsigned up = __ballot_sync(0xffffffffu, in && key > prefix);
+    const unsigned at = __ballot_sync(0xffffffffu, in && key == prefix);
+    const int rank_at = equal + __popc(at & below);
+    if ((up >> lane & 1) || ((at >> lane & 1) && rank_at < limit))
+      kept[above + __popc(up & below) + min(rank_at, limit)] = t0 + i + lane;
+    above += __popc(up);
+    equal += __popc(at);
+  }
+  for (int i = wide; i < a.recent; i += width) kept[a.budget - a.recent + i] = n + i;
+  if constexpr (CTAS > 1) sync_all();   // no CTA leaves while another reads its counts
+}
 
-  // ---- move: a row's K and V take D / 4 lanes, 16 bytes each
-  constexpr int kLanes = D / 4, kTokens = 32 / kLanes * kMoveTokens;   // tokens of a warp
-  constexpr int kRound = kTokens * kEvictWarps * kEvictCluster;
-  for (int r0 = 0; r0 < new_len; r0 += kRound) {
+// The move: kept token i goes to row i of out_table's pages. A cluster of eight CTAs for each
+// (sequence, key head), in rounds of the cluster's width. Where out_table names pages of the
+// sequence itself, a cluster barrier between a round's reads and its writes keeps the order: a
+// token's new place is never behind its old one, so a later round's sources lie behind every
+// earlier destination. Reads go past L1: a row may share its line with one that another SM
+// writes.
+constexpr int kMoveThreads = 512, kMoveCluster = 8;
+constexpr int kMoveTokens = 8;   // 16-byte loads in flight for each lane
+
+template <int D>
+__global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThreads, 2)
+    fa_paged_move_kernel(const __grid_constant__ EvictArgs a) {
+  constexpr int kLanes = D / 4;   // a row's K and V, 16 bytes a lane
+  constexpr int kTokens = 32 / kLanes * kMoveTokens;   // tokens of a warp in a round
+  constexpr int kWarps = kMoveThreads / 32, kRound = kTokens * kWarps * kMoveCluster;
+  __shared__ int s_own;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int64_t unit = blockIdx.x / kMoveCluster;
+  const int b = static_cast<int>(unit / a.Hkv), hk = static_cast<int>(unit % a.Hkv);
+  const int ps = a.page_size;
+  const int* const src_table = a.table + static_cast<int64_t>(b) * a.max_pages;
+  const int* const dst_table = a.out_table + static_cast<int64_t>(b) * a.out_pages;
+  const int* const kept = a.kept + unit * a.budget;
+  // whether a destination is a page of the sequence (on the arguments alone: this runs beside
+  // the selection)
+  const int len = min(max(a.seqlens[b], 0), a.max_pages * ps), new_len = min(len, a.budget);
+  const int src_used = (len + ps - 1) / ps, dst_used = (new_len + ps - 1) / ps;
+  if (tid == 0) s_own = 0;
+  __syncthreads();
+  for (int64_t x = rank * kMoveThreads + tid; x < static_cast<int64_t>(dst_used) * src_used;
+       x += kMoveCluster * kMoveThreads)
+    if (dst_table[x / src_used] == src_table[x % src_used]) s_own = 1;
+  cluster.sync();
+  int own_pages = 0;
+#pragma unroll
+  for (int r = 0; r < kMoveCluster; ++r) own_pages |= *cluster.map_shared_rank(&s_own, r);
+  cluster.sync();   // no CTA leaves while another reads its flag
+  wait_prerequisites();
+  // (a sequence that was given up keeps nothing: its kept is all -1)
+  const int rows = new_len > 0 && __ldcg(kept) >= 0 ? new_len : 0;
+
+  const int part = lane % kLanes;
+  const int64_t chunk = part % (D / 8);
+  uint4* const pool = part < D / 8 ? a.k_pages : a.v_pages;
+  for (int r0 = 0; r0 < rows; r0 += kRound) {
     // lane e < kTokens looks up token i0 + e
-    const int i = r0 + (rank * kEvictWarps + warp) * kTokens + lane;
+    const int i = r0 + (rank * kWarps + warp) * kTokens + lane;
     int64_t src = -1, dst = -1, w_dst = 0;
     float w = 0.f;
-    if (lane < kTokens && i < new_len) {
+    if (lane < kTokens && i < rows) {
       const int t = __ldcg(kept + i);
       const int64_t src_page = src_table[t / ps], dst_page = dst_table[i / ps];
       const int src_row = t % ps, dst_row = i % ps;
@@ -307,9 +343,6 @@ __global__ void __cluster_dims__(kEvictCluster, 1, 1) __launch_bounds__(kEvictTh
         w_dst = (dst_page * a.Hkv + hk) * ps + dst_row;
       }
     }
-    const int part = lane % kLanes;
-    const int64_t chunk = part % (D / 8);
-    uint4* const pool = part < D / 8 ? a.k_pages : a.v_pages;
     uint4 v[kMoveTokens];
 #pragma unroll
     for (int u = 0; u < kMoveTokens; ++u) {
@@ -328,6 +361,31 @@ __global__ void __cluster_dims__(kEvictCluster, 1, 1) __launch_bounds__(kEvictTh
   }
 }
 
+template <int CTAS>
+cudaError_t launch_select(const EvictArgs& a, int64_t units, cudaStream_t stream) {
+  // the longest share of candidates a CTA can get
+  const int64_t most = (static_cast<int64_t>(a.max_pages) * a.page_size + CTAS - 1) / CTAS;
+  const int cache_keys = static_cast<int>(std::min<int64_t>(most, kMaxCache));
+  const int smem = ((CTAS > 1 ? 2 : 1) * kBins + cache_keys) * 4;
+  auto kernel = fa_paged_select_kernel<CTAS>;
+  cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * CTAS));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = CTAS > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a, cache_keys);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream) {
@@ -340,8 +398,7 @@ cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
+cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream) {
   const PagedCache& c = p.c;
   EvictArgs a;
   a.k_pages = static_cast<uint4*>(c.k_pages);
@@ -359,17 +416,24 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
   a.out_pages = p.out_pages;
   a.budget = p.budget;
   a.recent = p.recent;
-  const int smem = static_cast<int>(kEvictSmem);
-  cudaError_t err = cudaFuncSetAttribute(fa_paged_evict_kernel<D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int64_t units = static_cast<int64_t>(c.B) * c.Hkv;
+  // One CTA for a head's selection while its tokens fit in its shared memory, else eight.
+  cudaError_t err = static_cast<int64_t>(c.max_pages) * c.page_size <= kMaxCache
+                        ? launch_select<1>(a, units, stream)
+                        : launch_select<8>(a, units, stream);
   if (err != cudaSuccess) return err;
-  const int64_t ctas = static_cast<int64_t>(c.B) * c.Hkv * kEvictCluster;
-  fa_paged_evict_kernel<D><<<static_cast<unsigned>(ctas), kEvictThreads, smem, stream>>>(a);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream) {
-  return p.c.d == 64 ? launch_evict<64>(p, stream) : launch_evict<128>(p, stream);
+  // the move may start its checks while the selection runs
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * kMoveCluster));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return c.d == 64 ? cudaLaunchKernelEx(&cfg, fa_paged_move_kernel<64>, a)
+                   : cudaLaunchKernelEx(&cfg, fa_paged_move_kernel<128>, a);
 }
 
 cudaError_t read_and_clear_paged_error(int* value) {

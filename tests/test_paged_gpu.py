@@ -496,9 +496,16 @@ def test_evict_ties_and_special_weights(kind):
     check_evict(c, free_table(c, 350), 350, 40)
 
 
-def test_evict_long():
-    c = Cache([70001], 256, 1, 64, "bf16", seed=7, weights=True, spare=24)
-    check_evict(c, free_table(c, 5000), 5000, 1000)
+@pytest.mark.parametrize("n,in_place,ties", [(49152, False, False), (49153, True, True),
+                                             (70001, False, True), (70001, True, False),
+                                             (395000, False, True)])
+def test_evict_long(n, in_place, ties):
+    """Around and past what one CTA, and a cluster of them, keep of the weights on chip."""
+    c = Cache([n, 300], 256, 1, 64, "bf16", seed=7, weights=True, spare=44,
+              max_pages=-(-n // 256))
+    if ties:
+        c.w = torch.randint(0, 9, c.w.shape, generator=c.g).float().cuda()
+    check_evict(c, c.table.clone() if in_place else free_table(c, 5000), 5000, 1000)
 
 
 @pytest.mark.parametrize("in_place", [False, True])
