@@ -75,7 +75,7 @@ struct EvictArgs {
   const int* out_table;
   int* kept;
   int* new_seqlens;
-  int Hkv, page_size, num_pages, max_pages, out_pages, budget, recent;
+  int Hkv, page_shift, num_pages, max_pages, out_pages, budget, recent;   // 2^page_shift tokens
 };
 
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
@@ -90,6 +90,23 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Whether a page of the tables is outside the pool, or a page of dst stands in src at a later
+// place; for warp `w` of `warps` that share the checks.
+__device__ __forceinline__ bool tables_bad(const int* src, int src_used, const int* dst,
+                                           int dst_used, int num_pages, int w, int warps) {
+  const int lane = threadIdx.x % 32;
+  bool bad = false;
+  for (int j = w * 32 + lane; j < src_used; j += warps * 32)
+    bad |= src[j] < 0 || src[j] >= num_pages;
+  for (int i = w; i < dst_used; i += warps) {
+    const int page = dst[i];
+    bad |= page < 0 || page >= num_pages;
+#pragma unroll 4
+    for (int j = i + 1 + lane; j < src_used; j += 32) bad |= src[j] == page;
+  }
+  return bad;
+}
+
 // CTAS CTAs (a cluster) for each (sequence, key head), each with its share of the candidates:
 // the flags, histograms and counts are exchanged through distributed shared memory. One CTA
 // needs no exchange, which costs 3 us a digit. `cache` keys fit in the dynamic shared memory.
@@ -98,7 +115,6 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     fa_paged_select_kernel(const __grid_constant__ EvictArgs a, int cache_keys) {
   extern __shared__ uint32_t smem[];
   uint32_t* const hist = smem;                            // [kBins] (two of them with a cluster)
-  uint32_t* const cache = smem + (CTAS > 1 ? 2 : 1) * kBins;
   __shared__ uint32_t s_warp[kSelectWarps], s_found[2];
   __shared__ int2 s_count, s_warp_count[kSelectWarps];   // candidates above and at the threshold
   __shared__ int s_bad;                                  // flag of this CTA's share of the checks
@@ -120,45 +136,50 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
   };
   const int64_t unit = blockIdx.x / CTAS;
   const int b = static_cast<int>(unit / a.Hkv), hk = static_cast<int>(unit % a.Hkv);
-  const int ps = a.page_size;
   const int* const src_table = a.table + static_cast<int64_t>(b) * a.max_pages;
   const int* const dst_table = a.out_table + static_cast<int64_t>(b) * a.out_pages;
   int* const kept = a.kept + unit * a.budget;
   launch_dependents();
 
   const int raw_len = a.seqlens[b];
-  const bool bad_len = raw_len < 0 || raw_len > a.max_pages * ps;
+  const bool bad_len = raw_len < 0 || raw_len > a.max_pages << a.page_shift;
   const int len = bad_len ? 0 : raw_len, new_len = min(len, a.budget);
-  const int src_used = (len + ps - 1) / ps, dst_used = (new_len + ps - 1) / ps;
   auto in_pool = [&](int page) { return page >= 0 && page < a.num_pages; };
   if (tid == 0) s_bad = bad_len;
   for (int i = tid; i < (CTAS > 1 ? 2 : 1) * kBins; i += kSelectThreads) hist[i] = 0;
   __syncthreads();
-  // the pages are in the pool, and no destination stands in the sequence at a later place
-  for (int i = wide; i < src_used; i += width)
-    if (!in_pool(src_table[i])) s_bad = 1;
-  for (int i = wide; i < dst_used; i += width)
-    if (!in_pool(dst_table[i])) s_bad = 1;
-  for (int64_t x = wide; x < static_cast<int64_t>(dst_used) * src_used; x += width) {
-    const int i = static_cast<int>(x / src_used), j = static_cast<int>(x % src_used);
-    if (j > i && dst_table[i] == src_table[j]) s_bad = 1;
-  }
 
   const bool select = len > a.budget;
   const int n = select ? len - a.recent : 0;         // candidates: tokens [0, n)
   uint32_t want = select ? a.budget - a.recent : 0;  // of them stay
-  const int share = (n + CTAS - 1) / CTAS;
-  const int t0 = min(rank * share, n), mine = min(share, n - t0);   // this CTA's: [t0, t0 + mine)
-  auto load_key = [&](int t) {
-    const int page = src_table[t / ps];
-    // (a bad page: the sequence is given up below)
-    return in_pool(page)
-               ? order_key(a.weights[(static_cast<int64_t>(page) * a.Hkv + hk) * ps + t % ps])
-               : 0u;
+  // this CTA's: [t0, t0 + mine), in groups of four, which lie in one page
+  const int share = (n + 4 * CTAS - 1) / (4 * CTAS) * 4;
+  const int t0 = min(rank * share, n), mine = min(share, n - t0);
+  const int groups = (mine + 3) / 4, cached = min(groups, cache_keys / 4);
+  uint4* const cache = reinterpret_cast<uint4*>(smem + (CTAS > 1 ? 2 : 1) * kBins);
+  auto load_group = [&](int g) {
+    const int t = t0 + 4 * g, page = src_table[t >> a.page_shift];
+    if (!in_pool(page)) return make_uint4(0, 0, 0, 0);   // the sequence is given up below
+    const float4 w = *reinterpret_cast<const float4*>(
+        a.weights + ((static_cast<int64_t>(page) * a.Hkv + hk) << a.page_shift) +
+        (t & ((1 << a.page_shift) - 1)));
+    return make_uint4(order_key(w.x), order_key(w.y), order_key(w.z), order_key(w.w));
   };
-  const int cached = min(mine, cache_keys);
-#pragma unroll 8
-  for (int i = tid; i < cached; i += kSelectThreads) cache[i] = load_key(t0 + i);
+#pragma unroll 4
+  for (int g = tid; g < cached; g += kSelectThreads) cache[g] = load_group(g);
+  // f(first token of the group within this CTA's, its four keys), group g of every `step`
+  auto for_groups = [&](int g0, int g1, int step, auto&& f) {
+    int g = g0;
+#pragma unroll 4
+    for (; g < min(g1, cached); g += step) f(4 * g, cache[g]);
+    for (; g < g1; g += step) f(4 * g, load_group(g));
+  };
+
+  // the pages are in the pool, and no destination stands in the sequence at a later place
+  if (tables_bad(src_table, (len + (1 << a.page_shift) - 1) >> a.page_shift, dst_table,
+                 (new_len + (1 << a.page_shift) - 1) >> a.page_shift, a.num_pages,
+                 rank * kSelectWarps + warp, CTAS * kSelectWarps))
+    s_bad = 1;
   sync_all();
   int bad = 0;
 #pragma unroll
@@ -173,7 +194,6 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     return;
   }
   if (wide == 0 && hk == 0) a.new_seqlens[b] = new_len;
-  auto key_at = [&](int i) { return i < cached ? cache[i] : load_key(t0 + i); };
 
   uint32_t prefix = 0;   // digits found so far
 #pragma unroll
@@ -181,12 +201,17 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     constexpr int kShift[3] = {21, 10, 0};
     const int shift = kShift[pass], bits = pass == 2 ? 10 : 11;
     uint32_t* const h = hist + (CTAS > 1 ? (pass & 1) * kBins : 0);
+    auto count_key = [&](bool in, uint32_t key) {
+      if (in && (pass == 0 || (key >> (shift + bits)) == prefix))
+        atomicAdd(&h[(key >> shift) & ((1u << bits) - 1)], 1u);
+    };
     if (want)
-      for (int i = tid; i < mine; i += kSelectThreads) {
-        const uint32_t key = key_at(i);
-        if (pass == 0 || (key >> (shift + bits)) == prefix)
-          atomicAdd(&h[(key >> shift) & ((1u << bits) - 1)], 1u);
-      }
+      for_groups(tid, groups, kSelectThreads, [&](int i, uint4 key) {
+        count_key(true, key.x);
+        count_key(i + 1 < mine, key.y);
+        count_key(i + 2 < mine, key.z);
+        count_key(i + 3 < mine, key.w);
+      });
     sync_all();
     if (want) {
       // two bins a thread, from the top; `before`: the keys in the bins of earlier threads
@@ -233,47 +258,76 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
   }
   // The tokens above the threshold and the oldest `want` at it, in order: every warp counts a
   // run of its own, then places it behind the runs before.
-  const bool any = a.budget > a.recent;
-  const int per_warp = (mine + kSelectThreads - 1) / kSelectThreads * 32;
-  const int w0 = min(warp * per_warp, mine), w1 = min(w0 + per_warp, mine);
-  int2 count = make_int2(0, 0);
-#pragma unroll 4
-  for (int i = w0; i < w1; i += 32) {
-    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
-    const bool in = any && i + lane < w1;
-    count.x += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
-    count.y += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
-  }
-  if (lane == 0) s_warp_count[warp] = count;
-  __syncthreads();
-  const int2 mine_of = s_warp_count[lane];
-  int above = lane < warp ? mine_of.x : 0, equal = lane < warp ? mine_of.y : 0;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    above += __shfl_xor_sync(0xffffffffu, above, off);
-    equal += __shfl_xor_sync(0xffffffffu, equal, off);
-  }
-  if constexpr (CTAS > 1) {
-    if (tid == kSelectThreads - 1) s_count = make_int2(above + count.x, equal + count.y);
-    sync_all();
-    for (int r = 0; r < rank; ++r) {
-      const int2 c = *of_rank(&s_count, r);
-      above += c.x;
-      equal += c.y;
-    }
-  }
-  const unsigned below = (1u << lane) - 1;
   const int limit = static_cast<int>(want);
-  for (int i = w0; i < w1; i += 32) {
-    const uint32_t key = i + lane < w1 ? key_at(i + lane) : 0u;
-    const bool in = any && i + lane < w1;
-    const unsigned up = __ballot_sync(0xffffffffu, in && key > prefix);
-    const unsigned at = __ballot_sync(0xffffffffu, in && key == prefix);
-    const int rank_at = equal + __popc(at & below);
-    if ((up >> lane & 1) || ((at >> lane & 1) && rank_at < limit))
-      kept[above + __popc(up & below) + min(rank_at, limit)] = t0 + i + lane;
-    above += __popc(up);
-    equal += __popc(at);
+  if (a.budget > a.recent) {
+    const int per_warp = (groups + kSelectThreads - 1) / kSelectThreads * 32;
+    const int g0 = min(warp * per_warp, groups), g1 = min(g0 + per_warp, groups);
+    // keys above the threshold in the low half, at it in the high half: at most 4 of a group
+    auto count4 = [&](int i, uint4 key) {
+      uint32_t c = key.x > prefix ? 1u : key.x == prefix ? 0x10000u : 0u;
+      if (i + 1 < mine) c += key.y > prefix ? 1u : key.y == prefix ? 0x10000u : 0u;
+      if (i + 2 < mine) c += key.z > prefix ? 1u : key.z == prefix ? 0x10000u : 0u;
+      if (i + 3 < mine) c += key.w > prefix ? 1u : key.w == prefix ? 0x10000u : 0u;
+      return c;
+    };
+    int2 count = make_int2(0, 0);
+    for_groups(g0 + lane, g1, 32, [&](int i, uint4 key) {
+      const uint32_t c = count4(i, key);
+      count.x += c & 0xffff;
+      count.y += c >> 16;
+    });
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      count.x += __shfl_xor_sync(0xffffffffu, count.x, off);
+      count.y += __shfl_xor_sync(0xffffffffu, count.y, off);
+    }
+    if (lane == 0) s_warp_count[warp] = count;
+    __syncthreads();
+    const int2 of_lane = s_warp_count[lane];
+    int above = lane < warp ? of_lane.x : 0, equal = lane < warp ? of_lane.y : 0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      above += __shfl_xor_sync(0xffffffffu, above, off);
+      equal += __shfl_xor_sync(0xffffffffu, equal, off);
+    }
+    if constexpr (CTAS > 1) {
+      if (tid == kSelectThreads - 1) s_count = make_int2(above + count.x, equal + count.y);
+      sync_all();
+      for (int r = 0; r < rank; ++r) {
+        const int2 c = *of_rank(&s_count, r);
+        above += c.x;
+        equal += c.y;
+      }
+    }
+    // a token a lane: its place comes from two ballots
+    const uint32_t* const keys = reinterpret_cast<const uint32_t*>(cache);
+    const unsigned below = (1u << lane) - 1;
+    const int end = min(4 * g1, mine), on_chip = min(end, 4 * cached);
+    auto place = [&](bool in, int i, uint32_t key) {
+      const unsigned up = __ballot_sync(0xffffffffu, in && key > prefix);
+      const unsigned at = __ballot_sync(0xffffffffu, in && key == prefix);
+      const int rank_at = equal + __popc(at & below);
+      if (in && (key > prefix || (key == prefix && rank_at < limit)))
+        kept[above + __popc(up & below) + min(rank_at, limit)] = t0 + i;
+      above += __popc(up);
+      equal += __popc(at);
+    };
+    int i = 4 * g0;
+#pragma unroll 4
+    for (; i < on_chip; i += 32) {
+      const bool in = i + lane < on_chip;
+      place(in, i + lane, in ? keys[i + lane] : 0u);
+    }
+    for (i = max(4 * g0, on_chip); i < end; i += 32) {
+      const bool in = i + lane < end;
+      uint32_t key = 0;
+      if (in) {
+        const uint4 four = load_group((i + lane) / 4);
+        const int e = (i + lane) & 3;
+        key = e == 0 ? four.x : e == 1 ? four.y : e == 2 ? four.z : four.w;
+      }
+      place(in, i + lane, key);
+    }
   }
   for (int i = wide; i < a.recent; i += width) kept[a.budget - a.recent + i] = n + i;
   if constexpr (CTAS > 1) sync_all();   // no CTA leaves while another reads its counts
@@ -300,19 +354,23 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t unit = blockIdx.x / kMoveCluster;
   const int b = static_cast<int>(unit / a.Hkv), hk = static_cast<int>(unit % a.Hkv);
-  const int ps = a.page_size;
   const int* const src_table = a.table + static_cast<int64_t>(b) * a.max_pages;
   const int* const dst_table = a.out_table + static_cast<int64_t>(b) * a.out_pages;
   const int* const kept = a.kept + unit * a.budget;
+  const int shift = a.page_shift, in_page = (1 << shift) - 1;
   // whether a destination is a page of the sequence (on the arguments alone: this runs beside
   // the selection)
-  const int len = min(max(a.seqlens[b], 0), a.max_pages * ps), new_len = min(len, a.budget);
-  const int src_used = (len + ps - 1) / ps, dst_used = (new_len + ps - 1) / ps;
+  const int len = min(max(a.seqlens[b], 0), a.max_pages << shift), new_len = min(len, a.budget);
+  const int src_used = (len + in_page) >> shift, dst_used = (new_len + in_page) >> shift;
   if (tid == 0) s_own = 0;
   __syncthreads();
-  for (int64_t x = rank * kMoveThreads + tid; x < static_cast<int64_t>(dst_used) * src_used;
-       x += kMoveCluster * kMoveThreads)
-    if (dst_table[x / src_used] == src_table[x % src_used]) s_own = 1;
+  bool own = false;
+  for (int i = rank * kWarps + warp; i < dst_used; i += kMoveCluster * kWarps) {
+    const int page = dst_table[i];
+#pragma unroll 4
+    for (int j = lane; j < src_used; j += 32) own |= src_table[j] == page;
+  }
+  if (own) s_own = 1;
   cluster.sync();
   int own_pages = 0;
 #pragma unroll
@@ -332,15 +390,15 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
     float w = 0.f;
     if (lane < kTokens && i < rows) {
       const int t = __ldcg(kept + i);
-      const int64_t src_page = src_table[t / ps], dst_page = dst_table[i / ps];
-      const int src_row = t % ps, dst_row = i % ps;
-      src = ((src_page * ps + src_row) * a.Hkv + hk) * (D / 8);
-      dst = ((dst_page * ps + dst_row) * a.Hkv + hk) * (D / 8);
+      const int64_t src_page = src_table[t >> shift], dst_page = dst_table[i >> shift];
+      const int src_row = t & in_page, dst_row = i & in_page;
+      src = (((src_page << shift) + src_row) * a.Hkv + hk) * (D / 8);
+      dst = (((dst_page << shift) + dst_row) * a.Hkv + hk) * (D / 8);
       if (src == dst) {   // in place already
         src = -1;
       } else {
-        w = __ldcg(a.weights + (src_page * a.Hkv + hk) * ps + src_row);
-        w_dst = (dst_page * a.Hkv + hk) * ps + dst_row;
+        w = __ldcg(a.weights + ((src_page * a.Hkv + hk) << shift) + src_row);
+        w_dst = ((dst_page * a.Hkv + hk) << shift) + dst_row;
       }
     }
     uint4 v[kMoveTokens];
@@ -364,7 +422,8 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
 template <int CTAS>
 cudaError_t launch_select(const EvictArgs& a, int64_t units, cudaStream_t stream) {
   // the longest share of candidates a CTA can get
-  const int64_t most = (static_cast<int64_t>(a.max_pages) * a.page_size + CTAS - 1) / CTAS;
+  const int64_t most =
+      ((static_cast<int64_t>(a.max_pages) << a.page_shift) + 4 * CTAS - 1) / (4 * CTAS) * 4;
   const int cache_keys = static_cast<int>(std::min<int64_t>(most, kMaxCache));
   const int smem = ((CTAS > 1 ? 2 : 1) * kBins + cache_keys) * 4;
   auto kernel = fa_paged_select_kernel<CTAS>;
@@ -410,7 +469,8 @@ cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream) {
   a.kept = p.kept;
   a.new_seqlens = p.new_seqlens;
   a.Hkv = c.Hkv;
-  a.page_size = c.page_size;
+  a.page_shift = 0;
+  while (1 << a.page_shift < c.page_size) ++a.page_shift;
   a.num_pages = c.num_pages;
   a.max_pages = c.max_pages;
   a.out_pages = p.out_pages;
