@@ -70,14 +70,15 @@ struct Args {
   void* o;
   float* lse;
   float* weights;
-  float* part_o;      // [2 * CTAs][16][D]: CTA c's first run at slot 2c, its last at 2c + 1
-  float2* part_ml;    // [2 * CTAs][16]: maximum (log2 units) and sum of the part
+  float* part_o;      // [2 * CTAs][part_rows][D]: CTA c's first run at slot 2c, its last at 2c + 1
+  float2* part_ml;    // [2 * CTAs][part_rows]: maximum (log2 units) and sum of the part
   int2* units;        // [B * Hkv * blocks]: slot of the unit's first part, number of parts (0: the
                       // unit was one run's, and is written)
   float2* stats;      // [B * Hq]: maximum and 1 / sum of a head that one run covered, when the
                       // cache keeps weights
   float* scores;      // [B * Hq][capacity], log2 units, when the cache keeps weights
   int B, Hq, Hkv, G, blocks;   // blocks of 16 query heads for each key head
+  int part_rows;               // query heads of a unit, at most: min(G, 16)
   int page_size, num_pages, max_pages, capacity, box_rows;
   int window_left;
   float scale_log2;
@@ -553,9 +554,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x < kRows) {
       float m, l;
       row_stats(threadIdx.x, m, l);
-      if (!sg.whole) {
-        a.part_ml[slot * kRows + threadIdx.x] = make_float2(m, l);
-      } else if (static_cast<int>(threadIdx.x) < rows) {
+      if (static_cast<int>(threadIdx.x) >= rows) {
+        // a row without a query head
+      } else if (!sg.whole) {
+        a.part_ml[slot * a.part_rows + threadIdx.x] = make_float2(m, l);
+      } else {
         a.lse[head0 + threadIdx.x] = lse_of(m, l);
         if constexpr (WEIGHTS) a.stats[head0 + threadIdx.x] = make_float2(m, inverse(l));
       }
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             sum.w += v.w;
           }
           if (!sg.whole) {
-            *reinterpret_cast<float4*>(a.part_o + (slot * kRows + row) * D + ch * 64 + c) = sum;
+            *reinterpret_cast<float4*>(a.part_o + (slot * a.part_rows + row) * D + ch * 64 + c) = sum;
           } else {
             float mr, lr;
             row_stats(row, mr, lr);
@@ -620,12 +623,12 @@ __device__ __forceinline__ float2 join_stats(const Args& a, int2 info, int row) 
   const int lane = threadIdx.x % 32;
   float m = -INFINITY, l = 0.f;
   for (int p = lane; p < info.y; p += 32)
-    m = fmaxf(m, a.part_ml[part_slot(info, p) * kRows + row].x);
+    m = fmaxf(m, a.part_ml[static_cast<int64_t>(part_slot(info, p)) * a.part_rows + row].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   const float u = m == -INFINITY ? 0.f : m;
   for (int p = lane; p < info.y; p += 32) {
-    const float2 ml = a.part_ml[part_slot(info, p) * kRows + row];
+    const float2 ml = a.part_ml[static_cast<int64_t>(part_slot(info, p)) * a.part_rows + row];
     l += ml.y * ptx::exp2_approx(ml.x - u);
   }
 #pragma unroll
@@ -651,7 +654,7 @@ __device__ __forceinline__ void join_head(const Args& a, int64_t head) {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int p = set; p < info.y; p += kSets) {
-    const int64_t at = static_cast<int64_t>(part_slot(info, p)) * kRows + row;
+    const int64_t at = static_cast<int64_t>(part_slot(info, p)) * a.part_rows + row;
     const float f = ptx::exp2_approx(a.part_ml[at].x - u);
     const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + 4 * x);
     acc.x += v.x * f;
@@ -785,8 +788,9 @@ struct Layout {
 Layout layout(int B, int Hq, int Hkv, int d, int64_t capacity, bool with_weights) {
   const size_t slots = 2 * static_cast<size_t>(grid_size(B, Hq, Hkv, capacity));
   Layout l;
-  l.part_ml = slots * kRows * d * 4;
-  l.units = l.part_ml + slots * kRows * 8;
+  const size_t rows = std::min(Hq / Hkv, kRows);
+  l.part_ml = slots * rows * d * 4;
+  l.units = l.part_ml + slots * rows * 8;
   const size_t blocks = (Hq / Hkv + kRows - 1) / kRows;
   l.stats = l.units + static_cast<size_t>(B) * Hkv * blocks * 8;
   const size_t heads = static_cast<size_t>(B) * Hq;
@@ -818,6 +822,7 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
   a.Hkv = c.Hkv;
   a.G = p.Hq / c.Hkv;
   a.blocks = (a.G + kRows - 1) / kRows;
+  a.part_rows = std::min(a.G, kRows);
   a.page_size = c.page_size;
   a.num_pages = c.num_pages;
   a.max_pages = c.max_pages;

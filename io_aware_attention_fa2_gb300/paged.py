@@ -79,8 +79,11 @@ def _workspace(need, workspace, device, stream):
     if need == 0:
         return None, None, 0
     import torch
-    with _stream_of(stream, device):
+    if stream is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        with _stream_of(stream, device):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
     return workspace, workspace.data_ptr(), need
 
 
