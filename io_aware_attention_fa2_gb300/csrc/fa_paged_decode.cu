@@ -234,13 +234,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32 * kWarps) {
     abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(full(s), 1);
       ptx::mbar_init(empty(s), kWarps);
     }
     ptx::fence_barrier_init();
+    ptx::prefetch_tensormap(&tm_k);
+    ptx::prefetch_tensormap(&tm_v);
   }
   // where this CTA's run starts: the sequence, and the tile within it
   if (warp == 0) {
@@ -290,10 +292,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == kWarps) {
     // ------------------------------------------------------------------ producer
-    if (lane == 0) {
-      ptx::prefetch_tensormap(&tm_k);
-      ptx::prefetch_tensormap(&tm_v);
-    }
     const int br = a.box_rows, boxes = kTile / br;
     const uint32_t box_bytes = static_cast<uint32_t>(br) * D * 2;
     int n = 0;   // tiles loaded so far: tile n goes through stage n % kStages
@@ -640,42 +638,58 @@ __device__ __forceinline__ int2 unit_info(const Args& a, int b, int h) {
   return a.units[static_cast<int64_t>(b) * a.Hkv * a.blocks + unit];
 }
 
+// O and LSE of a head from its parts. A thread has four columns of every kSets-th part and a
+// running maximum of its own, so that statistics and O of the parts are loaded together.
 template <int D, bool FP16>
 __device__ __forceinline__ void join_head(const Args& a, int64_t head) {
-  constexpr int kLanes = D / 4, kSets = kFinishThreads / kLanes;   // threads of a row; parts at once
+  constexpr int kLanes = D / 4, kSets = kFinishThreads / kLanes;
   __shared__ float4 s_acc[kSets][kLanes];
+  __shared__ float2 s_ml[kSets];
   const int b = static_cast<int>(head / a.Hq), h = static_cast<int>(head % a.Hq);
   const int row = h % a.G % kRows;
   const int2 info = unit_info(a, b, h);
   if (info.y == 0) return;   // one run covered the unit: written already
-  const float2 ml = join_stats(a, info, row);
-  const float u = ml.x == -INFINITY ? 0.f : ml.x;
   const int set = threadIdx.x / kLanes, x = threadIdx.x % kLanes;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
 #pragma unroll 4
   for (int p = set; p < info.y; p += kSets) {
     const int64_t at = static_cast<int64_t>(part_slot(info, p)) * a.part_rows + row;
-    const float f = ptx::exp2_approx(a.part_ml[at].x - u);
+    const float2 ml = a.part_ml[at];
     const float4 v = *reinterpret_cast<const float4*>(a.part_o + at * D + 4 * x);
+    const float n = fmaxf(m, ml.x), u = n == -INFINITY ? 0.f : n;
+    const float f = ptx::exp2_approx(m - u), g = ptx::exp2_approx(ml.x - u);
+    m = n;
+    l = l * f + ml.y * g;
+    acc.x = acc.x * f + v.x * g;
+    acc.y = acc.y * f + v.y * g;
+    acc.z = acc.z * f + v.z * g;
+    acc.w = acc.w * f + v.w * g;
+  }
+  s_acc[set][x] = acc;
+  if (x == 0) s_ml[set] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x >= kLanes) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int y = 0; y < kSets; ++y) m = fmaxf(m, s_ml[y].x);
+  const float u = m == -INFINITY ? 0.f : m;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
+#pragma unroll
+  for (int y = 0; y < kSets; ++y) {
+    const float f = ptx::exp2_approx(s_ml[y].x - u);
+    const float4 v = s_acc[y][x];
+    l += s_ml[y].y * f;
     acc.x += v.x * f;
     acc.y += v.y * f;
     acc.z += v.z * f;
     acc.w += v.w * f;
   }
-  s_acc[set][x] = acc;
-  __syncthreads();
-  if (threadIdx.x >= kLanes) return;
-  acc = s_acc[0][x];
-  for (int y = 1; y < kSets; ++y) {
-    acc.x += s_acc[y][x].x;
-    acc.y += s_acc[y][x].y;
-    acc.z += s_acc[y][x].z;
-    acc.w += s_acc[y][x].w;
-  }
-  const float inv = inverse(ml.y);
+  const float inv = inverse(l);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + head * D + 4 * x) = make_uint2(
       pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
-  if (x == 0) a.lse[head] = lse_of(ml.x, ml.y);
+  if (x == 0) a.lse[head] = lse_of(m, l);
 }
 
 // weights[page, hk, row] += sum over the group's heads of 2^(score - maximum) / sum. Four
