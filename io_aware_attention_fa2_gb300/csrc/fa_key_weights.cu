@@ -99,10 +99,19 @@ struct QueryMask {
   }
 };
 
-// Sum over 64 queries of 2^(scale_log2 s + nl), of the queries [lo, hi) alone when MASKED.
+// Bits [lo, hi) of 64.
+__device__ __forceinline__ uint64_t bit_range(int lo, int hi) {
+  lo = min(max(lo, 0), 64);
+  hi = min(max(hi, 0), 64);
+  if (hi <= lo) return 0;
+  return (hi == 64 ? ~0ull : (1ull << hi) - 1) & ~((1ull << lo) - 1);
+}
+
+// Sum over 64 queries of 2^(scale_log2 s + nl), of those with a bit in `visible` alone when
+// MASKED.
 template <bool MASKED>
 __device__ __forceinline__ float tile_sum(const uint32_t (&sr)[2][32], const float* nl,
-                                          float scale_log2, int lo, int hi) {
+                                          float scale_log2, uint64_t visible) {
   float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < kCols / 4; ++c) {
@@ -115,9 +124,10 @@ __device__ __forceinline__ float tile_sum(const uint32_t (&sr)[2][32], const flo
     ptx::fma2(e[2], e[3], __uint_as_float(s[o + 2]), __uint_as_float(s[o + 3]), scale_log2,
               scale_log2, n4.z, n4.w);
     if constexpr (MASKED) {
+      const uint32_t bits = static_cast<uint32_t>(visible >> (c < 8 ? 0 : 32)) >> (4 * (c % 8));
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (4 * c + k < lo || 4 * c + k >= hi) e[k] = -INFINITY;
+        if (!(bits & (1u << k))) e[k] = -INFINITY;
     }
     ptx::add2(t[0], t[1], t[0], t[1], ptx::exp2_approx(e[0]), ptx::exp2_approx(e[1]));
     ptx::add2(t[2], t[3], t[2], t[3], ptx::exp2_approx(e[2]), ptx::exp2_approx(e[3]));
@@ -275,9 +285,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float total = 0.f, comp = 0.f;
     int q0 = x0 * kQueries + half * 128;               // first of the warp's queries of tile i
     // Queries [q_lo, q_hi) see this key; queries inside [full_lo, full_hi) are seen by every key
-    // of the tile. (Keys at or past len are left out at the end.)
+    // of the tile, those outside [any_lo, any_hi) by none. (Keys at or past len are left out at
+    // the end.)
     const int q_lo = mask.lo(key), q_hi = mask.hi(key);
     const int full_lo = mask.lo(k0 + BLOCK_N - 1), full_hi = mask.hi(k0);
+    const int any_lo = mask.lo(k0), any_hi = mask.hi(k0 + BLOCK_N - 1);
     float next[4] = {0.f, 0.f, 0.f, 0.f};
     if (x1 > x0) {
 #pragma unroll
@@ -312,9 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::reg_fence(sr[0]);
         ptx::reg_fence(sr[1]);
         const int q = q0 + 64 * hf;
-        const bool full = q >= full_lo && q + 64 <= full_hi;
-        tile += full ? tile_sum<false>(sr, nl + 64 * hf, scale_log2, 0, 0)
-                     : tile_sum<true>(sr, nl + 64 * hf, scale_log2, q_lo - q, q_hi - q);
+        if (q >= full_lo && q + 64 <= full_hi)
+          tile += tile_sum<false>(sr, nl + 64 * hf, scale_log2, 0);
+        else if (q < any_hi && q + 64 > any_lo)
+          tile += tile_sum<true>(sr, nl + 64 * hf, scale_log2, bit_range(q_lo - q, q_hi - q));
       }
       const float y = tile - comp;
       const float sum = total + y;
