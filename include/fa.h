@@ -324,7 +324,8 @@ int fa_bwd_host_masked(const void* q_h, const void* k_h, const void* v_h, const 
  * followed: the kernel records FA_ERR_PAGE in the device error word and leaves those tokens out
  * (each entry point says how). Pages may be shared between sequences where they are only read;
  * a page that a call writes must belong to one sequence of that call (otherwise its contents
- * are those of any of the writers).
+ * are those of any of the writers), and stand in its table once.
+ * scale is used as in fa_fwd; scale * log2(e) has to be finite as well (FA_ERR_SCALE).
  */
 
 /*
@@ -383,7 +384,8 @@ int fa_paged_append(const void* k, const void* v, const float* w, void* k_pages,
  * A sequence with no visible token gets O = 0 and LSE = -inf. What the pages hold behind a
  * sequence's last token (NaN included) does not matter. A length beyond the table is taken as
  * the table's, and tokens in pages outside the pool are left out (FA_ERR_PAGE in the device
- * error word). The same call gives the same bits.
+ * error word). The same call gives the same bits (weights, too, of pages that stand in the
+ * tables once; a shared page gets one addition from each place it stands in, in any order).
  */
 int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, float* weights,
                     const int* block_table, const int* seqlens, void* o, float* lse, int B,
@@ -406,7 +408,8 @@ size_t fa_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_si
  *   out_table    device int32 [B, out_pages], out_pages * page_size >= budget: free pages, or
  *                the sequence's own (block_table's first entries again: eviction in place).
  *                A page of out_table may stand in the sequence's own block table at the same
- *                place or an earlier one, and must not stand in another sequence's tables.
+ *                place or an earlier one, and must not stand in another sequence's tables or
+ *                in out_table twice. Entries behind the last page needed are not read.
  *   kept         device int32 [B, Hkv, budget], written: the tokens kept, ascending; -1 behind
  *                the last
  *   new_seqlens  device int32 [B], written: min(seqlens, budget)

@@ -56,6 +56,18 @@ bool cache_shape_ok(int B, int Hkv, int d, int page_size, int num_pages, int max
   return (uint64_t)B * (uint64_t)Hkv < (1ull << 31);
 }
 
+// The kernels work in log2 units: scale * log2(e) has to be finite, too.
+constexpr float kLog2e = 1.4426950408889634f;
+bool scale_ok(float scale) { return isfinite(scale) && isfinite(scale * kLog2e); }
+
+// Query heads over a cache's key heads, for a decode: the grids (a block for each (b, h), and one
+// for each 1024 tokens of a (b, key head)) stay within 2^31 - 1.
+bool decode_shape_ok(int B, int Hq, int Hkv, int page_size, int max_pages) {
+  if (Hq < Hkv || Hq % Hkv) return false;
+  const uint64_t tokens = (uint64_t)max_pages * page_size;
+  return (uint64_t)B * (uint64_t)Hq * (tokens / 1024 + 2) < (1ull << 31);
+}
+
 uint64_t pool_bytes(int Hkv, int d, int page_size, int num_pages) {
   return (uint64_t)num_pages * page_size * Hkv * d * 2;
 }
@@ -95,7 +107,7 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, int
   if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || N < 1 || (d != 64 && d != 128))
     return FA_ERR_SHAPE;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
-  if (!isfinite(scale)) return FA_ERR_SCALE;
+  if (!scale_ok(scale)) return FA_ERR_SCALE;
   const uint64_t bh = (uint64_t)B * (uint64_t)Hq;
   // one CTA per (b, query head, 128 keys), at most 2^31 - 1; N + 128 stays an int
   if (bh >= (1ull << 31) || bh * (((uint64_t)N + 127) / 128) >= (1ull << 31) ||
@@ -138,7 +150,7 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, int
   p.window_right = window_right < 0 ? -1 : std::min(window_right, N);
   p.seqlens_k = seqlens_k;
   p.fp16 = fp16 ? 1 : 0;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale * kLog2e;
   return fa::launch_key_weights(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK : FA_ERR_LAUNCH;
 }
@@ -178,8 +190,8 @@ int fa_paged_append(const void* k, const void* v, const float* w, void* k_pages,
 
 size_t fa_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size,
                                       int max_pages, int with_weights) {
-  if (!cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) || Hq < Hkv || Hq % Hkv ||
-      (uint64_t)B * (uint64_t)Hq * (uint64_t)max_pages * page_size >= (1ull << 48))
+  if (!cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) ||
+      !decode_shape_ok(B, Hq, Hkv, page_size, max_pages))
     return 0;
   return fa::paged_decode_workspace(B, Hq, Hkv, d, page_size, max_pages, with_weights != 0);
 }
@@ -191,13 +203,11 @@ int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, flo
                     size_t workspace_bytes, fa_stream_t stream) {
   if (!q || !k_pages || !v_pages || !block_table || !seqlens || !o || !lse || !workspace)
     return FA_ERR_NULL;
-  if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages) || Hq < Hkv || Hq % Hkv ||
-      (uint64_t)B * (uint64_t)Hq >= (1ull << 31) ||
-      // tiles of all units stay far inside 64 bits
-      (uint64_t)B * (uint64_t)Hq * (uint64_t)max_pages * page_size >= (1ull << 48))
+  if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages) ||
+      !decode_shape_ok(B, Hq, Hkv, page_size, max_pages))
     return FA_ERR_SHAPE;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
-  if (!isfinite(scale)) return FA_ERR_SCALE;
+  if (!scale_ok(scale)) return FA_ERR_SCALE;
   const uint64_t ws_need =
       fa::paged_decode_workspace(B, Hq, Hkv, d, page_size, max_pages, weights != nullptr);
   if (workspace_bytes < ws_need) return FA_ERR_WORKSPACE;
@@ -224,7 +234,7 @@ int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, flo
   p.Hq = Hq;
   p.window_left = window_left < 0 ? -1 : window_left;
   p.fp16 = dtype == FA_FP16 ? 1 : 0;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale * kLog2e;
   return fa::launch_paged_decode(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK : FA_ERR_LAUNCH;
 }

@@ -74,6 +74,7 @@ def test_key_weights_refusals(lib):
         assert key_weights(lib, **bad) == SHAPE, bad
     assert key_weights(lib, dtype=2) == DTYPE
     assert key_weights(lib, scale=NAN) == SCALE
+    assert key_weights(lib, scale=3e38) == SCALE          # infinite in log2 units
     assert key_weights(lib, q=A[0] + 8) == ALIGN
     assert key_weights(lib, ws=A[4] + 4) == ALIGN
     assert key_weights(lib, lens=A[5] + 2) == ALIGN
@@ -102,7 +103,8 @@ def test_decode_refusals(lib):
     for name in ("q", "kp", "vp", "table", "lens", "o", "lse", "ws"):
         assert decode(lib, **{name: 0}) == NULL
     for bad in (dict(B=0), dict(Hq=0), dict(Hkv=0), dict(Hq=3), dict(Hq=1), dict(d=256),
-                dict(page=48), dict(pages=-1), dict(width=0), dict(B=1 << 16, Hq=1 << 15, Hkv=1)):
+                dict(page=48), dict(pages=-1), dict(width=0), dict(B=1 << 16, Hq=1 << 15, Hkv=1),
+                dict(B=1 << 14, Hq=1 << 10, Hkv=1, width=1 << 13)):
         assert decode(lib, **bad) == SHAPE, bad
     assert decode(lib, dtype=7) == DTYPE
     assert decode(lib, scale=math.inf) == SCALE
@@ -121,7 +123,7 @@ def test_evict_refusals(lib):
         assert evict(lib, **{name: 0}) == NULL
     for bad in (dict(B=0), dict(Hkv=0), dict(d=100), dict(page=0), dict(pages=0), dict(width=0),
                 dict(out_pages=0), dict(budget=0), dict(budget=33), dict(recent=-1),
-                dict(recent=21), dict(out_pages=1 << 27)):
+                dict(recent=21), dict(out_pages=1 << 27), dict(B=1 << 14, Hkv=1 << 14)):
         assert evict(lib, **bad) == SHAPE, bad
     assert evict(lib, dtype=3) == DTYPE
     assert evict(lib, vp=A[1] + 4) == ALIGN
