@@ -23,15 +23,21 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 
+from . import binding
 from .binding import FA_OK, FaError, _dtype_code, load_library
 
 _NO_CONTEXT = contextlib.nullcontext()
 
 
+def _library():
+    return binding._lib or load_library()
+
+
 def _check(name, t, shape, dtype, device):
-    if (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor %s on %s" % (
             name, str(dtype).replace("torch.", ""), list(shape), device))
 
@@ -46,7 +52,7 @@ def _first(name, t, dims):
 def _on(device):
     """The library works on the current device: make it the tensors'."""
     import torch
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         return _NO_CONTEXT
     return torch.cuda.device(device)
 
@@ -111,6 +117,7 @@ def _default_scale(d):
     return ctypes.c_float(1.0 / math.sqrt(d)).value
 
 
+@functools.lru_cache(maxsize=256)
 def key_weights_workspace_size(B: int, Hq: int, Hkv: int, N: int) -> int:
     """Bytes of workspace fa_key_weights needs (0 unless query heads share key heads)."""
     return int(load_library().fa_key_weights_workspace_size(B, Hq, Hkv, N))
@@ -132,7 +139,7 @@ def fa_key_weights(q, k, lse, w, causal: bool, scale: float, workspace=None, str
     _check("w", w, (B, Hkv, N), torch.float32, device)
     if seqlens_k is not None:
         _check("seqlens_k", seqlens_k, (B,), torch.int32, device)
-    lib = load_library()
+    lib = _library()
     left, right = (int(x) for x in window)
     with _on(device):
         keep, ws, ws_bytes = _workspace(key_weights_workspace_size(B, Hq, Hkv, N), workspace,
@@ -182,7 +189,7 @@ def fa_paged_append(k, v, k_pages, v_pages, block_table, seqlens, new_lens=None,
             raise ValueError("w needs a cache with weights")
         _check("w", w, (B, Hkv, N), torch.float32, device)
     with _on(device):
-        rc = load_library().fa_paged_append(
+        rc = _library().fa_paged_append(
             k.data_ptr(), v.data_ptr(), _ptr(w), k_pages.data_ptr(), v_pages.data_ptr(),
             _ptr(weights), block_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens), B, N, Hkv,
             d, page_size, num_pages, max_pages, _dtype_code(k), _handle(stream, device))
@@ -190,6 +197,7 @@ def fa_paged_append(k, v, k_pages, v_pages, block_table, seqlens, new_lens=None,
         raise FaError(rc, "fa_paged_append")
 
 
+@functools.lru_cache(maxsize=256)
 def paged_decode_workspace_size(B: int, Hq: int, Hkv: int, d: int, page_size: int,
                                 max_pages: int, with_weights: bool = False) -> int:
     """Bytes of workspace fa_paged_decode needs."""
@@ -213,10 +221,10 @@ def fa_paged_decode(q, k_pages, v_pages, block_table, seqlens, o, lse, scale: fl
     _check("q", q, (B, Hq, d), dtype, device)
     _check("o", o, (B, Hq, d), dtype, device)
     _check("lse", lse, (B, Hq), torch.float32, device)
-    lib = load_library()
+    lib = _library()
     with _on(device):
-        need = 0 if workspace is not None else int(lib.fa_paged_decode_workspace_size(
-            B, Hq, Hkv, d, page_size, max_pages, int(weights is not None)))
+        need = 0 if workspace is not None else paged_decode_workspace_size(
+            B, Hq, Hkv, d, page_size, max_pages, weights is not None)
         keep, ws, ws_bytes = _workspace(need, workspace, device, stream)
         rc = lib.fa_paged_decode(
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(weights),
@@ -265,7 +273,7 @@ def fa_paged_evict(k_pages, v_pages, weights, block_table, seqlens, out_table, k
     _check("out_table", out_table, (B, out_pages), torch.int32, device)
     _check("new_seqlens", new_seqlens, (B,), torch.int32, device)
     with _on(device):
-        rc = load_library().fa_paged_evict(
+        rc = _library().fa_paged_evict(
             k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), block_table.data_ptr(),
             seqlens.data_ptr(), out_table.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr(), B,
             Hkv, d, page_size, num_pages, max_pages, out_pages, budget, int(recent),
