@@ -379,8 +379,8 @@ int fa_paged_append(const void* k, const void* v, const float* w, void* k_pages,
  *   window_left  >= 0: only the last window_left + 1 tokens are visible; negative: all are
  *   weights      updated in place, or NULL
  *   workspace    device memory of at least fa_paged_decode_workspace_size(...) bytes, 16-byte
- *                aligned, not overlapping any other argument. Calls sharing a workspace must
- *                not overlap. Its contents need no initialisation.
+ *                aligned, not overlapping any other argument; NULL where that is 0. Calls
+ *                sharing a workspace must not overlap. Its contents need no initialisation.
  * A sequence with no visible token gets O = 0 and LSE = -inf. What the pages hold behind a
  * sequence's last token (NaN included) does not matter. A length beyond the table is taken as
  * the table's, and tokens in pages outside the pool are left out (FA_ERR_PAGE in the device
@@ -393,7 +393,8 @@ int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, flo
                     int window_left, float scale, int dtype, void* workspace,
                     size_t workspace_bytes, fa_stream_t stream);
 
-/* Bytes of workspace fa_paged_decode needs (with_weights: whether weights is passed). */
+/* Bytes of workspace fa_paged_decode needs (with_weights: whether weights is passed); 0 for short
+ * tables. */
 size_t fa_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size,
                                       int max_pages, int with_weights);
 

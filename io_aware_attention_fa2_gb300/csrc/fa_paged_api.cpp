@@ -201,8 +201,7 @@ int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, flo
                     int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
                     int window_left, float scale, int dtype, void* workspace,
                     size_t workspace_bytes, fa_stream_t stream) {
-  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !o || !lse || !workspace)
-    return FA_ERR_NULL;
+  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !o || !lse) return FA_ERR_NULL;
   if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages) ||
       !decode_shape_ok(B, Hq, Hkv, page_size, max_pages))
     return FA_ERR_SHAPE;
@@ -210,7 +209,12 @@ int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, flo
   if (!scale_ok(scale)) return FA_ERR_SCALE;
   const uint64_t ws_need =
       fa::paged_decode_workspace(B, Hq, Hkv, d, page_size, max_pages, weights != nullptr);
-  if (workspace_bytes < ws_need) return FA_ERR_WORKSPACE;
+  if (ws_need) {
+    if (!workspace) return FA_ERR_NULL;
+    if (workspace_bytes < ws_need) return FA_ERR_WORKSPACE;
+  } else {
+    workspace = nullptr;
+  }
   if (!aligned({q, k_pages, v_pages, o, weights, workspace}, 16) ||
       !aligned({block_table, seqlens, lse}, 4))
     return FA_ERR_ALIGN;

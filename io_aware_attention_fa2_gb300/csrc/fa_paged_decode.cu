@@ -30,7 +30,13 @@
 //
 // Weights need the final LSE: the scaled scores are kept (fp32, 4 G bytes a token against the
 // 4 d of K and V) and the second kernel adds exp2(score - maximum) / sum over the group's heads.
+// Short caches (the smallest calls, where latency counts) take one launch and no workspace: a
+// cluster of up to eight CTAs has one unit, up to four tiles each, all of them on their way at
+// once, and the parts are joined through distributed shared memory (choose_short has the rule).
+#include <cooperative_groups.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "fa_paged.cuh"
 
@@ -39,18 +45,23 @@ namespace fa {
 namespace {
 
 using namespace paged;
+namespace cg = cooperative_groups;
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kTile = 64;                      // tokens of a tile
-constexpr int kStages = 3;
+constexpr int kStagesLong = 3;                 // ring of tiles
+constexpr int kShortTiles = 4;                 // tiles of a CTA of a short unit, one stage each
 constexpr int kWarps = 4;                      // consumer warps, 16 tokens of a tile each
 constexpr int kThreads = 32 * (kWarps + 1);    // and the producer warp
 constexpr int kRows = 16;                      // query heads of a unit, at most
 constexpr int kMaxCtas = 2 * 152;              // two CTAs on each SM
+constexpr int kMaxShortCtas = 152;             // one on each SM
+constexpr int kMaxCluster = 8;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
-template <int D>
+template <int D, bool SHORT>
 struct Smem {
+  static constexpr int kStages = SHORT ? kShortTiles : kStagesLong;
   static constexpr uint32_t kTileBytes = kTile * D * 2;
   static constexpr uint32_t kK = 0;
   static constexpr uint32_t kV = kStages * kTileBytes;
@@ -60,7 +71,13 @@ struct Smem {
   static constexpr uint32_t kStats = kJoin + kWarps * 8 * kJoinPitch * 4;   // m, l [warp][row]
   static constexpr uint32_t kMask = kStats + 2 * kWarps * kRows * 4;        // uint64 per stage
   static constexpr uint32_t kBars = kMask + kStages * 8;                    // full, empty
-  static constexpr uint32_t kDynamic = kBars + 2 * kStages * 8 + 1024;      // 1 KiB alignment
+  // short units: this CTA's part (O, maxima and sums) and its scores
+  static constexpr uint32_t kPart = (kBars + 2 * kStages * 8 + 15) / 16 * 16;   // [16][D] floats
+  static constexpr uint32_t kPartMl = kPart + kRows * D * 4;                    // [16] float2
+  static constexpr int kScorePitch = kShortTiles * kTile + 8;                   // floats
+  static constexpr uint32_t kScores = kPartMl + kRows * 8;
+  static constexpr uint32_t kEnd = SHORT ? kScores + kRows * kScorePitch * 4 : kPart;
+  static constexpr uint32_t kDynamic = kEnd + 1024;   // slack for 1 KiB alignment
 };
 
 struct Args {
@@ -217,12 +234,15 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   }
 }
 
-template <int D, bool FP16, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads, 2)
+// SHORT: a cluster of CTAs has one unit, each CTA an equal share of its tiles. Otherwise: runs
+// over all units.
+template <int D, bool FP16, bool WEIGHTS, bool SHORT>
+__global__ void __launch_bounds__(kThreads, SHORT ? 1 : 2)
     fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ Args a) {
-  using L = Smem<D>;
+  using L = Smem<D, SHORT>;
+  constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag, s_seq;
   __shared__ int64_t s_at, s_left, s_start, s_total;
@@ -245,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     ptx::prefetch_tensormap(&tm_v);
   }
   // where this CTA's run starts: the sequence, and the tile within it
-  if (warp == 0) {
+  if (!SHORT && warp == 0) {
     const int64_t total = count_tiles(a) * a.Hkv * a.blocks;
     const int ctas = running(total, gridDim.x);
     const int64_t start = run_start(total, cta, ctas);
@@ -282,8 +302,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncthreads();
-  launch_dependents();
-  Walk walk{s_left, s_at, s_seq};
+  Walk walk{};
+  if constexpr (!SHORT) {
+    launch_dependents();
+    walk = Walk{s_left, s_at, s_seq};
+  }
+  const int rank = SHORT ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+  const int ranks = SHORT ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
+  // the segments of this CTA, one after the other: a short unit's share, or those of the run
+  auto more = [&](int done) { return SHORT ? done == 0 : walk.left > 0; };
+  auto next = [&](auto record, Tiles& t) {
+    if constexpr (SHORT) {
+      const int unit = cta / ranks, units = a.Hkv * a.blocks;
+      Segment s;
+      s.b = unit / units;
+      s.unit = unit % units;
+      t = tiles_of<decltype(record)::value>(a, s.b);
+      s.tile = t.count * rank / ranks;
+      s.count = t.count * (rank + 1) / ranks - s.tile;
+      s.whole = false;
+      return s;
+    } else {
+      return next_segment<decltype(record)::value>(a, walk, t);
+    }
+  };
   volatile int* abort_p = &abort_flag;
   auto give_up = [&] {
     *abort_p = 1;
@@ -296,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t box_bytes = static_cast<uint32_t>(br) * D * 2;
     int n = 0;   // tiles loaded so far: tile n goes through stage n % kStages
     bool ok = true;
-    while (walk.left > 0 && ok) {
+    for (int done = 0; ok && more(done); ++done) {
       Tiles t;
-      const Segment sg = next_segment<true>(a, walk, t);
+      const Segment sg = next(std::true_type{}, t);
       const int hk = sg.unit / a.blocks;
       const int row0 = (t.first + sg.tile) * kTile;      // first token of the segment
       const int total_boxes = sg.count * boxes;
@@ -356,6 +398,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     // Leave no copy in flight (on the normal path these phases completed long ago).
     for (int x = max(0, n - kStages); x < n; ++x)
       ptx::wait_bounded(full(x % kStages), (x / kStages) & 1, abort_p, kWaitLimitNs);
+    if constexpr (SHORT) {   // the consumers' two meetings of the cluster
+      __syncwarp();
+      cg::this_cluster().sync();
+      cg::this_cluster().sync();
+    }
     return;
   }
 
@@ -370,11 +417,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       (16 * warp / br) * static_cast<uint32_t>(br) * D * 2 + (16 * warp % br) * 128u;
   const uint32_t half_bytes = static_cast<uint32_t>(br) * 128;   // 64 columns of a box
   const int mi = lane / 8, l7 = lane % 8;          // ldmatrix: matrix and row of this lane
+  float* const scores = reinterpret_cast<float*>(gen + L::kScores);   // SHORT: [16][kScorePitch]
   int n = 0, runs = 0;
   bool ok = true;
-  while (walk.left > 0) {
+  for (; more(runs); ++runs) {
     Tiles t;
-    const Segment sg = next_segment<false>(a, walk, t);
+    const Segment sg = next(std::false_type{}, t);
     const int hk = sg.unit / a.blocks, h0 = (sg.unit % a.blocks) * kRows;
     const int rows = min(kRows, a.G - h0);
     const int64_t head0 = static_cast<int64_t>(sg.b) * a.Hq + hk * a.G + h0;   // row 0's (b, h)
@@ -440,7 +488,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int y = 0; y < 4; ++y)
               if (!(mask >> (8 * x + c0 + (y & 1)) & 1)) sv[x][y] = -INFINITY;
         }
-        if constexpr (WEIGHTS) {
+        if constexpr (WEIGHTS && SHORT) {
+          float* const at = scores + r0 * L::kScorePitch + i * kTile + 16 * warp + c0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            *reinterpret_cast<float2*>(at + 8 * x) = make_float2(sv[x][0], sv[x][1]);
+            *reinterpret_cast<float2*>(at + 8 * L::kScorePitch + 8 * x) =
+                make_float2(sv[x][2], sv[x][3]);
+          }
+        } else if constexpr (WEIGHTS) {
           const int token = (t.first + sg.tile + i) * kTile + 16 * warp + c0;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -540,7 +596,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         l += sm_l[w * kRows + r] * ptx::exp2_approx(sm_m[w * kRows + r] - u);
     };
     const int64_t slot = 2ll * cta + (runs > 0);
-    if (sg.tile == 0 && threadIdx.x == 0) {
+    float* const part = reinterpret_cast<float*>(gen + L::kPart);
+    float2* const part_ml = reinterpret_cast<float2*>(gen + L::kPartMl);
+    if (!SHORT && sg.tile == 0 && threadIdx.x == 0) {
       // this run holds the unit's first tile; its last is in the last run that starts before
       // the unit's end: the largest c with floor(total * c / ctas) < end
       const int ctas = running(s_total, gridDim.x);
@@ -552,7 +610,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x < kRows) {
       float m, l;
       row_stats(threadIdx.x, m, l);
-      if (static_cast<int>(threadIdx.x) >= rows) {
+      if constexpr (SHORT) {
+        part_ml[threadIdx.x] = make_float2(m, l);
+      } else if (static_cast<int>(threadIdx.x) >= rows) {
         // a row without a query head
       } else if (!sg.whole) {
         a.part_ml[slot * a.part_rows + threadIdx.x] = make_float2(m, l);
@@ -587,7 +647,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             sum.z += v.z;
             sum.w += v.w;
           }
-          if (!sg.whole) {
+          if constexpr (SHORT) {
+            *reinterpret_cast<float4*>(part + row * D + ch * 64 + c) = sum;
+          } else if (!sg.whole) {
             *reinterpret_cast<float4*>(a.part_o + (slot * a.part_rows + row) * D + ch * 64 + c) = sum;
           } else {
             float mr, lr;
@@ -601,7 +663,65 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::named_barrier_sync(1, 32 * kWarps);
       }
     }
-    ++runs;
+    if constexpr (SHORT) {
+      const cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();   // every CTA's part is in its shared memory
+      const int tid = threadIdx.x;
+      // four columns of a row a thread, the rows shared out over the cluster
+      for (int at = rank * 32 * kWarps + tid; at < rows * (D / 4); at += ranks * 32 * kWarps) {
+        const int row = at / (D / 4), x = at % (D / 4);
+        float m = -INFINITY, l = 0.f;
+        float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          if (r >= ranks) break;
+          const float2 ml = *cluster.map_shared_rank(part_ml + row, r);
+          const float4 v =
+              *reinterpret_cast<const float4*>(cluster.map_shared_rank(part + row * D + 4 * x, r));
+          const float top = fmaxf(m, ml.x), u = top == -INFINITY ? 0.f : top;
+          const float f = ptx::exp2_approx(m - u), g = ptx::exp2_approx(ml.x - u);
+          m = top;
+          l = l * f + ml.y * g;
+          acc4.x = acc4.x * f + v.x * g;
+          acc4.y = acc4.y * f + v.y * g;
+          acc4.z = acc4.z * f + v.z * g;
+          acc4.w = acc4.w * f + v.w * g;
+        }
+        const float inv = inverse(l);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (head0 + row) * D + 4 * x) =
+            make_uint2(pack2<FP16>(acc4.x * inv, acc4.y * inv),
+                       pack2<FP16>(acc4.z * inv, acc4.w * inv));
+        if (x == 0) a.lse[head0 + row] = lse_of(m, l);
+      }
+      if constexpr (WEIGHTS) {
+        // maximum and 1 / sum of every row (where the warps' statistics were), then the tokens of
+        // this CTA's tiles: the bits of a tile's mask are its visible tokens in good pages
+        float2* const stat = reinterpret_cast<float2*>(gen + L::kStats);
+        if (tid < rows) {
+          float m = -INFINITY, l = 0.f;
+          for (int r = 0; r < ranks; ++r) m = fmaxf(m, cluster.map_shared_rank(part_ml + tid, r)->x);
+          const float u = m == -INFINITY ? 0.f : m;
+          for (int r = 0; r < ranks; ++r) {
+            const float2 ml = *cluster.map_shared_rank(part_ml + tid, r);
+            l += ml.y * ptx::exp2_approx(ml.x - u);
+          }
+          stat[tid] = make_float2(u, inverse(l));
+        }
+        ptx::named_barrier_sync(1, 32 * kWarps);
+        for (int at = tid; ok && at < sg.count * kTile; at += 32 * kWarps) {
+          if (!(masks[at / kTile] >> (at % kTile) & 1)) continue;
+          float sum = 0.f;
+          for (int row = 0; row < rows; ++row)
+            sum += ptx::exp2_approx(scores[row * L::kScorePitch + at] - stat[row].x) * stat[row].y;
+          const int token = (t.first + sg.tile) * kTile + at;
+          const int64_t page =
+              a.table[static_cast<int64_t>(sg.b) * a.max_pages + token / a.page_size];
+          ptx::red_add_f32(a.weights + (page * a.Hkv + hk) * a.page_size + token % a.page_size,
+                           sum);
+        }
+      }
+      cluster.sync();   // no CTA leaves while another reads its part
+    }
   }
 }
 
@@ -794,6 +914,21 @@ int64_t grid_size(int B, int Hq, int Hkv, int64_t capacity) {
   return std::min<int64_t>(kMaxCtas, tiles);
 }
 
+// The smallest calls: 0, or the CTAs of a cluster that has one unit. Where every unit fits in a
+// cluster of CTAs with up to kShortTiles tiles each, and all of them run at once (one on each
+// SM), one launch without a workspace is faster than runs and their join: B=1 Hkv=8 d=64 with
+// 1001 tokens 8.3 us instead of 10.3 a replay of a graph, 19 us instead of 26 a call from
+// Python, which has no workspace to allocate. With weights the query
+// heads of a key head have to be one unit, so that every weight gets one addition.
+int choose_short(int B, int Hq, int Hkv, int64_t tiles, bool with_weights) {
+  const int64_t blocks = (Hq / Hkv + kRows - 1) / kRows, units = B * Hkv * blocks;
+  if (with_weights && blocks > 1) return 0;
+  for (int ctas = kMaxCluster; ctas >= 1; ctas /= 2)
+    if (units * ctas <= kMaxShortCtas && (ctas == 1 || ctas / 2 < tiles))
+      return tiles <= ctas * kShortTiles ? ctas : 0;
+  return 0;
+}
+
 // Workspace: the parts' O, their maxima and sums, the units' parts, then (with weights)
 // statistics and scores.
 struct Layout {
@@ -847,8 +982,31 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
   if (!encode_pages(&tm_k, c.k_pages, c, a.box_rows, FP16) ||
       !encode_pages(&tm_v, c.v_pages, c, a.box_rows, FP16))
     return cudaErrorInvalidValue;
-  auto kernel = fa_paged_decode_kernel<D, FP16, WEIGHTS>;
-  const int smem = static_cast<int>(Smem<D>::kDynamic);
+  // tiles of a unit, at most: a window's tokens span two more tiles than its length fills
+  int64_t tiles = (static_cast<int64_t>(a.capacity) + kTile - 1) / kTile;
+  if (a.window_left >= 0) tiles = std::min<int64_t>(tiles, a.window_left / kTile + 2);
+  if (const int cluster = choose_short(c.B, p.Hq, c.Hkv, tiles, WEIGHTS)) {
+    auto kernel = fa_paged_decode_kernel<D, FP16, WEIGHTS, true>;
+    const int smem = static_cast<int>(Smem<D, true>::kDynamic);
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(c.B * c.Hkv * a.blocks * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, a);
+  }
+  auto kernel = fa_paged_decode_kernel<D, FP16, WEIGHTS, false>;
+  const int smem = static_cast<int>(Smem<D, false>::kDynamic);
   cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
@@ -890,7 +1048,9 @@ cudaError_t launch_weights(const DecodeParams& p, cudaStream_t stream) {
 
 size_t paged_decode_workspace(int B, int Hq, int Hkv, int d, int page_size, int max_pages,
                               bool with_weights) {
-  return layout(B, Hq, Hkv, d, static_cast<int64_t>(max_pages) * page_size, with_weights).end;
+  const int64_t capacity = static_cast<int64_t>(max_pages) * page_size;
+  if (choose_short(B, Hq, Hkv, (capacity + kTile - 1) / kTile, with_weights)) return 0;
+  return layout(B, Hq, Hkv, d, capacity, with_weights).end;
 }
 
 cudaError_t launch_paged_decode(const DecodeParams& p, cudaStream_t stream) {

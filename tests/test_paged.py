@@ -37,7 +37,7 @@ def append(lib, k=A[0], v=A[1], w=A[2], kp=A[3], vp=A[4], weights=A[5], table=A[
 
 
 def decode(lib, q=A[0], kp=A[1], vp=A[2], weights=A[3], table=A[4], lens=A[5], o=A[6], lse=A[7],
-           B=2, Hq=4, Hkv=2, d=64, page=16, pages=8, width=4, window=-1, scale=0.1, dtype=0,
+           B=2, Hq=4, Hkv=2, d=64, page=16, pages=8, width=400, window=-1, scale=0.1, dtype=0,
            ws=A[8], ws_bytes=1 << 62):
     return lib.fa_paged_decode(q, kp, vp, weights, table, lens, o, lse, B, Hq, Hkv, d, page,
                                pages, width, window, scale, dtype, ws, ws_bytes, None)
@@ -54,9 +54,18 @@ def test_workspace_sizes(lib):
     assert lib.fa_key_weights_workspace_size(2, 8, 2, 100) == 2 * 8 * 100 * 4
     assert lib.fa_key_weights_workspace_size(2, 8, 8, 100) == 0
     assert lib.fa_key_weights_workspace_size(0, 8, 2, 100) == 0
-    small = lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 16, 10, 0)
-    with_w = lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 16, 10, 1)
-    assert 0 < small <= with_w
+    small = lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 16, 200, 0)
+    with_w = lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 16, 200, 1)
+    # 50 tiles for each of 4 units: 200 runs of 4 heads' parts, then the scores
+    assert small == 2 * 200 * 4 * (64 * 4 + 8) + 4 * 8
+    assert with_w == small + 16 * 8 + 16 * 3200 * 4
+    assert lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 16, 128, 1) == 0   # 32 tiles: short
+    assert lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 16, 129, 1) > 0
+    assert lib.fa_paged_decode_workspace_size(40, 8, 2, 64, 16, 16, 0) == 0   # 80 units, one CTA
+    assert lib.fa_paged_decode_workspace_size(40, 8, 2, 64, 16, 17, 0) > 0
+    assert lib.fa_paged_decode_workspace_size(80, 8, 2, 64, 16, 16, 0) > 0
+    assert lib.fa_paged_decode_workspace_size(1, 32, 1, 64, 16, 16, 0) == 0   # two blocks of heads
+    assert lib.fa_paged_decode_workspace_size(1, 32, 1, 64, 16, 16, 1) > 0
     assert lib.fa_paged_decode_workspace_size(2, 8, 3, 64, 16, 10, 0) == 0    # 8 % 3
     assert lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 17, 10, 0) == 0    # page size
     assert lib.fa_error_string(-13) == \

@@ -143,7 +143,8 @@ def test_refusals_of_the_binding():
         dec(x, c.k, c.v, c.table, c.seqlens)
     assert e.value.code == -4
     with pytest.raises(fa.FaError) as e:      # workspace too small
-        dec(q, c.k, c.v, c.table, c.seqlens,
+        long = torch.cat([c.table, torch.full((2, 300), -1, dtype=torch.int32, device="cuda")], 1)
+        dec(q, c.k, c.v, long, c.seqlens,
             workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     assert e.value.code == -11
     with pytest.raises(fa.FaError) as e:      # o over q

@@ -32,6 +32,29 @@ def decode(c, q, scale=None, **kw):
 LENS = [0, 1, 15, 16, 17, 63, 64, 65, 200, 1000]
 
 
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("d,dtype,Hq,Hkv", [(64, "fp16", 4, 4), (128, "bf16", 8, 2),
+                                            (128, "fp16", 16, 1), (64, "bf16", 40, 2)])
+@pytest.mark.parametrize("B,tokens,window", [(1, 2048, -1), (1, 2049, -1), (3, 64, -1),
+                                             (4, 700, -1), (4, 90000, 1700), (18, 500, -1),
+                                             (38, 256, -1), (60, 130, 40)])
+def test_decode_short_and_long_tables(page, d, dtype, Hq, Hkv, B, tokens, window):
+    """Both sides of the rule that gives a unit to a cluster: few and many units, tables up to
+    and past its tiles, windows that make long tables short."""
+    r = torch.Generator().manual_seed(B * tokens)
+    lens = [tokens] + torch.randint(0, min(tokens, 5000) + 1, (B - 1,), generator=r).tolist()
+    c = Cache(lens, page, Hkv, d, dtype, seed=tokens + page, weights=True)
+    q = c.query(Hq)
+    before = c.w.clone()
+    o, lse = decode(c, q, window_left=window)
+    assert same_bits(c.w, before)
+    ref = decode_ref(c, q, default_scale(d), window)
+    check_decode(c, q, o, lse, ref, (page, lens, window))
+    o2, lse2 = decode(c, q, window_left=window, weights=c.w)
+    check_decode(c, q, o2, lse2, ref, (page, lens, window, "weights"))
+    check_weights(c, before, ref)
+
+
 # ------------------------------------------------------------------------------------- decode
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("d,dtype", [(64, "fp16"), (64, "bf16"), (128, "fp16"), (128, "bf16")])
@@ -203,11 +226,12 @@ def test_decode_same_bits_again_and_in_any_batch():
     assert same_bits(o, o2) and same_bits(lse, lse2) and same_bits(w1, c.w)
 
 
-def test_decode_other_stream_and_graph():
+@pytest.mark.parametrize("max_pages", [None, 150])
+def test_decode_other_stream_and_graph(max_pages):
     """Captured on a side stream with a kept workspace, replayed for other lengths; two graphs
-    that share the workspace run one after the other."""
+    that share the workspace run one after the other. (The shorter table needs none.)"""
     import io_aware_attention_fa2_gb300 as fa
-    c = Cache([700, 300], 16, 2, 64, "fp16", seed=15, weights=True)
+    c = Cache([700, 300], 16, 2, 64, "fp16", seed=15, weights=True, max_pages=max_pages)
     q = c.query(8)
     ws = torch.empty(fa.paged_decode_workspace_size(2, 8, 2, 64, 16, c.max_pages, True),
                      dtype=torch.uint8, device="cuda")
