@@ -49,12 +49,19 @@ def _first(name, t, dims):
     return t.device, t.dtype
 
 
-def _on(device):
-    """The library works on the current device: make it the tensors'."""
+def _call(where, fn, device, stream, args):
+    """fn(*args, stream) on the tensors' device (the library works on the current one)."""
     import torch
-    if torch._C._cuda_getDevice() == device.index:
-        return _NO_CONTEXT
-    return torch.cuda.device(device)
+    if torch._C._cuda_getDevice() != device.index:
+        with torch.cuda.device(device):
+            return _call(where, fn, device, stream, args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
+    rc = fn(*args, stream or None)
+    if rc != FA_OK:
+        raise FaError(rc, where)
 
 
 def _stream_of(stream, device):
@@ -65,14 +72,6 @@ def _stream_of(stream, device):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
-
-
-def _handle(stream, device):
-    """The stream's handle; None: the current stream of the tensors' device."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device.index) or None
-    return getattr(stream, "cuda_stream", stream) or None
 
 
 def _workspace(need, workspace, device, stream):
@@ -97,12 +96,14 @@ def _cache(k_pages, v_pages, weights, block_table, seqlens):
     """Checks a cache's tensors: (device, dtype, B, Hkv, d, page_size, num_pages, max_pages)."""
     import torch
     device, dtype = _first("k_pages", k_pages, 4)
-    num_pages, page_size, Hkv, d = k_pages.shape
-    _check("v_pages", v_pages, (num_pages, page_size, Hkv, d), dtype, device)
-    if block_table.dim() != 2:
+    shape = k_pages.shape
+    num_pages, page_size, Hkv, d = shape
+    _check("v_pages", v_pages, shape, dtype, device)
+    table = block_table.shape
+    if len(table) != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    B, max_pages = block_table.shape
-    _check("block_table", block_table, (B, max_pages), torch.int32, device)
+    B, max_pages = table
+    _check("block_table", block_table, table, torch.int32, device)
     _check("seqlens", seqlens, (B,), torch.int32, device)
     if weights is not None:
         _check("weights", weights, (num_pages, Hkv, page_size), torch.float32, device)
@@ -139,17 +140,13 @@ def fa_key_weights(q, k, lse, w, causal: bool, scale: float, workspace=None, str
     _check("w", w, (B, Hkv, N), torch.float32, device)
     if seqlens_k is not None:
         _check("seqlens_k", seqlens_k, (B,), torch.int32, device)
-    lib = _library()
     left, right = (int(x) for x in window)
-    with _on(device):
-        keep, ws, ws_bytes = _workspace(key_weights_workspace_size(B, Hq, Hkv, N), workspace,
-                                        device, stream)
-        rc = lib.fa_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), w.data_ptr(), B, Hq,
-                                Hkv, N, d, int(bool(causal)), left, right, _ptr(seqlens_k),
-                                float(scale), _dtype_code(q), ws, ws_bytes,
-                                _handle(stream, device))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_key_weights")
+    keep, ws, ws_bytes = _workspace(key_weights_workspace_size(B, Hq, Hkv, N), workspace, device,
+                                    stream)
+    _call("fa_key_weights", _library().fa_key_weights, device, stream, (
+        q.data_ptr(), k.data_ptr(), lse.data_ptr(), w.data_ptr(), B, Hq, Hkv, N, d,
+        int(bool(causal)), left, right, _ptr(seqlens_k), float(scale), _dtype_code(q), ws,
+        ws_bytes))
 
 
 def key_weights(q, k, lse, causal: bool = False, scale: float | None = None, stream=None,
@@ -188,13 +185,10 @@ def fa_paged_append(k, v, k_pages, v_pages, block_table, seqlens, new_lens=None,
         if weights is None:
             raise ValueError("w needs a cache with weights")
         _check("w", w, (B, Hkv, N), torch.float32, device)
-    with _on(device):
-        rc = _library().fa_paged_append(
-            k.data_ptr(), v.data_ptr(), _ptr(w), k_pages.data_ptr(), v_pages.data_ptr(),
-            _ptr(weights), block_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens), B, N, Hkv,
-            d, page_size, num_pages, max_pages, _dtype_code(k), _handle(stream, device))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_paged_append")
+    _call("fa_paged_append", _library().fa_paged_append, device, stream, (
+        k.data_ptr(), v.data_ptr(), _ptr(w), k_pages.data_ptr(), v_pages.data_ptr(),
+        _ptr(weights), block_table.data_ptr(), seqlens.data_ptr(), _ptr(new_lens), B, N, Hkv, d,
+        page_size, num_pages, max_pages, _dtype_code(k)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -212,6 +206,13 @@ def fa_paged_decode(q, k_pages, v_pages, block_table, seqlens, o, lse, scale: fl
     its key head) is added to them. ``window_left`` >= 0: only the last window_left + 1 tokens
     are visible. ``workspace``: a CUDA tensor of at least ``paged_decode_workspace_size`` bytes
     (16-byte aligned), or None to let PyTorch allocate one."""
+    _decode(q, k_pages, v_pages, block_table, seqlens, o, lse, scale, weights, window_left,
+            workspace, stream)
+
+
+def _decode(q, k_pages, v_pages, block_table, seqlens, o, lse, scale, weights, window_left,
+            workspace, stream):
+    """fa_paged_decode; outputs that are None are allocated. Returns o, lse."""
     import torch
     device, dtype, B, Hkv, d, page_size, num_pages, max_pages = _cache(
         k_pages, v_pages, weights, block_table, seqlens)
@@ -219,20 +220,23 @@ def fa_paged_decode(q, k_pages, v_pages, block_table, seqlens, o, lse, scale: fl
         raise ValueError("q must be [B, Hq, d]")
     Hq = q.shape[1]
     _check("q", q, (B, Hq, d), dtype, device)
+    if o is None or lse is None:
+        with _stream_of(stream, device):
+            if o is None:
+                o = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
     _check("o", o, (B, Hq, d), dtype, device)
     _check("lse", lse, (B, Hq), torch.float32, device)
-    lib = _library()
-    with _on(device):
-        need = 0 if workspace is not None else paged_decode_workspace_size(
-            B, Hq, Hkv, d, page_size, max_pages, weights is not None)
-        keep, ws, ws_bytes = _workspace(need, workspace, device, stream)
-        rc = lib.fa_paged_decode(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(weights),
-            block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
-            d, page_size, num_pages, max_pages, int(window_left), float(scale), _dtype_code(q),
-            ws, ws_bytes, _handle(stream, device))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_paged_decode")
+    need = 0 if workspace is not None else paged_decode_workspace_size(
+        B, Hq, Hkv, d, page_size, max_pages, weights is not None)
+    keep, ws, ws_bytes = _workspace(need, workspace, device, stream)
+    _call("fa_paged_decode", _library().fa_paged_decode, device, stream, (
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(weights),
+        block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, d,
+        page_size, num_pages, max_pages, int(window_left), float(scale), _dtype_code(q), ws,
+        ws_bytes))
+    return o, lse
 
 
 def paged_attention(q, k_pages, v_pages, block_table, seqlens, scale: float | None = None,
@@ -241,17 +245,10 @@ def paged_attention(q, k_pages, v_pages, block_table, seqlens, scale: float | No
     """O, LSE = attention of one new token per sequence over a paged cache. The call a user makes
     for a decoding step (``fa_paged_decode`` with outputs allocated here unless given); ``scale``
     defaults to 1/sqrt(d) rounded to fp32."""
-    import torch
     if scale is None:
         scale = _default_scale(q.shape[-1])
-    with _stream_of(stream, q.device):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    fa_paged_decode(q, k_pages, v_pages, block_table, seqlens, out, lse, scale, weights,
-                    window_left, workspace, stream)
-    return out, lse
+    return _decode(q, k_pages, v_pages, block_table, seqlens, out, lse, scale, weights,
+                   window_left, workspace, stream)
 
 
 def fa_paged_evict(k_pages, v_pages, weights, block_table, seqlens, out_table, kept, new_seqlens,
@@ -272,14 +269,11 @@ def fa_paged_evict(k_pages, v_pages, weights, block_table, seqlens, out_table, k
     _check("kept", kept, (B, Hkv, budget), torch.int32, device)
     _check("out_table", out_table, (B, out_pages), torch.int32, device)
     _check("new_seqlens", new_seqlens, (B,), torch.int32, device)
-    with _on(device):
-        rc = _library().fa_paged_evict(
-            k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), block_table.data_ptr(),
-            seqlens.data_ptr(), out_table.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr(), B,
-            Hkv, d, page_size, num_pages, max_pages, out_pages, budget, int(recent),
-            _dtype_code(k_pages), _handle(stream, device))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_paged_evict")
+    _call("fa_paged_evict", _library().fa_paged_evict, device, stream, (
+        k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), block_table.data_ptr(),
+        seqlens.data_ptr(), out_table.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr(), B, Hkv,
+        d, page_size, num_pages, max_pages, out_pages, budget, int(recent),
+        _dtype_code(k_pages)))
 
 
 def paged_evict(k_pages, v_pages, weights, block_table, seqlens, out_table, budget: int,
