@@ -17,13 +17,16 @@
 //                queries of the tile; warps 10..17 the same for S_B. Nothing synchronises them
 //                but the S buffers: every warp keeps its own copy of the LSEs that it needs.
 // One half of the warps sums S_A while S_B is computed, and the other way round. Measured on B=1
-// H=16 N=16384 d=128 causal: 400 us (1374 TFLOP/s), of which the products alone take 309 and the
-// sums alone 375: the exponentials (32 a cycle and SM) and the instructions around them are
-// what is left. Slower: all sixteen warps on S_A, then on S_B (421 us); eight warps with twice
-// the columns (427); 32-column loads of S one ahead of the sums (439); products with 128
-// queries, whose operands are 8 KB of shared memory for 64 cycles of work (494).
+// H=16 N=16384 d=128 causal: 390 us (1411 TFLOP/s, 74 % of the measured dense bf16 peak), of
+// which the products alone take 309 and the sums alone 375: the exponentials (32 a cycle and
+// SM, 55 % busy) and the shared-memory reads of the LSEs share an issue queue, and four warps a
+// scheduler do not fill their latencies. Slower: all sixteen warps on S_A, then on S_B (421 us);
+// eight warps with twice the columns (427); 32-column loads of S one ahead of the sums (439);
+// 16x256b loads of S, which need half of the LSE reads (468); products with 128 queries, whose
+// operands are 8 KB of shared memory for 64 cycles of work (494). The same: CTAs that take
+// further units off the hardware's launch queue instead of ending (395).
 //
-// Sums: 32 bits, a query tile at a time in four chains, the tiles' sums added with Kahan's
+// Sums: 32 bits, 64 queries at a time in four chains, the tiles' sums added with Kahan's
 // compensation: a key of a long prompt is the sum of many thousand terms. With shared key heads
 // each query head writes its own sums (fp32 workspace) and a second kernel adds them in the order
 // of the heads, so that the result does not depend on which CTA ends first.
@@ -178,6 +181,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int u0 = a_any ? (b_any ? min(a0, b0) : a0) : b0;
   const int u1 = max(a1, b1);
 
+  // Q tile u0 + n into its stage of the ring
+  auto load_q = [&](int n) {
+    const int s = n % kStages;
+    ptx::mbar_arrive_expect_tx(bar(BAR_Q_FULL + s), L::kQTile);
+    for (int c = 0; c < D / BOX_COLS; ++c)
+      for (int r = 0; r < 2; ++r)
+        ptx::tma_load_4d(sQ + s * L::kQTile + (2 * c + r) * kBoxBytes, &tm_q, bar(BAR_Q_FULL + s),
+                         c * BOX_COLS, h, (u0 + n) * kQueries + r * BOX_ROWS, b);
+  };
   if (threadIdx.x == 0) {
     abort_flag = 0;
     ptx::mbar_init(bar(BAR_K_FULL), 1);
@@ -191,6 +203,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(bar(BAR_MMA_DONE), 1);
     ptx::fence_barrier_init();
+    // K and the first Q tiles are on their way before the other warps and TMEM are ready (B=1 H=8
+    // N=500 d=64: 10.2 -> 9.7 us)
+    if (any_work) {
+      ptx::mbar_arrive_expect_tx(bar(BAR_K_FULL), 2 * L::kKTile);
+      for (int x = 0; x < 2; ++x)
+        for (int c = 0; c < D / BOX_COLS; ++c)
+          ptx::tma_load_4d(sK + x * L::kKTile + c * kBoxBytes, &tm_k, bar(BAR_K_FULL),
+                           c * BOX_COLS, h / G, (2 * kblk + x) * BLOCK_N, b);
+      for (int n = 0; n < min(kStages, u1 - u0); ++n) load_q(n);
+    }
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(&tmem_base_slot), kTmemCols);
@@ -205,27 +227,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0 && any_work) {
-      ptx::prefetch_tensormap(&tm_q);
-      ptx::prefetch_tensormap(&tm_k);
-      ptx::mbar_arrive_expect_tx(bar(BAR_K_FULL), 2 * L::kKTile);
-      for (int x = 0; x < 2; ++x)
-        for (int c = 0; c < D / BOX_COLS; ++c)
-          ptx::tma_load_4d(sK + x * L::kKTile + c * kBoxBytes, &tm_k, bar(BAR_K_FULL),
-                           c * BOX_COLS, h / G, (2 * kblk + x) * BLOCK_N, b);
-      int issued = 0;
-      for (int n = 0; n < u1 - u0; ++n) {
-        const int s = n % kStages;
-        if (!ptx::wait_bounded(bar(BAR_Q_EMPTY + s), ((n / kStages) & 1) ^ 1, abort_p,
+      int issued = min(kStages, u1 - u0);
+      for (int n = issued; n < u1 - u0; ++n) {
+        if (!ptx::wait_bounded(bar(BAR_Q_EMPTY + n % kStages), ((n / kStages) & 1) ^ 1, abort_p,
                                kWaitLimitNs)) {
           record_timeout(abort_p);
           break;
         }
-        ptx::mbar_arrive_expect_tx(bar(BAR_Q_FULL + s), L::kQTile);
-        for (int c = 0; c < D / BOX_COLS; ++c)
-          for (int r = 0; r < 2; ++r)
-            ptx::tma_load_4d(sQ + s * L::kQTile + (2 * c + r) * kBoxBytes, &tm_q,
-                             bar(BAR_Q_FULL + s), c * BOX_COLS, h,
-                             (u0 + n) * kQueries + r * BOX_ROWS, b);
+        load_q(n);
         issued = n + 1;
       }
       // Leave no copy in flight (on the normal path these phases completed long ago).
