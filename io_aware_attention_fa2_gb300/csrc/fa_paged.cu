@@ -432,10 +432,12 @@ cudaError_t launch_select(const EvictArgs& a, int64_t units, cudaStream_t stream
   const int64_t most =
       ((static_cast<int64_t>(a.max_pages) << a.page_shift) + 4 * CTAS - 1) / (4 * CTAS) * 4;
   const int cache_keys = static_cast<int>(std::min<int64_t>(most, kMaxCache));
-  const int smem = ((CTAS > 1 ? 2 : 1) * kBins + cache_keys) * 4;
+  constexpr int kHist = (CTAS > 1 ? 2 : 1) * kBins;
+  const int smem = (kHist + cache_keys) * 4;
   auto kernel = fa_paged_select_kernel<CTAS>;
-  cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the function's, not the launch's: the same for all calls, which may overlap
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (kHist + kMaxCache) * 4);
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

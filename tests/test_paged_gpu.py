@@ -68,7 +68,7 @@ def test_decode_lengths(page, d, dtype):
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (8, 1), (12, 4), (16, 1), (20, 1), (34, 2),
-                                    (64, 1)])
+                                    (64, 1), (70, 1), (130, 1)])
 @pytest.mark.parametrize("weights", [False, True])
 def test_decode_head_groups(Hq, Hkv, weights):
     c = Cache([130, 1, 517], 32, Hkv, 128, "bf16", seed=Hq, weights=weights)
@@ -277,6 +277,65 @@ def test_decode_overlapping_streams():
         torch.cuda.synchronize()
         for (o, l), (o1, l1) in zip(got, alone):
             assert same_bits(o, o1) and same_bits(l, l1)
+
+
+def test_calls_from_several_threads():
+    """Decodes, evictions and key weights of different sizes enqueued by four threads at once, each
+    on its own stream, each as when alone."""
+    import threading
+
+    import io_aware_attention_fa2_gb300 as fa
+    jobs = []
+    for i in range(4):
+        n = [300, 60000, 1500, 9000][i]
+        c = Cache([n, n // 3], 64, 2, 64, "bf16", seed=40 + i, weights=True, spare=20)
+        q = c.query(4)
+        out = free_table(c, 128)
+        p = torch.randn((1, 100 + 70 * i, 2, 64), generator=c.g).to(c.dtype).cuda()
+        lse = torch.full((1, 2, p.shape[1]), 6.0, device="cuda")
+        jobs.append((c, q, out, p, lse))
+
+    def work(c, q, out, p, lse, stream=None):
+        o, l = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens, stream=stream)
+        kept, lens = fa.paged_evict(c.k, c.v, c.w, c.table, c.seqlens, out, 128, 16, stream=stream)
+        w = fa.key_weights(p, p, lse, causal=True, stream=stream)
+        return o, l, kept, lens, w
+
+    alone = [work(*j) for j in jobs]
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def thread(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(20):
+                got[i] = work(*jobs[i], stream=stream)
+            stream.synchronize()
+        except Exception as e:   # reported below: an exception would end the thread alone
+            errors.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for a, b in zip(alone, got):
+        for x, y in zip(a, b):
+            assert same_bits(x, y)
+
+
+def test_streams_given_as_handles():
+    import io_aware_attention_fa2_gb300 as fa
+    c = Cache([3000, 70], 32, 2, 64, "fp16", seed=50)
+    q = c.query(4)
+    want = decode(c, q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (0, side, side.cuda_stream, torch.cuda.default_stream()):
+        o, lse = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens, stream=stream)
+        torch.cuda.synchronize()
+        assert same_bits(o, want[0]) and same_bits(lse, want[1])
 
 
 def test_decode_pool_past_2_31_elements():
