@@ -14,6 +14,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
+#include "fa_paged_internal.h"
 
 namespace {
 

@@ -1,15 +1,12 @@
 // fa_internal.h -- declarations shared by the translation units of the CUDA library
 // (fa_api.cpp: argument checks, tensor maps, C ABI; fa_fwd_kernel.cu, fa_bwd_kernel.cu:
-// kernels and launch; fa_noalloc.cu: the entry point with a built-in workspace;
-// fa_paged_api.cpp, fa_paged.cu, fa_key_weights.cu: the paged key-value cache).
+// kernels and launch; fa_noalloc.cu: the entry point with a built-in workspace).
 // Not part of the public ABI (that is include/fa.h).
 #pragma once
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-
-#include <initializer_list>
 
 namespace fa {
 
@@ -80,78 +77,5 @@ int check_splitkv_args(const void* q, const void* k, const void* v, void* o, flo
 cudaError_t launch_bwd(const BwdParams& p, cudaStream_t stream);
 // The backward kernels' error word of the current device: read and clear (no synchronisation).
 cudaError_t read_and_clear_bwd_error(int* value);
-
-// ---- host-side helpers shared by the C ABI's translation units (fa_api.cpp)
-// FA_OK when the current device is sm_103 (its number in *device).
-int check_arch(int* device);
-// FA_OK when every non-null pointer is device memory usable by `device`, else FA_ERR_POINTER.
-int check_device_ptrs(int device, std::initializer_list<const void*> ptrs);
-bool overlaps(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes);
-// The driver's cuTensorMapEncodeTiled, or null.
-void* encode_tiled_entry();
-// [B, N, H, d] 16-bit tensor as a 4-D TMA map (d, H, N, B) with box (64, 1, 128, 1).
-bool encode_bnhd(CUtensorMap* map, const void* base, int B, int H, int N, int d, bool fp16);
-
-// ---- the paged key-value cache (include/fa.h has the layouts)
-struct KeyWeightsParams {
-  CUtensorMap tm_q, tm_k;   // [B, N, Hq, d] and [B, N, Hkv, d]
-  const void* q;
-  const void* k;
-  const float* lse;         // [B, Hq, N]
-  float* w;                 // [B, Hkv, N]
-  float* part;              // workspace [B, Hq, N] when Hq > Hkv, else null
-  int B, Hq, Hkv, N, d;
-  int causal, window_left, window_right;   // windows clamped to N, or -1
-  const int* seqlens_k;     // device int32 [B] or null
-  int fp16;
-  float scale_log2;
-};
-cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
-
-struct PagedCache {
-  void* k_pages;            // [num_pages, page_size, Hkv, d]
-  void* v_pages;
-  float* weights;           // [num_pages, Hkv, page_size] or null
-  const int* block_table;   // device int32 [B, max_pages]
-  const int* seqlens;       // device int32 [B]
-  int B, Hkv, d, page_size, num_pages, max_pages;
-};
-
-struct AppendParams {
-  PagedCache c;
-  const void* k;            // [B, N, Hkv, d]
-  const void* v;
-  const float* w;           // [B, Hkv, N] or null
-  const int* new_lens;      // device int32 [B] or null
-  int N;
-};
-cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream);
-
-struct DecodeParams {
-  PagedCache c;
-  const void* q;            // [B, Hq, d]
-  void* o;
-  float* lse;               // [B, Hq]
-  void* workspace;
-  int Hq, window_left, fp16;
-  float scale_log2;
-};
-cudaError_t launch_paged_decode(const DecodeParams& p, cudaStream_t stream);
-size_t paged_decode_workspace(int B, int Hq, int Hkv, int d, int page_size, int max_pages,
-                              bool with_weights);
-
-struct EvictParams {
-  PagedCache c;
-  const int* out_table;     // device int32 [B, out_pages]
-  int* kept;                // [B, Hkv, budget]
-  int* new_seqlens;         // [B]
-  int out_pages, budget, recent;
-};
-cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream);
-
-// The error words of these kernels on the current device: read and clear (no synchronisation).
-cudaError_t read_and_clear_key_weights_error(int* value);
-cudaError_t read_and_clear_paged_error(int* value);   // FA_ERR_TIMEOUT before FA_ERR_PAGE
-cudaError_t read_and_clear_decode_error(int* bits);   // or-ed in: 1 timeout, 2 bad page
 
 }  // namespace fa

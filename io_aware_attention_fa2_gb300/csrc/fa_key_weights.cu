@@ -35,7 +35,7 @@
 
 #include <algorithm>
 
-#include "fa_internal.h"
+#include "fa_paged_internal.h"
 #include "ptx_sm103.cuh"
 
 namespace fa {

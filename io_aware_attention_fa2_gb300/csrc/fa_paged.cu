@@ -97,21 +97,42 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Whether a page of the tables is outside the pool, or a page of dst stands in src at a later
-// place; for warp `w` of `warps` that share the checks.
-__device__ __forceinline__ bool tables_bad(const int* src, int src_used, const int* dst,
-                                           int dst_used, int num_pages, int w, int warps) {
+// Checks of a sequence's tables, by all threads of a block: `bad` when a page is outside the pool
+// or a page of dst stands in src at a later place, `own` when one stands in src at all. Warp w of
+// `warps` that share dst takes every warps-th entry. `bits`: kBins words of shared memory, zero
+// before; they get a bit for each page of src, so that only entries of dst that may be in src at
+// another place are looked for (src and dst have thousands of entries each for long sequences).
+struct TableChecks {
+  bool bad, own;
+};
+__device__ __forceinline__ TableChecks check_tables(const int* src, int src_used, const int* dst,
+                                                    int dst_used, int num_pages, int w, int warps,
+                                                    uint32_t* bits) {
   const int lane = threadIdx.x % 32;
-  bool bad = false;
-  for (int j = w * 32 + lane; j < src_used; j += warps * 32)
-    bad |= src[j] < 0 || src[j] >= num_pages;
-  for (int i = w; i < dst_used; i += warps) {
-    const int page = dst[i];
-    bad |= page < 0 || page >= num_pages;
-#pragma unroll 4
-    for (int j = i + 1 + lane; j < src_used; j += 32) bad |= src[j] == page;
+  TableChecks c{false, false};
+  for (int j = threadIdx.x; j < src_used; j += blockDim.x) {
+    const int page = src[j];
+    if (page < 0 || page >= num_pages)
+      c.bad = true;
+    else
+      atomicOr(&bits[(page >> 5) & (kBins - 1)], 1u << (page & 31));
   }
-  return bad;
+  __syncthreads();
+  for (int i = w; i < dst_used; i += warps) {   // dst_used <= src_used
+    const int page = dst[i];
+    if (page < 0 || page >= num_pages) {
+      c.bad = true;
+    } else if (src[i] == page) {
+      c.own = true;
+    } else if (bits[(page >> 5) & (kBins - 1)] >> (page & 31) & 1) {
+      for (int j = lane; j < src_used; j += 32)
+        if (src[j] == page) {
+          c.own = true;
+          if (j > i) c.bad = true;
+        }
+    }
+  }
+  return c;
 }
 
 // CTAS CTAs (a cluster) for each (sequence, key head), each with its share of the candidates:
@@ -172,6 +193,14 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
         (t & ((1 << a.page_shift) - 1)));
     return make_uint4(order_key(w.x), order_key(w.y), order_key(w.z), order_key(w.w));
   };
+  const int in_page = (1 << a.page_shift) - 1;
+  if (check_tables(src_table, (len + in_page) >> a.page_shift, dst_table,
+                   (new_len + in_page) >> a.page_shift, a.num_pages, rank * kSelectWarps + warp,
+                   CTAS * kSelectWarps, hist)
+          .bad)
+    s_bad = 1;
+  __syncthreads();
+  for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;   // (counted in after sync_all)
 #pragma unroll 4
   for (int g = tid; g < cached; g += kSelectThreads) cache[g] = load_group(g);
   // f(first token of the group within this CTA's, its four keys), group g of every `step`
@@ -182,11 +211,6 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     for (; g < g1; g += step) f(4 * g, load_group(g));
   };
 
-  // the pages are in the pool, and no destination stands in the sequence at a later place
-  if (tables_bad(src_table, (len + (1 << a.page_shift) - 1) >> a.page_shift, dst_table,
-                 (new_len + (1 << a.page_shift) - 1) >> a.page_shift, a.num_pages,
-                 rank * kSelectWarps + warp, CTAS * kSelectWarps))
-    s_bad = 1;
   sync_all();
   int bad = 0;
 #pragma unroll
@@ -356,6 +380,7 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
   constexpr int kTokens = 32 / kLanes * kMoveTokens;   // tokens of a warp in a round
   constexpr int kWarps = kMoveThreads / 32, kRound = kTokens * kWarps * kMoveCluster;
   __shared__ int s_own;
+  __shared__ uint32_t s_bits[kBins];
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -370,14 +395,12 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
   const int len = min(max(a.seqlens[b], 0), a.max_pages << shift), new_len = min(len, a.budget);
   const int src_used = (len + in_page) >> shift, dst_used = (new_len + in_page) >> shift;
   if (tid == 0) s_own = 0;
+  for (int i = tid; i < kBins; i += kMoveThreads) s_bits[i] = 0;
   __syncthreads();
-  bool own = false;
-  for (int i = rank * kWarps + warp; i < dst_used; i += kMoveCluster * kWarps) {
-    const int page = dst_table[i];
-#pragma unroll 4
-    for (int j = lane; j < src_used; j += 32) own |= src_table[j] == page;
-  }
-  if (own) s_own = 1;
+  if (check_tables(src_table, src_used, dst_table, dst_used, a.num_pages, rank * kWarps + warp,
+                   kMoveCluster * kWarps, s_bits)
+          .own)
+    s_own = 1;
   cluster.sync();
   int own_pages = 0;
 #pragma unroll

@@ -5,7 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "fa_internal.h"
+#include "fa_paged_internal.h"
 #include "ptx_sm103.cuh"
 
 namespace fa {

@@ -10,7 +10,7 @@
 #include <initializer_list>
 
 #include "fa.h"
-#include "fa_internal.h"
+#include "fa_paged_internal.h"
 
 namespace {
 
@@ -134,8 +134,6 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, int
   if (!fa::encode_bnhd(&p.tm_q, q, B, Hq, N, d, fp16) ||
       !fa::encode_bnhd(&p.tm_k, k, B, Hkv, N, d, fp16))
     return FA_ERR_CUDA;
-  p.q = q;
-  p.k = k;
   p.lse = lse;
   p.w = w;
   p.part = static_cast<float*>(workspace);

@@ -592,6 +592,16 @@ def test_evict_long(n, in_place, ties):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+def test_evict_long_tables(in_place):
+    """Thousands of pages in both tables; a pool past the bits that pre-select page numbers."""
+    n, budget = 120000, 70000
+    c = Cache([n, 40], 16, 1, 64, "fp16", seed=12, weights=True, spare=70000,
+              max_pages=n // 16)
+    out = c.table.clone() if in_place else free_table(c, budget)
+    check_evict(c, out, budget, 999)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_evict_again_and_again(in_place):
     """Evictions on end, as a decoding loop makes them."""
     c = Cache([600, 411], 16, 2, 64, "bf16", seed=8, weights=True, spare=80)
