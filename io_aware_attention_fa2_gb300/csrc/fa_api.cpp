@@ -603,14 +603,13 @@ int fa_selftest_wait_timeout(int limit_us, fa_stream_t stream) {
 }
 
 int fa_get_device_error(fa_stream_t stream) {
-  int value = 0, bwd_value = 0, kw_value = 0, paged_value = 0;
+  int value = 0, bwd_value = 0, paged_value = 0;
   if (fa::read_and_clear_device_error(reinterpret_cast<cudaStream_t>(stream), &value) !=
           cudaSuccess ||
       fa::read_and_clear_bwd_error(&bwd_value) != cudaSuccess ||
-      fa::read_and_clear_key_weights_error(&kw_value) != cudaSuccess ||
       fa::read_and_clear_paged_error(&paged_value) != cudaSuccess)
     return FA_ERR_CUDA;
-  if (value != 0 || bwd_value != 0 || kw_value != 0) return FA_ERR_TIMEOUT;
+  if (value != 0 || bwd_value != 0) return FA_ERR_TIMEOUT;
   return paged_value;
 }
 

@@ -30,20 +30,15 @@
 // compensation: a key of a long prompt is the sum of many thousand terms. With shared key heads
 // each query head writes its own sums (fp32 workspace) and a second kernel adds them in the order
 // of the heads, so that the result does not depend on which CTA ends first.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
-#include "fa_paged_internal.h"
-#include "ptx_sm103.cuh"
+#include "fa_paged.cuh"
 
 namespace fa {
 
-// Device error word: nonzero after a kernel wait ran past its limit.
-__device__ int g_key_weights_error = 0;
-
 namespace {
+
+using namespace paged;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kQueries = 256;                               // queries of a tile
@@ -51,7 +46,6 @@ constexpr int kThreads = 64 + 512;
 constexpr int kCols = 64;                                   // columns of S in registers
 constexpr uint32_t kBoxBytes = BOX_ROWS * BOX_COLS * 2;     // 16 KiB
 constexpr uint64_t kWaitLimitNs = 1000000000ull;            // 1 s per wait
-constexpr int kErrTimeout = -8;                             // FA_ERR_TIMEOUT
 constexpr uint32_t kTmemCols = 512;
 
 template <int D>
@@ -80,7 +74,7 @@ static_assert(BAR_COUNT <= 16, "barrier slots");
 
 __device__ __forceinline__ void record_timeout(volatile int* abort_flag) {
   *abort_flag = 1;
-  atomicCAS(&g_key_weights_error, 0, kErrTimeout);
+  atomicOr(&g_error, kTimeoutBit);
 }
 
 // The queries that see key j: [lo(j), hi(j)), both nondecreasing in j.
@@ -157,6 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return base + L::kBars + 8u * static_cast<uint32_t>(i); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
+  wait_prerequisites();
+  launch_dependents();
   // Unit from a 1-D grid: heads in groups whose Q stays in L2, in a group key block by key
   // block, the first (seen by the most queries when causal) first.
   const int num_kblk = (N + 2 * BLOCK_N - 1) / (2 * BLOCK_N);
@@ -366,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256)
     fa_key_weights_sum_kernel(const float* __restrict__ part, float* __restrict__ w, int G, int N,
                               int64_t count) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_prerequisites();
+  launch_dependents();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (at >= count) return;
   const int64_t head = at / N, j = at % N;
@@ -389,23 +386,13 @@ cudaError_t launch_impl(const KeyWeightsParams& p, cudaStream_t stream) {
   const int64_t q_bytes = 2ll * p.N * D;
   const int heads_per_group =
       static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(bh, (32ll << 20) / q_bytes)));
-  kernel<<<static_cast<unsigned>(bh * num_kblk), kThreads, smem, stream>>>(
-      p.tm_q, p.tm_k, p.lse, G > 1 ? p.part : p.w, p.Hq, G, p.N, p.causal, p.window_left,
-      p.window_right, p.seqlens_k, p.scale_log2, heads_per_group);
-  err = cudaGetLastError();
+  err = launch_chained(kernel, bh * num_kblk, kThreads, smem, stream, 0, p.tm_q, p.tm_k, p.lse,
+                       G > 1 ? p.part : p.w, p.Hq, G, p.N, p.causal, p.window_left, p.window_right,
+                       p.seqlens_k, p.scale_log2, heads_per_group);
   if (err != cudaSuccess || G == 1) return err;
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
   const int64_t count = static_cast<int64_t>(p.B) * p.Hkv * p.N;
-  cfg.gridDim = dim3(static_cast<unsigned>((count + 255) / 256));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_key_weights_sum_kernel, static_cast<const float*>(p.part),
-                            p.w, G, p.N, count);
+  return launch_chained(fa_key_weights_sum_kernel, (count + 255) / 256, 256, 0, stream, 0, p.part,
+                        p.w, G, p.N, count);
 }
 
 }  // namespace
@@ -416,11 +403,6 @@ cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream) {
   return p.fp16 ? launch_impl<128, true>(p, stream) : launch_impl<128, false>(p, stream);
 }
 
-cudaError_t read_and_clear_key_weights_error(int* value) {
-  cudaError_t err = cudaMemcpyFromSymbol(value, g_key_weights_error, sizeof(int));
-  if (err != cudaSuccess) return err;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_key_weights_error, &zero, sizeof(int));
-}
+cudaError_t read_and_clear_key_weights_error(int* bits) { return read_and_clear_error(bits); }
 
 }  // namespace fa

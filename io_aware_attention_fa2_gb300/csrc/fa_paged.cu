@@ -34,6 +34,8 @@ __global__ void __launch_bounds__(128)
                            const int* __restrict__ table, const int* __restrict__ seqlens,
                            const int* __restrict__ new_lens, int N, int Hkv, int d, int page_size,
                            int num_pages, int max_pages) {
+  wait_prerequisites();
+  launch_dependents();
   const int b = blockIdx.x / N, i = blockIdx.x % N;
   const int n = new_lens ? min(max(new_lens[b], 0), N) : N;
   if (i >= n) return;
@@ -167,6 +169,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
   const int* const src_table = a.table + static_cast<int64_t>(b) * a.max_pages;
   const int* const dst_table = a.out_table + static_cast<int64_t>(b) * a.out_pages;
   int* const kept = a.kept + unit * a.budget;
+  wait_prerequisites();
   launch_dependents();
 
   const int raw_len = a.seqlens[b];
@@ -462,31 +465,19 @@ cudaError_t launch_select(const EvictArgs& a, int64_t units, cudaStream_t stream
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (kHist + kMaxCache) * 4);
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CTAS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * CTAS));
-  cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = CTAS > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a, cache_keys);
+  return launch_chained(kernel, units * CTAS, kSelectThreads, smem, stream, CTAS > 1 ? CTAS : 0, a,
+                        cache_keys);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t stream) {
   const PagedCache& c = p.c;
-  fa_paged_append_kernel<<<static_cast<unsigned>(static_cast<int64_t>(c.B) * p.N), 128, 0,
-                           stream>>>(
+  return launch_chained(
+      fa_paged_append_kernel, static_cast<int64_t>(c.B) * p.N, 128, 0, stream, 0,
       static_cast<const uint4*>(p.k), static_cast<const uint4*>(p.v), p.w,
       static_cast<uint4*>(c.k_pages), static_cast<uint4*>(c.v_pages), c.weights, c.block_table,
       c.seqlens, p.new_lens, p.N, c.Hkv, c.d, c.page_size, c.num_pages, c.max_pages);
-  return cudaGetLastError();
 }
 
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream) {
@@ -514,24 +505,15 @@ cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream) {
                         ? launch_select<1>(a, units, stream)
                         : launch_select<8>(a, units, stream);
   if (err != cudaSuccess) return err;
-  // the move may start its checks while the selection runs
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * kMoveCluster));
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = stream;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  return c.d == 64 ? cudaLaunchKernelEx(&cfg, fa_paged_move_kernel<64>, a)
-                   : cudaLaunchKernelEx(&cfg, fa_paged_move_kernel<128>, a);
+  return launch_chained(c.d == 64 ? fa_paged_move_kernel<64> : fa_paged_move_kernel<128>,
+                        units * kMoveCluster, kMoveThreads, 0, stream, 0, a);
 }
 
 cudaError_t read_and_clear_paged_error(int* value) {
   int bits = 0;
   cudaError_t err = read_and_clear_error(&bits);
   if (err == cudaSuccess) err = read_and_clear_decode_error(&bits);
+  if (err == cudaSuccess) err = read_and_clear_key_weights_error(&bits);
   *value = bits & kTimeoutBit ? kErrTimeout : bits & kPageBit ? kErrPage : 0;
   return err;
 }

@@ -272,6 +272,8 @@ __global__ void __launch_bounds__(kThreads, SHORT ? 1 : 2)
     ptx::prefetch_tensormap(&tm_k);
     ptx::prefetch_tensormap(&tm_v);
   }
+  wait_prerequisites();
+  launch_dependents();
   // where this CTA's run starts: the sequence, and the tile within it
   if (!SHORT && warp == 0) {
     const int64_t total = count_tiles(a) * a.Hkv * a.blocks;
@@ -311,10 +313,7 @@ __global__ void __launch_bounds__(kThreads, SHORT ? 1 : 2)
   }
   __syncthreads();
   Walk walk{};
-  if constexpr (!SHORT) {
-    launch_dependents();
-    walk = Walk{s_left, s_at, s_seq};
-  }
+  if constexpr (!SHORT) walk = Walk{s_left, s_at, s_seq};
   const int rank = SHORT ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int ranks = SHORT ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
   // the segments of this CTA, one after the other: a short unit's share, or those of the run
@@ -883,6 +882,7 @@ template <int D, bool FP16, bool WEIGHTS>
 __global__ void __launch_bounds__(kFinishThreads)
     fa_paged_finish_kernel(const __grid_constant__ Args a, int64_t heads, int chunks) {
   wait_prerequisites();
+  launch_dependents();
   const int64_t at = blockIdx.x;
   if (at < heads)
     join_head<D, FP16>(a, at);
@@ -999,19 +999,8 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
     const cudaError_t err =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(c.B * c.Hkv * a.blocks * cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, a);
+    return launch_chained(kernel, static_cast<int64_t>(c.B) * c.Hkv * a.blocks * cluster, kThreads,
+                          smem, stream, cluster, tm_k, tm_v, a);
   }
   auto kernel = fa_paged_decode_kernel<D, FP16, WEIGHTS, false>;
   const int smem = static_cast<int>(Smem<D, false>::kDynamic);
@@ -1019,16 +1008,8 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   const int ctas = static_cast<int>(grid_size(c.B, p.Hq, c.Hkv, a.capacity));
-  kernel<<<ctas, kThreads, smem, stream>>>(tm_k, tm_v, a);
-  err = cudaGetLastError();
+  err = launch_chained(kernel, ctas, kThreads, smem, stream, 0, tm_k, tm_v, a);
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = stream;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
   // units of one tile are never split: no head to join
   const int64_t heads = a.capacity > kTile ? static_cast<int64_t>(c.B) * p.Hq : 0;
   int64_t blocks = heads;
@@ -1041,9 +1022,8 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
     blocks += static_cast<int64_t>(c.B) * c.Hkv * chunks;
   }
   if (blocks == 0) return cudaSuccess;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kFinishThreads);
-  return cudaLaunchKernelEx(&cfg, fa_paged_finish_kernel<D, FP16, WEIGHTS>, a, heads, chunks);
+  return launch_chained(fa_paged_finish_kernel<D, FP16, WEIGHTS>, blocks, kFinishThreads, 0, stream,
+                        0, a, heads, chunks);
 }
 
 template <int D, bool FP16>

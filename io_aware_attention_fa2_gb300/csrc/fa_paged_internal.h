@@ -77,8 +77,10 @@ struct EvictParams {
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream);
 
 // The error words of these kernels on the current device: read and clear (no synchronisation).
-cudaError_t read_and_clear_key_weights_error(int* value);
-cudaError_t read_and_clear_paged_error(int* value);   // FA_ERR_TIMEOUT before FA_ERR_PAGE
-cudaError_t read_and_clear_decode_error(int* bits);   // or-ed in: 1 timeout, 2 bad page
+// FA_OK, FA_ERR_TIMEOUT, or FA_ERR_PAGE (where no wait ran out).
+cudaError_t read_and_clear_paged_error(int* value);
+// Those of two of the translation units, or-ed in: 1 timeout, 2 bad page.
+cudaError_t read_and_clear_decode_error(int* bits);
+cudaError_t read_and_clear_key_weights_error(int* bits);
 
 }  // namespace fa

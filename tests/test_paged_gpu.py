@@ -338,6 +338,84 @@ def test_streams_given_as_handles():
         assert same_bits(o, want[0]) and same_bits(lse, want[1])
 
 
+def test_chain_behind_other_work():
+    """Every call right behind work that writes what it reads: copies, fills, PyTorch kernels and
+    other calls, in a stream, in a graph, and across streams. (The kernels may be launched before
+    the work in front of them ends, and must wait for it.)"""
+    import io_aware_attention_fa2_gb300 as fa
+    n = 4000
+    c = Cache([n, 900], 16, 2, 64, "bf16", seed=60, weights=True, spare=40)
+    q = c.query(8)
+    want = [decode(c, q), None]
+    ref_w = c.w.clone()
+    decode(c, q, weights=ref_w)
+    out = free_table(c, 256)
+    good = [x.clone() for x in (q, c.k, c.v, c.table, c.seqlens, c.w, out)]
+    state = [x.clone() for x in good]
+    gq, gk, gv, gt, gs, gw, go = state
+    o, lse = torch.empty_like(q), torch.empty(2, 8, device="cuda")
+    p = torch.randn((1, 500, 2, 64), generator=c.g).to(c.dtype).cuda()
+    pl = torch.full((1, 2, 500), 7.0, device="cuda")
+    want_pw = fa.key_weights(p, p, pl, causal=True)
+    gp, gpl, pw = torch.empty_like(p), torch.empty_like(pl), torch.empty_like(want_pw)
+    kept = torch.empty((2, 2, 256), dtype=torch.int32, device="cuda")
+    lens = torch.empty(2, dtype=torch.int32, device="cuda")
+    big = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def spoil():
+        for x in (*state, gp, gpl):
+            x.zero_()
+
+    def restore(kind):
+        for x, y in zip((*state, gp, gpl), (*good, p, pl)):
+            if kind == "copy":
+                x.copy_(y)                            # a copy node
+            else:                                     # a kernel (on the bits: NaN stays as it is)
+                kind_of = torch.int16 if x.element_size() == 2 else torch.int32
+                torch.bitwise_or(y.view(kind_of), 0, out=x.view(kind_of))
+
+    def calls():
+        fa.fa_key_weights(gp, gp, gpl, pw, True, default_scale(64))
+        fa.fa_paged_decode(gq, gk, gv, gt, gs, o, lse, default_scale(64), weights=gw)
+        fa.fa_paged_evict(gk, gv, gw, gt, gs, go, kept, lens, 31)
+        fa.fa_paged_decode(gq, gk, gv, go, lens, o2, lse2, default_scale(64))
+
+    o2, lse2 = torch.empty_like(q), torch.empty(2, 8, device="cuda")
+    results = []
+    for kind in ("copy", "kernel"):
+        for how in ("stream", "graph", "streams"):
+            spoil()
+            big.zero_()
+            torch.cuda.synchronize()
+            if how == "graph":
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    big.zero_()
+                    restore(kind)
+                    calls()
+                g.replay()
+            elif how == "stream":
+                big.zero_()
+                restore(kind)
+                calls()
+            else:
+                side = torch.cuda.Stream()
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    big.zero_()
+                    restore(kind)
+                torch.cuda.current_stream().wait_stream(side)
+                calls()
+            torch.cuda.synchronize()
+            assert same_bits(o, want[0][0]) and same_bits(lse, want[0][1]), (kind, how)
+            assert same_bits(pw, want_pw), (kind, how)
+            results.append([x.clone() for x in (kept, lens, o2, lse2, gk, gv, gw)])
+    for r in results[1:]:
+        for x, y in zip(r, results[0]):
+            assert same_bits(x, y)
+    assert results[0][1].tolist() == [256, 256]
+
+
 def test_decode_pool_past_2_31_elements():
     """Pages whose rows lie past 2^31 elements and 2^32 bytes."""
     page, Hkv, d = 64, 8, 128
