@@ -62,8 +62,8 @@ constexpr int kShortTiles = 4;                 // tiles of a CTA of a short unit
 constexpr int kWarps = 4;                      // consumer warps, 16 tokens of a tile each
 constexpr int kThreads = 32 * (kWarps + 1);    // and the producer warp
 constexpr int kRows = 16;                      // query heads of a unit, at most
-constexpr int kMaxCtas = 2 * 152;              // two CTAs on each SM
-constexpr int kMaxShortCtas = 152;             // one on each SM
+constexpr int kSms = 152;
+constexpr int kMaxCtas = 2 * kSms;             // two CTAs on each SM
 constexpr int kMaxCluster = 8;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
@@ -923,18 +923,24 @@ int64_t grid_size(int B, int Hq, int Hkv, int64_t capacity) {
 }
 
 // The smallest calls: 0, or the CTAs of a cluster that has one unit. Where every unit fits in a
-// cluster of CTAs with up to kShortTiles tiles each, and all of them run at once (one on each
-// SM), one launch without a workspace is faster than runs and their join: B=1 Hkv=8 d=64 with
-// 1001 tokens 8.3 us instead of 10.3 a replay of a graph, 19 us instead of 26 a call from
-// Python, which has no workspace to allocate. With weights the query
-// heads of a key head have to be one unit, so that every weight gets one addition.
-int choose_short(int B, int Hq, int Hkv, int64_t tiles, bool with_weights) {
+// cluster of CTAs with up to kShortTiles tiles each, and all of them run at once (one on each SM
+// at d = 128, two at d = 64: their shared memory), one launch without a workspace is faster than
+// runs and their join: B=1 Hkv=8 d=64 with 1001 tokens 8.3 us instead of 10.3 a replay of a graph,
+// 19 us instead of 26 a call from Python, which has no workspace to allocate. Units of one CTA may
+// take a second turn, each turn a single round trip to memory: 240 units of 250 tokens (d=64, 4
+// heads on a key head) 6.4 us instead of 11.3 a replay, 560 units 12.5 instead of 16.7; at d=128
+// 296 units 12.3 instead of 13.5, but a third and a fourth turn of 560 units of 100 tokens cost
+// 18.0 instead of 15.6. Clusters get no second turn: 32 units of 1000 tokens, d=128, 16.0 us in
+// two turns of eight CTAs, 6.8 in one of four. With weights the query heads of a key head have to
+// be one unit, so that every weight gets one addition.
+int choose_short(int B, int Hq, int Hkv, int d, int64_t tiles, bool with_weights) {
   const int64_t blocks = (Hq / Hkv + kRows - 1) / kRows, units = B * Hkv * blocks;
+  const int64_t resident = d == 64 ? 2 * kSms : kSms;
   if (with_weights && blocks > 1) return 0;
-  for (int ctas = kMaxCluster; ctas >= 1; ctas /= 2)
-    if (units * ctas <= kMaxShortCtas && (ctas == 1 || ctas / 2 < tiles))
+  for (int ctas = kMaxCluster; ctas >= 2; ctas /= 2)
+    if (units * ctas <= resident && ctas / 2 < tiles)
       return tiles <= ctas * kShortTiles ? ctas : 0;
-  return 0;
+  return units <= 2 * resident && tiles <= kShortTiles ? 1 : 0;
 }
 
 // Workspace: the parts' O, their maxima and sums, the units' parts, then (with weights)
@@ -993,7 +999,7 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
   // tiles of a unit, at most: a window's tokens span two more tiles than its length fills
   int64_t tiles = (static_cast<int64_t>(a.capacity) + kTile - 1) / kTile;
   if (a.window_left >= 0) tiles = std::min<int64_t>(tiles, a.window_left / kTile + 2);
-  if (const int cluster = choose_short(c.B, p.Hq, c.Hkv, tiles, WEIGHTS)) {
+  if (const int cluster = choose_short(c.B, p.Hq, c.Hkv, D, tiles, WEIGHTS)) {
     auto kernel = fa_paged_decode_kernel<D, FP16, WEIGHTS, true>;
     const int smem = static_cast<int>(Smem<D, true>::kDynamic);
     const cudaError_t err =
@@ -1037,7 +1043,7 @@ cudaError_t launch_weights(const DecodeParams& p, cudaStream_t stream) {
 size_t paged_decode_workspace(int B, int Hq, int Hkv, int d, int page_size, int max_pages,
                               bool with_weights) {
   const int64_t capacity = static_cast<int64_t>(max_pages) * page_size;
-  if (choose_short(B, Hq, Hkv, (capacity + kTile - 1) / kTile, with_weights)) return 0;
+  if (choose_short(B, Hq, Hkv, d, (capacity + kTile - 1) / kTile, with_weights)) return 0;
   return layout(B, Hq, Hkv, d, capacity, with_weights).end;
 }
 

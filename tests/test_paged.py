@@ -61,9 +61,14 @@ def test_workspace_sizes(lib):
     assert with_w == small + 16 * 8 + 16 * 3200 * 4
     assert lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 16, 128, 1) == 0   # 32 tiles: short
     assert lib.fa_paged_decode_workspace_size(2, 8, 2, 64, 16, 129, 1) > 0
-    assert lib.fa_paged_decode_workspace_size(40, 8, 2, 64, 16, 16, 0) == 0   # 80 units, one CTA
-    assert lib.fa_paged_decode_workspace_size(40, 8, 2, 64, 16, 17, 0) > 0
-    assert lib.fa_paged_decode_workspace_size(80, 8, 2, 64, 16, 16, 0) > 0
+    assert lib.fa_paged_decode_workspace_size(40, 8, 2, 64, 16, 32, 0) == 0   # 80 units, two CTAs
+    assert lib.fa_paged_decode_workspace_size(40, 8, 2, 64, 16, 33, 0) > 0
+    assert lib.fa_paged_decode_workspace_size(40, 8, 2, 128, 16, 16, 0) == 0  # one CTA
+    assert lib.fa_paged_decode_workspace_size(40, 8, 2, 128, 16, 17, 0) > 0
+    for d, units in ((64, 608), (128, 304)):                                  # two turns of one CTA
+        assert lib.fa_paged_decode_workspace_size(units, 4, 1, d, 16, 16, 1) == 0
+        assert lib.fa_paged_decode_workspace_size(units, 4, 1, d, 16, 17, 1) > 0
+        assert lib.fa_paged_decode_workspace_size(units + 1, 4, 1, d, 16, 16, 1) > 0
     assert lib.fa_paged_decode_workspace_size(1, 32, 1, 64, 16, 16, 0) == 0   # two blocks of heads
     assert lib.fa_paged_decode_workspace_size(1, 32, 1, 64, 16, 16, 1) > 0
     assert lib.fa_paged_decode_workspace_size(2, 8, 3, 64, 16, 10, 0) == 0    # 8 % 3

@@ -37,7 +37,8 @@ LENS = [0, 1, 15, 16, 17, 63, 64, 65, 200, 1000]
                                             (128, "fp16", 16, 1), (64, "bf16", 40, 2)])
 @pytest.mark.parametrize("B,tokens,window", [(1, 2048, -1), (1, 2049, -1), (3, 64, -1),
                                              (4, 700, -1), (4, 90000, 1700), (18, 500, -1),
-                                             (38, 256, -1), (60, 130, 40)])
+                                             (38, 256, -1), (60, 130, 40), (152, 200, -1),
+                                             (153, 250, -1)])
 def test_decode_short_and_long_tables(page, d, dtype, Hq, Hkv, B, tokens, window):
     """Both sides of the rule that gives a unit to a cluster: few and many units, tables up to
     and past its tiles, windows that make long tables short."""
