@@ -69,10 +69,14 @@ __global__ void __launch_bounds__(128)
 // the recent ones, by radix selection on the weights as ordered 32-bit keys (digits of 11, 11
 // and 10 bits), then the equal ones from the oldest until there are enough. The keys are read
 // once and kept in shared memory. The move is bound by HBM, the selection by instructions and
-// latency: eight sequences of up to 32768 tokens to 4096, Hkv=8 d=128 (277 MB): 69 us, of which
-// the selection 24 (64 CTAs) and the move 47 (268 MB, 85 % of the measured copy rate). Measured
-// slower: one kernel of eight CTAs for each head that selects and moves (134 us; 3 us for every
-// exchange of a histogram).
+// latency: eight sequences of up to 32768 tokens to 4096, Hkv=8 d=128 (277 MB): 65 us, of which
+// the selection 19 (64 CTAs) and the move 47 (268 MB, 85 % of the measured copy rate). In the
+// selection: weights and tables 5 us, histograms 2.6 + 2.1 + 1.7, counting 1.7, placing 4.8.
+// Measured slower: one kernel of eight CTAs for each head that selects and moves (134 us; 3 us
+// for every exchange of a histogram); several copies of the histogram against equal bins (+1 us);
+// a token a lane with two ballots (+0.5 us); a run of tokens for each thread (67 instead of 68 us
+// a replay here, but 99 instead of 86 where 300000 tokens have the heavy ones side by side: each
+// lane writes to lines of its own).
 namespace cg = cooperative_groups;
 
 struct EvictArgs {
@@ -97,6 +101,14 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   if (!(w == w)) return 0u;
   const uint32_t u = __float_as_uint(w + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ void copy_async_16(uint4* to, const float* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(to)), "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void wait_async_copies() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Checks of a sequence's tables, by all threads of a block: `bad` when a page is outside the pool
@@ -188,15 +200,28 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
   const int t0 = min(rank * share, n), mine = min(share, n - t0);
   const int groups = (mine + 3) / 4, cached = min(groups, cache_keys / 4);
   uint4* const cache = reinterpret_cast<uint4*>(smem + (CTAS > 1 ? 2 : 1) * kBins);
-  auto load_group = [&](int g) {
-    const int t = t0 + 4 * g, page = src_table[t >> a.page_shift];
-    if (!in_pool(page)) return make_uint4(0, 0, 0, 0);   // the sequence is given up below
-    const float4 w = *reinterpret_cast<const float4*>(
-        a.weights + ((static_cast<int64_t>(page) * a.Hkv + hk) << a.page_shift) +
-        (t & ((1 << a.page_shift) - 1)));
-    return make_uint4(order_key(w.x), order_key(w.y), order_key(w.z), order_key(w.w));
-  };
   const int in_page = (1 << a.page_shift) - 1;
+  auto group_at = [&](int g, int page) {
+    const int t = t0 + 4 * g;
+    return a.weights + ((static_cast<int64_t>(page) * a.Hkv + hk) << a.page_shift) + (t & in_page);
+  };
+  // Behind the last candidate the lowest key: it has no smaller ones to count it before, and of
+  // equal ones it comes after all candidates, so that it needs no test anywhere.
+  auto keys_of = [&](int i, float4 w) {
+    return make_uint4(order_key(w.x), i + 1 < mine ? order_key(w.y) : 0u,
+                      i + 2 < mine ? order_key(w.z) : 0u, i + 3 < mine ? order_key(w.w) : 0u);
+  };
+  auto load_group = [&](int g) {
+    return keys_of(4 * g, *reinterpret_cast<const float4*>(
+                              group_at(g, src_table[(t0 + 4 * g) >> a.page_shift])));
+  };
+  // The weights are on their way while the tables are checked. (With a page outside the pool
+  // the sequence is given up below, and nothing reads the group.)
+#pragma unroll 8
+  for (int g = tid; g < cached; g += kSelectThreads) {
+    const int page = src_table[(t0 + 4 * g) >> a.page_shift];
+    if (in_pool(page)) copy_async_16(cache + g, group_at(g, page));
+  }
   if (check_tables(src_table, (len + in_page) >> a.page_shift, dst_table,
                    (new_len + in_page) >> a.page_shift, a.num_pages, rank * kSelectWarps + warp,
                    CTAS * kSelectWarps, hist)
@@ -204,8 +229,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     s_bad = 1;
   __syncthreads();
   for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;   // (counted in after sync_all)
-#pragma unroll 4
-  for (int g = tid; g < cached; g += kSelectThreads) cache[g] = load_group(g);
+  wait_async_copies();   // of this thread, which is the one that makes keys of them
   // f(first token of the group within this CTA's, its four keys), group g of every `step`
   auto for_groups = [&](int g0, int g1, int step, auto&& f) {
     int g = g0;
@@ -235,16 +259,21 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     constexpr int kShift[3] = {21, 10, 0};
     const int shift = kShift[pass], bits = pass == 2 ? 10 : 11;
     uint32_t* const h = hist + (CTAS > 1 ? (pass & 1) * kBins : 0);
-    auto count_key = [&](bool in, uint32_t key) {
-      if (in && (pass == 0 || (key >> (shift + bits)) == prefix))
+    auto count_key = [&](uint32_t key) {
+      if (pass == 0 || (key >> (shift + bits)) == prefix)
         atomicAdd(&h[(key >> shift) & ((1u << bits) - 1)], 1u);
     };
     if (want)
       for_groups(tid, groups, kSelectThreads, [&](int i, uint4 key) {
-        count_key(true, key.x);
-        count_key(i + 1 < mine, key.y);
-        count_key(i + 2 < mine, key.z);
-        count_key(i + 3 < mine, key.w);
+        if (pass == 0 && i < 4 * cached) {
+          key = keys_of(i, make_float4(__uint_as_float(key.x), __uint_as_float(key.y),
+                                       __uint_as_float(key.z), __uint_as_float(key.w)));
+          cache[i / 4] = key;
+        }
+        count_key(key.x);
+        count_key(key.y);
+        count_key(key.z);
+        count_key(key.w);
       });
     sync_all();
     if (want) {
@@ -297,16 +326,15 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     const int per_warp = (groups + kSelectThreads - 1) / kSelectThreads * 32;
     const int g0 = min(warp * per_warp, groups), g1 = min(g0 + per_warp, groups);
     // keys above the threshold in the low half, at it in the high half: at most 4 of a group
-    auto count4 = [&](int i, uint4 key) {
-      uint32_t c = key.x > prefix ? 1u : key.x == prefix ? 0x10000u : 0u;
-      if (i + 1 < mine) c += key.y > prefix ? 1u : key.y == prefix ? 0x10000u : 0u;
-      if (i + 2 < mine) c += key.z > prefix ? 1u : key.z == prefix ? 0x10000u : 0u;
-      if (i + 3 < mine) c += key.w > prefix ? 1u : key.w == prefix ? 0x10000u : 0u;
+    auto count4 = [&](uint4 key) {
+      uint32_t c = 0;
+      for (uint32_t k : {key.x, key.y, key.z, key.w})
+        c += k > prefix ? 1u : k == prefix ? 0x10000u : 0u;
       return c;
     };
     int2 count = make_int2(0, 0);
-    for_groups(g0 + lane, g1, 32, [&](int i, uint4 key) {
-      const uint32_t c = count4(i, key);
+    for_groups(g0 + lane, g1, 32, [&](int, uint4 key) {
+      const uint32_t c = count4(key);
       count.x += c & 0xffff;
       count.y += c >> 16;
     });
@@ -333,34 +361,34 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
         equal += c.y;
       }
     }
-    // a token a lane: its place comes from two ballots
-    const uint32_t* const keys = reinterpret_cast<const uint32_t*>(cache);
-    const unsigned below = (1u << lane) - 1;
-    const int end = min(4 * g1, mine), on_chip = min(end, 4 * cached);
-    auto place = [&](bool in, int i, uint32_t key) {
-      const unsigned up = __ballot_sync(0xffffffffu, in && key > prefix);
-      const unsigned at = __ballot_sync(0xffffffffu, in && key == prefix);
-      const int rank_at = equal + __popc(at & below);
-      if (in && (key > prefix || (key == prefix && rank_at < limit)))
-        kept[above + __popc(up & below) + min(rank_at, limit)] = t0 + i;
-      above += __popc(up);
-      equal += __popc(at);
-    };
-    int i = 4 * g0;
-#pragma unroll 4
-    for (; i < on_chip; i += 32) {
-      const bool in = i + lane < on_chip;
-      place(in, i + lane, in ? keys[i + lane] : 0u);
-    }
-    for (i = max(4 * g0, on_chip); i < end; i += 32) {
-      const bool in = i + lane < end;
-      uint32_t key = 0;
-      if (in) {
-        const uint4 four = load_group((i + lane) / 4);
-        const int e = (i + lane) & 3;
-        key = e == 0 ? four.x : e == 1 ? four.y : e == 2 ? four.z : four.w;
+    // a group a lane: its place comes from a scan of the groups' counts
+    for (int g = g0; g < g1; g += 32) {
+      const int at = g + lane;
+      uint4 key = make_uint4(0, 0, 0, 0);
+      uint32_t c = 0;
+      if (at < g1) {
+        key = at < cached ? cache[at] : load_group(at);
+        c = count4(key);
       }
-      place(in, i + lane, key);
+      uint32_t inc = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += y;
+      }
+      const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
+      if (c) {   // the lane's kept tokens are consecutive ones
+        int same = equal + static_cast<int>((inc - c) >> 16), token = t0 + 4 * at;
+        int* to = kept + above + static_cast<int>((inc - c) & 0xffff) + min(same, limit);
+        for (uint32_t k : {key.x, key.y, key.z, key.w}) {
+          const bool level = k == prefix;
+          if (k > prefix || (level && same < limit)) *to++ = token;
+          same += level;
+          ++token;
+        }
+      }
+      above += static_cast<int>(all & 0xffff);
+      equal += static_cast<int>(all >> 16);
     }
   }
   for (int i = wide; i < a.recent; i += width) kept[a.budget - a.recent + i] = n + i;

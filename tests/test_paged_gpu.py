@@ -670,6 +670,21 @@ def test_evict_long(n, in_place, ties):
     check_evict(c, c.table.clone() if in_place else free_table(c, 5000), 5000, 1000)
 
 
+@pytest.mark.parametrize("rest", [0, 1, 2, 3])
+@pytest.mark.parametrize("n,budget", [(700, 300), (50000, 4000)])
+def test_evict_lowest_weights(n, budget, rest):
+    """Fewer weights than the budget that are not NaN: the oldest of the NaN ones fill it, for
+    candidates that end anywhere in a group of four and with NaN behind them."""
+    n += rest
+    c = Cache([n, n - 1], 64, 2, 64, "bf16", seed=n, weights=True, spare=2 * (budget // 64 + 1))
+    c.w = torch.where(torch.rand(c.w.shape, generator=c.g) < 0.002,
+                      torch.rand(c.w.shape, generator=c.g), torch.tensor(math.nan)).cuda()
+    check_evict(c, free_table(c, budget), budget, 16)
+    c.w = torch.full_like(c.w, math.nan)
+    c.w[c.table[0, (n - 17) // 64], :, (n - 17) % 64] = -math.inf    # the last candidate
+    check_evict(c, c.table.clone(), budget, 16)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_long_tables(in_place):
     """Thousands of pages in both tables; a pool past the bits that pre-select page numbers."""
