@@ -382,7 +382,8 @@ int fa_paged_append(const void* k, const void* v, const float* w, void* k_pages,
  *                aligned, not overlapping any other argument; NULL where that is 0. Calls
  *                sharing a workspace must not overlap. Its contents need no initialisation.
  * A sequence with no visible token gets O = 0 and LSE = -inf. What the pages hold behind a
- * sequence's last token (NaN included) does not matter. A length beyond the table is taken as
+ * sequence's last token (NaN included) does not matter. An infinite value of a visible token
+ * makes its column of O infinite, values of both signs or a NaN make it NaN. A length beyond the table is taken as
  * the table's, and tokens in pages outside the pool are left out (FA_ERR_PAGE in the device
  * error word). The same call gives the same bits (weights, too, of pages that stand in the
  * tables once; a shared page gets one addition from each place it stands in, in any order).

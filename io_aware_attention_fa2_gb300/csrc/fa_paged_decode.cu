@@ -231,6 +231,16 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
     lo = *reinterpret_cast<const uint32_t*>(&r);
   }
 }
+// Two 16-bit values with infinities (and NaN) replaced by the type's largest number of their sign.
+template <bool FP16>
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+  uint32_t r;
+  if constexpr (FP16)
+    asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7bff7bffu));
+  else
+    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7f7f7f7fu));
+  return r;
+}
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   if constexpr (FP16) {
@@ -573,6 +583,9 @@ __global__ void __launch_bounds__(kThreads, SHORT ? 1 : 2)
           vf[3] &= keep1;
           mma<FP16>(acc[2 * x], ph, vf[0], vf[1]);
           mma<FP16>(acc[2 * x + 1], ph, vf[2], vf[3]);
+          // the rest may be zero or negative: an infinite value counts in the first product alone
+#pragma unroll
+          for (int y = 0; y < 4; ++y) vf[y] = finite2<FP16>(vf[y]);
           mma<FP16>(acc[2 * x], pl, vf[0], vf[1]);
           mma<FP16>(acc[2 * x + 1], pl, vf[2], vf[3]);
         }

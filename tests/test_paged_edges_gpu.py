@@ -1,0 +1,53 @@
+"""Decoding over the paged cache at the edges of its numbers: infinite values, probabilities far
+below the largest one, arguments at the ends of their ranges."""
+import math
+
+import pytest
+import torch
+
+from paged_util import Cache, decode_ref, default_scale, same_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_error_left():
+    import io_aware_attention_fa2_gb300 as fa
+    fa.device_error()
+    yield
+    assert fa.device_error() == 0
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("lens", [[1], [40, 7], [3000, 1, 900]])
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (64, "bf16"), (128, "fp16"), (128, "bf16")])
+def test_infinite_values(d, dtype, lens, weights):
+    """A visible infinite value makes its column of O infinite, of its sign; two of both signs,
+    or a NaN, make it NaN; the other columns, LSE and the weights are as ever. Where the window
+    hides the token the value does not matter."""
+    import io_aware_attention_fa2_gb300 as fa
+    c = Cache(lens, 16, 2, d, dtype, seed=len(lens) + d, weights=weights)
+    q = c.query(8)
+    plain = c.v.clone()
+    for b, n in enumerate(lens):
+        pg, row = c.rows(c.table, b, n)
+        for t, col, value in ((0, 3, math.inf), (n // 2, 5, -math.inf), (n - 1, 7, math.inf),
+                              (0, d - 1, math.nan), (n // 3, 9, math.inf), (n - 1, 9, -math.inf)):
+            c.v[pg[t], row[t], :, col] = value
+    o, lse = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens,
+                                weights=None if c.w is None else c.w.clone())
+    ref = decode_ref(c, q, default_scale(d))
+    want, bound = ref[0], ref[3]
+    finite = torch.isfinite(want)
+    assert not finite[:, :, [3, 5, 7, d - 1]].any() and torch.isneginf(want[..., 5]).all()
+    got = o.double().cpu()
+    assert ((got - want).abs()[finite] <= bound[finite]).all()
+    assert torch.equal(got[~finite].nan_to_num(nan=7.0), want[~finite].nan_to_num(nan=7.0))
+    assert ((lse.double().cpu() - ref[1]).abs() <= ref[4]).all()
+    # one visible token, whose values are finite in these columns
+    o0, _ = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens, window_left=0)
+    for b, n in enumerate(lens):
+        pg, row = c.rows(c.table, b, n)
+        last = plain[pg[-1], row[-1]].repeat_interleave(4, 0)
+        cols = [x for x in range(d) if n > 1 and x not in (7, 9)]
+        assert same_bits(o0[b][:, cols].contiguous(), last[:, cols].contiguous())
