@@ -34,7 +34,10 @@
 // them until the run's end, when the four are joined through shared memory.
 //
 // P is kept as two 16-bit values, the rounded one and the rounded rest, for two products with V
-// into one fp32 accumulator: O then carries the rounding of the output alone.
+// into one fp32 accumulator: O then carries the rounding of the output alone. fp16 ends at 2^-24,
+// so there P is taken 2^15 times as large (at most 2^15 against a largest number of 65504) until
+// a run's end: what is lost are probabilities below 2^-40 of the largest, not 2^-25, which many
+// tokens behind a heavy one would miss.
 //
 // Weights need the final LSE: the scaled scores are kept (fp32, 4 G bytes a token against the
 // 4 d of K and V) and the second kernel adds exp2(score - maximum) / sum over the group's heads.
@@ -66,6 +69,11 @@ constexpr int kSms = 152;
 constexpr int kMaxCtas = 2 * kSms;             // two CTAs on each SM
 constexpr int kMaxCluster = 8;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+// P, its sums and the unnormalised O are 2^kPShift as large within a run.
+template <bool FP16>
+constexpr float kPShift = FP16 ? 15.f : 0.f;
+template <bool FP16>
+constexpr float kPUnshift = FP16 ? 1.f / 32768.f : 1.f;
 
 template <int D, bool SHORT>
 struct Smem {
@@ -548,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, SHORT ? 1 : 2)
             acc[x][3] *= f1;
           }
         }
-        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+        const float u0 = (m0 == -INFINITY ? 0.f : m0) - kPShift<FP16>;
+        const float u1 = (m1 == -INFINITY ? 0.f : m1) - kPShift<FP16>;
         float p[2][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -603,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, SHORT ? 1 : 2)
     if (lane % 4 == 0) {
       sm_m[warp * kRows + r0] = m0;
       sm_m[warp * kRows + r0 + 8] = m1;
-      sm_l[warp * kRows + r0] = l0;
-      sm_l[warp * kRows + r0 + 8] = l1;
+      sm_l[warp * kRows + r0] = l0 * kPUnshift<FP16>;
+      sm_l[warp * kRows + r0 + 8] = l1 * kPUnshift<FP16>;
     }
     ptx::named_barrier_sync(1, 32 * kWarps);
     auto row_stats = [&](int r, float& m, float& l) {
@@ -646,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, SHORT ? 1 : 2)
       if (rh * 8 >= rows) break;
       float m, l;
       row_stats(r0 + 8 * rh, m, l);
-      const float f = ptx::exp2_approx((rh ? m1 : m0) - (m == -INFINITY ? 0.f : m));
+      const float f =
+          ptx::exp2_approx((rh ? m1 : m0) - (m == -INFINITY ? 0.f : m)) * kPUnshift<FP16>;
 #pragma unroll
       for (int ch = 0; ch < D / 64; ++ch) {
 #pragma unroll

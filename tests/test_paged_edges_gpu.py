@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from paged_util import Cache, decode_ref, default_scale, same_bits
+from paged_util import Cache, check_decode, decode_ref, default_scale, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,40 @@ def test_infinite_values(d, dtype, lens, weights):
         last = plain[pg[-1], row[-1]].repeat_interleave(4, 0)
         cols = [x for x in range(d) if n > 1 and x not in (7, 9)]
         assert same_bits(o0[b][:, cols].contiguous(), last[:, cols].contiguous())
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "fp16"), (64, "bf16")])
+def test_many_small_probabilities_behind_heavy_tokens(d, dtype):
+    """Four heavy tokens with small values in front, all others e^-18 (below fp16's 2^-25) as
+    probable: what these add up to is most of O. 320 units, so that a run is a whole sequence and
+    every warp of it meets a heavy token in the first tile."""
+    import io_aware_attention_fa2_gb300 as fa
+    B, Hkv, n = 40, 8, 1024
+    c = Cache([n] * B, 256, Hkv, d, dtype, seed=d)
+    for b in range(B):
+        pg, row = c.rows(c.table, b, n)
+        c.k[pg, row] = 0
+        c.v[pg, row] *= 100
+        c.v[pg, row] += 1000
+        heavy = torch.arange(0, 64, 16)
+        c.k[pg[heavy], row[heavy], :, 0] = 18.0
+        c.v[pg[heavy], row[heavy]] *= 2.0 ** -20
+    q = c.query(Hkv) * 0
+    q[..., 0] = 1.0
+    o, lse = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens, scale=1.0)
+    check_decode(c, q, o, lse, decode_ref(c, q, 1.0), (d, dtype))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_largest_fp16_numbers(d):
+    """Values at the type's largest number, all probabilities equal: sums far past fp16."""
+    import io_aware_attention_fa2_gb300 as fa
+    c = Cache([5000, 130, 1], 64, 1, d, "fp16", seed=3, weights=True)
+    for b, n in enumerate(c.lens):
+        pg, row = c.rows(c.table, b, n)
+        c.v[pg, row] = torch.finfo(torch.float16).max
+    q = c.query(4) * 0
+    o, lse = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens, weights=c.w)
+    assert (o == torch.finfo(torch.float16).max).all()
+    want = torch.log(c.seqlens.double())[:, None].expand(3, 4)
+    assert ((lse.double() - want).abs() <= 2.0 ** -20 + want * 2.0 ** -22).all()
