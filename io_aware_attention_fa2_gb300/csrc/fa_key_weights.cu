@@ -136,10 +136,8 @@ template <int D, bool FP16>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
-                          const float* __restrict__ lse, float* __restrict__ out, int Hq, int G,
-                          int N, int causal, int left, int right,
-                          const int* __restrict__ seqlens, float scale_log2,
-                          int heads_per_group) {
+                          const float* lse, float* out, int Hq, int G, int N, int causal, int left,
+                          int right, const int* seqlens, float scale_log2, int heads_per_group) {
   using L = Smem<D>;
   constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -360,8 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // w[b, hk, j] = sum over the G query heads, in their order, of part[b, hk * G + g, j].
 __global__ void __launch_bounds__(256)
-    fa_key_weights_sum_kernel(const float* __restrict__ part, float* __restrict__ w, int G, int N,
-                              int64_t count) {
+    fa_key_weights_sum_kernel(const float* part, float* w, int G, int N, int64_t count) {
   wait_prerequisites();
   launch_dependents();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;

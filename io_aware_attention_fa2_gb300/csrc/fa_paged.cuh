@@ -34,8 +34,8 @@ struct Visible {
   int lo, hi;
 };
 template <bool RECORD>
-__device__ __forceinline__ Visible visible_tokens(const int* __restrict__ seqlens, int b,
-                                                  int capacity, int window_left) {
+__device__ __forceinline__ Visible visible_tokens(const int* seqlens, int b, int capacity,
+                                                  int window_left) {
   int len = seqlens[b];
   if (len > capacity || len < 0) {
     if (RECORD) record_page_error();
@@ -45,6 +45,9 @@ __device__ __forceinline__ Visible visible_tokens(const int* __restrict__ seqlen
 }
 
 // Programmatic stream serialisation: let the next kernel be launched; wait for the one before.
+// A kernel is resident while the one before it may still write its inputs, so none of them is
+// read-only for the kernel's life: no input is declared `const T* __restrict__` and none is read
+// through the non-coherent path, or the compiler could load it above the wait.
 __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

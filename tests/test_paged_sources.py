@@ -1,0 +1,42 @@
+"""Rules of the paged cache's CUDA sources that a wrong build need not show in its results."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "io_aware_attention_fa2_gb300", "csrc")
+
+
+def sources():
+    """File name -> text without comments."""
+    out = {}
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith((".cu", ".cuh")):
+            text = open(os.path.join(CSRC, name)).read()
+            out[name] = re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+    return out
+
+
+CHAINED = [name for name, text in sources().items() if "launch_chained" in text]
+
+
+def test_the_chained_kernels_are_found():
+    assert set(CHAINED) == {"fa_paged.cu", "fa_paged.cuh", "fa_paged_decode.cu",
+                            "fa_key_weights.cu"}
+
+
+@pytest.mark.parametrize("name", CHAINED)
+def test_inputs_of_chained_kernels_are_not_declared_read_only(name):
+    """A kernel that is launched while the one before it still writes its inputs must not let the
+    compiler load them through the non-coherent path or above the wait."""
+    text = sources()[name]
+    for word in ("__restrict__", "__ldg", ".nc", "restrict"):
+        assert word not in text, word
+
+
+@pytest.mark.parametrize("name", CHAINED)
+def test_every_chained_kernel_waits(name):
+    """Every kernel of these files waits for the one before it."""
+    text = sources()[name]
+    assert text.count("__global__") == text.count("  wait_prerequisites();")
