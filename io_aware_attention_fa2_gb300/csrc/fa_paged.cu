@@ -95,6 +95,27 @@ constexpr int kBins = 2048, kBinsPerThread = kBins / kSelectThreads;
 constexpr int kMaxCache = 49152;   // keys a CTA keeps in shared memory; further ones are read from
                                    // the pages in every pass
 
+// Loads past L1 that stay where they stand in the program, behind a wait and in front of a
+// barrier: the compiler's own intrinsic promises no order with either.
+__device__ __forceinline__ int load_l2(const int* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_l2(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_l2(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // Weights as unsigned numbers in the same order: NaN lowest, -0 equal to +0.
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (!(w == w)) return 0u;
@@ -438,7 +459,7 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
   cluster.sync();   // no CTA leaves while another reads its flag
   wait_prerequisites();
   // (a sequence that was given up keeps nothing: its kept is all -1)
-  const int rows = new_len > 0 && __ldcg(kept) >= 0 ? new_len : 0;
+  const int rows = new_len > 0 && load_l2(kept) >= 0 ? new_len : 0;
 
   const int part = lane % kLanes;
   const int64_t chunk = part % (D / 8);
@@ -449,7 +470,7 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
     int64_t src = -1, dst = -1, w_dst = 0;
     float w = 0.f;
     if (lane < kTokens && i < rows) {
-      const int t = __ldcg(kept + i);
+      const int t = load_l2(kept + i);
       const int64_t src_page = src_table[t >> shift], dst_page = dst_table[i >> shift];
       const int src_row = t & in_page, dst_row = i & in_page;
       src = (((src_page << shift) + src_row) * a.Hkv + hk) * (D / 8);
@@ -457,7 +478,7 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
       if (src == dst) {   // in place already
         src = -1;
       } else {
-        w = __ldcg(a.weights + ((src_page * a.Hkv + hk) << shift) + src_row);
+        w = load_l2(a.weights + ((src_page * a.Hkv + hk) << shift) + src_row);
         w_dst = ((dst_page * a.Hkv + hk) << shift) + dst_row;
       }
     }
@@ -465,7 +486,7 @@ __global__ void __cluster_dims__(kMoveCluster, 1, 1) __launch_bounds__(kMoveThre
 #pragma unroll
     for (int u = 0; u < kMoveTokens; ++u) {
       const int64_t from = __shfl_sync(0xffffffffu, src, u * (32 / kLanes) + lane / kLanes);
-      if (from >= 0) v[u] = __ldcg(pool + from + chunk);
+      if (from >= 0) v[u] = load_l2(pool + from + chunk);
     }
     if (own_pages) cluster.sync();
 #pragma unroll

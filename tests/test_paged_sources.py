@@ -36,6 +36,16 @@ def test_inputs_of_chained_kernels_are_not_declared_read_only(name):
 
 
 @pytest.mark.parametrize("name", CHAINED)
+def test_loads_past_l1_keep_their_place(name):
+    """The move's loads must stay behind its wait and in front of its cluster barrier: they are
+    assembly that is volatile and clobbers memory, not intrinsics without a promised order."""
+    text = sources()[name]
+    assert not re.search(r"__ld(cg|ca|cs|cv|lu)\b", text)
+    for asm in re.findall(r"asm[^;]*?\(\s*\"ld\.global.*?\);", text, flags=re.S):
+        assert asm.startswith("asm volatile") and '"memory"' in asm, asm
+
+
+@pytest.mark.parametrize("name", CHAINED)
 def test_every_chained_kernel_waits(name):
     """Every kernel of these files waits for the one before it."""
     text = sources()[name]
