@@ -175,7 +175,7 @@ __device__ __forceinline__ TableChecks check_tables(const int* src, int src_used
 template <int CTAS>
 __global__ void __launch_bounds__(kSelectThreads, 1)
     fa_paged_select_kernel(const __grid_constant__ EvictArgs a, int cache_keys) {
-  extern __shared__ uint32_t smem[];
+  extern __shared__ __align__(16) uint32_t smem[];   // groups of four keys behind the histograms
   uint32_t* const hist = smem;                            // [kBins] (two of them with a cluster)
   __shared__ uint32_t s_warp[kSelectWarps], s_found[2];
   __shared__ int2 s_count, s_warp_count[kSelectWarps];   // candidates above and at the threshold

@@ -50,3 +50,17 @@ def test_every_chained_kernel_waits(name):
     """Every kernel of these files waits for the one before it."""
     text = sources()[name]
     assert text.count("__global__") == text.count("  wait_prerequisites();")
+
+
+def test_dynamic_shared_memory_is_aligned():
+    """A dynamic shared array is declared with the alignment of its widest access (16 bytes), or
+    its base is rounded up by hand."""
+    found = 0
+    for name, text in sources().items():
+        for line in re.findall(r"extern __shared__[^;]*;", text):
+            found += 1
+            if "smem_raw" in line:
+                assert "(smem_raw) + 1023u) & ~1023u" in text, name
+            else:
+                assert "__align__(16)" in line, (name, line)
+    assert found >= 5
