@@ -945,25 +945,39 @@ int64_t grid_size(int B, int Hq, int Hkv, int64_t capacity) {
   return std::min<int64_t>(kMaxCtas, tiles);
 }
 
+// Clusters of `ctas` CTAs of a short call that run at once. A CTA's shared memory leaves room for
+// one on each SM at d = 128, two at d = 64; a cluster has to lie within one of the groups of SMs
+// that the GPU is made of, so that the larger ones leave SMs over (as the runtime's occupancy
+// query counts them on a GB300).
+int resident_clusters(int ctas, int d) {
+  const bool small = d == 64;
+  switch (ctas) {
+    case 8: return small ? 36 : 15;
+    case 4: return small ? 74 : 36;
+    case 2: return small ? 152 : 76;
+    default: return small ? 304 : 152;
+  }
+}
+
 // The smallest calls: 0, or the CTAs of a cluster that has one unit. Where every unit fits in a
-// cluster of CTAs with up to kShortTiles tiles each, and all of them run at once (one on each SM
-// at d = 128, two at d = 64: their shared memory), one launch without a workspace is faster than
-// runs and their join: B=1 Hkv=8 d=64 with 1001 tokens 8.3 us instead of 10.3 a replay of a graph,
-// 19 us instead of 26 a call from Python, which has no workspace to allocate. Units of one CTA may
-// take a second turn, each turn a single round trip to memory: 240 units of 250 tokens (d=64, 4
-// heads on a key head) 6.4 us instead of 11.3 a replay, 560 units 12.5 instead of 16.7; at d=128
-// 296 units 12.3 instead of 13.5, but a third and a fourth turn of 560 units of 100 tokens cost
-// 18.0 instead of 15.6. Clusters get no second turn: 32 units of 1000 tokens, d=128, 16.0 us in
-// two turns of eight CTAs, 6.8 in one of four. With weights the query heads of a key head have to
-// be one unit, so that every weight gets one addition.
+// cluster of CTAs with up to kShortTiles tiles each, and all of them run at once, one launch
+// without a workspace is faster than runs and their join: B=1 Hkv=8 d=64 with 1001 tokens 8.3 us
+// instead of 10.3 a replay of a graph, 19 us instead of 26 a call from Python, which has no
+// workspace to allocate. Units of one CTA may take a second turn, each turn a single round trip to
+// memory: 240 units of 250 tokens (d=64, 4 heads on a key head) 6.4 us instead of 11.3 a replay,
+// 560 units 12.5 instead of 16.7; at d=128 296 units 12.3 instead of 13.5, but a third and a
+// fourth turn of 560 units of 100 tokens cost 18.0 instead of 15.6. Clusters get no second turn:
+// 16 units of 2000 tokens, d=128, take 21.0 us in two turns of clusters of eight and 18.9 as runs
+// (15 units in one turn 14.9), 37 units of 1000 tokens 21.0 in clusters of four and 18.9 as runs.
+// With weights the query heads of a key head have to be one unit, so that every weight gets one
+// addition.
 int choose_short(int B, int Hq, int Hkv, int d, int64_t tiles, bool with_weights) {
   const int64_t blocks = (Hq / Hkv + kRows - 1) / kRows, units = B * Hkv * blocks;
-  const int64_t resident = d == 64 ? 2 * kSms : kSms;
   if (with_weights && blocks > 1) return 0;
   for (int ctas = kMaxCluster; ctas >= 2; ctas /= 2)
-    if (units * ctas <= resident && ctas / 2 < tiles)
+    if (units <= resident_clusters(ctas, d) && ctas / 2 < tiles)
       return tiles <= ctas * kShortTiles ? ctas : 0;
-  return units <= 2 * resident && tiles <= kShortTiles ? 1 : 0;
+  return units <= 2 * resident_clusters(1, d) && tiles <= kShortTiles ? 1 : 0;
 }
 
 // Workspace: the parts' O, their maxima and sums, the units' parts, then (with weights)

@@ -1,0 +1,27 @@
+"""The rules that choose a path of the paged cache's operators, as their workspace sizes show
+them, on the CPU."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from io_aware_attention_fa2_gb300 import binding
+    from io_aware_attention_fa2_gb300 import build as fa_build
+    fa_build.build()
+    return binding.load_library()
+
+
+@pytest.mark.parametrize("d,tiles,units", [
+    (128, 32, 15), (128, 17, 15), (128, 16, 36), (128, 9, 36), (128, 8, 76), (128, 5, 76),
+    (128, 4, 304), (128, 1, 304), (64, 32, 36), (64, 16, 74), (64, 8, 152), (64, 4, 608)])
+def test_short_calls_take_as_many_units_as_run_at_once(lib, d, tiles, units):
+    """A unit in a cluster of eight, four, two or (in two turns) one CTA of four tiles each, as
+    long as all clusters run at once: 8 x 15 CTAs at d = 128, not 152, since a cluster cannot
+    span the groups of SMs. One unit more, or one tile more than the clusters hold, takes runs,
+    which need a workspace."""
+    def need(units, tiles):
+        return lib.fa_paged_decode_workspace_size(units, 1, 1, d, 64, tiles, 0)
+    assert need(units, tiles) == 0
+    assert need(units + 1, tiles) > 0
+    if tiles in (32, 16, 8, 4):
+        assert need(units, tiles + 1) > 0
