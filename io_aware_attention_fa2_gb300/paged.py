@@ -30,6 +30,7 @@ from . import binding
 from .binding import FA_OK, FaError, _dtype_code, load_library
 
 _NO_CONTEXT = contextlib.nullcontext()
+_INT_MAX = 2 ** 31 - 1   # ctypes would pass the low 32 bits of a larger number
 
 
 def _library():
@@ -40,6 +41,20 @@ def _check(name, t, shape, dtype, device):
     if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor %s on %s" % (
             name, str(dtype).replace("torch.", ""), list(shape), device))
+
+
+def _count(name, n):
+    """A number that the library takes as an int."""
+    n = int(n)
+    if not -_INT_MAX <= n <= _INT_MAX:
+        raise ValueError("%s is out of range: %d" % (name, n))
+    return n
+
+
+def _bound(n):
+    """A window bound: any negative number is none, and one past every length is as good."""
+    n = int(n)
+    return -1 if n < 0 else min(n, _INT_MAX)
 
 
 def _first(name, t, dims):
@@ -103,6 +118,8 @@ def _cache(k_pages, v_pages, weights, block_table, seqlens):
     if len(table) != 2:
         raise ValueError("block_table must be [B, max_pages]")
     B, max_pages = table
+    if B > _INT_MAX or max_pages > _INT_MAX:
+        raise ValueError("block_table is too large: %s" % list(table))
     _check("block_table", block_table, table, torch.int32, device)
     _check("seqlens", seqlens, (B,), torch.int32, device)
     if weights is not None:
@@ -140,7 +157,7 @@ def fa_key_weights(q, k, lse, w, causal: bool, scale: float, workspace=None, str
     _check("w", w, (B, Hkv, N), torch.float32, device)
     if seqlens_k is not None:
         _check("seqlens_k", seqlens_k, (B,), torch.int32, device)
-    left, right = (int(x) for x in window)
+    left, right = (_bound(x) for x in window)
     keep, ws, ws_bytes = _workspace(key_weights_workspace_size(B, Hq, Hkv, N), workspace, device,
                                     stream)
     _call("fa_key_weights", _library().fa_key_weights, device, stream, (
@@ -234,7 +251,7 @@ def _decode(q, k_pages, v_pages, block_table, seqlens, o, lse, scale, weights, w
     _call("fa_paged_decode", _library().fa_paged_decode, device, stream, (
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(weights),
         block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, d,
-        page_size, num_pages, max_pages, int(window_left), float(scale), _dtype_code(q), ws,
+        page_size, num_pages, max_pages, _bound(window_left), float(scale), _dtype_code(q), ws,
         ws_bytes))
     return o, lse
 
@@ -265,14 +282,14 @@ def fa_paged_evict(k_pages, v_pages, weights, block_table, seqlens, out_table, k
         raise ValueError("eviction goes by the cache's weights")
     if kept.dim() != 3 or out_table.dim() != 2:
         raise ValueError("kept must be [B, Hkv, budget] and out_table [B, out_pages]")
-    budget, out_pages = kept.shape[2], out_table.shape[1]
+    budget, out_pages = _count("budget", kept.shape[2]), _count("out_pages", out_table.shape[1])
     _check("kept", kept, (B, Hkv, budget), torch.int32, device)
     _check("out_table", out_table, (B, out_pages), torch.int32, device)
     _check("new_seqlens", new_seqlens, (B,), torch.int32, device)
     _call("fa_paged_evict", _library().fa_paged_evict, device, stream, (
         k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(), block_table.data_ptr(),
         seqlens.data_ptr(), out_table.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr(), B, Hkv,
-        d, page_size, num_pages, max_pages, out_pages, budget, int(recent),
+        d, page_size, num_pages, max_pages, out_pages, budget, _count("recent", recent),
         _dtype_code(k_pages)))
 
 
@@ -281,7 +298,7 @@ def paged_evict(k_pages, v_pages, weights, block_table, seqlens, out_table, budg
     """kept, new_seqlens = eviction of all but ``budget`` tokens per sequence and key head (see
     ``fa_paged_evict``); the kept tokens are then the first ones of out_table's pages."""
     import torch
-    if budget < 1:
+    if _count("budget", budget) < 1:
         raise ValueError("budget must be at least 1")
     with _stream_of(stream, k_pages.device):
         kept = torch.empty((block_table.shape[0], k_pages.shape[2], budget), dtype=torch.int32,

@@ -88,3 +88,32 @@ def test_largest_fp16_numbers(d):
     assert (o == torch.finfo(torch.float16).max).all()
     want = torch.log(c.seqlens.double())[:, None].expand(3, 4)
     assert ((lse.double() - want).abs() <= 2.0 ** -20 + want * 2.0 ** -22).all()
+
+
+def test_integers_past_32_bits():
+    """A window past every length is none; counts that the library's ints cannot hold are
+    refused, not cut to their low 32 bits."""
+    import io_aware_attention_fa2_gb300 as fa
+    c = Cache([300], 16, 1, 64, "bf16", seed=4, weights=True, spare=20)
+    q = c.query(2)
+    want = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens)
+    for window in (2 ** 32, 2 ** 31, 2 ** 63 - 1, 2 ** 31 - 1, -1, -2 ** 31, -2 ** 32 + 5):
+        o, lse = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens, window_left=window)
+        assert same_bits(o, want[0]) and same_bits(lse, want[1]), window
+    p = torch.randn((1, 200, 1, 64), generator=c.g).to(c.dtype).cuda()
+    lse = torch.full((1, 1, 200), 6.0, device="cuda")
+    w = fa.key_weights(p, p, lse)
+    for window in ((2 ** 32, 2 ** 33), (2 ** 31, -1), (-2 ** 32, -2 ** 40 + 3)):
+        assert same_bits(fa.key_weights(p, p, lse, window=window), w), window
+    out = c.free[:4].view(1, 4).cuda()
+    before = [x.clone() for x in (c.k, c.v, c.w)]
+    for budget, recent in ((50, 2 ** 32 + 5), (50, -2 ** 32 + 5), (2 ** 32 + 5, 2)):
+        with pytest.raises(ValueError, match="out of range"):
+            fa.paged_evict(c.k, c.v, c.w, c.table, c.seqlens, out, budget, recent)
+    with pytest.raises(ValueError, match="too large"):
+        wide = torch.empty((1, 2 ** 32 + 19), dtype=torch.int32, device="cuda")
+        fa.paged_attention(q, c.k, c.v, wide, c.seqlens)
+    del wide
+    torch.cuda.empty_cache()
+    for x, y in zip((c.k, c.v, c.w), before):
+        assert same_bits(x, y)
