@@ -336,7 +336,7 @@ int fa_bwd_host_masked(const void* q_h, const void* k_h, const void* v_h, const 
  * with the masks of fa_fwd_masked (queries and keys share N). Queries at or past seqlens_k[b]
  * are padding and add nothing; a masked key gets 0; a query whose LSE is -inf adds nothing.
  *
- *   q            [B, N, Hq, d] dtype;  k  [B, N, Hkv, d] dtype
+ *   q            [B, N, Hq, d] dtype;  k  [B, N, Hkv, d] dtype; N at most 2^30 - 128
  *   lse          [B, Hq, N] fp32: the forward's LSE for the same q, k, masks and scale
  *   w            [B, Hkv, N] fp32, written (every element)
  *   workspace    device memory of at least fa_key_weights_workspace_size(B, Hq, Hkv, N) bytes,

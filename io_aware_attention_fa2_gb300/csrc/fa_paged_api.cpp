@@ -109,9 +109,10 @@ int fa_key_weights(const void* q, const void* k, const float* lse, float* w, int
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
   if (!scale_ok(scale)) return FA_ERR_SCALE;
   const uint64_t bh = (uint64_t)B * (uint64_t)Hq;
-  // one CTA per (b, query head, 128 keys), at most 2^31 - 1; N + 128 stays an int
+  // one CTA per (b, query head, 256 keys), at most 2^31 - 1; a key of the last CTA (at most N + 254)
+  // plus a window bound (at most N) plus 1 stays an int
   if (bh >= (1ull << 31) || bh * (((uint64_t)N + 127) / 128) >= (1ull << 31) ||
-      N > (1 << 30) || bh * (uint64_t)N > (1ull << 62) / 256)
+      N > (1 << 30) - 128 || bh * (uint64_t)N > (1ull << 62) / 256)
     return FA_ERR_SHAPE;
   const uint64_t ws_need = fa_key_weights_workspace_size(B, Hq, Hkv, N);
   if (ws_need) {

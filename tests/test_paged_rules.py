@@ -25,3 +25,15 @@ def test_short_calls_take_as_many_units_as_run_at_once(lib, d, tiles, units):
     assert need(units + 1, tiles) > 0
     if tiles in (32, 16, 8, 4):
         assert need(units, tiles + 1) > 0
+
+
+def test_key_weights_index_sums_stay_within_int(lib):
+    """The largest key index that a CTA forms, N rounded up to 256, less one, plus a window as wide
+    as the sequence, plus one: within 32 bits for every length that is accepted."""
+    def call(N):   # one byte of workspace: an accepted length stops there
+        a = [0x100000 * (i + 1) for i in range(5)]
+        return lib.fa_key_weights(*a[:4], 1, 2, 1, N, 64, 1, 2 ** 31 - 1, -1, None, 0.1, 0, a[4], 1,
+                                  None)
+    most = max(N for N in range((1 << 30) - 300, (1 << 30) + 300) if call(N) == -11)
+    assert call(most + 1) == -2
+    assert -(-most // 256) * 256 - 1 + most + 1 < 2 ** 31
