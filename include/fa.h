@@ -52,7 +52,8 @@ enum fa_dtype {
 enum fa_status {
     FA_OK = 0,
     FA_ERR_NULL = -1,     /* a required pointer is NULL */
-    FA_ERR_SHAPE = -2,    /* B, H or N < 1; d not 64 or 128; or B*N*H*d does not fit int64 */
+    FA_ERR_SHAPE = -2,    /* B, H or N < 1; d not 64 or 128; B*N*H*d does not fit int64; or a size
+                             that the entry point does not take */
     FA_ERR_DTYPE = -3,    /* dtype is not an fa_dtype */
     FA_ERR_ALIGN = -4,    /* q, k, v or o not 16-byte aligned; lse or seqlens_k not 4-byte */
     FA_ERR_ALIAS = -5,    /* o or lse overlaps q, k, v or seqlens_k, or o overlaps lse */
@@ -61,7 +62,8 @@ enum fa_status {
     FA_ERR_TIMEOUT = -8,  /* a kernel wait ran past its limit; outputs are undefined */
     FA_ERR_SCALE = -9,    /* scale is not finite */
     FA_ERR_CUDA = -10,    /* a CUDA runtime or driver query failed */
-    FA_ERR_WORKSPACE = -11, /* workspace smaller than fa_fwd_splitkv_workspace_size() */
+    FA_ERR_WORKSPACE = -11, /* workspace smaller than the entry point's ..._workspace_size() (the
+                               text of fa_error_string names fa_fwd_splitkv's for all) */
     FA_ERR_POINTER = -12,   /* a device-side argument is not device memory of the current device */
     FA_ERR_PAGE = -13       /* a block table or length named a token outside the cache (found on the
                                device, read with fa_get_device_error) */

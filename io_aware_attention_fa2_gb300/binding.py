@@ -16,7 +16,15 @@ LIB_NAME = "libfa_gb300.so"
 FA_BF16, FA_FP16 = 0, 1
 FA_OK = 0
 FA_ERR_TIMEOUT = -8
+FA_ERR_WORKSPACE = -11
 FA_ERR_PAGE = -13
+
+# The size query of each entry point that takes a workspace (the library has one text for all).
+_WORKSPACE_SIZE = {"fa_fwd_splitkv": "fa_fwd_splitkv_workspace_size",
+                   "fa_bwd_masked": "fa_bwd_workspace_size",
+                   "fa_bwd_host_masked": "fa_bwd_workspace_size",
+                   "fa_key_weights": "fa_key_weights_workspace_size",
+                   "fa_paged_decode": "fa_paged_decode_workspace_size"}
 
 _lock = threading.Lock()
 _lib = None
@@ -27,7 +35,10 @@ class FaError(RuntimeError):
 
     def __init__(self, code: int, where: str):
         self.code = code
-        super().__init__("%s failed: %s (%d)" % (where, error_string(code), code))
+        text = error_string(code)
+        if code == FA_ERR_WORKSPACE and where in _WORKSPACE_SIZE:
+            text = "workspace smaller than %s()" % _WORKSPACE_SIZE[where]
+        super().__init__("%s failed: %s (%d)" % (where, text, code))
 
 
 def library_path() -> str:

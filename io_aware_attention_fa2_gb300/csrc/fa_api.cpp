@@ -117,7 +117,8 @@ const char* fa_error_string(int code) {
     case FA_ERR_NULL: return "a required pointer is NULL";
     case FA_ERR_SHAPE:
       return "unsupported shape (B, H, Nq >= 1; Nk >= Nq; d in {64, 128}; 1 <= num_splits <= "
-             "128; size overflow)";
+             "128; Hq a multiple of Hkv; pages of 16, 32, 64, 128 or 256 tokens; recent <= budget "
+             "<= tokens of out_table; size overflow)";
     case FA_ERR_DTYPE: return "dtype is not FA_BF16 or FA_FP16";
     case FA_ERR_ALIGN:
       return "misaligned pointer (q, k, v, o: 16 bytes; lse, seqlens_k: 4 bytes)";

@@ -37,3 +37,16 @@ def test_key_weights_index_sums_stay_within_int(lib):
     most = max(N for N in range((1 << 30) - 300, (1 << 30) + 300) if call(N) == -11)
     assert call(most + 1) == -2
     assert -(-most // 256) * 256 - 1 + most + 1 < 2 ** 31
+
+
+def test_messages_name_what_the_call_needs(lib):
+    from io_aware_attention_fa2_gb300 import FaError
+    for where, size in (("fa_paged_decode", "fa_paged_decode_workspace_size"),
+                        ("fa_key_weights", "fa_key_weights_workspace_size"),
+                        ("fa_bwd_masked", "fa_bwd_workspace_size"),
+                        ("fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size")):
+        e = FaError(-11, where)
+        assert e.code == -11
+        assert str(e) == "%s failed: workspace smaller than %s() (-11)" % (where, size)
+        assert hasattr(lib, size)
+    assert "pages of 16, 32, 64, 128 or 256" in str(FaError(-2, "fa_paged_decode"))
