@@ -170,14 +170,17 @@ def key_weights(q, k, lse, causal: bool = False, scale: float | None = None, str
                 window=(-1, -1), seqlens_k=None, out=None):
     """w [B, Hkv, N]: the attention weight every key of a prompt received from the queries (and
     query heads) that see it. ``lse`` is what ``attention_forward`` returned for the same q, k
-    and masks; ``scale`` defaults to 1/sqrt(d) rounded to fp32."""
+    and masks (``seqlens_k`` may be on the host, as there); ``scale`` defaults to 1/sqrt(d) rounded
+    to fp32."""
     import torch
     if scale is None:
         scale = _default_scale(q.shape[-1])
-    if out is None:
-        with _stream_of(stream, q.device):
+    with _stream_of(stream, q.device):
+        if out is None:
             out = torch.empty((q.shape[0], k.shape[2], q.shape[1]), dtype=torch.float32,
                               device=q.device)
+        if seqlens_k is not None:
+            seqlens_k = seqlens_k.to(q.device, torch.int32)
     fa_key_weights(q, k, lse, out, causal, scale, None, stream, window, seqlens_k)
     return out
 

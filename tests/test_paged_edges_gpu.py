@@ -117,3 +117,22 @@ def test_integers_past_32_bits():
     torch.cuda.empty_cache()
     for x, y in zip((c.k, c.v, c.w), before):
         assert same_bits(x, y)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_key_weights_take_the_lengths_that_the_forward_takes(side):
+    """Host lengths and other integer types, as attention_forward accepts them."""
+    import io_aware_attention_fa2_gb300 as fa
+    g = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randn((2, 300, 2, 64), generator=g).to(torch.bfloat16).cuda()
+               for _ in range(3))
+    lens = torch.tensor([300, 77])
+    _, lse = fa.attention_forward(q, k, v, causal=True, seqlens_k=lens)
+    want = fa.key_weights(q, k, lse, causal=True, seqlens_k=lens.to(torch.int32).cuda())
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream() if side else None
+    for given in (lens, lens.to(torch.int32), lens.cuda()):
+        torch.cuda.synchronize()
+        got = fa.key_weights(q, k, lse, causal=True, seqlens_k=given, stream=stream)
+        torch.cuda.synchronize()
+        assert same_bits(got, want)
