@@ -14,6 +14,7 @@ say which rows belong to which sequence. The life of a sequence:
         o1, lse1 = paged_attention(q1, k_pages, v_pages, block_table, seqlens, weights=weights)
     kept, seqlens = paged_evict(k_pages, v_pages, weights, block_table, seqlens, free_pages,
                                 budget, recent)
+    block_table, free_pages = free_pages, block_table          # where the kept tokens are now
 
 Every tensor is a contiguous CUDA tensor of one device; calls run on that device and, unless a
 ``stream`` is given, on its current stream. A block-table entry or length that names a token
