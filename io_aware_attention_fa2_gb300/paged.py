@@ -4,9 +4,10 @@ of ``include/fa.h`` (argument marshalling only, like ``binding``).
 A cache is two tensors ``k_pages``, ``v_pages`` [num_pages, page_size, Hkv, d] and, when it is to
 be kept within a budget, ``weights`` float32 [num_pages, Hkv, page_size]: the attention weight
 every token has received so far. ``block_table`` int32 [B, max_pages] and ``seqlens`` int32 [B]
-say which rows belong to which sequence. The life of a sequence:
+say which rows belong to which sequence. The life of a sequence, with G = Hq // Hkv query heads to
+a key head (the forward wants keys and values for every query head):
 
-    o, lse = attention_forward(q, k, v, causal=True)          # the prompt
+    o, lse = attention_forward(q, k.repeat_interleave(G, 2), v.repeat_interleave(G, 2), causal=True)
     w = key_weights(q, k, lse, causal=True)
     fa_paged_append(k, v, k_pages, v_pages, block_table, seqlens, w=w, weights=weights)
     for each new token:                                        # seqlens counts it already
