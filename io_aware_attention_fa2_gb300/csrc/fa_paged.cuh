@@ -19,14 +19,19 @@ constexpr int kTimeoutBit = 1, kPageBit = 2;
 
 __device__ __forceinline__ void record_page_error() { atomicOr(&g_error, kPageBit); }
 
-// Read and clear g_error of the translation unit that calls it; bits are or-ed into *bits.
+static __global__ void clear_error_kernel(int bits) { atomicAnd(&g_error, ~bits); }
+
+// Read and clear g_error of the translation unit that calls it; bits are or-ed into *bits. Only
+// the bits that were read are cleared, on the device: kernels of other streams may be adding to
+// the word (read and then written with a zero, it lost what they added in between).
 static inline cudaError_t read_and_clear_error(int* bits) {
   int value = 0;
   cudaError_t err = cudaMemcpyFromSymbol(&value, g_error, sizeof(int));
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess || value == 0) return err;
   *bits |= value;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_error, &zero, sizeof(int));
+  clear_error_kernel<<<1, 1>>>(value);
+  err = cudaGetLastError();
+  return err == cudaSuccess ? cudaStreamSynchronize(nullptr) : err;
 }
 
 // Tokens of sequence b that are visible to its newest one.

@@ -45,9 +45,9 @@ def test_loads_past_l1_keep_their_place(name):
         assert asm.startswith("asm volatile") and '"memory"' in asm, asm
 
 
-@pytest.mark.parametrize("name", CHAINED)
+@pytest.mark.parametrize("name", [n for n in CHAINED if n.endswith(".cu")])
 def test_every_chained_kernel_waits(name):
-    """Every kernel of these files waits for the one before it."""
+    """Every kernel of these files is launched so, and waits for the one before it."""
     text = sources()[name]
     assert text.count("__global__") == text.count("  wait_prerequisites();")
 
