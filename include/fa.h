@@ -397,7 +397,8 @@ int fa_paged_decode(const void* q, const void* k_pages, const void* v_pages, flo
                     size_t workspace_bytes, fa_stream_t stream);
 
 /* Bytes of workspace fa_paged_decode needs (with_weights: whether weights is passed); 0 for short
- * tables. */
+ * tables. It goes by the table's width, not by the lengths: with weights it holds
+ * 4 * B * Hq * max_pages * page_size bytes of scores. */
 size_t fa_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int page_size,
                                       int max_pages, int with_weights);
 

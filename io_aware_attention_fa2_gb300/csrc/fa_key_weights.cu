@@ -17,8 +17,9 @@
 //                queries of the tile; warps 10..17 the same for S_B. Nothing synchronises them
 //                but the S buffers: every warp keeps its own copy of the LSEs that it needs.
 // One half of the warps sums S_A while S_B is computed, and the other way round. Measured on B=1
-// H=16 N=16384 d=128 causal: 390 us (1411 TFLOP/s, 74 % of the measured dense bf16 peak), of
-// which the products alone take 309 and the sums alone 375: the exponentials (32 a cycle and
+// H=16 N=16384 d=128 causal: 390 us alone (1411 TFLOP/s, 74 % of the measured dense bf16 peak),
+// 413-417 among other calls, at the power limit (d=64: 363). Of the 390 the products alone take
+// 309 and the sums alone 375: the exponentials (32 a cycle and
 // SM, 55 % busy) and the shared-memory reads of the LSEs share an issue queue, and four warps a
 // scheduler do not fill their latencies. Slower: all sixteen warps on S_A, then on S_B (421 us);
 // eight warps with twice the columns (427); 32-column loads of S one ahead of the sums (439);

@@ -21,12 +21,11 @@
 // fixed order. Each CTA recomputes where its run starts from seqlens.
 //
 // Measured (calls one after the other over three caches): B=16 GQA 4 lengths to 16K, pages of 16:
-// 102-104 us, 6.2-6.3 TB/s, 91-93 % of the measured copy rate; B=4 GQA 8 to 64K: 54-55 us (79 %:
-// 5 are the first loads' latency, 4 the join); B=8 GQA 4 to 32K with weights: 124-126 us (80 %;
-// keeping the scores costs 8 us, adding the weights 11). The second product with P's rest costs
-// nothing measurable; two stages instead of three 2 % at B=16, one CTA of six stages on each SM
-// 12 %; L2 hints for K and V (evict first) and the scores (evict last) keep the scores out of HBM
-// and gain 1 %.
+// 102-106 us, 6.1-6.3 TB/s, 90-93 % of the measured copy rate; B=4 GQA 8 to 64K: 54-56 us (77-80 %:
+// 5 are the first loads' latency, 4 the join); B=8 GQA 4 to 32K with weights: 124-128 us (79-81 %;
+// keeping the scores, most of which go through HBM, costs 8 us, adding the weights 11). The second
+// product with P's rest costs nothing measurable, nor does keeping infinities out of it; two
+// stages instead of three cost 2 % at B=16, one CTA of six stages on each SM 12 %.
 //
 // One CTA: warp 4 loads (TMA boxes of up to 64 rows of a page, all d columns of one head, into a
 // ring of three tiles of K and V, 128-byte swizzle); warps 0..3 each take 16 tokens of every tile
@@ -65,7 +64,7 @@ constexpr int kShortTiles = 4;                 // tiles of a CTA of a short unit
 constexpr int kWarps = 4;                      // consumer warps, 16 tokens of a tile each
 constexpr int kThreads = 32 * (kWarps + 1);    // and the producer warp
 constexpr int kRows = 16;                      // query heads of a unit, at most
-constexpr int kSms = 152;
+constexpr int kSms = 152;                      // of a GB300; on another count only speed differs
 constexpr int kMaxCtas = 2 * kSms;             // two CTAs on each SM
 constexpr int kMaxCluster = 8;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
