@@ -555,15 +555,16 @@ __global__ void __launch_bounds__(kThreads, SHORT ? 1 : 2)
             acc[x][3] *= f1;
           }
         }
-        const float u0 = (m0 == -INFINITY ? 0.f : m0) - kPShift<FP16>;
-        const float u1 = (m1 == -INFINITY ? 0.f : m1) - kPShift<FP16>;
+        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+        // (the shift comes after the difference: next to a large maximum it would be rounded)
+        auto prob = [](float s, float u) { return ptx::exp2_approx((s - u) + kPShift<FP16>); };
         float p[2][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          p[x][0] = ptx::exp2_approx(sv[x][0] - u0);
-          p[x][1] = ptx::exp2_approx(sv[x][1] - u0);
-          p[x][2] = ptx::exp2_approx(sv[x][2] - u1);
-          p[x][3] = ptx::exp2_approx(sv[x][3] - u1);
+          p[x][0] = prob(sv[x][0], u0);
+          p[x][1] = prob(sv[x][1], u0);
+          p[x][2] = prob(sv[x][2], u1);
+          p[x][3] = prob(sv[x][3], u1);
         }
         l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
         l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);

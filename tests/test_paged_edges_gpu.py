@@ -136,3 +136,36 @@ def test_key_weights_take_the_lengths_that_the_forward_takes(side):
         got = fa.key_weights(q, k, lse, causal=True, seqlens_k=given, stream=stream)
         torch.cuda.synchronize()
         assert same_bits(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("lens", [[100], [3000, 64]])
+def test_large_scores(dtype, lens):
+    """Equal scores from 2^9 to 2^31 (log2 units), where a step of fp32 is up to 256: the
+    probabilities are equal all the same, and O is the mean of the values."""
+    import io_aware_attention_fa2_gb300 as fa
+    c = Cache(lens, 16, 1, 64, dtype, seed=11, weights=True)
+    q = c.query(3) * 0
+    q[..., 0] = 2.0 ** 15
+    for b, n in enumerate(lens):
+        pg, row = c.rows(c.table, b, n)
+        c.k[pg, row] = 0
+        c.k[pg, row, :, 0] = 2.0 ** 15
+    half = torch.finfo(c.dtype).eps / 2
+    for e in range(-21, 1):
+        for sign in (1.0, -1.0):
+            w = c.w.clone()
+            o, lse = fa.paged_attention(q, c.k, c.v, c.table, c.seqlens, scale=sign * 0.7 * 2.0 ** e,
+                                        weights=w)
+            for b, n in enumerate(lens):
+                pg, row = c.rows(c.table, b, n)
+                v = c.v[pg, row, 0].double()
+                want, size = v.mean(0), v.abs().mean(0)
+                # the output's rounding; P in two parts and sums in 32 bits
+                bound = half * want.abs() + 2.0 ** -15 * size
+                assert ((o[b].double() - want).abs() <= bound).all(), (e, sign)
+                s = sign * 0.7 * 2.0 ** (e + 30)
+                assert ((lse[b].double() - s - math.log(n)).abs() <= abs(s) * 2.0 ** -22
+                        + 2.0 ** -19).all(), (e, sign)
+                added = (w[pg, :, row] - c.w[pg, :, row]).double()
+                assert (added - 3.0 / n).abs().max() <= 2.0 ** -18 / n + 2.0 ** -23, (e, sign)
