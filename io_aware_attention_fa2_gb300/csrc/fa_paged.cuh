@@ -29,8 +29,10 @@ static inline cudaError_t read_and_clear_error(int* bits) {
   cudaError_t err = cudaMemcpyFromSymbol(&value, g_error, sizeof(int));
   if (err != cudaSuccess || value == 0) return err;
   *bits |= value;
-  clear_error_kernel<<<1, 1>>>(value);
-  err = cudaGetLastError();
+  // (the launch's own status: cudaGetLastError may hold that of an earlier call)
+  void* args[] = {&value};
+  err = cudaLaunchKernel(reinterpret_cast<const void*>(clear_error_kernel), dim3(1), dim3(1), args,
+                         0, nullptr);
   return err == cudaSuccess ? cudaStreamSynchronize(nullptr) : err;
 }
 

@@ -64,3 +64,11 @@ def test_dynamic_shared_memory_is_aligned():
             else:
                 assert "__align__(16)" in line, (name, line)
     assert found >= 5
+
+
+def test_launches_report_their_own_status():
+    """No launch of the cache's files asks for the last error, which an earlier call may have
+    left: the error query would then fail after it has cleared the word."""
+    for name in CHAINED:
+        text = sources()[name]
+        assert "<<<" not in text and "cudaGetLastError" not in text, name
