@@ -1,7 +1,8 @@
 /*
  * fa.h -- C ABI of fused exact attention for GB300 (sm_103a): the forward (with masks and a
  * split-K/V form), its backward, host-buffer forms of both, and a paged key-value cache
- * (fa_key_weights, fa_paged_append, fa_paged_decode, fa_paged_evict).
+ * (fa_key_weights, fa_paged_append, fa_paged_decode, fa_paged_evict; for drafted and branching
+ * sequences fa_paged_tree, fa_paged_accept, fa_paged_copy, fa_paged_fork, fa_paged_resize).
  *
  * The operation ("FlashAttention 优化原理与实现要点解析" §1, §2, §4.3, §5, §7):
  *
@@ -65,8 +66,9 @@ enum fa_status {
     FA_ERR_WORKSPACE = -11, /* workspace smaller than the entry point's ..._workspace_size() (the
                                text of fa_error_string names fa_fwd_splitkv's for all) */
     FA_ERR_POINTER = -12,   /* a device-side argument is not device memory of the current device */
-    FA_ERR_PAGE = -13       /* a block table or length named a token outside the cache (found on the
-                               device, read with fa_get_device_error) */
+    FA_ERR_PAGE = -13       /* a block table or length named a token outside the cache, or a draft's
+                               parent none of its earlier tokens, or a pool's entry none of its
+                               pages (found on the device, read with fa_get_device_error) */
 };
 
 /*
@@ -428,6 +430,138 @@ int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* bloc
                    const int* seqlens, const int* out_table, int* kept, int* new_seqlens, int B,
                    int Hkv, int d, int page_size, int num_pages, int max_pages, int out_pages,
                    int budget, int recent, int dtype, fa_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Drafted tokens and branching sequences over the paged cache
+ *
+ * A step of speculative decoding, for the whole batch: room for the drafted tokens
+ * (fa_paged_resize), their keys and values into the pages (fa_paged_append), their attention
+ * (fa_paged_tree), and, once it is known which of them stay, these moved behind the context
+ * (fa_paged_accept) and the pages behind them given back (fa_paged_resize). Several continuations
+ * of a sequence share its pages (fa_paged_fork, and fa_paged_copy for the last one, which is
+ * filled in part).
+ *
+ *   drafted tokens  the last n_b tokens of sequence b, which seqlens counts already:
+ *                n_b = new_lens[b] clamped to [0, T]; new_lens NULL: T for every sequence; T at
+ *                most 1024. Drafted token i is token seqlens[b] - n_b + i of the sequence; the
+ *                tokens before them are the context.
+ *   parents      device int32 [B, T]: of drafted token i the one before it, an earlier one
+ *                (0 .. i - 1) or -1 for the context: several trees, in an order in which parents
+ *                come first. NULL: chains (the parent of i is i - 1). Entries at or past n_b are
+ *                not read.
+ */
+
+/*
+ * fa_paged_tree -- attention of the drafted tokens: token i sees the context, its ancestors and
+ * itself,
+ *   O[b, i, h] = softmax(scale * Q K^T) V over those, and LSE.
+ *
+ *   q, o         [B, T, Hq, d] dtype, o written (every element)
+ *   lse          [B, Hq, T] fp32, written (every element)
+ *   window_left  >= 0: a token stands at position (context's length) + (number of its ancestors),
+ *                and sees only tokens at most window_left positions before it; negative: no bound
+ *   workspace    device memory of at least fa_paged_tree_workspace_size(...) bytes, 16-byte
+ *                aligned, not overlapping any other argument; NULL where that is 0. Calls
+ *                sharing a workspace must not overlap. Its contents need no initialisation.
+ * The cache's weights get nothing: which of the tokens will stay is not known yet. Rows at or
+ * past n_b, and of tokens that see nothing, get O = 0 and LSE = -inf. What is in keys and values
+ * that a token does not see (NaN included) does not matter to it; an infinite value of a token
+ * that it sees makes its column of O infinite, values of both signs or a NaN make it NaN. A sequence
+ * whose length is beyond the table or below n_b sees nothing, tokens in pages outside the pool are
+ * left out, and a parent that is not an earlier token counts as -1 (each FA_ERR_PAGE in the
+ * device error word). The same call gives the same bits.
+ */
+int fa_paged_tree(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                  const int* seqlens, const int* parents, const int* new_lens, void* o, float* lse,
+                  int B, int T, int Hq, int Hkv, int d, int page_size, int num_pages,
+                  int max_pages, int window_left, float scale, int dtype, void* workspace,
+                  size_t workspace_bytes, fa_stream_t stream);
+
+/* Bytes of workspace fa_paged_tree needs; 0 where no sequence's tokens are shared out. */
+size_t fa_paged_tree_workspace_size(int B, int T, int Hq, int Hkv, int d, int page_size,
+                                    int max_pages);
+
+/*
+ * fa_paged_accept -- the drafted tokens that stay: leaf[b] and its ancestors, in their order from
+ * the tree's root, become the first tokens behind the context. Keys, values and (where the cache
+ * keeps them) weights of their rows move; the sequence ends with them.
+ *
+ *   leaf         device int32 [B]: 0 .. n_b - 1, or -1: none stays
+ *   weights      the cache's weights, or NULL
+ *   path         device int32 [B, T], written: the accepted tokens, ascending; -1 behind them
+ *   new_seqlens  device int32 [B], written: the context's length + the accepted tokens
+ * The rows behind the new length are left as they were, or as the moved tokens left them.
+ * Where a length, the leaf, a parent on its path or a page that a moved token leaves or enters is
+ * bad, nothing of that sequence moves: its path is all -1, its new length the old one, and the
+ * device error word gets FA_ERR_PAGE. The pages written must belong to one sequence (whole pages
+ * of a context may be shared).
+ */
+int fa_paged_accept(void* k_pages, void* v_pages, float* weights, const int* block_table,
+                    const int* seqlens, const int* parents, const int* leaf, const int* new_lens,
+                    int* path, int* new_seqlens, int B, int T, int Hkv, int d, int page_size,
+                    int num_pages, int max_pages, int dtype, fa_stream_t stream);
+
+/*
+ * fa_paged_copy -- the first rows[m] rows of page src[m], keys, values and (where the cache keeps
+ * them) weights, to page dst[m].
+ *
+ *   src, dst     device int32 [M]; both negative: no copy. No page of dst may stand in dst twice
+ *                or in src.
+ *   rows         device int32 [M], 0 .. page_size; NULL: whole pages
+ * A page outside the pool, or a number of rows that a page does not have, copies nothing
+ * (FA_ERR_PAGE in the device error word).
+ */
+int fa_paged_copy(void* k_pages, void* v_pages, float* weights, const int* src, const int* dst,
+                  const int* rows, int M, int Hkv, int d, int page_size, int num_pages, int dtype,
+                  fa_stream_t stream);
+
+/* The pool of pages, for fa_paged_fork and fa_paged_resize:
+ *   refs         device int32 [num_pages]: in how many tables a page stands (0: free)
+ *   free_pages   device int32 [num_pages]: the first num_free[0] entries are the free pages, a
+ *                stack whose last entry is taken first; a place that is taken becomes -1
+ *   num_free     device int32 [1]
+ * All three are updated; calls on one pool must not overlap. A caller starts with refs all 0 and
+ * every page in free_pages. Batches of at most 8192 sequences; B * max_pages below 2^31 - 1. */
+
+/*
+ * fa_paged_fork -- new sequences that continue others: sequence c of the new tables has the tokens
+ * of sequence source[c]. Its whole pages are the source's (one more reference each); where its
+ * last page is filled in part, it gets a page of its own from the pool and an entry in the list of
+ * copies, which fa_paged_copy then makes in the caches of every layer.
+ *
+ *   block_table, seqlens  of B sequences, which stay as they are
+ *   source       device int32 [C]: 0 .. B - 1 (any of them several times), or -1: empty
+ *   out_table    device int32 [C, max_pages], written (every element; -1 behind the last page)
+ *   out_seqlens  device int32 [C], written: the lengths; -1 for a sequence that got no page
+ *                because the pool was empty, or whose source or length is bad (FA_ERR_PAGE in the
+ *                device error word): it holds nothing
+ *   copy_src, copy_dst, copy_rows  device int32 [C], written: fa_paged_copy's src, dst and rows;
+ *                -1, -1 and 0 without a copy
+ * Pages come from the pool in the order of c. A page outside the pool in the source's table is
+ * passed on as -1 (FA_ERR_PAGE).
+ */
+int fa_paged_fork(const int* block_table, const int* seqlens, const int* source, int* refs,
+                  int* free_pages, int* num_free, int* out_table, int* out_seqlens, int* copy_src,
+                  int* copy_dst, int* copy_rows, int B, int C, int page_size, int num_pages,
+                  int max_pages, fa_stream_t stream);
+
+/*
+ * fa_paged_resize -- tables with the pages for other lengths. Sequence b has pages for old_lens[b]
+ * tokens and gets those for new_lens[b] (0: it ends; no tokens move, and none are cleared):
+ *   - of shorter sequences the pages behind the new length lose a reference, and those without
+ *     another return to the pool; their entries become -1;
+ *   - longer sequences then take pages from the pool, in the order of b; a sequence for which
+ *     they do not suffice gets none, nor do those behind it that need any.
+ *
+ *   granted      device int32 [B], written: new_lens[b], or old_lens[b] where the pool did not
+ *                suffice or a length is negative or beyond the table (FA_ERR_PAGE)
+ * Pages return to the pool in the order of the tables (a page that several give up at once by the
+ * last of them). An entry outside the pool, or of a page without references, is not returned
+ * (FA_ERR_PAGE). The same call gives the same result whatever the timing.
+ */
+int fa_paged_resize(int* block_table, const int* old_lens, const int* new_lens, int* granted,
+                    int* refs, int* free_pages, int* num_free, int B, int page_size, int num_pages,
+                    int max_pages, fa_stream_t stream);
 
 /* Static English text for a status code (never NULL). */
 const char* fa_error_string(int code);

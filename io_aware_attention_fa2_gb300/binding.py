@@ -24,7 +24,8 @@ _WORKSPACE_SIZE = {"fa_fwd_splitkv": "fa_fwd_splitkv_workspace_size",
                    "fa_bwd_masked": "fa_bwd_workspace_size",
                    "fa_bwd_host_masked": "fa_bwd_workspace_size",
                    "fa_key_weights": "fa_key_weights_workspace_size",
-                   "fa_paged_decode": "fa_paged_decode_workspace_size"}
+                   "fa_paged_decode": "fa_paged_decode_workspace_size",
+                   "fa_paged_tree": "fa_paged_tree_workspace_size"}
 
 _lock = threading.Lock()
 _lib = None
@@ -102,6 +103,18 @@ def load_library() -> ctypes.CDLL:
             lib.fa_paged_decode_workspace_size.restype = szt
             lib.fa_paged_evict.argtypes = [vp] * 8 + [i32] * 10 + [vp]
             lib.fa_paged_evict.restype = i32
+            lib.fa_paged_tree.argtypes = [vp] * 9 + [i32] * 9 + [f32, i32, vp, szt, vp]
+            lib.fa_paged_tree.restype = i32
+            lib.fa_paged_tree_workspace_size.argtypes = [i32] * 7
+            lib.fa_paged_tree_workspace_size.restype = szt
+            lib.fa_paged_accept.argtypes = [vp] * 10 + [i32] * 8 + [vp]
+            lib.fa_paged_accept.restype = i32
+            lib.fa_paged_copy.argtypes = [vp] * 6 + [i32] * 6 + [vp]
+            lib.fa_paged_copy.restype = i32
+            lib.fa_paged_fork.argtypes = [vp] * 11 + [i32] * 5 + [vp]
+            lib.fa_paged_fork.restype = i32
+            lib.fa_paged_resize.argtypes = [vp] * 7 + [i32] * 4 + [vp]
+            lib.fa_paged_resize.restype = i32
             lib.fa_error_string.argtypes = [i32]
             lib.fa_error_string.restype = ctypes.c_char_p
             lib.fa_get_device_error.argtypes = [vp]

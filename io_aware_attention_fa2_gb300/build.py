@@ -20,7 +20,8 @@ BUILD_DIR = os.path.join(_PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libfa_gb300.so")
 
 SOURCES = ["fa_fwd_kernel.cu", "fa_bwd_kernel.cu", "fa_api.cpp", "fa_noalloc.cu",
-           "fa_paged_api.cpp", "fa_paged.cu", "fa_paged_decode.cu", "fa_key_weights.cu"]
+           "fa_paged_api.cpp", "fa_paged.cu", "fa_paged_decode.cu", "fa_key_weights.cu",
+           "fa_paged_tree.cu", "fa_paged_pool.cu"]
 HEADERS = ["fa_internal.h", "fa_paged_internal.h", "fa_paged.cuh", "ptx_sm103.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -95,27 +95,6 @@ constexpr int kBins = 2048, kBinsPerThread = kBins / kSelectThreads;
 constexpr int kMaxCache = 49152;   // keys a CTA keeps in shared memory; further ones are read from
                                    // the pages in every pass
 
-// Loads past L1 that stay where they stand in the program, behind a wait and in front of a
-// barrier: the compiler's own intrinsic promises no order with either.
-__device__ __forceinline__ int load_l2(const int* p) {
-  int v;
-  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ float load_l2(const float* p) {
-  float v;
-  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 load_l2(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-
 // Weights as unsigned numbers in the same order: NaN lowest, -0 equal to +0.
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (!(w == w)) return 0u;
@@ -562,6 +541,8 @@ cudaError_t read_and_clear_paged_error(int* value) {
   cudaError_t err = read_and_clear_error(&bits);
   if (err == cudaSuccess) err = read_and_clear_decode_error(&bits);
   if (err == cudaSuccess) err = read_and_clear_key_weights_error(&bits);
+  if (err == cudaSuccess) err = read_and_clear_pool_error(&bits);
+  if (err == cudaSuccess) err = read_and_clear_tree_error(&bits);
   *value = bits & kTimeoutBit ? kErrTimeout : bits & kPageBit ? kErrPage : 0;
   return err;
 }

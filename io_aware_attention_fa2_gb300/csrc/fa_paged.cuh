@@ -51,6 +51,27 @@ __device__ __forceinline__ Visible visible_tokens(const int* seqlens, int b, int
   return {window_left >= 0 ? max(0, len - 1 - window_left) : 0, len};
 }
 
+// Loads past L1 that stay where they stand in the program, behind a wait and in front of a
+// barrier: the compiler's own intrinsic promises no order with either.
+__device__ __forceinline__ int load_l2(const int* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_l2(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_l2(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // Programmatic stream serialisation: let the next kernel be launched; wait for the one before.
 // A kernel is resident while the one before it may still write its inputs, so none of them is
 // read-only for the kernel's life: no input is declared `const T* __restrict__` and none is read
@@ -86,6 +107,25 @@ cudaError_t launch_chained(void (*kernel)(Params...), int64_t grid, int block, s
   cfg.attrs = attrs;
   cfg.numAttrs = cluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The same without a cluster, or with one, for the files of drafted and forked sequences.
+template <typename... Params, typename... Args>
+cudaError_t launch_paged(void (*kernel)(Params...), int64_t grid, int block, size_t smem,
+                         cudaStream_t stream, int cluster, const Args&... args) {
+  return launch_chained(kernel, grid, block, smem, stream, cluster, args...);
+}
+
+// Drafted tokens of sequence b: they are its last ones, tokens [base, base + count). A sequence
+// whose length is negative, beyond the table or shorter than its draft has count = -1.
+struct Draft {
+  int base, count;
+};
+__device__ __forceinline__ Draft draft_of(const int* seqlens, const int* new_lens, int b, int T,
+                                          int capacity) {
+  const int len = seqlens[b], n = new_lens ? min(max(new_lens[b], 0), T) : T;
+  if (len < n || len > capacity) return {0, -1};
+  return {len - n, n};
 }
 
 }  // namespace paged

@@ -68,6 +68,20 @@ bool decode_shape_ok(int B, int Hq, int Hkv, int page_size, int max_pages) {
   return (uint64_t)B * (uint64_t)Hq * (tokens / 1024 + 2) < (1ull << 31);
 }
 
+// Drafted tokens: up to kMaxDraft of each sequence, rows (b, t, h) within 2^31 - 1.
+bool tree_shape_ok(int B, int T, int Hq, int Hkv) {
+  if (T < 1 || T > fa::kMaxDraft || Hq < Hkv || Hq % Hkv) return false;
+  return (uint64_t)B * (uint64_t)T * (uint64_t)Hq < (1ull << 31);
+}
+
+// Tables of a pool's pages: entries within 2^31 - 1, as places in an order of them are ints.
+bool pool_shape_ok(int B, int page_size, int num_pages, int max_pages) {
+  if (B < 1 || B > fa::kMaxPoolBatch || num_pages < 1 || max_pages < 1) return false;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return false;
+  if ((int64_t)max_pages * page_size > (1ll << 30)) return false;
+  return (uint64_t)B * (uint64_t)max_pages < (1ull << 31) - 1;
+}
+
 uint64_t pool_bytes(int Hkv, int d, int page_size, int num_pages) {
   return (uint64_t)num_pages * page_size * Hkv * d * 2;
 }
@@ -279,6 +293,202 @@ int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* bloc
   p.budget = budget;
   p.recent = recent;
   return fa::launch_paged_evict(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_LAUNCH;
+}
+
+size_t fa_paged_tree_workspace_size(int B, int T, int Hq, int Hkv, int d, int page_size,
+                                    int max_pages) {
+  if (!cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) || !tree_shape_ok(B, T, Hq, Hkv))
+    return 0;
+  return fa::paged_tree_workspace(B, T, Hq, Hkv, d, page_size, max_pages);
+}
+
+int fa_paged_tree(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                  const int* seqlens, const int* parents, const int* new_lens, void* o, float* lse,
+                  int B, int T, int Hq, int Hkv, int d, int page_size, int num_pages,
+                  int max_pages, int window_left, float scale, int dtype, void* workspace,
+                  size_t workspace_bytes, fa_stream_t stream) {
+  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !o || !lse) return FA_ERR_NULL;
+  if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages) ||
+      !tree_shape_ok(B, T, Hq, Hkv))
+    return FA_ERR_SHAPE;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
+  if (!scale_ok(scale)) return FA_ERR_SCALE;
+  const uint64_t ws_need = fa::paged_tree_workspace(B, T, Hq, Hkv, d, page_size, max_pages);
+  if (ws_need) {
+    if (!workspace) return FA_ERR_NULL;
+    if (workspace_bytes < ws_need) return FA_ERR_WORKSPACE;
+  } else {
+    workspace = nullptr;
+  }
+  if (!aligned({q, k_pages, v_pages, o, workspace}, 16) ||
+      !aligned({block_table, seqlens, parents, new_lens, lse}, 4))
+    return FA_ERR_ALIGN;
+  const uint64_t pool = pool_bytes(Hkv, d, page_size, num_pages);
+  const uint64_t rows = (uint64_t)B * T * Hq, lens = (uint64_t)B * 4;
+  int rc = check_spans({{q, rows * d * 2}, {k_pages, pool}, {v_pages, pool},
+                        {block_table, lens * max_pages}, {seqlens, lens}, {parents, lens * T},
+                        {new_lens, lens}},
+                       {{o, rows * d * 2}, {lse, rows * 4}, {workspace, ws_need}});
+  if (rc != FA_OK) return rc;
+  rc = check_device({q, k_pages, v_pages, block_table, seqlens, parents, new_lens, o, lse,
+                     workspace});
+  if (rc != FA_OK) return rc;
+
+  fa::TreeParams p;
+  p.c = make_cache(k_pages, v_pages, nullptr, block_table, seqlens, B, Hkv, d, page_size,
+                   num_pages, max_pages);
+  p.q = q;
+  p.parents = parents;
+  p.new_lens = new_lens;
+  p.o = o;
+  p.lse = lse;
+  p.workspace = workspace;
+  p.T = T;
+  p.Hq = Hq;
+  p.window_left = window_left < 0 ? -1 : window_left;
+  p.fp16 = dtype == FA_FP16 ? 1 : 0;
+  p.scale_log2 = scale * kLog2e;
+  return fa::launch_paged_tree(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_paged_accept(void* k_pages, void* v_pages, float* weights, const int* block_table,
+                    const int* seqlens, const int* parents, const int* leaf, const int* new_lens,
+                    int* path, int* new_seqlens, int B, int T, int Hkv, int d, int page_size,
+                    int num_pages, int max_pages, int dtype, fa_stream_t stream) {
+  if (!k_pages || !v_pages || !block_table || !seqlens || !leaf || !path || !new_seqlens)
+    return FA_ERR_NULL;
+  if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages) || T < 1 || T > fa::kMaxDraft)
+    return FA_ERR_SHAPE;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
+  if (!aligned({k_pages, v_pages, weights}, 16) ||
+      !aligned({block_table, seqlens, parents, leaf, new_lens, path, new_seqlens}, 4))
+    return FA_ERR_ALIGN;
+  const uint64_t pool = pool_bytes(Hkv, d, page_size, num_pages), lens = (uint64_t)B * 4;
+  int rc = check_spans({{block_table, lens * max_pages}, {seqlens, lens}, {parents, lens * T},
+                        {leaf, lens}, {new_lens, lens}},
+                       {{k_pages, pool}, {v_pages, pool}, {weights, pool / d * 2},
+                        {path, lens * T}, {new_seqlens, lens}});
+  if (rc != FA_OK) return rc;
+  rc = check_device({k_pages, v_pages, weights, block_table, seqlens, parents, leaf, new_lens,
+                     path, new_seqlens});
+  if (rc != FA_OK) return rc;
+
+  fa::AcceptParams p;
+  p.c = make_cache(k_pages, v_pages, weights, block_table, seqlens, B, Hkv, d, page_size,
+                   num_pages, max_pages);
+  p.parents = parents;
+  p.leaf = leaf;
+  p.new_lens = new_lens;
+  p.path = path;
+  p.new_seqlens = new_seqlens;
+  p.T = T;
+  return fa::launch_paged_accept(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_paged_copy(void* k_pages, void* v_pages, float* weights, const int* src, const int* dst,
+                  const int* rows, int M, int Hkv, int d, int page_size, int num_pages, int dtype,
+                  fa_stream_t stream) {
+  if (!k_pages || !v_pages || !src || !dst) return FA_ERR_NULL;
+  if (!cache_shape_ok(1, Hkv, d, page_size, num_pages, 1) || M < 1) return FA_ERR_SHAPE;
+  // blocks of 16 KiB of each page's K and V, at most 2^31 - 1
+  const uint64_t parts = ((uint64_t)page_size * Hkv * d * 2 + 16383) / 16384;
+  if ((uint64_t)M * 2 * parts >= (1ull << 31)) return FA_ERR_SHAPE;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
+  if (!aligned({k_pages, v_pages, weights}, 16) || !aligned({src, dst, rows}, 4))
+    return FA_ERR_ALIGN;
+  const uint64_t pool = pool_bytes(Hkv, d, page_size, num_pages), list = (uint64_t)M * 4;
+  int rc = check_spans({{src, list}, {dst, list}, {rows, list}},
+                       {{k_pages, pool}, {v_pages, pool}, {weights, pool / d * 2}});
+  if (rc != FA_OK) return rc;
+  rc = check_device({k_pages, v_pages, weights, src, dst, rows});
+  if (rc != FA_OK) return rc;
+
+  fa::CopyParams p;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.weights = weights;
+  p.src = src;
+  p.dst = dst;
+  p.rows = rows;
+  p.M = M;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  return fa::launch_paged_copy(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_paged_fork(const int* block_table, const int* seqlens, const int* source, int* refs,
+                  int* free_pages, int* num_free, int* out_table, int* out_seqlens, int* copy_src,
+                  int* copy_dst, int* copy_rows, int B, int C, int page_size, int num_pages,
+                  int max_pages, fa_stream_t stream) {
+  if (!block_table || !seqlens || !source || !refs || !free_pages || !num_free || !out_table ||
+      !out_seqlens || !copy_src || !copy_dst || !copy_rows)
+    return FA_ERR_NULL;
+  if (!pool_shape_ok(B, page_size, num_pages, max_pages) ||
+      !pool_shape_ok(C, page_size, num_pages, max_pages))
+    return FA_ERR_SHAPE;
+  if (!aligned({block_table, seqlens, source, refs, free_pages, num_free, out_table, out_seqlens,
+                copy_src, copy_dst, copy_rows}, 4))
+    return FA_ERR_ALIGN;
+  const uint64_t lens = (uint64_t)B * 4, outs = (uint64_t)C * 4, pages = (uint64_t)num_pages * 4;
+  int rc = check_spans({{block_table, lens * max_pages}, {seqlens, lens}, {source, outs}},
+                       {{refs, pages}, {free_pages, pages}, {num_free, 4},
+                        {out_table, outs * max_pages}, {out_seqlens, outs}, {copy_src, outs},
+                        {copy_dst, outs}, {copy_rows, outs}});
+  if (rc != FA_OK) return rc;
+  rc = check_device({block_table, seqlens, source, refs, free_pages, num_free, out_table,
+                     out_seqlens, copy_src, copy_dst, copy_rows});
+  if (rc != FA_OK) return rc;
+
+  fa::ForkParams p;
+  p.pool = fa::PagePool{refs, free_pages, num_free, num_pages};
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.source = source;
+  p.out_table = out_table;
+  p.out_seqlens = out_seqlens;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.copy_rows = copy_rows;
+  p.B = B;
+  p.C = C;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  return fa::launch_paged_fork(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_paged_resize(int* block_table, const int* old_lens, const int* new_lens, int* granted,
+                    int* refs, int* free_pages, int* num_free, int B, int page_size, int num_pages,
+                    int max_pages, fa_stream_t stream) {
+  if (!block_table || !old_lens || !new_lens || !granted || !refs || !free_pages || !num_free)
+    return FA_ERR_NULL;
+  if (!pool_shape_ok(B, page_size, num_pages, max_pages)) return FA_ERR_SHAPE;
+  if (!aligned({block_table, old_lens, new_lens, granted, refs, free_pages, num_free}, 4))
+    return FA_ERR_ALIGN;
+  const uint64_t lens = (uint64_t)B * 4, pages = (uint64_t)num_pages * 4;
+  int rc = check_spans({{old_lens, lens}, {new_lens, lens}},
+                       {{block_table, lens * max_pages}, {granted, lens}, {refs, pages},
+                        {free_pages, pages}, {num_free, 4}});
+  if (rc != FA_OK) return rc;
+  rc = check_device({block_table, old_lens, new_lens, granted, refs, free_pages, num_free});
+  if (rc != FA_OK) return rc;
+
+  fa::ResizeParams p;
+  p.pool = fa::PagePool{refs, free_pages, num_free, num_pages};
+  p.block_table = block_table;
+  p.old_lens = old_lens;
+  p.new_lens = new_lens;
+  p.granted = granted;
+  p.B = B;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  return fa::launch_paged_resize(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK : FA_ERR_LAUNCH;
 }
 

@@ -76,11 +76,84 @@ struct EvictParams {
 };
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream);
 
+// ---- drafted and forked sequences
+struct TreeParams {
+  PagedCache c;
+  const void* q;            // [B, T, Hq, d]
+  const int* parents;       // device int32 [B, T] or null (chains)
+  const int* new_lens;      // device int32 [B] or null
+  void* o;                  // [B, T, Hq, d]
+  float* lse;               // [B, Hq, T]
+  void* workspace;
+  int T, Hq, window_left, fp16;
+  float scale_log2;
+};
+cudaError_t launch_paged_tree(const TreeParams& p, cudaStream_t stream);
+size_t paged_tree_workspace(int B, int T, int Hq, int Hkv, int d, int page_size, int max_pages);
+constexpr int kMaxDraft = 1024;
+
+struct AcceptParams {
+  PagedCache c;
+  const int* parents;       // as in TreeParams
+  const int* leaf;          // device int32 [B]
+  const int* new_lens;
+  int* path;                // [B, T]
+  int* new_seqlens;         // [B]
+  int T;
+};
+cudaError_t launch_paged_accept(const AcceptParams& p, cudaStream_t stream);
+
+struct CopyParams {
+  void* k_pages;
+  void* v_pages;
+  float* weights;           // or null
+  const int* src;           // device int32 [M]
+  const int* dst;
+  const int* rows;          // device int32 [M] or null (whole pages)
+  int M, Hkv, d, page_size, num_pages;
+};
+cudaError_t launch_paged_copy(const CopyParams& p, cudaStream_t stream);
+
+// Pages that no table holds, and how many tables hold each.
+struct PagePool {
+  int* refs;                // [num_pages]
+  int* free_pages;          // [num_pages]: the first *num_free are free
+  int* num_free;            // [1]
+  int num_pages;
+};
+constexpr int kMaxPoolBatch = 8192;   // sequences of a fork or resize
+
+struct ForkParams {
+  PagePool pool;
+  const int* block_table;   // [B, max_pages]
+  const int* seqlens;       // [B]
+  const int* source;        // [C]
+  int* out_table;           // [C, max_pages]
+  int* out_seqlens;         // [C]
+  int* copy_src;            // [C] each
+  int* copy_dst;
+  int* copy_rows;
+  int B, C, page_size, max_pages;
+};
+cudaError_t launch_paged_fork(const ForkParams& p, cudaStream_t stream);
+
+struct ResizeParams {
+  PagePool pool;
+  int* block_table;         // [B, max_pages], updated
+  const int* old_lens;      // [B]
+  const int* new_lens;      // [B]
+  int* granted;             // [B]
+  int B, page_size, max_pages;
+};
+cudaError_t launch_paged_resize(const ResizeParams& p, cudaStream_t stream);
+
 // The error words of these kernels on the current device: read and clear (no synchronisation).
 // FA_OK, FA_ERR_TIMEOUT, or FA_ERR_PAGE (where no wait ran out).
 cudaError_t read_and_clear_paged_error(int* value);
-// Those of two of the translation units, or-ed in: 1 timeout, 2 bad page.
+// Those of the other translation units, or-ed in: 1 timeout, 2 bad page.
 cudaError_t read_and_clear_decode_error(int* bits);
 cudaError_t read_and_clear_key_weights_error(int* bits);
+cudaError_t read_and_clear_pool_error(int* bits);
+cudaError_t read_and_clear_tree_error(int* bits);
 
 }  // namespace fa

@@ -1,0 +1,532 @@
+// fa_paged_pool.cu -- the paged cache's pages as sequences branch and change their lengths: accept
+// (drafted tokens that stay), copy, fork, resize (include/fa.h has the rules).
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+namespace {
+
+using namespace paged;
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------------------------------------
+// Accept. The path from the accepted token up to its tree's root, then the rows of that path
+// moved behind the context: path[j] >= j, so in rounds over ascending j, each with all its reads
+// before its writes, no row is written before it has been read. A few tokens of each sequence:
+// bound by the latency of a chain of loads (lengths, parents, table, rows). One block for each
+// (sequence, key head), which finds the path by itself.
+constexpr int kAcceptThreads = 128, kAcceptTokens = 8;   // 16-byte loads in flight for each lane
+
+struct AcceptArgs {
+  uint4* k_pages;
+  uint4* v_pages;
+  float* weights;
+  const int* table;
+  const int* seqlens;
+  const int* parents;
+  const int* leaf;
+  const int* new_lens;
+  int* path;
+  int* new_seqlens;
+  int T, Hkv, page_shift, num_pages, max_pages;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAcceptThreads)
+    fa_paged_accept_kernel(const __grid_constant__ AcceptArgs a) {
+  constexpr int kLanes = D / 4;                        // a row's K and V, 16 bytes a lane
+  constexpr int kTokens = 32 / kLanes * kAcceptTokens; // tokens of a warp in a round
+  constexpr int kWarps = kAcceptThreads / 32, kRound = kTokens * kWarps;
+  __shared__ short s_parent[kMaxDraft], s_path[kMaxDraft];
+  __shared__ int s_count, s_bad;
+  const int b = blockIdx.x / a.Hkv, hk = blockIdx.x % a.Hkv;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  wait_prerequisites();
+  launch_dependents();
+
+  const Draft dr = draft_of(a.seqlens, a.new_lens, b, a.T, a.max_pages << a.page_shift);
+  const int leaf = a.leaf[b];
+  if (tid == 0) s_bad = dr.count < 0 || leaf < -1 || leaf >= dr.count;
+  // (parents that are not earlier tokens are found below if the path meets them)
+  if (a.parents)
+    for (int i = tid; i < dr.count; i += kAcceptThreads) {
+      const int parent = a.parents[static_cast<int64_t>(b) * a.T + i];
+      s_parent[i] = static_cast<short>(parent >= -1 && parent < i ? parent : -2);
+    }
+  __syncthreads();
+  const bool given_up = s_bad;
+  if (!given_up && tid == 0) {
+    int n = 0, at = leaf;   // from the leaf: the path's other end first
+    for (; at >= 0; at = a.parents ? s_parent[at] : at - 1) s_path[n++] = static_cast<short>(at);
+    if (at < -1) s_bad = 1;
+    s_count = n;
+  }
+  __syncthreads();
+  const int count = given_up ? 0 : s_count;
+  const int* const table = a.table + static_cast<int64_t>(b) * a.max_pages;
+  const int in_page = (1 << a.page_shift) - 1;
+  auto from = [&](int j) { return dr.base + s_path[count - 1 - j]; };
+  // every page that a moved row leaves or enters
+  if (!s_bad)
+    for (int j = tid; j < count; j += kAcceptThreads)
+      if (from(j) != dr.base + j)
+        for (int t : {from(j), dr.base + j}) {
+          const int page = table[t >> a.page_shift];
+          if (page < 0 || page >= a.num_pages) s_bad = 1;
+        }
+  __syncthreads();
+  const bool bad = s_bad;
+  if (hk == 0) {
+    for (int j = tid; j < a.T; j += kAcceptThreads)
+      a.path[static_cast<int64_t>(b) * a.T + j] = !bad && j < count ? s_path[count - 1 - j] : -1;
+    if (tid == 0) {
+      a.new_seqlens[b] = bad ? a.seqlens[b] : dr.base + count;
+      if (bad) record_page_error();
+    }
+  }
+  if (bad) return;
+
+  const int part = lane % kLanes;
+  const int64_t chunk = part % (D / 8);
+  uint4* const pool = part < D / 8 ? a.k_pages : a.v_pages;
+  for (int r0 = 0; r0 < count; r0 += kRound) {
+    // lane e < kTokens looks up token j of the path
+    const int j = r0 + warp * kTokens + lane;
+    int64_t src = -1, dst = -1, w_dst = 0;
+    float w = 0.f;
+    if (lane < kTokens && j < count && from(j) != dr.base + j) {
+      const int t = from(j), to = dr.base + j;
+      const int64_t src_page = table[t >> a.page_shift], dst_page = table[to >> a.page_shift];
+      src = (((src_page << a.page_shift) + (t & in_page)) * a.Hkv + hk) * (D / 8);
+      dst = (((dst_page << a.page_shift) + (to & in_page)) * a.Hkv + hk) * (D / 8);
+      if (a.weights) {
+        w = load_l2(a.weights + ((src_page * a.Hkv + hk) << a.page_shift) + (t & in_page));
+        w_dst = ((dst_page * a.Hkv + hk) << a.page_shift) + (to & in_page);
+      }
+    }
+    uint4 v[kAcceptTokens];
+#pragma unroll
+    for (int u = 0; u < kAcceptTokens; ++u) {
+      const int64_t at = __shfl_sync(0xffffffffu, src, u * (32 / kLanes) + lane / kLanes);
+      if (at >= 0) v[u] = load_l2(pool + at + chunk);
+    }
+    __syncthreads();   // the round's reads, then its writes
+#pragma unroll
+    for (int u = 0; u < kAcceptTokens; ++u) {
+      const int e = u * (32 / kLanes) + lane / kLanes;
+      const int64_t at = __shfl_sync(0xffffffffu, src, e), to = __shfl_sync(0xffffffffu, dst, e);
+      if (at >= 0) pool[to + chunk] = v[u];
+    }
+    if (a.weights && src >= 0) a.weights[w_dst] = w;
+    __syncthreads();   // a later round reads behind what this one has written
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Copy. Bound by HBM. The first rows of a page are contiguous in K and in V: a block has kCopyBytes
+// of one of them, all its loads before its stores. Weights, [Hkv][page_size] of a page, go to the
+// blocks of K.
+constexpr int kCopyThreads = 256, kCopyLoads = 4;
+constexpr int kCopyChunks = kCopyThreads * kCopyLoads;   // 16 bytes each
+
+struct CopyArgs {
+  uint4* k_pages;
+  uint4* v_pages;
+  float* weights;
+  const int* src;
+  const int* dst;
+  const int* rows;
+  int Hkv, d, page_size, num_pages, parts;   // blocks for a page of K (or V)
+};
+
+__global__ void __launch_bounds__(kCopyThreads)
+    fa_paged_copy_kernel(const __grid_constant__ CopyArgs a) {
+  wait_prerequisites();
+  launch_dependents();
+  const int m = blockIdx.x / (2 * a.parts), at = blockIdx.x % (2 * a.parts);
+  const int part = at % a.parts;
+  const int src = a.src[m], dst = a.dst[m];
+  if (src < 0 && dst < 0) return;   // no copy
+  const int rows = a.rows ? a.rows[m] : a.page_size;
+  if (src < 0 || dst < 0 || src >= a.num_pages || dst >= a.num_pages || rows < 0 ||
+      rows > a.page_size) {
+    record_page_error();
+    return;
+  }
+  const int64_t row = static_cast<int64_t>(a.Hkv) * a.d / 8, page = row * a.page_size;
+  const int64_t n = row * rows, first = static_cast<int64_t>(part) * kCopyChunks + threadIdx.x;
+  uint4* const pool = at < a.parts ? a.k_pages : a.v_pages;
+  const uint4* const from = pool + src * page;
+  uint4* const to = pool + dst * page;
+  uint4 v[kCopyLoads];
+#pragma unroll
+  for (int u = 0; u < kCopyLoads; ++u)
+    if (first + u * kCopyThreads < n) v[u] = from[first + u * kCopyThreads];
+#pragma unroll
+  for (int u = 0; u < kCopyLoads; ++u)
+    if (first + u * kCopyThreads < n) to[first + u * kCopyThreads] = v[u];
+  if (a.weights && at < a.parts) {
+    const int64_t all = static_cast<int64_t>(a.Hkv) * a.page_size;
+    for (int64_t i = static_cast<int64_t>(part) * kCopyThreads + threadIdx.x; i < all;
+         i += static_cast<int64_t>(a.parts) * kCopyThreads)
+      if (static_cast<int>(i & (a.page_size - 1)) < rows)
+        a.weights[dst * all + i] = a.weights[src * all + i];
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Sum of x over the threads before this one, and (in *all) over the block.
+template <int THREADS>
+__device__ __forceinline__ int block_scan(int x, int* s_warp, int* all) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int inc = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += y;
+  }
+  __syncthreads();   // s_warp may still be read by an earlier call
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  const int w = lane < THREADS / 32 ? s_warp[lane] : 0;
+  int before = lane < warp ? w : 0, sum = w;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  }
+  *all = sum;
+  return before + inc - x;
+}
+
+// Free pages of the pool as the call finds them (a number outside the pool is recorded).
+__device__ __forceinline__ int free_pages_of(const PagePool& p) {
+  const int n = load_l2(p.num_free);
+  if (n < 0 || n > p.num_pages) {
+    record_page_error();
+    return 0;
+  }
+  return n;
+}
+// The page at place i of the stack, which leaves it; -1 (recorded) when it is outside the pool.
+__device__ __forceinline__ int take_page(const PagePool& p, int i) {
+  const int page = load_l2(p.free_pages + i);
+  p.free_pages[i] = -1;
+  if (page < 0 || page >= p.num_pages) {
+    record_page_error();
+    return -1;
+  }
+  p.refs[page] = 1;
+  return page;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Fork, in two kernels: lengths, pages from the pool and the list of copies by one block; then the
+// tables' rows and the references of shared pages, a block for each 1024 entries.
+constexpr int kForkThreads = 1024;
+
+__global__ void __launch_bounds__(kForkThreads)
+    fa_paged_fork_plan_kernel(const __grid_constant__ ForkParams p) {
+  __shared__ int s_warp[32];
+  wait_prerequisites();
+  launch_dependents();
+  const int have = free_pages_of(p.pool);
+  const int64_t capacity = static_cast<int64_t>(p.max_pages) * p.page_size;
+  int taken = 0;
+  for (int c0 = 0; c0 < p.C; c0 += kForkThreads) {
+    const int c = c0 + threadIdx.x;
+    int len = -1, from = -1;
+    if (c < p.C) {
+      from = p.source[c];
+      if (from == -1) {
+        len = 0;   // a new sequence
+      } else if (from >= 0 && from < p.B) {
+        len = p.seqlens[from];
+        if (len < 0 || len > capacity) len = -1;
+      }
+      if (len < 0) record_page_error();
+    }
+    const int tail = len > 0 ? len % p.page_size : 0;
+    int all;
+    const int place = taken + block_scan<kForkThreads>(tail > 0, s_warp, &all);
+    if (c < p.C) {
+      int src = -1, dst = -1, rows = 0;
+      if (tail > 0) {
+        if (place < have) {
+          src = p.block_table[static_cast<int64_t>(from) * p.max_pages + len / p.page_size];
+          dst = take_page(p.pool, have - 1 - place);
+          rows = tail;
+        } else {
+          len = -1;   // the pool is empty
+        }
+      }
+      p.out_seqlens[c] = len;
+      p.copy_src[c] = src;
+      p.copy_dst[c] = dst;
+      p.copy_rows[c] = rows;
+    }
+    taken += all;
+  }
+  if (threadIdx.x == 0) *p.pool.num_free = have - min(taken, have);
+}
+
+__global__ void __launch_bounds__(kForkThreads)
+    fa_paged_fork_kernel(const __grid_constant__ ForkParams p, int blocks_per_row) {
+  wait_prerequisites();
+  launch_dependents();
+  const int c = blockIdx.x / blocks_per_row;
+  const int col = (blockIdx.x % blocks_per_row) * kForkThreads + threadIdx.x;
+  if (col >= p.max_pages) return;
+  const int len = load_l2(p.out_seqlens + c);
+  const int full = len > 0 ? len / p.page_size : 0;
+  int page = -1;
+  if (col < full) {
+    page = p.block_table[static_cast<int64_t>(p.source[c]) * p.max_pages + col];
+    if (page >= 0 && page < p.pool.num_pages) {
+      atomicAdd(p.pool.refs + page, 1);
+    } else {
+      record_page_error();
+      page = -1;
+    }
+  } else if (col == full && len > 0 && len % p.page_size) {
+    page = load_l2(p.copy_dst + c);
+  }
+  p.out_table[static_cast<int64_t>(c) * p.max_pages + col] = page;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Resize, by one cluster: first the pages that shorter sequences give back, then those that
+// longer ones take. The order of the stack is the tables' order, whatever the number of threads
+// and their timing: a page that several tables give back at once goes by the last of them. That
+// one is found through refs: each gives up its reference, and where none is left each bids -1 -
+// its place in the order, by an atomic minimum; the one whose bid stands pushes the page.
+constexpr int kResizeThreads = 1024, kResizeCluster = 8;
+
+__global__ void __launch_bounds__(kResizeThreads, 1)
+    fa_paged_resize_kernel(const __grid_constant__ ResizeParams p) {
+  extern __shared__ __align__(16) int s_prefix[];   // [B + 1] releases, [B + 1] takes
+  __shared__ int s_warp[32], s_total;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int64_t capacity = static_cast<int64_t>(p.max_pages) * p.page_size;
+  int* const s_release = s_prefix;
+  int* const s_take = s_prefix + p.B + 1;
+  wait_prerequisites();
+  launch_dependents();
+
+  // the prefixes over the sequences, by every CTA for itself
+  const int have = free_pages_of(p.pool);
+  auto pages_of = [&](int tokens) { return (tokens + p.page_size - 1) / p.page_size; };
+  int releases = 0, takes = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kResizeThreads) {
+    const int b = b0 + tid;
+    int gone = 0, more = 0;
+    if (b < p.B) {
+      const int from = p.old_lens[b], to = p.new_lens[b];
+      if (from >= 0 && to >= 0 && from <= capacity && to <= capacity) {
+        const int a = pages_of(from), z = pages_of(to);
+        gone = max(a - z, 0);
+        more = max(z - a, 0);
+      } else if (rank == 0) {
+        record_page_error();
+      }
+    }
+    int all;
+    const int r = releases + block_scan<kResizeThreads>(gone, s_warp, &all);
+    releases += all;
+    const int t = takes + block_scan<kResizeThreads>(more, s_warp, &all);
+    takes += all;
+    if (b < p.B) {
+      s_release[b] = r;
+      s_take[b] = t;
+    }
+  }
+  if (tid == 0) {
+    s_release[p.B] = releases;
+    s_take[p.B] = takes;
+  }
+  __syncthreads();
+  // the sequence of item f: the last one whose first item is at or before it and which has any
+  auto sequence_of = [&](const int* prefix, int f) {
+    int lo = 0, hi = p.B;   // prefix[lo] <= f < prefix[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (prefix[mid] <= f)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  };
+
+  int pushed = 0;
+  if (releases > 0) {
+    // this warp's items, in order
+    const int warps = ranks * (kResizeThreads / 32), w = rank * (kResizeThreads / 32) + warp;
+    const int f0 = static_cast<int>(static_cast<int64_t>(releases) * w / warps);
+    const int f1 = static_cast<int>(static_cast<int64_t>(releases) * (w + 1) / warps);
+    auto entry = [&](int f) {
+      const int b = sequence_of(s_release, f);
+      return p.block_table + static_cast<int64_t>(b) * p.max_pages + pages_of(p.new_lens[b]) + f -
+             s_release[b];
+    };
+    for (int f = f0 + lane; f < f1; f += 32) {
+      int* const at = entry(f);
+      const int page = *at;
+      bool ok = page >= 0 && page < p.pool.num_pages;
+      if (ok && atomicSub(p.pool.refs + page, 1) <= 0) {
+        atomicAdd(p.pool.refs + page, 1);   // no table should hold it
+        ok = false;
+      }
+      if (!ok) {
+        record_page_error();
+        *at = -1;
+      }
+    }
+    cluster.sync();
+    for (int f = f0 + lane; f < f1; f += 32) {
+      const int page = *entry(f);
+      if (page >= 0 && load_l2(p.pool.refs + page) <= 0) atomicMin(p.pool.refs + page, -1 - f);
+    }
+    cluster.sync();
+    int count = 0;
+    for (int f = f0 + lane; f < f1; f += 32) {
+      const int page = *entry(f);
+      count += page >= 0 && load_l2(p.pool.refs + page) == -1 - f;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) count += __shfl_xor_sync(0xffffffffu, count, off);
+    int all;
+    int before = block_scan<kResizeThreads>(lane == 0 ? count : 0, s_warp, &all);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    if (tid == 0) s_total = all;
+    cluster.sync();
+    for (int r = 0; r < ranks; ++r) {
+      const int n = *cluster.map_shared_rank(&s_total, r);
+      pushed += n;
+      if (r < rank) before += n;
+    }
+    for (int f = f0; f < f1; f += 32) {
+      int* const at = f + lane < f1 ? entry(f + lane) : nullptr;
+      const int page = at ? *at : -1;
+      const bool mine = page >= 0 && load_l2(p.pool.refs + page) == -1 - (f + lane);
+      const unsigned all_mine = __ballot_sync(0xffffffffu, mine);
+      if (mine) {
+        const int place = have + before + __popc(all_mine & ((1u << lane) - 1));
+        if (place < p.pool.num_pages)
+          p.pool.free_pages[place] = page;
+        else
+          record_page_error();   // more free pages than the pool has
+        p.pool.refs[page] = 0;
+      }
+      if (at) *at = -1;
+      before += __popc(all_mine);
+    }
+    pushed = min(pushed, p.pool.num_pages - have);
+    cluster.sync();   // the stack is whole; no CTA leaves while another reads its count
+  }
+
+  const int stack = have + pushed;
+  for (int f = rank * kResizeThreads + tid; f < takes; f += ranks * kResizeThreads) {
+    const int b = sequence_of(s_take, f);
+    if (s_take[b + 1] > stack) continue;   // does not fit
+    p.block_table[static_cast<int64_t>(b) * p.max_pages + pages_of(p.old_lens[b]) + f - s_take[b]] =
+        take_page(p.pool, stack - 1 - f);
+  }
+  // what fits is a prefix of the takes
+  for (int b = rank * kResizeThreads + tid; b < p.B; b += ranks * kResizeThreads) {
+    const int from = p.old_lens[b], to = p.new_lens[b];
+    const bool ok = from >= 0 && to >= 0 && from <= capacity && to <= capacity;
+    const bool fits = s_take[b + 1] == s_take[b] || s_take[b + 1] <= stack;
+    p.granted[b] = ok && fits ? to : from;
+  }
+  if (ranks > 1) cluster.sync();   // every CTA has read num_free
+  if (rank == 0) {
+    // takes of the sequences that fit: the largest prefix within the stack
+    int most = 0;
+    for (int b = tid; b < p.B; b += kResizeThreads)
+      if (s_take[b + 1] <= stack) most = max(most, s_take[b + 1]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    __syncthreads();
+    if (lane == 0) s_warp[warp] = most;
+    __syncthreads();
+    if (tid < 32) {
+      most = __reduce_max_sync(0xffffffffu, s_warp[tid]);
+      if (tid == 0) *p.pool.num_free = stack - most;
+    }
+  }
+}
+
+int shift_of(int page_size) {
+  int shift = 0;
+  while (1 << shift < page_size) ++shift;
+  return shift;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_accept(const AcceptParams& p, cudaStream_t stream) {
+  const PagedCache& c = p.c;
+  AcceptArgs a;
+  a.k_pages = static_cast<uint4*>(c.k_pages);
+  a.v_pages = static_cast<uint4*>(c.v_pages);
+  a.weights = c.weights;
+  a.table = c.block_table;
+  a.seqlens = c.seqlens;
+  a.parents = p.parents;
+  a.leaf = p.leaf;
+  a.new_lens = p.new_lens;
+  a.path = p.path;
+  a.new_seqlens = p.new_seqlens;
+  a.T = p.T;
+  a.Hkv = c.Hkv;
+  a.page_shift = shift_of(c.page_size);
+  a.num_pages = c.num_pages;
+  a.max_pages = c.max_pages;
+  return launch_paged(c.d == 64 ? fa_paged_accept_kernel<64> : fa_paged_accept_kernel<128>,
+                      static_cast<int64_t>(c.B) * c.Hkv, kAcceptThreads, 0, stream, 0, a);
+}
+
+cudaError_t launch_paged_copy(const CopyParams& p, cudaStream_t stream) {
+  CopyArgs a;
+  a.k_pages = static_cast<uint4*>(p.k_pages);
+  a.v_pages = static_cast<uint4*>(p.v_pages);
+  a.weights = p.weights;
+  a.src = p.src;
+  a.dst = p.dst;
+  a.rows = p.rows;
+  a.Hkv = p.Hkv;
+  a.d = p.d;
+  a.page_size = p.page_size;
+  a.num_pages = p.num_pages;
+  const int64_t chunks = static_cast<int64_t>(p.page_size) * p.Hkv * p.d / 8;
+  a.parts = static_cast<int>((chunks + kCopyChunks - 1) / kCopyChunks);
+  return launch_paged(fa_paged_copy_kernel, static_cast<int64_t>(p.M) * 2 * a.parts, kCopyThreads,
+                      0, stream, 0, a);
+}
+
+cudaError_t launch_paged_fork(const ForkParams& p, cudaStream_t stream) {
+  cudaError_t err = launch_paged(fa_paged_fork_plan_kernel, 1, kForkThreads, 0, stream, 0, p);
+  if (err != cudaSuccess) return err;
+  const int blocks = (p.max_pages + kForkThreads - 1) / kForkThreads;
+  return launch_paged(fa_paged_fork_kernel, static_cast<int64_t>(p.C) * blocks, kForkThreads, 0,
+                      stream, 0, p, blocks);
+}
+
+cudaError_t launch_paged_resize(const ResizeParams& p, cudaStream_t stream) {
+  constexpr int kMost = 2 * (kMaxPoolBatch + 1) * 4;
+  const cudaError_t err = cudaFuncSetAttribute(
+      fa_paged_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (err != cudaSuccess) return err;
+  return launch_paged(fa_paged_resize_kernel, kResizeCluster, kResizeThreads, 2 * (p.B + 1) * 4,
+                      stream, kResizeCluster, p);
+}
+
+cudaError_t read_and_clear_pool_error(int* bits) { return read_and_clear_error(bits); }
+
+}  // namespace fa
