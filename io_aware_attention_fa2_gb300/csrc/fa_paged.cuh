@@ -116,6 +116,71 @@ cudaError_t launch_paged(void (*kernel)(Params...), int64_t grid, int block, siz
   return launch_chained(kernel, grid, block, smem, stream, cluster, args...);
 }
 
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A run of equal length for each CTA, of tiles counted over all units of a call.
+// CTAs that get a run: every one of them at least a tile, so that no part of a unit is empty.
+__device__ __forceinline__ int running(int64_t total, int ctas) {
+  return static_cast<int>(min(total, static_cast<int64_t>(ctas)));
+}
+// First tile of CTA c's run, of `total` tiles over `ctas` running CTAs: floor(total * c / ctas).
+__device__ __forceinline__ int64_t run_start(int64_t total, int c, int ctas) {
+  return total / ctas * c + total % ctas * c / ctas;
+}
+
+// 1 / sum of a row's probabilities: 0 for a row without any, NaN for a NaN.
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+// LSE in natural units from the maximum (log2 units) and the sum.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (FP16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
+}
+
+// k_pages or v_pages as a 5-D TMA map: 64 columns, head, row of the page, 64-column half, page.
+// A box is box_rows rows of one page and head, `halves` 64-column halves of them one after the other.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static inline bool encode_pages(CUtensorMap* map, void* pages, const PagedCache& c, int box_rows,
+                                int halves, bool fp16) {
+  const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(encode_tiled_entry());
+  if (!fn) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(c.Hkv) * c.d * 2;
+  const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(c.Hkv),
+                              static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.d / 64),
+                              static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(c.d) * 2, row, 128, row * c.page_size};
+  const cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(halves), 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+            pages, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Drafted tokens of sequence b: they are its last ones, tokens [base, base + count). A sequence
 // whose length is negative, beyond the table or shorter than its draft has count = -1.
 struct Draft {

@@ -57,7 +57,6 @@ namespace {
 using namespace paged;
 namespace cg = cooperative_groups;
 
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kTile = 64;                      // tokens of a tile
 constexpr int kStagesLong = 3;                 // ring of tiles
 constexpr int kShortTiles = 4;                 // tiles of a CTA of a short unit, one stage each
@@ -137,22 +136,6 @@ __device__ __forceinline__ int64_t count_tiles(const Args& a) {
   return x;
 }
 
-// CTAs that get a run: every one of them at least a tile, so that no part of a unit is empty.
-__device__ __forceinline__ int running(int64_t total, int ctas) {
-  return static_cast<int>(min(total, static_cast<int64_t>(ctas)));
-}
-// First tile of CTA c's run, of `total` tiles over `ctas` running CTAs: floor(total * c / ctas).
-__device__ __forceinline__ int64_t run_start(int64_t total, int c, int ctas) {
-  return total / ctas * c + total % ctas * c / ctas;
-}
-
-// 1 / sum of a row's probabilities: 0 for a row without any, NaN for a NaN.
-__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
-// LSE in natural units from the maximum (log2 units) and the sum.
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 // A run as its segments: consecutive tiles of one unit.
 struct Segment {
   int b, unit, tile, count;   // unit of the sequence, first tile of it, tiles
@@ -179,15 +162,6 @@ __device__ __forceinline__ Segment next_segment(const Args& a, Walk& w, Tiles& t
     ++w.b;
   }
   return s;
-}
-
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int c0, int c1, int c2, int c3, int c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
-      : "memory");
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -248,17 +222,6 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
     asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7f7f7f7fu));
   return r;
 }
-template <bool FP16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (FP16) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
 // SHORT: a cluster of CTAs has one unit, each CTA an equal share of its tiles. Otherwise: runs
 // over all units.
 template <int D, bool FP16, bool WEIGHTS, bool SHORT>
@@ -913,31 +876,6 @@ __global__ void __launch_bounds__(kFinishThreads)
     add_weights(a, (at - heads) / chunks, static_cast<int>((at - heads) % chunks));
 }
 
-// k_pages or v_pages as a 5-D TMA map: 64 columns, head, row of the page, 64-column half, page.
-// A box is box_rows rows of one page and head with all their columns, half by half.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-bool encode_pages(CUtensorMap* map, void* pages, const PagedCache& c, int box_rows, bool fp16) {
-  const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(encode_tiled_entry());
-  if (!fn) return false;
-  const cuuint64_t row = static_cast<cuuint64_t>(c.Hkv) * c.d * 2;
-  const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(c.Hkv),
-                              static_cast<cuuint64_t>(c.page_size),
-                              static_cast<cuuint64_t>(c.d / 64),
-                              static_cast<cuuint64_t>(c.num_pages)};
-  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(c.d) * 2, row, 128, row * c.page_size};
-  const cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(box_rows),
-                             static_cast<cuuint32_t>(c.d / 64), 1};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
-            pages, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // CTAs for a call: two on each SM, or one for each tile where there are fewer.
 int64_t grid_size(int B, int Hq, int Hkv, int64_t capacity) {
   const int64_t blocks = (Hq / Hkv + kRows - 1) / kRows;
@@ -1030,8 +968,8 @@ cudaError_t launch_impl(const DecodeParams& p, cudaStream_t stream) {
   a.window_left = p.window_left;
   a.scale_log2 = p.scale_log2;
   CUtensorMap tm_k, tm_v;
-  if (!encode_pages(&tm_k, c.k_pages, c, a.box_rows, FP16) ||
-      !encode_pages(&tm_v, c.v_pages, c, a.box_rows, FP16))
+  if (!encode_pages(&tm_k, c.k_pages, c, a.box_rows, D / 64, FP16) ||
+      !encode_pages(&tm_v, c.v_pages, c, a.box_rows, D / 64, FP16))
     return cudaErrorInvalidValue;
   // tiles of a unit, at most: a window's tokens span two more tiles than its length fills
   int64_t tiles = (static_cast<int64_t>(a.capacity) + kTile - 1) / kTile;
