@@ -68,10 +68,14 @@ bool decode_shape_ok(int B, int Hq, int Hkv, int page_size, int max_pages) {
   return (uint64_t)B * (uint64_t)Hq * (tokens / 1024 + 2) < (1ull << 31);
 }
 
-// Drafted tokens: up to kMaxDraft of each sequence, rows (b, t, h) within 2^31 - 1.
-bool tree_shape_ok(int B, int T, int Hq, int Hkv) {
+// Drafted tokens: up to kMaxDraft of each sequence, rows (b, t, h) within 2^31 - 1, and as many
+// tiles of 128 keys of all blocks of 128 rows (places in an order of them are ints).
+bool tree_shape_ok(int B, int T, int Hq, int Hkv, int page_size, int max_pages) {
   if (T < 1 || T > fa::kMaxDraft || Hq < Hkv || Hq % Hkv) return false;
-  return (uint64_t)B * (uint64_t)T * (uint64_t)Hq < (1ull << 31);
+  const uint64_t rows = (uint64_t)B * (uint64_t)T * (uint64_t)Hq;
+  const uint64_t blocks = ((uint64_t)T * (uint64_t)(Hq / Hkv) + 127) / 128;
+  const uint64_t tiles = ((uint64_t)max_pages * page_size + 127) / 128;
+  return rows < (1ull << 31) && (uint64_t)B * Hkv * blocks * tiles < (1ull << 31);
 }
 
 // Tables of a pool's pages: entries within 2^31 - 1, as places in an order of them are ints.
@@ -298,7 +302,7 @@ int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* bloc
 
 size_t fa_paged_tree_workspace_size(int B, int T, int Hq, int Hkv, int d, int page_size,
                                     int max_pages) {
-  if (!cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) || !tree_shape_ok(B, T, Hq, Hkv))
+  if (!cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) || !tree_shape_ok(B, T, Hq, Hkv, page_size, max_pages))
     return 0;
   return fa::paged_tree_workspace(B, T, Hq, Hkv, d, page_size, max_pages);
 }
@@ -310,7 +314,7 @@ int fa_paged_tree(const void* q, const void* k_pages, const void* v_pages, const
                   size_t workspace_bytes, fa_stream_t stream) {
   if (!q || !k_pages || !v_pages || !block_table || !seqlens || !o || !lse) return FA_ERR_NULL;
   if (!cache_shape_ok(B, Hkv, d, page_size, num_pages, max_pages) ||
-      !tree_shape_ok(B, T, Hq, Hkv))
+      !tree_shape_ok(B, T, Hq, Hkv, page_size, max_pages))
     return FA_ERR_SHAPE;
   if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_DTYPE;
   if (!scale_ok(scale)) return FA_ERR_SCALE;

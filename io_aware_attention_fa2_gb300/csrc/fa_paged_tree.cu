@@ -36,6 +36,8 @@
 // P is rounded to the type once for the product with V, a rounding of the same size as the
 // output's. fp16 ends at 2^-24, so there P is taken 2^11 times as large, and up to 2^4 more until
 // a grown maximum moves the offset: what is lost are probabilities below 2^-36 of the largest.
+#include <stddef.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -48,12 +50,15 @@ namespace {
 using namespace paged;
 
 constexpr int kTile = 128;                     // tokens of a tile, and rows of a row tile
-constexpr int kSoftmaxThreads = 256;
+constexpr int kSoftmaxThreads = 512;
 constexpr int kThreads = 128 + kSoftmaxThreads;
 constexpr int kSms = 152;                      // of a GB300; on another count only speed differs
 constexpr uint32_t kHalfBytes = kTile * 64 * 2;   // 128 rows of 64 columns
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
-constexpr int kInfoSlots = 8;                  // more than the tiles between a load and its softmax
+constexpr int kMaxStages = 6;
+// A slot is written again with the tile kInfoSlots on, for which a K stage has to be free: the
+// softmax of the tile kMaxStages + 2 before it is over by then.
+constexpr int kInfoSlots = kMaxStages + 2;
 
 // The offset of a row's exponents is its maximum less kShift, and moves when the maximum has
 // grown by more than kLag (log2 units).
@@ -61,20 +66,6 @@ template <bool FP16>
 constexpr float kShift = FP16 ? 11.f : 0.f;
 template <bool FP16>
 constexpr float kLag = FP16 ? 4.f : 8.f;
-
-template <int D, int QT>
-struct Smem {
-  static constexpr int kStages = QT == 2 && D == 128 ? 2 : 3;
-  static constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
-  static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kK = kQ + QT * kTileBytes;
-  static constexpr uint32_t kV = kK + kStages * kTileBytes;
-  static constexpr uint32_t kInfo = kV + kStages * kTileBytes;      // uint4: the tile's loaded keys
-  static constexpr uint32_t kBars = kInfo + kInfoSlots * 16;
-  static constexpr uint32_t kEnd = kBars + 32 * 8;
-  static constexpr uint32_t kDynamic = kEnd + 1024;   // slack for 1 KiB alignment
-};
-static_assert(Smem<128, 1>::kDynamic + 1300 <= 232448, "with the static shared memory");
 
 struct Args {
   const void* q;
@@ -121,69 +112,79 @@ __device__ __forceinline__ Draft draft(const Args& a, int b) {
 }
 // Tiles of all row blocks of a key head of sequence b.
 template <int ROWS>
-__device__ __forceinline__ int64_t head_tiles(const Args& a, int b) {
+__device__ __forceinline__ int head_tiles(const Args& a, int b) {
   const Draft dr = draft(a, b);
-  int64_t n = 0;
+  int n = 0;
+#pragma unroll 1
   for (int rb = 0; rb < a.blocks; ++rb) n += unit_of<ROWS>(a, dr, rb).count;
   return n;
 }
-
-// A run as its segments: consecutive tiles of one unit.
-struct Segment {
-  Draft dr;
-  Unit u;
-  int b, hk, rb, tile, count;   // first tile within the unit's, tiles
-  bool whole, empty;
-};
-struct Walk {
-  int64_t left;    // tiles of the run that are left
-  int b, hk, rb;
-  int tile;        // within the unit
-};
-template <int ROWS>
-__device__ __forceinline__ Segment next_segment(const Args& a, Walk& w) {
-  Segment s;
-  s.dr = draft(a, w.b);
-  s.u = unit_of<ROWS>(a, s.dr, w.rb);
-  s.b = w.b;
-  s.hk = w.hk;
-  s.rb = w.rb;
-  s.tile = w.tile;
-  s.count = static_cast<int>(min(static_cast<int64_t>(s.u.count - w.tile), w.left));
-  s.whole = s.count == s.u.count;
-  s.empty = s.u.i1 <= s.u.i0;
-  w.left -= s.count;
-  w.tile += s.count;
-  if (w.tile == s.u.count) {
-    w.tile = 0;
-    if (++w.rb == a.blocks) {
-      w.rb = 0;
-      if (++w.hk == a.Hkv) {
-        w.hk = 0;
-        ++w.b;
-      }
-    }
-  }
-  return s;
+// First tile of CTA c's run: `total` tiles (all within 31 bits) over `ctas` CTAs.
+__device__ __forceinline__ int first_tile(int total, int c, int ctas) {
+  return total / ctas * c + total % ctas * c / ctas;
 }
 
+// A part of a run: consecutive tiles of one unit.
+struct Segment {
+  int b, hk, base;          // sequence, key head, length of the context
+  int drafted;              // drafted tokens
+  int r0, live;             // the unit's first row, and its rows that are not padding
+  int first_key, count;     // of the segment; its tiles (0: there is no further segment)
+  int lo, hi;               // keys that some row sees are within [lo, hi)
+  int full_lo, full_hi;     // every row sees all keys of a tile within these
+  int whole;                // the segment is the unit
+  int slot;                 // of its part otherwise
+};
+
 // Barrier slots.
-constexpr int kMaxStages = 3;
+constexpr int kSegments = 4;               // segments that are known ahead
+constexpr int kConsumers = 3 + kSoftmaxThreads / 32;   // warps that read them
 enum : int {
   BAR_K_FULL = 0,                          // + stage
   BAR_K_EMPTY = BAR_K_FULL + kMaxStages,   // + stage
   BAR_V_FULL = BAR_K_EMPTY + kMaxStages,   // + stage
   BAR_V_EMPTY = BAR_V_FULL + kMaxStages,   // + stage
-  BAR_INFO = BAR_V_EMPTY + kMaxStages,     // + slot: the tile's loaded keys are in kInfo
-  BAR_S_FULL = BAR_INFO + kInfoSlots,      // + group: S computed
-  BAR_P_FULL = BAR_S_FULL + 2,             // + group: P in TMEM, O rescaled, V cleaned (128)
-  BAR_O_DONE = BAR_P_FULL + 2,             // + group: P V computed
-  BAR_Q_FULL = BAR_O_DONE + 2,             // Q of the segment in shared memory (256)
-  BAR_O_FREE = BAR_Q_FULL + 1,             // O of the segment out of TMEM (256)
+  BAR_INFO = BAR_V_EMPTY + kMaxStages,     // + slot: the tile's loaded keys and masks are known
+  BAR_SEG_FULL = BAR_INFO + kInfoSlots,    // + slot: a segment is there
+  BAR_SEG_EMPTY = BAR_SEG_FULL + kSegments,   // + slot: and was read by all
+  BAR_S_FULL = BAR_SEG_EMPTY + kSegments,  // + stream: S computed
+  BAR_P_FULL = BAR_S_FULL + 2,             // + stream: P in TMEM, O rescaled, V cleaned (256)
+  BAR_O_DONE = BAR_P_FULL + 2,             // + stream: the segment's last P V computed
+  BAR_Q_FULL = BAR_O_DONE + 2,             // Q of the segment in shared memory (512)
+  BAR_O_FREE = BAR_Q_FULL + 1,             // O of the segment out of TMEM (512)
   BAR_MMA_DONE = BAR_O_FREE + 1,
   BAR_COUNT = BAR_MMA_DONE + 1
 };
-static_assert(BAR_COUNT <= 32, "barrier slots");
+
+// What is in shared memory besides Q and the rings.
+struct Misc {
+  uint64_t bars[BAR_COUNT];
+  uint4 loaded[kInfoSlots];     // bits of a tile's keys that exist and were loaded
+  int masked[kInfoSlots];       // some row does not see all of a tile's keys
+  float red[2][2][kTile];       // [stream][half][row]: exchange of maxima and sums
+  Segment seg[kSegments];
+  uint32_t tmem_base;
+  int abort;
+  int go;                       // the softmax warps have another segment
+  int not_finite;               // segment (+ 1) in whose masked tiles V had such values
+};
+
+template <int D, int QT>
+struct Smem {
+  static constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
+  static constexpr int kStages = D == 64 ? 6 : QT == 1 ? 3 : 2;
+  static constexpr uint32_t kQ = 0;
+  // Q's place is also that of 32 rows of kChunk columns of O (fp32) for each softmax warp
+  static constexpr int kChunk = QT == 2 && D == 128 ? 32 : 16;
+  static constexpr uint32_t kStageBytes = kSoftmaxThreads * kChunk * 4;
+  static constexpr uint32_t kK = kQ + (QT * kTileBytes > kStageBytes ? QT * kTileBytes : kStageBytes);
+  static constexpr uint32_t kV = kK + kStages * kTileBytes;
+  static constexpr uint32_t kMisc = kV + kStages * kTileBytes;
+  static constexpr uint32_t kDynamic = kMisc + sizeof(Misc);
+};
+static_assert(Smem<128, 1>::kDynamic <= 232448 && Smem<128, 2>::kDynamic <= 232448 &&
+                  Smem<64, 1>::kDynamic <= 232448 && Smem<64, 2>::kDynamic <= 232448,
+              "shared memory");
 
 // Bits [lo, hi) of 32, for any lo and hi.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
@@ -201,21 +202,25 @@ __device__ __forceinline__ int parent_of(const Args& a, int b, int i) {
   return -1;
 }
 
-// A row's token: what it sees.
-struct Row {
-  int b, i;        // i < 0: no token
-  int lo;          // its first key of the context (window)
-};
-// Keys k0 .. k0 + 127 that the row sees, as bits.
-__device__ __forceinline__ void visible_bits(const Args& a, const Row& r, int base, int k0,
-                                             uint32_t (&vis)[4]) {
-  const int hi = a.parents ? base : base + r.i + 1;   // a chain's keys are a range, too
+// Keys k0 .. k0 + 127 that drafted token i of sequence b sees, as bits, of those in `loaded`.
+__device__ __noinline__ uint4 visible_bits(const Args& a, int b, int base, int i, int k0,
+                                           uint4 loaded) {
+  int lo = 0;
+  if (a.window_left >= 0) {
+    int depth = i;
+    if (a.parents) {
+      depth = 0;
+      for (int at = parent_of(a, b, i); at >= 0; at = parent_of(a, b, at)) ++depth;
+    }
+    lo = max(0, base + depth - a.window_left);
+  }
+  const int hi = a.parents ? base : base + i + 1;   // a chain's keys are a range, too
+  uint32_t vis[4];
 #pragma unroll
-  for (int w = 0; w < 4; ++w)
-    vis[w] = r.i < 0 ? 0u : bit_range(r.lo - k0 - 32 * w, hi - k0 - 32 * w);
-  if (a.parents && r.i >= 0 && k0 + kTile > base) {
+  for (int w = 0; w < 4; ++w) vis[w] = bit_range(lo - k0 - 32 * w, hi - k0 - 32 * w);
+  if (a.parents && k0 + kTile > base) {
     int steps = 0;
-    for (int at = r.i; at >= 0 && base + at >= k0; at = parent_of(a, r.b, at), ++steps) {
+    for (int at = i; at >= 0 && base + at >= k0; at = parent_of(a, b, at), ++steps) {
       if (a.window_left >= 0 && steps > a.window_left) break;
       const int t = base + at - k0;
 #pragma unroll
@@ -223,6 +228,7 @@ __device__ __forceinline__ void visible_bits(const Args& a, const Row& r, int ba
         if (t >> 5 == w) vis[w] |= 1u << (t & 31);
     }
   }
+  return make_uint4(vis[0] & loaded.x, vis[1] & loaded.y, vis[2] & loaded.z, vis[3] & loaded.w);
 }
 
 // Halves of v that are infinite or NaN, as ones.
@@ -240,33 +246,59 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
 }
 
+// V of a masked tile, by the 256 threads of a stream: zeros for the rows of no token, and for what
+// is not finite (then true).
+template <int D, bool FP16>
+__device__ __noinline__ bool clean_values(uint8_t* tile, uint4 loaded, int t) {
+  constexpr int kChunks = D / 8;
+  bool found = false;
+#pragma unroll 4
+  for (int u = t; u < kTile * kChunks; u += 256) {
+    const int r = u / kChunks, c = u % kChunks;
+    const uint32_t bits = r < 64 ? (r < 32 ? loaded.x : loaded.y) : (r < 96 ? loaded.z : loaded.w);
+    uint4* const at = reinterpret_cast<uint4*>(tile + (c / 8) * kHalfBytes + r * 128 +
+                                               (((c % 8) ^ (r & 7)) << 4));
+    if (!(bits >> (r % 32) & 1)) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 v = *at;
+    const uint32_t x = not_finite2<FP16>(v.x), y = not_finite2<FP16>(v.y),
+                   z = not_finite2<FP16>(v.z), w = not_finite2<FP16>(v.w);
+    if (x | y | z | w) {
+      found = true;
+      *at = make_uint4(v.x & ~x, v.y & ~y, v.z & ~z, v.w & ~w);
+    }
+  }
+  return found;
+}
+
 // The rare end of a segment in whose masked tiles V was not finite: those values, which the
-// products have taken as 0, added to the thread's row (fp32 part or output, columns [c0, c0 + cols))
-// for the keys that it sees.
+// products have taken as 0, added to the row of token i (fp32 part or output, columns
+// [c0, c0 + cols)) for the keys that it sees.
 template <bool FP16>
-__device__ __noinline__ void add_not_finite(const Args& a, const Row& rw, int base, int hk, int d,
-                                            int first_key, int tiles, int full_lo, int full_hi,
-                                            int c0, int cols, float* part, uint16_t* out) {
-  const int* const tab = a.table + static_cast<int64_t>(rw.b) * a.max_pages;
-  for (int j = 0; j < tiles; ++j) {
-    const int k0 = first_key + j * kTile;
-    bool masked = k0 < full_lo || k0 + kTile > full_hi;
+__device__ __noinline__ void add_not_finite(const Args& a, const Segment& sg, int i, int d, int c0,
+                                            int cols, float* part, uint16_t* out) {
+  const int* const tab = a.table + static_cast<int64_t>(sg.b) * a.max_pages;
+  const uint4 all = make_uint4(~0u, ~0u, ~0u, ~0u);
+  for (int j = 0; j < sg.count; ++j) {
+    const int k0 = sg.first_key + j * kTile;
+    bool masked = k0 < sg.full_lo || k0 + kTile > sg.full_hi;
     for (int t = k0; t < k0 + kTile && !masked; t += a.box_rows) {   // all within [0, full_hi)
       const int page = tab[t >> a.page_shift];
       masked = page < 0 || page >= a.num_pages;
     }
     if (!masked) continue;
-    uint32_t vis[4];
-    visible_bits(a, rw, base, k0, vis);
+    const uint4 vis = visible_bits(a, sg.b, sg.base, i, k0, all);
     for (int t = 0; t < kTile; ++t) {
-      const uint32_t word = t < 64 ? (t < 32 ? vis[0] : vis[1]) : (t < 96 ? vis[2] : vis[3]);
+      const uint32_t word = t < 64 ? (t < 32 ? vis.x : vis.y) : (t < 96 ? vis.z : vis.w);
       if (!(word >> (t % 32) & 1)) continue;
       const int page = tab[(k0 + t) >> a.page_shift];
       if (page < 0 || page >= a.num_pages) continue;
       const int64_t at = (static_cast<int64_t>(page) << a.page_shift) +
                          ((k0 + t) & ((1 << a.page_shift) - 1));
       const uint32_t* const src = reinterpret_cast<const uint32_t*>(
-          static_cast<const uint16_t*>(a.v_pages) + (at * a.Hkv + hk) * d + c0);
+          static_cast<const uint16_t*>(a.v_pages) + (at * a.Hkv + sg.hk) * d + c0);
       for (int c = 0; c < cols; c += 2) {
         const uint32_t w = src[c / 2];
         if (!not_finite2<FP16>(w)) continue;
@@ -293,22 +325,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Smem<D, QT>;
   constexpr int kStages = L::kStages, kRows = QT * kTile;
   constexpr uint32_t kTmemO = 2 * kTile, kTmemCols = 512;   // S_A, S_B, O_A, O_B
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint32_t tmem_base_slot;
-  __shared__ int abort_flag, s_not_finite;    // segment (+ 1) whose masked tiles had such values
-  __shared__ float2 s_ml[kTile];              // one row tile: a group's offsets and sums
-  __shared__ int64_t s_left, s_start, s_total;
-  __shared__ int s_at[4];
+  // (there is no room for a base that is not aligned)
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
-  uint8_t* const gen = smem_raw + (base - ptx::smem_addr(smem_raw));
-  auto bar = [&](int i) { return base + L::kBars + 8u * static_cast<uint32_t>(i); };
-  uint4* const info = reinterpret_cast<uint4*>(gen + L::kInfo);
+  if (base != ptx::smem_addr(smem_raw)) {
+    atomicOr(&g_error, kTimeoutBit);
+    return;
+  }
+  Misc& ms = *reinterpret_cast<Misc*>(smem_raw + L::kMisc);
+  const uint32_t bars = base + L::kMisc + static_cast<uint32_t>(offsetof(Misc, bars));
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    abort_flag = 0;
-    s_not_finite = 0;
+    ms.abort = 0;
+    ms.not_finite = 0;
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(bar(BAR_K_FULL + s), 1);
       ptx::mbar_init(bar(BAR_K_EMPTY + s), 1);
@@ -316,9 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(BAR_V_EMPTY + s), 1);
     }
     for (int s = 0; s < kInfoSlots; ++s) ptx::mbar_init(bar(BAR_INFO + s), 1);
+    for (int s = 0; s < kSegments; ++s) {
+      ptx::mbar_init(bar(BAR_SEG_FULL + s), 1);
+      ptx::mbar_init(bar(BAR_SEG_EMPTY + s), kConsumers);
+    }
     for (int x = 0; x < 2; ++x) {
       ptx::mbar_init(bar(BAR_S_FULL + x), 1);
-      ptx::mbar_init(bar(BAR_P_FULL + x), 128);
+      ptx::mbar_init(bar(BAR_P_FULL + x), kSoftmaxThreads / 2);
       ptx::mbar_init(bar(BAR_O_DONE + x), 1);
     }
     ptx::mbar_init(bar(BAR_Q_FULL), kSoftmaxThreads);
@@ -329,88 +365,173 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_tensormap(&tm_v);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_addr(&tmem_base_slot), kTmemCols);
+    ptx::tmem_alloc(ptx::smem_addr(&ms.tmem_base), kTmemCols);
     ptx::tmem_relinquish();
-  }
-  wait_prerequisites();
-  launch_dependents();
-  // where this CTA's run starts
-  if (warp == 2) {
-    int64_t total = 0;
-    for (int b = lane; b < a.B; b += 32) total += head_tiles<kRows>(a, b);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    total *= a.Hkv;
-    const int ctas = running(total, gridDim.x);
-    const int64_t start = run_start(total, cta, ctas);
-    // the sequence that holds tile `start`
-    int64_t before = 0, at = start;
-    int seq = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane;
-      const int64_t n = b < a.B ? head_tiles<kRows>(a, b) * a.Hkv : 0;
-      int64_t inc = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += y;
-      }
-      const int64_t first = before + inc - n;
-      const unsigned here = __ballot_sync(0xffffffffu, n > 0 && first <= start &&
-                                                           start < before + inc);
-      if (here) {
-        const int src = __ffs(here) - 1;
-        seq = b0 + src;
-        at = start - __shfl_sync(0xffffffffu, first, src);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) {
-      const int64_t per_head = head_tiles<kRows>(a, seq);
-      const Draft dr = draft(a, seq);
-      const int hk = static_cast<int>(at / per_head);
-      at %= per_head;
-      int rb = 0;
-      for (; rb < a.blocks - 1; ++rb) {
-        const int n = unit_of<kRows>(a, dr, rb).count;
-        if (at < n) break;
-        at -= n;
-      }
-      s_at[0] = seq;
-      s_at[1] = hk;
-      s_at[2] = rb;
-      s_at[3] = static_cast<int>(at);
-      s_left = cta < ctas ? run_start(total, cta + 1, ctas) - start : 0;
-      s_start = start;
-      s_total = total;
-    }
   }
   ptx::tc_fence_before_sync();
   __syncthreads();
   ptx::tc_fence_after_sync();
-  const uint32_t tmem = tmem_base_slot;
-  Walk walk{s_left, s_at[0], s_at[1], s_at[2], s_at[3]};
-  volatile int* abort_p = &abort_flag;
+  wait_prerequisites();
+  launch_dependents();
+  const uint32_t tmem = ms.tmem_base;
+  volatile int* abort_p = &ms.abort;
   auto give_up = [&] {
     *abort_p = 1;
     atomicOr(&g_error, kTimeoutBit);
   };
+  // Segment s of the run for the warps that read them; false when a wait has run out.
+  auto segment = [&](int s) {
+    return ptx::wait_bounded(bar(BAR_SEG_FULL + s % kSegments), (s / kSegments) & 1, abort_p,
+                             kWaitLimitNs);
+  };
+  auto segment_read = [&](int s) { ptx::mbar_arrive(bar(BAR_SEG_EMPTY + s % kSegments)); };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ producer
+  if (warp == 3) {
+    // ------------------------------------------------------------------ scheduler
+    // Where this CTA's run starts: tiles of the sequences summed up to it. The first 32 sequences'
+    // stay in registers.
+    const int mine = lane < a.B ? head_tiles<kRows>(a, lane) : 0;
+    int total = mine;
+#pragma unroll 1
+    for (int b = 32 + lane; b < a.B; b += 32) total += head_tiles<kRows>(a, b);
+    total = __reduce_add_sync(0xffffffffu, total) * a.Hkv;
+    const int ctas = min(total, static_cast<int>(gridDim.x));   // each gets at least one tile
+    const int start = first_tile(total, cta, ctas);
+    int left = cta < ctas ? first_tile(total, cta + 1, ctas) - start : 0;
+    int b = 0, at = 0, per_head = 1;
+#pragma unroll 1
+    for (int b0 = 0, before = 0; b0 < a.B; b0 += 32) {
+      const int head = b0 == 0 ? mine : b0 + lane < a.B ? head_tiles<kRows>(a, b0 + lane) : 0;
+      int inc = head * a.Hkv;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += y;
+      }
+      const unsigned here = __ballot_sync(0xffffffffu, start < before + inc);
+      if (here) {   // the first sequence that ends behind it
+        const int src = __ffs(here) - 1;
+        b = b0 + src;
+        per_head = __shfl_sync(0xffffffffu, head, src);
+        at = start - before - __shfl_sync(0xffffffffu, inc, src) + per_head * a.Hkv;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    int hk = at / per_head, rb = 0, segs = 0, taken = 0;
+    int tile = at % per_head;   // within the unit, once rb is known
+    bool ok = true, found = false;
+#pragma unroll 1
+    while (left > 0) {
+      const Draft dr = draft(a, b);
+      const Unit u = unit_of<kRows>(a, dr, rb);
+      if (!found && tile >= u.count && rb + 1 < a.blocks) {
+        tile -= u.count;
+        ++rb;
+        continue;
+      }
+      found = true;
+      const int count = min(u.count - tile, left), r0 = rb * kRows;
+      const int rows = min(kRows, a.T * a.G - r0), live = min(rows, dr.count * a.G - r0);
+      const int slot = 2 * cta + (taken > 0);
+      if (dr.count < 0 && lane == 0) record_page_error();
+      if (u.i1 > u.i0) {
+        const int s = segs % kSegments;
+        if (!ptx::wait_bounded_warp(bar(BAR_SEG_EMPTY + s), ((segs / kSegments) & 1) ^ 1, abort_p,
+                                    kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          Segment& g = ms.seg[s];
+          g.b = b;
+          g.hk = hk;
+          g.base = dr.base;
+          g.drafted = dr.count;
+          g.r0 = r0;
+          g.live = live;
+          g.first_key = (u.first + tile) * kTile;
+          g.count = count;
+          g.lo = a.window_left < 0 ? 0 : max(0, dr.base - a.window_left);
+          g.hi = dr.base + u.i1;
+          g.full_lo = a.window_left < 0 ? 0 : dr.base + u.i1 - 1 - a.window_left;
+          g.full_hi = a.parents ? dr.base : dr.base + u.i0 + 1;
+          g.whole = count == u.count;
+          g.slot = slot;
+          ptx::mbar_arrive(bar(BAR_SEG_FULL + s));
+        }
+        ++segs;
+      }
+      if (tile == 0) {
+        if (lane == 0) {
+          // This run holds the unit's first tile; its last is in the last run that starts before
+          // the unit's end.
+          const int end = start + taken + u.count;
+          int last = cta;
+          if (count < u.count) {
+            last = static_cast<int>(static_cast<float>(end) / static_cast<float>(total) * ctas);
+            last = min(max(last, cta), ctas - 1);
+            while (first_tile(total, last, ctas) >= end) --last;
+            while (last + 1 < ctas && first_tile(total, last + 1, ctas) < end) ++last;
+          }
+          a.units[(static_cast<int64_t>(b) * a.Hkv + hk) * a.blocks + rb] =
+              make_int2(slot, count == u.count ? 0 : last - cta + 1);
+        }
+        // the padding's rows
+        constexpr int kChunks = D / 8;
+#pragma unroll 1
+        for (int w = max(live, 0) * kChunks + lane; w < rows * kChunks; w += 32) {
+          const int r = r0 + w / kChunks, token = r / a.G, head = hk * a.G + r % a.G;
+          reinterpret_cast<uint4*>(
+              static_cast<uint16_t*>(a.o) +
+              ((static_cast<int64_t>(b) * a.T + token) * a.Hq + head) * D)[w % kChunks] =
+              make_uint4(0, 0, 0, 0);
+          if (w % kChunks == 0)
+            a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = -INFINITY;
+        }
+      }
+      left -= count;
+      taken += count;
+      tile += count;
+      if (tile == u.count) {
+        tile = 0;
+        if (++rb == a.blocks) {
+          rb = 0;
+          if (++hk == a.Hkv) {
+            hk = 0;
+            ++b;
+          }
+        }
+      }
+    }
+    if (ok) {   // the end
+      const int s = segs % kSegments;
+      ok = ptx::wait_bounded_warp(bar(BAR_SEG_EMPTY + s), ((segs / kSegments) & 1) ^ 1, abort_p,
+                                  kWaitLimitNs);
+      if (ok && lane == 0) {
+        ms.seg[s].count = 0;
+        ptx::mbar_arrive(bar(BAR_SEG_FULL + s));
+      }
+    }
+    if (!ok && lane == 0) give_up();
+  } else if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------------ producers of K and V
+    const bool is_v = warp == 2;
+    const CUtensorMap* const map = is_v ? &tm_v : &tm_k;
+    const uint32_t ring = base + (is_v ? L::kV : L::kK);
+    const int full = is_v ? BAR_V_FULL : BAR_K_FULL, empty = is_v ? BAR_V_EMPTY : BAR_K_EMPTY;
     const int br = a.box_rows, boxes = kTile / br;
     const uint32_t box_bytes = static_cast<uint32_t>(br) * 128;   // 64 columns of its rows
-    int n = 0, k_issued = 0, v_issued = 0;   // tiles so far: tile n goes through stage n % kStages
+    int n = 0;   // tiles so far: tile n goes through stage n % kStages
     bool ok = true;
-    while (ok && walk.left > 0) {
-      const Segment sg = next_segment<kRows>(a, walk);
-      if (sg.dr.count < 0 && lane == 0) record_page_error();
-      if (sg.empty) continue;
-      const int row0 = (sg.u.first + sg.tile) * kTile;   // first token of the segment
-      const int lo = a.window_left < 0 ? 0 : max(0, sg.dr.base - a.window_left);
-      const int hi = sg.dr.base + sg.u.i1;
-      const int total_boxes = sg.count * boxes;
+#pragma unroll 1
+    for (int segs = 0; ok; ++segs) {
+      ok = __all_sync(0xffffffffu, segment(segs));
+      const Segment& sg = ms.seg[segs % kSegments];
+      const int count = ok ? sg.count : 0;
+      if (count == 0) break;
+      const int row0 = sg.first_key, hk = sg.hk, lo = sg.lo, hi = sg.hi;
+      const int total_boxes = count * boxes;
       const int* tab = a.table + static_cast<int64_t>(sg.b) * a.max_pages;
       // Box j holds tokens row0 + j * br ..; lane x keeps the table entries of boxes x, 32 + x,
       // ... one batch of 32 ahead of the loads.
@@ -420,64 +541,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto entry = [&](int j) { return needed(j) ? tab[(row0 + j * br) >> a.page_shift] : -1; };
       int cur = entry(lane), nxt = entry(32 + lane);
-      for (int i = 0; i < sg.count; ++i, ++n) {
+#pragma unroll 1
+      for (int i = 0; i < count; ++i, ++n) {
         const int j0 = i * boxes;
         if (i > 0 && j0 % 32 == 0) {
           cur = nxt;
           nxt = entry(j0 + 32 + lane);
         }
         const int s = n % kStages;
-        const uint32_t ph = (n / kStages) & 1;
-        if (!ptx::wait_bounded_warp(bar(BAR_K_EMPTY + s), ph ^ 1, abort_p, kWaitLimitNs)) {
-          ok = false;
-          break;
-        }
         // lane x < boxes loads box x of this tile
         const int page = __shfl_sync(0xffffffffu, cur, (j0 + lane) % 32);
         const bool need = lane < boxes && needed(j0 + lane);
         const bool load = need && page >= 0 && page < a.num_pages;
-        if (need && !load) record_page_error();
         const int r = row0 + (j0 + lane) * br;   // first token of this lane's box
         const unsigned loads = __ballot_sync(0xffffffffu, load);
-        const int end = load ? lane * br + min(hi - r, br) : 0;
-        uint32_t m[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          m[w] = __reduce_or_sync(0xffffffffu,
-                                  load ? bit_range(lane * br - 32 * w, end - 32 * w) : 0u);
-        const uint32_t bytes = (D / 64) * box_bytes * __popc(loads);
-        if (lane == 0) {
-          info[n % kInfoSlots] = make_uint4(m[0], m[1], m[2], m[3]);
-          ptx::mbar_arrive(bar(BAR_INFO + n % kInfoSlots));
-          ptx::mbar_arrive_expect_tx(bar(BAR_K_FULL + s), bytes);
-        }
-        __syncwarp();
-        const uint32_t dst = base + s * L::kTileBytes + lane * box_bytes;
-        const int row = r & ((1 << a.page_shift) - 1);
-        if (load)
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_5d(dst + L::kK + c * kHalfBytes, &tm_k, bar(BAR_K_FULL + s), 0, sg.hk, row, c,
-                        page);
-        k_issued = n + 1;
-        if (!ptx::wait_bounded_warp(bar(BAR_V_EMPTY + s), ph ^ 1, abort_p, kWaitLimitNs)) {
+        if (!ptx::wait_bounded_warp(bar(empty + s), ((n / kStages) & 1) ^ 1, abort_p,
+                                    kWaitLimitNs)) {
           ok = false;
           break;
         }
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(BAR_V_FULL + s), bytes);
+        if (lane == 0)
+          ptx::mbar_arrive_expect_tx(bar(full + s), (D / 64) * box_bytes * __popc(loads));
         __syncwarp();
+        const uint32_t dst = ring + s * L::kTileBytes + lane * box_bytes;
         if (load)
           for (int c = 0; c < D / 64; ++c)
-            tma_load_5d(dst + L::kV + c * kHalfBytes, &tm_v, bar(BAR_V_FULL + s), 0, sg.hk, row, c,
-                        page);
-        v_issued = n + 1;
+            tma_load_5d(dst + c * kHalfBytes, map, bar(full + s), 0, hk,
+                        r & ((1 << a.page_shift) - 1), c, page);
+        __syncwarp();
+        if (!is_v) {
+          // what the softmax has to know of the tile
+          if (need && !load) record_page_error();
+          const int end = load ? lane * br + min(hi - r, br) : 0;
+          uint32_t m[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            m[w] = __reduce_or_sync(0xffffffffu,
+                                    load ? bit_range(lane * br - 32 * w, end - 32 * w) : 0u);
+          if (lane == 0) {
+            const int k0 = row0 + i * kTile;
+            ms.loaded[n % kInfoSlots] = make_uint4(m[0], m[1], m[2], m[3]);
+            ms.masked[n % kInfoSlots] = (m[0] & m[1] & m[2] & m[3]) != 0xffffffffu ||
+                                        k0 < sg.full_lo || k0 + kTile > sg.full_hi;
+            ptx::mbar_arrive(bar(BAR_INFO + n % kInfoSlots));
+          }
+        }
       }
+      __syncwarp();
+      if (ok && lane == 0) segment_read(segs);
     }
     if (!ok && lane == 0) give_up();
     // Leave no copy in flight (on the normal path these phases completed long ago).
-    for (int x = max(0, k_issued - kStages); x < k_issued; ++x)
-      ptx::wait_bounded(bar(BAR_K_FULL + x % kStages), (x / kStages) & 1, abort_p, kWaitLimitNs);
-    for (int x = max(0, v_issued - kStages); x < v_issued; ++x)
-      ptx::wait_bounded(bar(BAR_V_FULL + x % kStages), (x / kStages) & 1, abort_p, kWaitLimitNs);
+    for (int x = max(0, n - kStages); x < n; ++x)
+      ptx::wait_bounded(bar(full + x % kStages), (x / kStages) & 1, abort_p, kWaitLimitNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
@@ -502,72 +618,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mma_commit(bar(BAR_S_FULL + x));
       };
-      // O_x (+)= P_x V_n, P_x from TMEM
-      auto issue_pv = [&](int x, int n, bool first) {
+      // O_x (+)= P_x V_n, P_x from TMEM: keys 0 .. 63 in the first 32 columns of S_x, the others in
+      // those from 64 on
+      auto issue_pv = [&](int x, int n, bool first, bool last) {
         ptx::tc_fence_after_sync();
         const ptx::SmemDesc v_desc = ptx::smem_desc_sw128_split(
             base + L::kV + (n % kStages) * L::kTileBytes, kHalfBytes, 1024);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          ptx::mma_f16_ts(tmem + kTmemO + x * D, tmem + x * kTile + kk * 8,
+          ptx::mma_f16_ts(tmem + kTmemO + x * D, tmem + x * kTile + (kk / 4) * 64 + (kk % 4) * 8,
                           v_desc.at(kk * 16 * 128), idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        ptx::mma_commit(bar(BAR_O_DONE + x));
+        if (last) ptx::mma_commit(bar(BAR_O_DONE + x));
       };
-      int n0 = 0, segs = 0, done[2] = {0, 0};   // tiles, segments, and tiles of each group so far
+      int n0 = 0, done[2] = {0, 0};   // tiles, and tiles of each stream so far
       bool ok = true;
-      while (ok && walk.left > 0) {
-        const Segment sg = next_segment<kRows>(a, walk);
-        if (sg.empty) continue;
-        const int count = sg.count;
-        const bool b_any = QT == 1 || (sg.dr.count * a.G - sg.rb * kRows) > kTile;
-        ok = wait(BAR_Q_FULL, segs) && wait_k(n0);
-        if (!ok) break;
-        issue_s(0, n0);
-        if constexpr (QT == 2) {
-          if (b_any) issue_s(1, n0);
-          ptx::mma_commit(bar(BAR_K_EMPTY + n0 % kStages));
-        } else {
-          ptx::mma_commit(bar(BAR_K_EMPTY + n0 % kStages));
-          if (count > 1) {
-            if (!wait_k(n0 + 1)) { ok = false; break; }
-            issue_s(1, n0 + 1);
-            ptx::mma_commit(bar(BAR_K_EMPTY + (n0 + 1) % kStages));
-          }
-        }
-        for (int j = 0; j < count; ++j) {
+#pragma unroll 1
+      for (int segs = 0; ok; ++segs) {
+        ok = segment(segs);
+        const Segment& sg = ms.seg[segs % kSegments];
+        const int count = ok ? sg.count : 0;
+        if (count == 0) break;
+        const bool b_any = QT == 1 || sg.live > kTile;
+        segment_read(segs);
+        ok = wait(BAR_Q_FULL, segs);
+        // S of the first tile (one row tile: of the first two), then P V of every tile and S of
+        // the stream's next one
+#pragma unroll 1
+        for (int j = QT == 2 ? -1 : -2; ok && j < count; ++j) {
           const int n = n0 + j;
-          if (!wait_v(n)) { ok = false; break; }
-          // O of the segment before has to be out of TMEM
-          if (j == 0 && segs > 0 && !wait(BAR_O_FREE, segs - 1)) { ok = false; break; }
+          const int next = QT == 2 ? j + 1 : j + 2;   // tile of the S
+          const bool s_next = next < count;
+          if (j >= 0) {
+            if (!wait_v(n)) { ok = false; break; }
+            // O of the segment before has to be out of TMEM
+            if (j == 0 && segs > 0 && !wait(BAR_O_FREE, segs - 1)) { ok = false; break; }
+          }
           if constexpr (QT == 2) {
-            const bool next = j + 1 < count;
-            if (!wait(BAR_P_FULL + 0, done[0]++)) { ok = false; break; }
-            issue_pv(0, n, j == 0);
-            if (next && !wait_k(n + 1)) { ok = false; break; }
-            if (next) issue_s(0, n + 1);
-            if (b_any) {
-              if (!wait(BAR_P_FULL + 1, done[1]++)) { ok = false; break; }
-              issue_pv(1, n, j == 0);
+            if (j >= 0) {
+              if (!wait(BAR_P_FULL + 0, done[0]++)) { ok = false; break; }
+              issue_pv(0, n, j == 0, !s_next);
             }
-            ptx::mma_commit(bar(BAR_V_EMPTY + n % kStages));
-            if (next) {
-              if (b_any) issue_s(1, n + 1);
-              ptx::mma_commit(bar(BAR_K_EMPTY + (n + 1) % kStages));
+            if (s_next) {
+              if (!wait_k(n0 + next)) { ok = false; break; }
+              issue_s(0, n0 + next);
+            }
+            if (j >= 0) {
+              if (b_any) {
+                if (!wait(BAR_P_FULL + 1, done[1]++)) { ok = false; break; }
+                issue_pv(1, n, j == 0, !s_next);
+              }
+              ptx::mma_commit(bar(BAR_V_EMPTY + n % kStages));
+            }
+            if (s_next) {
+              if (b_any) issue_s(1, n0 + next);
+              ptx::mma_commit(bar(BAR_K_EMPTY + (n0 + next) % kStages));
             }
           } else {
             const int x = j & 1;
-            if (!wait(BAR_P_FULL + x, done[x]++)) { ok = false; break; }
-            issue_pv(x, n, j < 2);
-            ptx::mma_commit(bar(BAR_V_EMPTY + n % kStages));
-            if (j + 2 < count) {
-              if (!wait_k(n + 2)) { ok = false; break; }
-              issue_s(x, n + 2);
-              ptx::mma_commit(bar(BAR_K_EMPTY + (n + 2) % kStages));
+            if (j >= 0) {
+              if (!wait(BAR_P_FULL + x, done[x]++)) { ok = false; break; }
+              issue_pv(x, n, j < 2, !s_next);
+              ptx::mma_commit(bar(BAR_V_EMPTY + n % kStages));
+            }
+            if (s_next) {
+              if (!wait_k(n0 + next)) { ok = false; break; }
+              issue_s(x, n0 + next);
+              ptx::mma_commit(bar(BAR_K_EMPTY + (n0 + next) % kStages));
             }
           }
         }
         n0 += count;
-        ++segs;
       }
       if (!ok) give_up();
       // Every MMA this thread issued has completed before TMEM can be released.
@@ -575,19 +695,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(BAR_MMA_DONE, 0);
     }
     __syncwarp();
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------------ softmax groups
-    const int x = (warp - 4) / 4;                  // group: 0 = A, 1 = B
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int x = (warp - 4) / 8;                  // stream: 0 = A, 1 = B
+    const int half = (warp - 4) / 4 % 2;           // of the tile's keys, and of O's columns
     const int quarter = warp & 3;                  // TMEM lanes [32q, 32q+32)
     const int row = quarter * 32 + lane;           // row within the row tile
-    const int tid = threadIdx.x - 128, gtid = tid % 128;   // within the groups, within the group
+    const int my = (QT == 2 ? x * kTile : 0) + row;   // of the unit
+    const int tid = threadIdx.x - 128;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_off + x * kTile;
+    const uint32_t tS = tmem + lane_off + x * kTile + half * 64;   // this thread's keys of S, then P
     const uint32_t tO = tmem + lane_off + kTmemO;  // O_A; O_B is D columns on
-    const bool scale_pos = a.scale_log2 > 0.f;
-    const float scale = a.scale_log2;
-    int n0 = 0, segs = 0, done = 0;   // tiles, segments with tiles, and this group's tiles so far
-    int64_t before = 0;               // tiles of the run before the segment, empty units' among them
+    // Q takes the scale's sign, and a scale of 0: the exponents' factor is positive
+    const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+    int n0 = 0;               // tiles so far
+    int done = 0, ends = 0;   // this stream's tiles and segments with tiles
     bool ok = true;
     // after a wait has run out the loop goes on without data, so that every warp reaches the
     // barriers below
@@ -598,131 +720,114 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return ok;
     };
-    while (walk.left > 0) {
-      const Segment sg = next_segment<kRows>(a, walk);
-      const int r0 = sg.rb * kRows;                              // first row of the unit
-      const int rows = min(kRows, a.T * a.G - r0);               // padding's rows among them
-      const int live = min(rows, sg.dr.count * a.G - r0);        // and without them
-      const int my = (QT == 2 ? x * kTile : 0) + row;            // this thread's row of the unit
-      const int token = (r0 + my) / a.G, head = sg.hk * a.G + (r0 + my) % a.G;
-      const int64_t out_row = (static_cast<int64_t>(sg.b) * a.T + token) * a.Hq + head;
-      float* const lse = a.lse + (static_cast<int64_t>(sg.b) * a.Hq + head) * a.T + token;
-      const int64_t slot = 2ll * cta + (before > 0);
-      if (sg.tile == 0 && tid == 0) {
-        // this run holds the unit's first tile; its last is in the last run that starts before
-        // the unit's end: the largest c with floor(total * c / ctas) < end
-        const int ctas = running(s_total, gridDim.x);
-        const int64_t end = s_start + before + sg.u.count;
-        const int last = static_cast<int>((end * ctas - 1) / s_total);
-        a.units[(static_cast<int64_t>(sg.b) * a.Hkv + sg.hk) * a.blocks + sg.rb] =
-            make_int2(static_cast<int>(slot), sg.whole ? 0 : last - cta + 1);
+#pragma unroll 1
+    for (int segs = 0;; ++segs) {
+      // whether there is a segment is decided by one warp for all of them, which meet below
+      if (tid < 32) {
+        const bool there = wait(BAR_SEG_FULL + segs % kSegments, segs / kSegments);
+        if (lane == 0) ms.go = there && ms.seg[segs % kSegments].count > 0;
       }
-      before += sg.count;
-      if (sg.tile == 0 && my >= live && my < rows && (QT == 2 || x == 0)) {   // padding
-        uint4* const dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out_row * D);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-        *lse = -INFINITY;
-      }
-      if (sg.empty) continue;
+      ptx::named_barrier_sync(1, kSoftmaxThreads);
+      if (!ms.go) break;
+      const Segment& sg = ms.seg[segs % kSegments];
+      const int live = sg.live, count = sg.count;
 
       // ---- Q: no S of the segment before is still to be computed (its last one has been read)
       {
-        constexpr int kChunks = D / 8, kLoaders = QT == 2 ? 128 : kSoftmaxThreads;
-        constexpr int kEach = kTile * kChunks / kLoaders;
-        const int t = QT == 2 ? gtid : tid, first = QT == 2 ? x * kTile : 0;
-        const uint32_t dst = base + L::kQ + (QT == 2 ? x : 0) * L::kTileBytes;
+        constexpr int kChunks = D / 8, kStep = kSoftmaxThreads / kChunks, kEach = kRows / kStep;
+        const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u;
+        const uint32_t q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const int c = tid % kChunks, step_t = kStep / a.G, step_h = kStep % a.G;
+        int token = (sg.r0 + tid / kChunks) / a.G, h = (sg.r0 + tid / kChunks) % a.G;
+        const uint16_t* const q = static_cast<const uint16_t*>(a.q) +
+                                  (static_cast<int64_t>(sg.b) * a.T * a.Hq + sg.hk * a.G) * D + c * 8;
         uint4 v[kEach];
 #pragma unroll
         for (int u = 0; u < kEach; ++u) {
-          const int r = (u * kLoaders + t) / kChunks, c = (u * kLoaders + t) % kChunks;
-          if (first + r < live) {
-            const int tok = (r0 + first + r) / a.G, h = sg.hk * a.G + (r0 + first + r) % a.G;
-            v[u] = *reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(a.q) +
-                ((static_cast<int64_t>(sg.b) * a.T + tok) * a.Hq + h) * D + c * 8);
-          } else {
-            v[u] = make_uint4(0, 0, 0, 0);
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (u * kStep + tid / kChunks < live)
+            v[u] = *reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(token) * a.Hq + h) * D);
+          token += step_t;
+          h += step_h;
+          if (h >= a.G) {
+            h -= a.G;
+            ++token;
           }
         }
 #pragma unroll
         for (int u = 0; u < kEach; ++u) {
-          const int r = (u * kLoaders + t) / kChunks, c = (u * kLoaders + t) % kChunks;
-          ptx::st_shared_v4(dst + (c / 8) * kHalfBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4), v[u].x,
-                            v[u].y, v[u].z, v[u].w);
+          const int r = u * kStep + tid / kChunks;
+          ptx::st_shared_v4(base + L::kQ + (r / kTile) * L::kTileBytes + (c / 8) * kHalfBytes +
+                                r % kTile * 128 + (((c % 8) ^ (r & 7)) << 4),
+                            (v[u].x & q_and) ^ q_xor, (v[u].y & q_and) ^ q_xor,
+                            (v[u].z & q_and) ^ q_xor, (v[u].w & q_and) ^ q_xor);
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(bar(BAR_Q_FULL));
       }
 
-      Row rw{sg.b, my < live ? token : -1, 0};
-      if (a.window_left >= 0 && rw.i >= 0) {
-        int depth = rw.i;
-        if (a.parents) {
-          depth = 0;
-          for (int at = parent_of(a, sg.b, rw.i); at >= 0; at = parent_of(a, sg.b, at)) ++depth;
-        }
-        rw.lo = max(0, sg.dr.base + depth - a.window_left);
-      }
-      // every row sees all keys of a tile within [full_lo, full_hi)
-      const int full_lo = a.window_left < 0 ? 0 : sg.dr.base + sg.u.i1 - 1 - a.window_left;
-      const int full_hi = a.parents ? sg.dr.base : sg.dr.base + sg.u.i0 + 1;
-      const int first_key = (sg.u.first + sg.tile) * kTile;
       const bool active = (QT == 2 ? x * kTile : 0) + quarter * 32 < live;   // rows of this warp
       const int j_first = QT == 2 ? 0 : x, j_step = QT == 2 ? 1 : 2;
-      const int j_end = QT == 2 && x == 1 && live <= kTile ? 0 : sg.count;
-      float m = -INFINITY, l = 0.f;   // offset of the exponents (log2 units), sum
+      const int j_end = QT == 2 && x == 1 && live <= kTile ? 0 : count;
+      // offset of the exponents (log2 units), sum over this thread's keys
+      float m = -INFINITY, l = 0.f;
 
+#pragma unroll 1
       for (int j = j_first; j < j_end; j += j_step, ++done) {
-        const int n = n0 + j, k0 = first_key + j * kTile;
-        wait(BAR_INFO + n % kInfoSlots, n / kInfoSlots);
-        // (the product of the tile before is done, too: it was issued before this S)
-        if (!wait(BAR_S_FULL + x, done) || (j > j_first && !wait(BAR_O_DONE + x, done - 1)))
+        const int n = n0 + j;
+        // (a warp that has given up meets its partner all the same)
+        const bool known = wait(BAR_INFO + n % kInfoSlots, n / kInfoSlots);
+        const bool masked = known && ms.masked[n % kInfoSlots];
+        uint32_t vis0 = ~0u, vis1 = ~0u;
+        if (masked && active) {
+          const Segment& now = ms.seg[segs % kSegments];
+          uint4 vis = make_uint4(0, 0, 0, 0);
+          if (my < now.live)
+            vis = visible_bits(a, now.b, now.base, (now.r0 + my) / a.G, now.first_key + j * kTile,
+                               ms.loaded[n % kInfoSlots]);
+          vis0 = half ? vis.z : vis.x;
+          vis1 = half ? vis.w : vis.y;
+          __syncwarp();
+        }
+        if (!wait(BAR_S_FULL + x, done)) {
+          if (active) ptx::named_barrier_sync(2 + x * 4 + quarter, 64);
           continue;
-        const uint4 loaded = info[n % kInfoSlots];
-        const bool masked = (loaded.x & loaded.y & loaded.z & loaded.w) != 0xffffffffu ||
-                            k0 < full_lo || k0 + kTile > full_hi;
+        }
         ptx::tc_fence_after_sync();
         if (active) {
-          uint32_t sr[kTile / 32][32];
+          // S is read twice, for the maximum and for P: kept, it would take the registers of all
+          // else
+          float mt;
+          {
+            uint32_t s0[32], s1[32];
+            ptx::tmem_ld_32x32b_x32(tS, s0);
+            ptx::tmem_ld_32x32b_x32(tS + 32, s1);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence(s0);
+            ptx::reg_fence(s1);
+            if (masked) {
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) ptx::tmem_ld_32x32b_x32(tS + c * 32, sr[c]);
-          ptx::tmem_wait_ld();
-          float s[kTile];
+              for (int t = 0; t < 32; ++t) {
+                if (!(vis0 >> t & 1)) s0[t] = 0xff800000u;   // -inf
+                if (!(vis1 >> t & 1)) s1[t] = 0xff800000u;
+              }
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) {
-            ptx::reg_fence(sr[c]);
-#pragma unroll
-            for (int t = 0; t < 32; ++t) s[c * 32 + t] = __uint_as_float(sr[c][t]);
+            for (int t = 0; t < 32; t += 4) {
+              mx[0] = ptx::max3(mx[0], __uint_as_float(s0[t]), __uint_as_float(s0[t + 1]));
+              mx[1] = ptx::max3(mx[1], __uint_as_float(s0[t + 2]), __uint_as_float(s0[t + 3]));
+              mx[2] = ptx::max3(mx[2], __uint_as_float(s1[t]), __uint_as_float(s1[t + 1]));
+              mx[3] = ptx::max3(mx[3], __uint_as_float(s1[t + 2]), __uint_as_float(s1[t + 3]));
+            }
+            mt = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
           }
-          if (!scale_pos) {
-            // scale first, so that the maximum below is the maximum of the scaled scores
-#pragma unroll
-            for (int t = 0; t < kTile; t += 2)
-              ptx::mul2(s[t], s[t + 1], s[t], s[t + 1], scale, scale);
-          }
-          if (masked) {
-            uint32_t vis[4];
-            visible_bits(a, rw, sg.dr.base, k0, vis);
-            vis[0] &= loaded.x;
-            vis[1] &= loaded.y;
-            vis[2] &= loaded.z;
-            vis[3] &= loaded.w;
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < kTile; ++t)
-              if (!(vis[t / 32] >> (t % 32) & 1)) s[t] = -INFINITY;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int t = 0; t < kTile; t += 8) {
-            mx[0] = ptx::max3(mx[0], s[t + 0], s[t + 1]);
-            mx[1] = ptx::max3(mx[1], s[t + 2], s[t + 3]);
-            mx[2] = ptx::max3(mx[2], s[t + 4], s[t + 5]);
-            mx[3] = ptx::max3(mx[3], s[t + 6], s[t + 7]);
-          }
-          const float mt = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
-          const float m_tile = (scale_pos ? mt * scale : mt) - kShift<FP16>;
+          // the row's maximum over both halves (the slots are read before the next S, which the
+          // arrivals below let be computed)
+          ms.red[x][half][row] = mt;
+          ptx::named_barrier_sync(2 + x * 4 + quarter, 64);
+          mt = fmaxf(mt, ms.red[x][half ^ 1][row]);
+          const float m_tile = mt * scale - kShift<FP16>;
           float alpha = 1.f;
           const bool rescale = __any_sync(0xffffffffu, m_tile > m + kLag<FP16>);
           if (rescale) {
@@ -733,19 +838,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = m_new;
           }
           const float m_use = m == -INFINITY ? 0.f : m;
-          // P = 2^(scaled score - offset) over the first 64 columns of S, two keys to a column
+          // P = 2^(scaled score - offset) over the S of these keys, two of them to a column
           float rs0 = 0.f, rs1 = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t s[32], pr[16];
+            ptx::tmem_ld_32x32b_x32(tS + c * 32, s);
+            const uint32_t vis = c ? vis1 : vis0;
+            ptx::tmem_wait_ld();
+            ptx::reg_fence(s);
+            if (masked) {
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) {
-            uint32_t pr[16];
+              for (int t = 0; t < 32; ++t)
+                if (!(vis >> t & 1)) s[t] = 0xff800000u;
+            }
 #pragma unroll
             for (int t = 0; t < 16; ++t) {
               float e0, e1;
-              if (scale_pos)
-                ptx::fma2(e0, e1, s[32 * c + 2 * t], s[32 * c + 2 * t + 1], scale, scale, -m_use,
-                          -m_use);
-              else
-                ptx::add2(e0, e1, s[32 * c + 2 * t], s[32 * c + 2 * t + 1], -m_use, -m_use);
+              ptx::fma2(e0, e1, __uint_as_float(s[2 * t]), __uint_as_float(s[2 * t + 1]), scale,
+                        scale, -m_use, -m_use);
               const float p0 = ptx::exp2_approx(e0), p1 = ptx::exp2_approx(e1);
               ptx::add2(rs0, rs1, rs0, rs1, p0, p1);
               pr[t] = pack2<FP16>(p0, p1);
@@ -755,51 +866,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += rs0 + rs1;
           if (rescale && j > j_first) {
             // the product before has completed: it was issued before this S
-            uint32_t orr[D / 32][32];
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c)
-              ptx::tmem_ld_32x32b_x32(tO + x * D + c * 32, orr[c]);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              ptx::reg_fence(orr[c]);
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t orr[32];
+              ptx::tmem_ld_32x32b_x32(tO + x * D + half * (D / 2) + c * 32, orr);
+              ptx::tmem_wait_ld();
+              ptx::reg_fence(orr);
 #pragma unroll
               for (int t = 0; t < 32; t += 2) {
-                float a0 = __uint_as_float(orr[c][t]), a1 = __uint_as_float(orr[c][t + 1]);
+                float a0 = __uint_as_float(orr[t]), a1 = __uint_as_float(orr[t + 1]);
                 ptx::mul2(a0, a1, a0, a1, alpha, alpha);
-                orr[c][t] = __float_as_uint(a0);
-                orr[c][t + 1] = __float_as_uint(a1);
+                orr[t] = __float_as_uint(a0);
+                orr[t + 1] = __float_as_uint(a1);
               }
-              ptx::tmem_st_32x32b_x32(tO + x * D + c * 32, orr[c]);
+              ptx::tmem_st_32x32b_x32(tO + x * D + half * (D / 2) + c * 32, orr);
             }
           }
           ptx::tmem_wait_st();
         }
         if (masked && (QT == 1 || x == 0) && wait(BAR_V_FULL + n % kStages, n / kStages)) {
-          // V: zeros for the rows of no token, and for what is not finite
-          constexpr int kChunks = D / 8;
-          const uint32_t vt = L::kV + (n % kStages) * L::kTileBytes;
-          bool found = false;
-#pragma unroll 4
-          for (int u = gtid; u < kTile * kChunks; u += 128) {
-            const int r = u / kChunks, c = u % kChunks;
-            const uint32_t bits = r < 64 ? (r < 32 ? loaded.x : loaded.y)
-                                         : (r < 96 ? loaded.z : loaded.w);
-            uint4* const at = reinterpret_cast<uint4*>(
-                gen + vt + (c / 8) * kHalfBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4));
-            if (!(bits >> (r % 32) & 1)) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 v = *at;
-            const uint32_t bx = not_finite2<FP16>(v.x), by = not_finite2<FP16>(v.y),
-                           bz = not_finite2<FP16>(v.z), bw = not_finite2<FP16>(v.w);
-            if (bx | by | bz | bw) {
-              found = true;
-              *at = make_uint4(v.x & ~bx, v.y & ~by, v.z & ~bz, v.w & ~bw);
-            }
-          }
-          if (found) s_not_finite = segs + 1;
+          if (clean_values<D, FP16>(smem_raw + L::kV + (n % kStages) * L::kTileBytes,
+                                    ms.loaded[n % kInfoSlots], tid % 256))
+            ms.not_finite = segs + 1;
           ptx::fence_proxy_async_smem();
         }
         ptx::tc_fence_before_sync();
@@ -807,87 +895,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- the segment's end
-      if (j_end > j_first) wait(BAR_O_DONE + x, done - 1);
-      // one row tile: the groups exchange their offsets and sums, A's first, then B's in its place
-      if (QT == 1 && x == 0) s_ml[row] = make_float2(m, l);
+      if (j_end > j_first) wait(BAR_O_DONE + x, ends++);
       ptx::tc_fence_before_sync();
+      // one row tile: the streams exchange offsets; both: the halves (and streams) exchange sums
+      float fa = 1.f, fb = 0.f;
+      ptx::named_barrier_sync(1, kSoftmaxThreads);   // (the maxima have been read)
+      if constexpr (QT == 1) {
+        ms.red[x][half][row] = m;
+        ptx::named_barrier_sync(1, kSoftmaxThreads);
+        const float m_a = ms.red[0][half][row], m_b = ms.red[1][half][row];
+        m = fmaxf(m_a, m_b);
+        const float u = m == -INFINITY ? 0.f : m;
+        fa = ptx::exp2_approx(m_a - u);
+        fb = ptx::exp2_approx(m_b - u);
+        ptx::named_barrier_sync(1, kSoftmaxThreads);
+      }
+      ms.red[x][half][row] = l;
       ptx::named_barrier_sync(1, kSoftmaxThreads);
       ptx::tc_fence_after_sync();
-      float2 other = make_float2(-INFINITY, 0.f);
-      if constexpr (QT == 1) {
-        if (x == 1) {
-          other = s_ml[row];
-          s_ml[row] = make_float2(m, l);
-        }
-        ptx::named_barrier_sync(1, kSoftmaxThreads);
-        if (x == 0) other = s_ml[row];
-      }
-      constexpr int kCols = QT == 2 ? D : D / 2;   // columns of this thread's row: [c_first, ..)
-      const int c_first = QT == 2 ? 0 : x * kCols;
-      const bool two = QT == 1 && sg.count > 1;    // both groups have an O
-      float fa = 1.f, fb = 0.f;
-      if (QT == 1) {
-        const float2 mine = make_float2(m, l), ml_a = x == 0 ? mine : other,
-                     ml_b = x == 0 ? other : mine;
-        m = fmaxf(ml_a.x, ml_b.x);
-        const float u = m == -INFINITY ? 0.f : m;
-        fa = ptx::exp2_approx(ml_a.x - u);
-        fb = ptx::exp2_approx(ml_b.x - u);
-        l = ml_a.y * fa + ml_b.y * fb;
-      }
-      const float inv = inverse(l);
-      if (ok && (QT == 1 ? active : j_end > 0 && active)) {
+      if constexpr (QT == 1)
+        l = (ms.red[0][0][row] + ms.red[0][1][row]) * fa +
+            (ms.red[1][0][row] + ms.red[1][1][row]) * fb;
+      else
+        l = ms.red[x][0][row] + ms.red[x][1][row];
+      if (ok && active) {
+        const Segment& sn = ms.seg[segs % kSegments];
+        const bool whole = sn.whole, two = QT == 1 && sn.count > 1;   // two: both streams have an O
+        const bool mine = my < sn.live;
+        // (rows behind the last get addresses, too, that nothing is written to)
+        const int token = (sn.r0 + my) / a.G, head = sn.hk * a.G + (sn.r0 + my) % a.G;
+        const float f = whole ? inverse(l) : 1.f;
+        fa *= f;
+        fb *= f;
+        const int64_t part = static_cast<int64_t>(sn.slot) * a.part_rows + my;
+        uint16_t* const o_row = static_cast<uint16_t*>(a.o) +
+                                ((static_cast<int64_t>(sn.b) * a.T + token) * a.Hq + head) * D;
+        // where this thread's row goes; a row's 16-byte pieces are written by consecutive lanes (from
+        // a thread's own row each store would touch 32 lines: 11000 cycles for 256 rows, not 4000)
+        char* const own = whole ? reinterpret_cast<char*>(o_row)
+                                : reinterpret_cast<char*>(a.part_o + part * D);
+        const int wide = whole ? 2 : 4;         // bytes of a value
+        const int live_rows = sn.live - (my - lane);   // of this warp's 32
+        // this thread's columns of the row, kChunk at a time through this warp's share of Q's place
+        constexpr int kCols = QT == 2 ? D / 2 : D / 4, kChunk = L::kChunk;
+        const int c0 = (QT == 2 ? half : 2 * x + half) * kCols;
+        const int shift = (kChunk == 32 ? 3 : 2) - (whole ? 1 : 0);   // 2^shift pieces of a row's chunk
+        uint8_t* const stage = smem_raw + L::kQ + (warp - 4) * (32 * kChunk * 4);
+        auto piece = [&](int r, int c) {
+          const int twist = kChunk == 32 ? r : r >> 1;   // pieces of eight rows in different banks
+          return reinterpret_cast<uint4*>(stage + (((r << shift) + (c ^ (twist & ((1 << shift) - 1))))
+                                                   << 4));
+        };
 #pragma unroll 1
-        for (int c = 0; c < kCols / 32; ++c) {
-          const int col = c_first + c * 32;
-          uint32_t oa[32], ob[32];
+        for (int col = c0; col < c0 + kCols; col += kChunk) {
+          uint32_t oa[kChunk], ob[16];
           __syncwarp();
-          ptx::tmem_ld_32x32b_x32(tO + (QT == 2 ? x * D : 0) + col, oa);
-          if (two) ptx::tmem_ld_32x32b_x32(tO + D + col, ob);
+          if constexpr (kChunk == 32) {
+            ptx::tmem_ld_32x32b_x32(tO + x * D + col, oa);
+          } else {
+            ptx::tmem_ld_32x32b_x16(tO + (QT == 2 ? x * D : 0) + col, oa);
+            if (two) ptx::tmem_ld_32x32b_x16(tO + D + col, ob);
+          }
           ptx::tmem_wait_ld();
           ptx::reg_fence(oa);
           if (two) ptx::reg_fence(ob);
-          float v[32];
+          float v[kChunk];
 #pragma unroll
-          for (int t = 0; t < 32; ++t) {
-            v[t] = __uint_as_float(oa[t]);
-            if (QT == 1) v[t] = v[t] * fa + (two ? __uint_as_float(ob[t]) * fb : 0.f);
+          for (int t = 0; t < kChunk; ++t) {
+            v[t] = __uint_as_float(oa[t]) * fa;
+            if (two) v[t] += __uint_as_float(ob[t % 16]) * fb;
           }
-          if (my < live) {
-            if (sg.whole) {
-              uint4* const dst =
-                  reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out_row * D + col);
+          if (whole) {
 #pragma unroll
-              for (int t = 0; t < 4; ++t)
-                dst[t] = make_uint4(pack2<FP16>(v[8 * t] * inv, v[8 * t + 1] * inv),
-                                    pack2<FP16>(v[8 * t + 2] * inv, v[8 * t + 3] * inv),
-                                    pack2<FP16>(v[8 * t + 4] * inv, v[8 * t + 5] * inv),
-                                    pack2<FP16>(v[8 * t + 6] * inv, v[8 * t + 7] * inv));
-            } else {
-              float4* const dst =
-                  reinterpret_cast<float4*>(a.part_o + (slot * a.part_rows + my) * D + col);
+            for (int t = 0; t < kChunk / 8; ++t)
+              *piece(lane, t) = make_uint4(pack2<FP16>(v[8 * t], v[8 * t + 1]),
+                                           pack2<FP16>(v[8 * t + 2], v[8 * t + 3]),
+                                           pack2<FP16>(v[8 * t + 4], v[8 * t + 5]),
+                                           pack2<FP16>(v[8 * t + 6], v[8 * t + 7]));
+          } else {
 #pragma unroll
-              for (int t = 0; t < 8; ++t)
-                dst[t] = make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
-            }
+            for (int t = 0; t < kChunk / 4; ++t)
+              *piece(lane, t) = make_uint4(__float_as_uint(v[4 * t]), __float_as_uint(v[4 * t + 1]),
+                                           __float_as_uint(v[4 * t + 2]),
+                                           __float_as_uint(v[4 * t + 3]));
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int i = lane; i < 32 << shift; i += 32) {
+            const int r = i >> shift, c = i & ((1 << shift) - 1);
+            char* const to = reinterpret_cast<char*>(__shfl_sync(
+                0xffffffffu, reinterpret_cast<unsigned long long>(own), r));
+            if (r < live_rows) *reinterpret_cast<uint4*>(to + col * wide + c * 16) = *piece(r, c);
           }
         }
-        if (s_not_finite == segs + 1 && rw.i >= 0)
-          add_not_finite<FP16>(
-              a, rw, sg.dr.base, sg.hk, D, first_key, sg.count, full_lo, full_hi, c_first, kCols,
-              sg.whole ? nullptr : a.part_o + (slot * a.part_rows + my) * D,
-              sg.whole ? static_cast<uint16_t*>(a.o) + out_row * D : nullptr);
-        if (my < live && (QT == 2 || x == 0)) {
-          if (sg.whole)
-            *lse = lse_of(m, l);
+        __syncwarp();
+        if (ms.not_finite == segs + 1 && mine)
+          add_not_finite<FP16>(a, sn, token, D, c0, kCols, whole ? nullptr : a.part_o + part * D,
+                               whole ? o_row : nullptr);
+        if (mine && c0 == 0) {
+          if (whole)
+            a.lse[(static_cast<int64_t>(sn.b) * a.Hq + head) * a.T + token] = lse_of(m, l);
           else
-            a.part_ml[slot * a.part_rows + my] = make_float2(m, l);
+            a.part_ml[part] = make_float2(m, l);
         }
       }
+      n0 += ms.seg[segs % kSegments].count;
+      __syncwarp();
+      if (lane == 0) segment_read(segs);
       ptx::tc_fence_before_sync();
       ptx::mbar_arrive(bar(BAR_O_FREE));
-      n0 += sg.count;
-      ++segs;
     }
   }
 

@@ -63,7 +63,8 @@ def test_tree_refusals(lib):
         assert tree(lib, **{name: 0}) == NULL
     for bad in (dict(B=0), dict(T=0), dict(T=1025), dict(Hq=0), dict(Hkv=0), dict(Hq=3),
                 dict(Hq=1), dict(d=256), dict(page=48), dict(page=512), dict(pages=0),
-                dict(width=0), dict(width=1 << 27), dict(B=1 << 16, T=1 << 10, Hq=32, Hkv=1)):
+                dict(width=0), dict(width=1 << 27), dict(B=1 << 16, T=1 << 10, Hq=32, Hkv=1),
+                dict(B=1 << 11, T=1, Hq=1, Hkv=1, width=1 << 23)):
         assert tree(lib, **bad) == SHAPE, bad
     assert tree(lib, dtype=7) == DTYPE
     assert tree(lib, scale=math.nan) == SCALE
