@@ -166,20 +166,21 @@ struct Misc {
   uint32_t tmem_base;
   int abort;
   int go;                       // the softmax warps have another segment
-  int not_finite;               // segment (+ 1) in whose masked tiles V had such values
+  int not_finite[2];            // by segments in turns: the segment (+ 1) in whose masked tiles V
+                                // had such values
 };
 
 template <int D, int QT>
 struct Smem {
   static constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
-  static constexpr int kStages = D == 64 ? 6 : QT == 1 ? 3 : 2;
+  static constexpr int kStages = D == 128 ? (QT == 1 ? 3 : 2) : (QT == 1 ? 6 : 5);
   static constexpr uint32_t kQ = 0;
-  // Q's place is also that of 32 rows of kChunk columns of O (fp32) for each softmax warp
-  static constexpr int kChunk = QT == 2 && D == 128 ? 32 : 16;
-  static constexpr uint32_t kStageBytes = kSoftmaxThreads * kChunk * 4;
-  static constexpr uint32_t kK = kQ + (QT * kTileBytes > kStageBytes ? QT * kTileBytes : kStageBytes);
+  static constexpr uint32_t kK = kQ + QT * kTileBytes;
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
-  static constexpr uint32_t kMisc = kV + kStages * kTileBytes;
+  // two row tiles: for each softmax warp 32 rows of kChunk columns of O (fp32) on their way out
+  static constexpr int kChunk = 16;
+  static constexpr uint32_t kOut = kV + kStages * kTileBytes;
+  static constexpr uint32_t kMisc = kOut + (QT == 2 ? kSoftmaxThreads * kChunk * 4 : 0);
   static constexpr uint32_t kDynamic = kMisc + sizeof(Misc);
 };
 static_assert(Smem<128, 1>::kDynamic <= 232448 && Smem<128, 2>::kDynamic <= 232448 &&
@@ -229,6 +230,43 @@ __device__ __noinline__ uint4 visible_bits(const Args& a, int b, int base, int i
     }
   }
   return make_uint4(vis[0] & loaded.x, vis[1] & loaded.y, vis[2] & loaded.z, vis[3] & loaded.w);
+}
+
+// One lane of a converged warp: nonzero in it.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one;
+}
+// ptx::mma_f16_ss, mma_f16_ts and mma_commit, by the lanes whose `one` is not zero.
+__device__ __forceinline__ void mma_ss_if(uint32_t one, uint32_t d_tmem, uint64_t a_desc,
+                                          uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t one, uint32_t d_tmem, uint32_t a_tmem,
+                                          uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(one)
+      : "memory");
 }
 
 // Halves of v that are infinite or NaN, as ones.
@@ -340,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     ms.abort = 0;
-    ms.not_finite = 0;
+    ms.not_finite[0] = ms.not_finite[1] = 0;
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(bar(BAR_K_FULL + s), 1);
       ptx::mbar_init(bar(BAR_K_EMPTY + s), 1);
@@ -373,7 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after_sync();
   wait_prerequisites();
   launch_dependents();
-  const uint32_t tmem = ms.tmem_base;
+  // (an allocation of all 512 columns starts at address 0, which the products use as a constant)
+  const uint32_t tmem = 0;
   volatile int* abort_p = &ms.abort;
   auto give_up = [&] {
     *abort_p = 1;
@@ -596,105 +635,119 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::wait_bounded(bar(full + x % kStages), (x / kStages) & 1, abort_p, kWaitLimitNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = ptx::idesc_f16(FP16, kTile, kTile, false);
-      constexpr uint32_t idesc_pv = ptx::idesc_f16(FP16, kTile, D, true);
-      auto wait = [&](int slot, uint32_t parity) {
-        return ptx::wait_bounded(bar(slot), parity & 1, abort_p, kWaitLimitNs);
-      };
-      auto wait_k = [&](int n) { return wait(BAR_K_FULL + n % kStages, n / kStages); };
-      auto wait_v = [&](int n) { return wait(BAR_V_FULL + n % kStages, n / kStages); };
-      // S_x = Q K_n^T
-      auto issue_s = [&](int x, int n) {
-        ptx::tc_fence_after_sync();
-        const ptx::SmemDesc q_desc = ptx::smem_desc_sw128_split(
-            base + L::kQ + (QT == 2 ? x : 0) * L::kTileBytes, 16, 1024);
-        const ptx::SmemDesc k_desc =
-            ptx::smem_desc_sw128_split(base + L::kK + (n % kStages) * L::kTileBytes, 16, 1024);
+    // The whole warp runs the loop without a branch on the lane, and one lane's instructions count:
+    // descriptors, addresses and counters are then the same for all lanes as the compiler sees it.
+    constexpr uint32_t idesc_qk = ptx::idesc_f16(FP16, kTile, kTile, false);
+    constexpr uint32_t idesc_pv = ptx::idesc_f16(FP16, kTile, D, true);
+    const uint32_t one = elect_one();
+    auto wait = [&](int slot, uint32_t parity) {
+      return ptx::wait_bounded_warp(bar(slot), parity & 1, abort_p, kWaitLimitNs);
+    };
+    // (stage and phase of the next K, and of the next V)
+    int ks = 0, vs = 0;
+    uint32_t kp = 0, vp = 0;
+    auto commit = [&](int slot) { commit_if(one, bar(slot)); };
+    // S_x = Q K^T of the K stage
+    auto issue_s = [&](int x) {
+      ptx::tc_fence_after_sync();
+      const ptx::SmemDesc q_desc = ptx::smem_desc_sw128_split(
+          base + L::kQ + (QT == 2 ? x : 0) * L::kTileBytes, 16, 1024);
+      const ptx::SmemDesc k_desc =
+          ptx::smem_desc_sw128_split(base + L::kK + ks * L::kTileBytes, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * kHalfBytes + (kk % 4) * 32;
-          ptx::mma_f16_ss(tmem + x * kTile, q_desc.at(off), k_desc.at(off), idesc_qk, kk > 0);
-        }
-        ptx::mma_commit(bar(BAR_S_FULL + x));
-      };
-      // O_x (+)= P_x V_n, P_x from TMEM: keys 0 .. 63 in the first 32 columns of S_x, the others in
-      // those from 64 on
-      auto issue_pv = [&](int x, int n, bool first, bool last) {
-        ptx::tc_fence_after_sync();
-        const ptx::SmemDesc v_desc = ptx::smem_desc_sw128_split(
-            base + L::kV + (n % kStages) * L::kTileBytes, kHalfBytes, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          ptx::mma_f16_ts(tmem + kTmemO + x * D, tmem + x * kTile + (kk / 4) * 64 + (kk % 4) * 8,
-                          v_desc.at(kk * 16 * 128), idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        if (last) ptx::mma_commit(bar(BAR_O_DONE + x));
-      };
-      int n0 = 0, done[2] = {0, 0};   // tiles, and tiles of each stream so far
-      bool ok = true;
-#pragma unroll 1
-      for (int segs = 0; ok; ++segs) {
-        ok = segment(segs);
-        const Segment& sg = ms.seg[segs % kSegments];
-        const int count = ok ? sg.count : 0;
-        if (count == 0) break;
-        const bool b_any = QT == 1 || sg.live > kTile;
-        segment_read(segs);
-        ok = wait(BAR_Q_FULL, segs);
-        // S of the first tile (one row tile: of the first two), then P V of every tile and S of
-        // the stream's next one
-#pragma unroll 1
-        for (int j = QT == 2 ? -1 : -2; ok && j < count; ++j) {
-          const int n = n0 + j;
-          const int next = QT == 2 ? j + 1 : j + 2;   // tile of the S
-          const bool s_next = next < count;
-          if (j >= 0) {
-            if (!wait_v(n)) { ok = false; break; }
-            // O of the segment before has to be out of TMEM
-            if (j == 0 && segs > 0 && !wait(BAR_O_FREE, segs - 1)) { ok = false; break; }
-          }
-          if constexpr (QT == 2) {
-            if (j >= 0) {
-              if (!wait(BAR_P_FULL + 0, done[0]++)) { ok = false; break; }
-              issue_pv(0, n, j == 0, !s_next);
-            }
-            if (s_next) {
-              if (!wait_k(n0 + next)) { ok = false; break; }
-              issue_s(0, n0 + next);
-            }
-            if (j >= 0) {
-              if (b_any) {
-                if (!wait(BAR_P_FULL + 1, done[1]++)) { ok = false; break; }
-                issue_pv(1, n, j == 0, !s_next);
-              }
-              ptx::mma_commit(bar(BAR_V_EMPTY + n % kStages));
-            }
-            if (s_next) {
-              if (b_any) issue_s(1, n0 + next);
-              ptx::mma_commit(bar(BAR_K_EMPTY + (n0 + next) % kStages));
-            }
-          } else {
-            const int x = j & 1;
-            if (j >= 0) {
-              if (!wait(BAR_P_FULL + x, done[x]++)) { ok = false; break; }
-              issue_pv(x, n, j < 2, !s_next);
-              ptx::mma_commit(bar(BAR_V_EMPTY + n % kStages));
-            }
-            if (s_next) {
-              if (!wait_k(n0 + next)) { ok = false; break; }
-              issue_s(x, n0 + next);
-              ptx::mma_commit(bar(BAR_K_EMPTY + (n0 + next) % kStages));
-            }
-          }
-        }
-        n0 += count;
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * kHalfBytes + (kk % 4) * 32;
+        mma_ss_if(one, x * kTile, q_desc.at(off), k_desc.at(off), idesc_qk, kk > 0);
       }
-      if (!ok) give_up();
-      // Every MMA this thread issued has completed before TMEM can be released.
-      ptx::mma_commit(bar(BAR_MMA_DONE));
-      wait(BAR_MMA_DONE, 0);
+      commit(BAR_S_FULL + x);
+    };
+    // O_x (+)= P_x V of the V stage, P_x from TMEM: keys 0 .. 63 in the first 32 columns of S_x, the
+    // others in those from 64 on
+    auto issue_pv = [&](int x, bool first, bool last) {
+      ptx::tc_fence_after_sync();
+      const ptx::SmemDesc v_desc =
+          ptx::smem_desc_sw128_split(base + L::kV + vs * L::kTileBytes, kHalfBytes, 1024);
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        mma_ts_if(one, kTmemO + x * D, x * kTile + (kk / 4) * 64 + (kk % 4) * 8,
+                  v_desc.at(kk * 16 * 128), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+      if (last) commit(BAR_O_DONE + x);
+    };
+    auto k_done = [&] {
+      commit(BAR_K_EMPTY + ks);
+      if (++ks == kStages) {
+        ks = 0;
+        kp ^= 1;
+      }
+    };
+    auto v_done = [&] {
+      commit(BAR_V_EMPTY + vs);
+      if (++vs == kStages) {
+        vs = 0;
+        vp ^= 1;
+      }
+    };
+    uint32_t done0 = 0, done1 = 0;   // tiles of each stream so far
+    bool ok = true;
+#pragma unroll 1
+    for (int segs = 0; ok; ++segs) {
+      ok = __all_sync(0xffffffffu, segment(segs));
+      const Segment& sg = ms.seg[segs % kSegments];
+      const int count = __shfl_sync(0xffffffffu, ok ? sg.count : 0, 0);
+      if (count == 0) break;
+      const bool b_any = QT == 1 || __shfl_sync(0xffffffffu, sg.live, 0) > kTile;
+      __syncwarp();
+      if (lane == 0) segment_read(segs);
+      ok = wait(BAR_Q_FULL, segs);
+      // S of the first tile (one row tile: of the first two), then P V of every tile and S of
+      // the stream's next one
+#pragma unroll 1
+      for (int j = QT == 2 ? -1 : -2; ok && j < count; ++j) {
+        const bool s_next = (QT == 2 ? j + 1 : j + 2) < count;
+        if (j >= 0) {
+          if (!wait(BAR_V_FULL + vs, vp)) { ok = false; break; }
+          // O of the segment before has to be out of TMEM
+          if (j == 0 && segs > 0 && !wait(BAR_O_FREE, segs - 1)) { ok = false; break; }
+        }
+        if constexpr (QT == 2) {
+          if (j >= 0) {
+            if (!wait(BAR_P_FULL + 0, done0++)) { ok = false; break; }
+            issue_pv(0, j == 0, !s_next);
+          }
+          if (s_next) {
+            if (!wait(BAR_K_FULL + ks, kp)) { ok = false; break; }
+            issue_s(0);
+          }
+          if (j >= 0) {
+            if (b_any) {
+              if (!wait(BAR_P_FULL + 1, done1++)) { ok = false; break; }
+              issue_pv(1, j == 0, !s_next);
+            }
+            v_done();
+          }
+          if (s_next) {
+            if (b_any) issue_s(1);
+            k_done();
+          }
+        } else {
+          const int x = j & 1;
+          if (j >= 0) {
+            if (!wait(BAR_P_FULL + x, x ? done1++ : done0++)) { ok = false; break; }
+            issue_pv(x, j < 2, !s_next);
+            v_done();
+          }
+          if (s_next) {
+            if (!wait(BAR_K_FULL + ks, kp)) { ok = false; break; }
+            issue_s(x);
+            k_done();
+          }
+        }
+      }
     }
-    __syncwarp();
+    if (!ok && lane == 0) give_up();
+    // Every MMA lane 0 issued has completed before TMEM can be released.
+    commit(BAR_MMA_DONE);
+    wait(BAR_MMA_DONE, 0);
   } else {
     // ------------------------------------------------------------------ softmax
     const int x = (warp - 4) / 8;                  // stream: 0 = A, 1 = B
@@ -720,52 +773,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return ok;
     };
-#pragma unroll 1
-    for (int segs = 0;; ++segs) {
-      // whether there is a segment is decided by one warp for all of them, which meet below
+    // Whether there is a segment s is decided by one warp for all of them, which meet here.
+    auto next_segment = [&](int s) {
       if (tid < 32) {
-        const bool there = wait(BAR_SEG_FULL + segs % kSegments, segs / kSegments);
-        if (lane == 0) ms.go = there && ms.seg[segs % kSegments].count > 0;
+        const bool there = wait(BAR_SEG_FULL + s % kSegments, s / kSegments);
+        if (lane == 0) ms.go = there && ms.seg[s % kSegments].count > 0;
       }
       ptx::named_barrier_sync(1, kSoftmaxThreads);
-      if (!ms.go) break;
-      const Segment& sg = ms.seg[segs % kSegments];
-      const int live = sg.live, count = sg.count;
-
-      // ---- Q: no S of the segment before is still to be computed (its last one has been read)
-      {
-        constexpr int kChunks = D / 8, kStep = kSoftmaxThreads / kChunks, kEach = kRows / kStep;
-        const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u;
-        const uint32_t q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-        const int c = tid % kChunks, step_t = kStep / a.G, step_h = kStep % a.G;
-        int token = (sg.r0 + tid / kChunks) / a.G, h = (sg.r0 + tid / kChunks) % a.G;
-        const uint16_t* const q = static_cast<const uint16_t*>(a.q) +
-                                  (static_cast<int64_t>(sg.b) * a.T * a.Hq + sg.hk * a.G) * D + c * 8;
-        uint4 v[kEach];
+      return ms.go != 0;
+    };
+    // Q of segment s into shared memory: no S that reads the one before is still to be computed.
+    auto load_q = [&](int s) {
+      constexpr int kChunks = D / 8, kStep = kSoftmaxThreads / kChunks, kEach = kRows / kStep;
+      const Segment& sg = ms.seg[s % kSegments];
+      const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u;
+      const uint32_t q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+      const int c = tid % kChunks, step_t = kStep / a.G, step_h = kStep % a.G, live = sg.live;
+      int token = (sg.r0 + tid / kChunks) / a.G, h = (sg.r0 + tid / kChunks) % a.G;
+      const uint16_t* const q = static_cast<const uint16_t*>(a.q) +
+                                (static_cast<int64_t>(sg.b) * a.T * a.Hq + sg.hk * a.G) * D + c * 8;
+      uint4 v[kEach];
 #pragma unroll
-        for (int u = 0; u < kEach; ++u) {
-          v[u] = make_uint4(0, 0, 0, 0);
-          if (u * kStep + tid / kChunks < live)
-            v[u] = *reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(token) * a.Hq + h) * D);
-          token += step_t;
-          h += step_h;
-          if (h >= a.G) {
-            h -= a.G;
-            ++token;
-          }
+      for (int u = 0; u < kEach; ++u) {
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (u * kStep + tid / kChunks < live)
+          v[u] = *reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(token) * a.Hq + h) * D);
+        token += step_t;
+        h += step_h;
+        if (h >= a.G) {
+          h -= a.G;
+          ++token;
         }
-#pragma unroll
-        for (int u = 0; u < kEach; ++u) {
-          const int r = u * kStep + tid / kChunks;
-          ptx::st_shared_v4(base + L::kQ + (r / kTile) * L::kTileBytes + (c / 8) * kHalfBytes +
-                                r % kTile * 128 + (((c % 8) ^ (r & 7)) << 4),
-                            (v[u].x & q_and) ^ q_xor, (v[u].y & q_and) ^ q_xor,
-                            (v[u].z & q_and) ^ q_xor, (v[u].w & q_and) ^ q_xor);
-        }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(bar(BAR_Q_FULL));
       }
-
+#pragma unroll
+      for (int u = 0; u < kEach; ++u) {
+        const int r = u * kStep + tid / kChunks;
+        ptx::st_shared_v4(base + L::kQ + (r / kTile) * L::kTileBytes + (c / 8) * kHalfBytes +
+                              r % kTile * 128 + (((c % 8) ^ (r & 7)) << 4),
+                          (v[u].x & q_and) ^ q_xor, (v[u].y & q_and) ^ q_xor,
+                          (v[u].z & q_and) ^ q_xor, (v[u].w & q_and) ^ q_xor);
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(bar(BAR_Q_FULL));
+    };
+    bool go = next_segment(0);
+    if (go) load_q(0);
+#pragma unroll 1
+    for (int segs = 0; go; ++segs) {
+      const int live = ms.seg[segs % kSegments].live, count = ms.seg[segs % kSegments].count;
       const bool active = (QT == 2 ? x * kTile : 0) + quarter * 32 < live;   // rows of this warp
       const int j_first = QT == 2 ? 0 : x, j_step = QT == 2 ? 1 : 2;
       const int j_end = QT == 2 && x == 1 && live <= kTile ? 0 : count;
@@ -887,37 +942,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (masked && (QT == 1 || x == 0) && wait(BAR_V_FULL + n % kStages, n / kStages)) {
           if (clean_values<D, FP16>(smem_raw + L::kV + (n % kStages) * L::kTileBytes,
                                     ms.loaded[n % kInfoSlots], tid % 256))
-            ms.not_finite = segs + 1;
+            ms.not_finite[segs & 1] = segs + 1;
           ptx::fence_proxy_async_smem();
         }
         ptx::tc_fence_before_sync();
         ptx::mbar_arrive(bar(BAR_P_FULL + x));
       }
 
-      // ---- the segment's end
+      // ---- the segment's end. The next one's Q comes first, so that its first S is computed
+      // while this one's O leaves.
       if (j_end > j_first) wait(BAR_O_DONE + x, ends++);
       ptx::tc_fence_before_sync();
-      // one row tile: the streams exchange offsets; both: the halves (and streams) exchange sums
-      float fa = 1.f, fb = 0.f;
-      ptx::named_barrier_sync(1, kSoftmaxThreads);   // (the maxima have been read)
-      if constexpr (QT == 1) {
-        ms.red[x][half][row] = m;
-        ptx::named_barrier_sync(1, kSoftmaxThreads);
-        const float m_a = ms.red[0][half][row], m_b = ms.red[1][half][row];
-        m = fmaxf(m_a, m_b);
-        const float u = m == -INFINITY ? 0.f : m;
-        fa = ptx::exp2_approx(m_a - u);
-        fb = ptx::exp2_approx(m_b - u);
-        ptx::named_barrier_sync(1, kSoftmaxThreads);
-      }
-      ms.red[x][half][row] = l;
-      ptx::named_barrier_sync(1, kSoftmaxThreads);
+      go = next_segment(segs + 1);   // (here both streams' products are done)
       ptx::tc_fence_after_sync();
-      if constexpr (QT == 1)
-        l = (ms.red[0][0][row] + ms.red[0][1][row]) * fa +
-            (ms.red[1][0][row] + ms.red[1][1][row]) * fb;
-      else
-        l = ms.red[x][0][row] + ms.red[x][1][row];
+      if (go) load_q(segs + 1);
+      // the halves exchange their sums; one row tile: then the streams their offsets and sums
+      float fa = 1.f, fb = 0.f;
+      if (active) {
+        const int pair = 2 + x * 4 + quarter;
+        ms.red[x][half][row] = l;
+        ptx::named_barrier_sync(pair, 64);
+        l += ms.red[x][half ^ 1][row];
+        ptx::named_barrier_sync(pair, 64);
+        if constexpr (QT == 1) {
+          ms.red[x][half][row] = half ? l : m;
+          ptx::named_barrier_sync(10 + quarter, 128);
+          const float m_a = ms.red[0][0][row], m_b = ms.red[1][0][row];
+          m = fmaxf(m_a, m_b);
+          const float u = m == -INFINITY ? 0.f : m;
+          fa = ptx::exp2_approx(m_a - u);
+          fb = ptx::exp2_approx(m_b - u);
+          l = ms.red[0][1][row] * fa + ms.red[1][1][row] * fb;
+          ptx::named_barrier_sync(10 + quarter, 128);
+        }
+      }
       if (ok && active) {
         const Segment& sn = ms.seg[segs % kSegments];
         const bool whole = sn.whole, two = QT == 1 && sn.count > 1;   // two: both streams have an O
@@ -930,32 +988,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t part = static_cast<int64_t>(sn.slot) * a.part_rows + my;
         uint16_t* const o_row = static_cast<uint16_t*>(a.o) +
                                 ((static_cast<int64_t>(sn.b) * a.T + token) * a.Hq + head) * D;
-        // where this thread's row goes; a row's 16-byte pieces are written by consecutive lanes (from
-        // a thread's own row each store would touch 32 lines: 11000 cycles for 256 rows, not 4000)
+        // Where this thread's row goes. Two row tiles: a row's 16-byte pieces are written by
+        // consecutive lanes, by way of shared memory (from its own thread each store touches 32
+        // lines: 11000 cycles for 256 rows, not 6000).
         char* const own = whole ? reinterpret_cast<char*>(o_row)
                                 : reinterpret_cast<char*>(a.part_o + part * D);
-        const int wide = whole ? 2 : 4;         // bytes of a value
+        const int wide = whole ? 2 : 4;                // bytes of a value
         const int live_rows = sn.live - (my - lane);   // of this warp's 32
-        // this thread's columns of the row, kChunk at a time through this warp's share of Q's place
         constexpr int kCols = QT == 2 ? D / 2 : D / 4, kChunk = L::kChunk;
-        const int c0 = (QT == 2 ? half : 2 * x + half) * kCols;
-        const int shift = (kChunk == 32 ? 3 : 2) - (whole ? 1 : 0);   // 2^shift pieces of a row's chunk
-        uint8_t* const stage = smem_raw + L::kQ + (warp - 4) * (32 * kChunk * 4);
-        auto piece = [&](int r, int c) {
-          const int twist = kChunk == 32 ? r : r >> 1;   // pieces of eight rows in different banks
-          return reinterpret_cast<uint4*>(stage + (((r << shift) + (c ^ (twist & ((1 << shift) - 1))))
-                                                   << 4));
+        const int c0 = (QT == 2 ? half : 2 * x + half) * kCols;   // this thread's columns
+        const int shift = whole ? 1 : 2;               // 2^shift pieces of a row's chunk
+        uint8_t* const stage = smem_raw + L::kOut + (warp - 4) * (32 * kChunk * 4);
+        auto piece = [&](int r, int c) {   // (those of eight rows in different banks)
+          return reinterpret_cast<uint4*>(
+              stage + (((r << shift) + (c ^ ((r >> 1) & ((1 << shift) - 1)))) << 4));
         };
 #pragma unroll 1
         for (int col = c0; col < c0 + kCols; col += kChunk) {
-          uint32_t oa[kChunk], ob[16];
+          uint32_t oa[kChunk], ob[kChunk];
           __syncwarp();
-          if constexpr (kChunk == 32) {
-            ptx::tmem_ld_32x32b_x32(tO + x * D + col, oa);
-          } else {
-            ptx::tmem_ld_32x32b_x16(tO + (QT == 2 ? x * D : 0) + col, oa);
-            if (two) ptx::tmem_ld_32x32b_x16(tO + D + col, ob);
-          }
+          ptx::tmem_ld_32x32b_x16(tO + (QT == 2 ? x * D : 0) + col, oa);
+          if (two) ptx::tmem_ld_32x32b_x16(tO + D + col, ob);
           ptx::tmem_wait_ld();
           ptx::reg_fence(oa);
           if (two) ptx::reg_fence(ob);
@@ -963,33 +1016,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < kChunk; ++t) {
             v[t] = __uint_as_float(oa[t]) * fa;
-            if (two) v[t] += __uint_as_float(ob[t % 16]) * fb;
+            if (two) v[t] += __uint_as_float(ob[t]) * fb;
           }
+          auto put = [&](int t, uint4 w) {
+            if constexpr (QT == 2)
+              *piece(lane, t) = w;
+            else if (mine)
+              *reinterpret_cast<uint4*>(own + col * wide + t * 16) = w;
+          };
           if (whole) {
 #pragma unroll
             for (int t = 0; t < kChunk / 8; ++t)
-              *piece(lane, t) = make_uint4(pack2<FP16>(v[8 * t], v[8 * t + 1]),
-                                           pack2<FP16>(v[8 * t + 2], v[8 * t + 3]),
-                                           pack2<FP16>(v[8 * t + 4], v[8 * t + 5]),
-                                           pack2<FP16>(v[8 * t + 6], v[8 * t + 7]));
+              put(t, make_uint4(pack2<FP16>(v[8 * t], v[8 * t + 1]),
+                                pack2<FP16>(v[8 * t + 2], v[8 * t + 3]),
+                                pack2<FP16>(v[8 * t + 4], v[8 * t + 5]),
+                                pack2<FP16>(v[8 * t + 6], v[8 * t + 7])));
           } else {
 #pragma unroll
             for (int t = 0; t < kChunk / 4; ++t)
-              *piece(lane, t) = make_uint4(__float_as_uint(v[4 * t]), __float_as_uint(v[4 * t + 1]),
-                                           __float_as_uint(v[4 * t + 2]),
-                                           __float_as_uint(v[4 * t + 3]));
+              put(t, make_uint4(__float_as_uint(v[4 * t]), __float_as_uint(v[4 * t + 1]),
+                                __float_as_uint(v[4 * t + 2]), __float_as_uint(v[4 * t + 3])));
           }
-          __syncwarp();
+          if constexpr (QT == 2) {
+            __syncwarp();
 #pragma unroll 1
-          for (int i = lane; i < 32 << shift; i += 32) {
-            const int r = i >> shift, c = i & ((1 << shift) - 1);
-            char* const to = reinterpret_cast<char*>(__shfl_sync(
-                0xffffffffu, reinterpret_cast<unsigned long long>(own), r));
-            if (r < live_rows) *reinterpret_cast<uint4*>(to + col * wide + c * 16) = *piece(r, c);
+            for (int i = lane; i < 32 << shift; i += 32) {
+              const int r = i >> shift, c = i & ((1 << shift) - 1);
+              char* const to = reinterpret_cast<char*>(__shfl_sync(
+                  0xffffffffu, reinterpret_cast<unsigned long long>(own), r));
+              if (r < live_rows) *reinterpret_cast<uint4*>(to + col * wide + c * 16) = *piece(r, c);
+            }
           }
         }
         __syncwarp();
-        if (ms.not_finite == segs + 1 && mine)
+        if (ms.not_finite[segs & 1] == segs + 1 && mine)
           add_not_finite<FP16>(a, sn, token, D, c0, kCols, whole ? nullptr : a.part_o + part * D,
                                whole ? o_row : nullptr);
         if (mine && c0 == 0) {
@@ -1012,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after_sync();
-    ptx::tmem_dealloc(tmem, kTmemCols);
+    ptx::tmem_dealloc(ms.tmem_base, kTmemCols);
   }
 }
 
