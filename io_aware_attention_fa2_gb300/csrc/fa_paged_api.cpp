@@ -74,7 +74,7 @@ bool tree_shape_ok(int B, int T, int Hq, int Hkv, int page_size, int max_pages) 
   if (T < 1 || T > fa::kMaxDraft || Hq < Hkv || Hq % Hkv) return false;
   const uint64_t rows = (uint64_t)B * (uint64_t)T * (uint64_t)Hq;
   const uint64_t blocks = ((uint64_t)T * (uint64_t)(Hq / Hkv) + 127) / 128;
-  const uint64_t tiles = ((uint64_t)max_pages * page_size + 127) / 128;
+  const uint64_t tiles = ((uint64_t)max_pages * page_size + 127) / 128 + 16;
   return rows < (1ull << 31) && (uint64_t)B * Hkv * blocks * tiles < (1ull << 31);
 }
 

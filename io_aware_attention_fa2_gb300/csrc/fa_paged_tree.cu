@@ -110,17 +110,24 @@ __device__ __forceinline__ Unit unit_of(const Args& a, Draft dr, int rb) {
 __device__ __forceinline__ Draft draft(const Args& a, int b) {
   return draft_of(a.seqlens, a.new_lens, b, a.T, a.max_pages << a.page_shift);
 }
-// Tiles of all row blocks of a key head of sequence b.
+// What a unit costs in a run, in tiles: its tiles and, for its start and end, kUnitCost.
 template <int ROWS>
-__device__ __forceinline__ int head_tiles(const Args& a, int b) {
+constexpr int kUnitCost = ROWS == 2 * kTile ? 8 : 6;
+template <int ROWS>
+__device__ __forceinline__ int cost_of(const Unit& u) {
+  return u.i1 > u.i0 ? u.count + kUnitCost<ROWS> : 1;
+}
+// That of all row blocks of a key head of sequence b.
+template <int ROWS>
+__device__ __forceinline__ int head_cost(const Args& a, int b) {
   const Draft dr = draft(a, b);
   int n = 0;
 #pragma unroll 1
-  for (int rb = 0; rb < a.blocks; ++rb) n += unit_of<ROWS>(a, dr, rb).count;
+  for (int rb = 0; rb < a.blocks; ++rb) n += cost_of<ROWS>(unit_of<ROWS>(a, dr, rb));
   return n;
 }
-// First tile of CTA c's run: `total` tiles (all within 31 bits) over `ctas` CTAs.
-__device__ __forceinline__ int first_tile(int total, int c, int ctas) {
+// Where CTA c's run starts: a cost of `total` (within 31 bits) over `ctas` CTAs.
+__device__ __forceinline__ int first_place(int total, int c, int ctas) {
   return total / ctas * c + total % ctas * c / ctas;
 }
 
@@ -192,6 +199,10 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   const uint32_t below_hi = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1;
   const uint32_t below_lo = lo >= 32 ? ~0u : lo <= 0 ? 0u : (1u << lo) - 1;
   return below_hi & ~below_lo;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 
 // Parent of drafted token i of sequence b, -1 for the context and (recorded) for what is no
@@ -427,20 +438,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 3) {
     // ------------------------------------------------------------------ scheduler
-    // Where this CTA's run starts: tiles of the sequences summed up to it. The first 32 sequences'
-    // stay in registers.
-    const int mine = lane < a.B ? head_tiles<kRows>(a, lane) : 0;
+    // Where this CTA's run starts: the cost of the sequences summed up to it. The first 32
+    // sequences' stays in registers.
+    const int mine = lane < a.B ? head_cost<kRows>(a, lane) : 0;
     int total = mine;
 #pragma unroll 1
-    for (int b = 32 + lane; b < a.B; b += 32) total += head_tiles<kRows>(a, b);
+    for (int b = 32 + lane; b < a.B; b += 32) total += head_cost<kRows>(a, b);
     total = __reduce_add_sync(0xffffffffu, total) * a.Hkv;
-    const int ctas = min(total, static_cast<int>(gridDim.x));   // each gets at least one tile
-    const int start = first_tile(total, cta, ctas);
-    int left = cta < ctas ? first_tile(total, cta + 1, ctas) - start : 0;
+    const int ctas = min(total, static_cast<int>(gridDim.x));   // each gets at least one
+    const int start = first_place(total, cta, ctas);
+    int left = cta < ctas ? first_place(total, cta + 1, ctas) - start : 0;
     int b = 0, at = 0, per_head = 1;
 #pragma unroll 1
     for (int b0 = 0, before = 0; b0 < a.B; b0 += 32) {
-      const int head = b0 == 0 ? mine : b0 + lane < a.B ? head_tiles<kRows>(a, b0 + lane) : 0;
+      const int head = b0 == 0 ? mine : b0 + lane < a.B ? head_cost<kRows>(a, b0 + lane) : 0;
       int inc = head * a.Hkv;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -458,23 +469,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
     int hk = at / per_head, rb = 0, segs = 0, taken = 0;
-    int tile = at % per_head;   // within the unit, once rb is known
-    bool ok = true, found = false;
+    int pos = at % per_head;   // within the unit's cost, once rb is known
+    bool ok = true, found = false, first = true;
 #pragma unroll 1
     while (left > 0) {
       const Draft dr = draft(a, b);
       const Unit u = unit_of<kRows>(a, dr, rb);
-      if (!found && tile >= u.count && rb + 1 < a.blocks) {
-        tile -= u.count;
+      const int cost = cost_of<kRows>(u), before = cost - u.count;
+      if (!found && pos >= cost && rb + 1 < a.blocks) {
+        pos -= cost;
         ++rb;
         continue;
       }
       found = true;
-      const int count = min(u.count - tile, left), r0 = rb * kRows;
-      const int rows = min(kRows, a.T * a.G - r0), live = min(rows, dr.count * a.G - r0);
-      const int slot = 2 * cta + (taken > 0);
+      // the run's share of the unit's cost, and the tiles in it, which stand at its end
+      const int share = min(cost - pos, left);
+      const int tile = max(pos - before, 0), count = max(pos + share - before, 0) - tile;
+      const int r0 = rb * kRows, rows = min(kRows, a.T * a.G - r0);
+      const int live = min(rows, dr.count * a.G - r0);
+      const int slot = 2 * cta + (first ? 0 : 1);
       if (dr.count < 0 && lane == 0) record_page_error();
-      if (u.i1 > u.i0) {
+      if (u.i1 > u.i0 && count > 0) {
         const int s = segs % kSegments;
         if (!ptx::wait_bounded_warp(bar(BAR_SEG_EMPTY + s), ((segs / kSegments) & 1) ^ 1, abort_p,
                                     kWaitLimitNs)) {
@@ -500,18 +515,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(bar(BAR_SEG_FULL + s));
         }
         ++segs;
+        first = false;
+        // its Q and parents, which are read when the segment before ends
+        if (segs > 1) {
+          for (int r = lane; r < live; r += 32) {
+            const int64_t at = (static_cast<int64_t>(b) * a.T + (r0 + r) / a.G) * a.Hq + hk * a.G +
+                               (r0 + r) % a.G;
+            for (int c = 0; c < D; c += 64) prefetch_l2(static_cast<const uint16_t*>(a.q) + at * D + c);
+          }
+        }
       }
-      if (tile == 0) {
+      if (tile == 0 && count > 0) {
         if (lane == 0) {
           // This run holds the unit's first tile; its last is in the last run that starts before
           // the unit's end.
-          const int end = start + taken + u.count;
+          const int end = start + taken - pos + cost;
           int last = cta;
           if (count < u.count) {
             last = static_cast<int>(static_cast<float>(end) / static_cast<float>(total) * ctas);
             last = min(max(last, cta), ctas - 1);
-            while (first_tile(total, last, ctas) >= end) --last;
-            while (last + 1 < ctas && first_tile(total, last + 1, ctas) < end) ++last;
+            while (first_place(total, last, ctas) >= end) --last;
+            while (last + 1 < ctas && first_place(total, last + 1, ctas) < end) ++last;
           }
           a.units[(static_cast<int64_t>(b) * a.Hkv + hk) * a.blocks + rb] =
               make_int2(slot, count == u.count ? 0 : last - cta + 1);
@@ -529,11 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = -INFINITY;
         }
       }
-      left -= count;
-      taken += count;
-      tile += count;
-      if (tile == u.count) {
-        tile = 0;
+      left -= share;
+      taken += share;
+      pos += share;
+      if (pos == cost) {
+        pos = 0;
         if (++rb == a.blocks) {
           rb = 0;
           if (++hk == a.Hkv) {

@@ -26,9 +26,59 @@ from __future__ import annotations
 import functools
 from typing import NamedTuple
 
-from .binding import _dtype_code, load_library
-from .paged import (_bound, _cache, _call, _check, _count, _default_scale, _library, _ptr,
+from .binding import FA_OK, FaError, _dtype_code, load_library
+from .paged import (_bound, _call, _check, _count, _default_scale, _first, _library, _ptr,
                     _stream_of, _workspace)
+
+_INT_MAX = 2 ** 31 - 1
+
+
+@functools.lru_cache(maxsize=None)
+def _torch():
+    """torch and what the calls below take of it: a few microseconds of GPU work stand against
+    every name looked up."""
+    import torch
+    return (torch, torch.int32, torch.float32, torch.empty_like, torch._C._cuda_getDevice,
+            torch._C._cuda_getCurrentRawStream)
+
+
+def _fits(name, t, shape, dtype, device):
+    """``_check`` with the device's number, which is quicker to ask for than the device."""
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != device
+            or not t.is_contiguous()):
+        _check(name, t, shape, dtype, _torch()[0].device("cuda", device))
+
+
+def _pages(k_pages, v_pages):
+    """Checks a cache's pages: (device, dtype, num_pages, page_size, Hkv, d)."""
+    if k_pages.dim() != 4 or not k_pages.is_cuda or not k_pages.is_contiguous():
+        _first("k_pages", k_pages, 4)
+    device, dtype, shape = k_pages.get_device(), k_pages.dtype, k_pages.shape
+    _fits("v_pages", v_pages, shape, dtype, device)
+    return (device, dtype, *shape)
+
+
+def _sequences(block_table, device):
+    """Checks a block table: (B, max_pages)."""
+    shape = block_table.shape
+    if len(shape) != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = shape
+    if B > _INT_MAX or max_pages > _INT_MAX:
+        raise ValueError("block_table is too large: %s" % list(shape))
+    _fits("block_table", block_table, shape, _torch()[1], device)
+    return B, max_pages
+
+
+def _enqueue(where, fn, device, stream, args):
+    """fn(*args, stream) on device number `device`."""
+    torch, _, _, _, current, raw_stream = _torch()
+    if stream is None and current() == device:
+        rc = fn(*args, raw_stream(device) or None)
+        if rc != FA_OK:
+            raise FaError(rc, where)
+    else:
+        _call(where, fn, torch.device("cuda", device), stream, args)
 
 
 @functools.lru_cache(maxsize=256)
@@ -53,33 +103,34 @@ def fa_paged_tree(q, k_pages, v_pages, block_table, seqlens, o, lse, scale: floa
 def _tree(q, k_pages, v_pages, block_table, seqlens, o, lse, scale, parents, new_lens, window_left,
           workspace, stream):
     """fa_paged_tree; outputs that are None are allocated. Returns o, lse."""
-    import torch
-    device, dtype, B, Hkv, d, page_size, num_pages, max_pages = _cache(
-        k_pages, v_pages, None, block_table, seqlens)
+    torch, int32, float32, empty_like, _, _ = _torch()
+    device, dtype, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages)
+    B, max_pages = _sequences(block_table, device)
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hq, d]")
-    T, Hq = q.shape[1], q.shape[2]
-    _check("q", q, (B, T, Hq, d), dtype, device)
+    _, T, Hq, _ = shape = q.shape
+    _fits("q", q, (B, T, Hq, d), dtype, device)
+    _fits("seqlens", seqlens, (B,), int32, device)
     if parents is not None:
-        _check("parents", parents, (B, T), torch.int32, device)
+        _fits("parents", parents, (B, T), int32, device)
     if new_lens is not None:
-        _check("new_lens", new_lens, (B,), torch.int32, device)
+        _fits("new_lens", new_lens, (B,), int32, device)
     if o is None or lse is None:
-        with _stream_of(stream, device):
+        with _stream_of(stream, q.device):
             if o is None:
-                o = torch.empty_like(q)
+                o = empty_like(q)
             if lse is None:
-                lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
-    _check("o", o, (B, T, Hq, d), dtype, device)
-    _check("lse", lse, (B, Hq, T), torch.float32, device)
+                lse = q.new_empty((B, Hq, T), dtype=float32)
+    _fits("o", o, shape, dtype, device)
+    _fits("lse", lse, (B, Hq, T), float32, device)
     need = 0 if workspace is not None else paged_tree_workspace_size(
         B, T, Hq, Hkv, d, page_size, max_pages)
-    keep, ws, ws_bytes = _workspace(need, workspace, device, stream)
-    _call("fa_paged_tree", _library().fa_paged_tree, device, stream, (
+    keep, ws, ws_bytes = _workspace(need, workspace, q.device, stream)
+    _enqueue("fa_paged_tree", _library().fa_paged_tree, device, stream, (
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         seqlens.data_ptr(), _ptr(parents), _ptr(new_lens), o.data_ptr(), lse.data_ptr(), B, T, Hq,
-        Hkv, d, page_size, num_pages, max_pages, _bound(window_left), float(scale), _dtype_code(q),
-        ws, ws_bytes))
+        Hkv, d, page_size, num_pages, max_pages, _bound(window_left), scale, _dtype_code(q), ws,
+        ws_bytes))
     return o, lse
 
 
@@ -100,20 +151,23 @@ def fa_paged_accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seql
     """Enqueue the move of the drafted tokens that stay behind the context: leaf[b] (int32 [B];
     -1: none) and its ancestors. path int32 [B, T] gets them in their order (-1 behind the last),
     new_seqlens int32 [B] the new lengths; ``weights`` of a cache that keeps them move, too."""
-    import torch
-    device, dtype, B, Hkv, d, page_size, num_pages, max_pages = _cache(
-        k_pages, v_pages, weights, block_table, seqlens)
+    _, int32, float32, _, _, _ = _torch()
+    device, dtype, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages)
+    B, max_pages = _sequences(block_table, device)
     if path.dim() != 2:
         raise ValueError("path must be [B, T]")
     T = _count("T", path.shape[1])
-    _check("path", path, (B, T), torch.int32, device)
-    _check("leaf", leaf, (B,), torch.int32, device)
-    _check("new_seqlens", new_seqlens, (B,), torch.int32, device)
+    _fits("path", path, (B, T), int32, device)
+    _fits("seqlens", seqlens, (B,), int32, device)
+    _fits("leaf", leaf, (B,), int32, device)
+    _fits("new_seqlens", new_seqlens, (B,), int32, device)
+    if weights is not None:
+        _fits("weights", weights, (num_pages, Hkv, page_size), float32, device)
     if parents is not None:
-        _check("parents", parents, (B, T), torch.int32, device)
+        _fits("parents", parents, (B, T), int32, device)
     if new_lens is not None:
-        _check("new_lens", new_lens, (B,), torch.int32, device)
-    _call("fa_paged_accept", _library().fa_paged_accept, device, stream, (
+        _fits("new_lens", new_lens, (B,), int32, device)
+    _enqueue("fa_paged_accept", _library().fa_paged_accept, device, stream, (
         k_pages.data_ptr(), v_pages.data_ptr(), _ptr(weights), block_table.data_ptr(),
         seqlens.data_ptr(), _ptr(parents), leaf.data_ptr(), _ptr(new_lens), path.data_ptr(),
         new_seqlens.data_ptr(), B, T, Hkv, d, page_size, num_pages, max_pages,
@@ -124,12 +178,11 @@ def paged_accept(k_pages, v_pages, block_table, seqlens, leaf, parents, new_lens
                  weights=None, stream=None):
     """path, new_seqlens = the drafted tokens that stay, moved behind the context (see
     ``fa_paged_accept``)."""
-    import torch
     if parents.dim() != 2:
         raise ValueError("parents must be [B, T]")
+    empty_like = _torch()[3]
     with _stream_of(stream, k_pages.device):
-        path = torch.empty_like(parents)
-        new_seqlens = torch.empty_like(seqlens)
+        path, new_seqlens = empty_like(parents), empty_like(seqlens)
     fa_paged_accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seqlens, parents,
                     new_lens, weights, stream)
     return path, new_seqlens
@@ -139,21 +192,18 @@ def fa_paged_copy(k_pages, v_pages, src, dst, rows=None, weights=None, stream=No
     """Enqueue copies of pages: the first rows[m] rows (int32 [M]; None: all) of page src[m] to page
     dst[m] (int32 [M]; both negative: no copy), keys, values and ``weights`` of a cache that keeps
     them."""
-    import torch
-    from .paged import _first
-    device, dtype = _first("k_pages", k_pages, 4)
-    num_pages, page_size, Hkv, d = k_pages.shape
-    _check("v_pages", v_pages, k_pages.shape, dtype, device)
+    _, int32, float32, _, _, _ = _torch()
+    device, dtype, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages)
     if weights is not None:
-        _check("weights", weights, (num_pages, Hkv, page_size), torch.float32, device)
+        _fits("weights", weights, (num_pages, Hkv, page_size), float32, device)
     if src.dim() != 1:
         raise ValueError("src must be [M]")
     M = _count("M", src.shape[0])
-    _check("src", src, (M,), torch.int32, device)
-    _check("dst", dst, (M,), torch.int32, device)
+    _fits("src", src, (M,), int32, device)
+    _fits("dst", dst, (M,), int32, device)
     if rows is not None:
-        _check("rows", rows, (M,), torch.int32, device)
-    _call("fa_paged_copy", _library().fa_paged_copy, device, stream, (
+        _fits("rows", rows, (M,), int32, device)
+    _enqueue("fa_paged_copy", _library().fa_paged_copy, device, stream, (
         k_pages.data_ptr(), v_pages.data_ptr(), _ptr(weights), src.data_ptr(), dst.data_ptr(),
         _ptr(rows), M, Hkv, d, page_size, num_pages, _dtype_code(k_pages)))
 
@@ -179,19 +229,18 @@ def new_page_pool(num_pages: int, device="cuda") -> PagePool:
 
 def _tables(pool, block_table):
     """Checks a pool and a block table: (device, B, max_pages, num_pages)."""
-    import torch
     if block_table.dim() != 2 or not block_table.is_cuda or not block_table.is_contiguous():
         raise ValueError("block_table must be a contiguous 2-D CUDA tensor")
-    device, (B, max_pages) = block_table.device, block_table.shape
-    num_pages = pool.refs.numel()
-    _count("num_pages", num_pages)
-    _count("B", B)
-    _count("max_pages", max_pages)
-    _check("block_table", block_table, (B, max_pages), torch.int32, device)
-    _check("refs", pool.refs, (num_pages,), torch.int32, device)
-    _check("free_pages", pool.free_pages, (num_pages,), torch.int32, device)
-    _check("num_free", pool.num_free, (1,), torch.int32, device)
-    return device, B, max_pages, num_pages
+    int32, device = _torch()[1], block_table.get_device()
+    B, max_pages = _sequences(block_table, device)
+    refs, free_pages, num_free = pool
+    shape = refs.shape
+    if len(shape) != 1 or shape[0] > _INT_MAX:
+        raise ValueError("refs must be [num_pages]")
+    _fits("refs", refs, shape, int32, device)
+    _fits("free_pages", free_pages, shape, int32, device)
+    _fits("num_free", num_free, (1,), int32, device)
+    return device, B, max_pages, shape[0]
 
 
 class Forked(NamedTuple):
@@ -208,35 +257,37 @@ def fa_paged_fork(pool, block_table, seqlens, source, out: Forked, page_size: in
                   stream=None) -> None:
     """Enqueue a fork: sequence c of ``out`` continues sequence source[c] (int32 [C]; -1: empty),
     with its whole pages shared and its last one, where it is filled in part, from the pool."""
-    import torch
+    int32 = _torch()[1]
     device, B, max_pages, num_pages = _tables(pool, block_table)
-    _check("seqlens", seqlens, (B,), torch.int32, device)
+    refs, free_pages, num_free = pool
+    table, lens, src, dst, rows = out
+    _fits("seqlens", seqlens, (B,), int32, device)
     if source.dim() != 1:
         raise ValueError("source must be [C]")
-    C = _count("C", source.shape[0])
-    _check("source", source, (C,), torch.int32, device)
-    _check("out.block_table", out.block_table, (C, max_pages), torch.int32, device)
-    for name in ("seqlens", "copy_src", "copy_dst", "copy_rows"):
-        _check("out." + name, getattr(out, name), (C,), torch.int32, device)
-    _call("fa_paged_fork", _library().fa_paged_fork, device, stream, (
-        block_table.data_ptr(), seqlens.data_ptr(), source.data_ptr(), pool.refs.data_ptr(),
-        pool.free_pages.data_ptr(), pool.num_free.data_ptr(), out.block_table.data_ptr(),
-        out.seqlens.data_ptr(), out.copy_src.data_ptr(), out.copy_dst.data_ptr(),
-        out.copy_rows.data_ptr(), B, C, _count("page_size", page_size), num_pages, max_pages))
+    shape = source.shape
+    C = _count("C", shape[0])
+    _fits("source", source, shape, int32, device)
+    _fits("out.block_table", table, (C, max_pages), int32, device)
+    _fits("out.seqlens", lens, shape, int32, device)
+    _fits("out.copy_src", src, shape, int32, device)
+    _fits("out.copy_dst", dst, shape, int32, device)
+    _fits("out.copy_rows", rows, shape, int32, device)
+    _enqueue("fa_paged_fork", _library().fa_paged_fork, device, stream, (
+        block_table.data_ptr(), seqlens.data_ptr(), source.data_ptr(), refs.data_ptr(),
+        free_pages.data_ptr(), num_free.data_ptr(), table.data_ptr(), lens.data_ptr(),
+        src.data_ptr(), dst.data_ptr(), rows.data_ptr(), B, C, _count("page_size", page_size),
+        num_pages, max_pages))
 
 
 def paged_fork(pool, block_table, seqlens, source, page_size: int, stream=None) -> Forked:
     """New sequences that continue others (see ``fa_paged_fork``), in tables of their own."""
-    import torch
     if block_table.dim() != 2 or source.dim() != 1:
         raise ValueError("block_table must be [B, max_pages] and source [C]")
-    C = source.shape[0]
+    torch, int32, _, empty_like, _, _ = _torch()
     with _stream_of(stream, block_table.device):
-        # one allocation for the lists: the call is a few microseconds long
-        lists = torch.empty((4, C), dtype=torch.int32, device=block_table.device)
-        table = torch.empty((C, block_table.shape[1]), dtype=torch.int32,
-                            device=block_table.device)
-    out = Forked(table, *lists.unbind(0))
+        out = Forked(block_table.new_empty((source.shape[0], block_table.shape[1])),
+                     empty_like(source), empty_like(source), empty_like(source),
+                     empty_like(source))
     fa_paged_fork(pool, block_table, seqlens, source, out, page_size, stream)
     return out
 
@@ -246,20 +297,22 @@ def fa_paged_resize(pool, block_table, old_lens, new_lens, granted, page_size: i
     """Enqueue a change of lengths: sequence b has pages for old_lens[b] tokens and gets those for
     new_lens[b], given back to the pool or taken from it, in its row of block_table. granted
     int32 [B] gets new_lens[b], or old_lens[b] where the pool did not suffice."""
-    import torch
+    int32 = _torch()[1]
     device, B, max_pages, num_pages = _tables(pool, block_table)
-    for name, t in (("old_lens", old_lens), ("new_lens", new_lens), ("granted", granted)):
-        _check(name, t, (B,), torch.int32, device)
-    _call("fa_paged_resize", _library().fa_paged_resize, device, stream, (
+    refs, free_pages, num_free = pool
+    shape = (B,)
+    _fits("old_lens", old_lens, shape, int32, device)
+    _fits("new_lens", new_lens, shape, int32, device)
+    _fits("granted", granted, shape, int32, device)
+    _enqueue("fa_paged_resize", _library().fa_paged_resize, device, stream, (
         block_table.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(), granted.data_ptr(),
-        pool.refs.data_ptr(), pool.free_pages.data_ptr(), pool.num_free.data_ptr(), B,
+        refs.data_ptr(), free_pages.data_ptr(), num_free.data_ptr(), B,
         _count("page_size", page_size), num_pages, max_pages))
 
 
 def paged_resize(pool, block_table, old_lens, new_lens, page_size: int, stream=None):
     """granted int32 [B]: the lengths that the tables have pages for after ``fa_paged_resize``."""
-    import torch
     with _stream_of(stream, block_table.device):
-        granted = torch.empty_like(old_lens)
+        granted = _torch()[3](old_lens)
     fa_paged_resize(pool, block_table, old_lens, new_lens, granted, page_size, stream)
     return granted
