@@ -300,16 +300,45 @@ __global__ void __launch_bounds__(kForkThreads)
 
 // ---------------------------------------------------------------------------------------------
 // Resize, by one cluster: first the pages that shorter sequences give back, then those that
-// longer ones take. The order of the stack is the tables' order, whatever the number of threads
-// and their timing: a page that several tables give back at once goes by the last of them. That
-// one is found through refs: each gives up its reference, and where none is left each bids -1 -
-// its place in the order, by an atomic minimum; the one whose bid stands pushes the page.
-constexpr int kResizeThreads = 1024, kResizeCluster = 8;
+// longer ones take. Bound by latency (a few pages), or by the atomics and scattered accesses of the
+// cluster's SMs (many: XX us for 330000 pages).
+//
+// The order of the stack is the tables' order, whatever the number of threads and their timing: a
+// page that several tables give back at once goes by the last of them. Each gives up its
+// reference; the one that took the last reference pushes the page, unless the page was given up
+// by others of this call as well. Only if there is such a page do all bid for theirs: -1 - the
+// place in the order, by an atomic minimum on the references; the one whose bid stands pushes it.
+//
+// A warp has consecutive items (entries that are given back, or taken), kBatch at a time for each
+// lane, so that as many accesses are on their way; item f belongs to the sequence whose prefix it
+// lies behind, which a lane finds by search once and then by steps.
+constexpr int kResizeThreads = 1024, kResizeCluster = 16, kBatch = 4;
+constexpr int kSmallTables = 8192;   // entries of the tables of a call that one block has
+
+struct ItemWalk {
+  const int* prefix;   // [B + 1], shared memory
+  int b;               // the item's sequence
+  __device__ __forceinline__ ItemWalk(const int* p, int B, int f) : prefix(p) {
+    int lo = 0, hi = B;   // prefix[lo] <= f < prefix[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (prefix[mid] <= f)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;
+  }
+  __device__ __forceinline__ int to(int f) {   // f within the items, no smaller than before
+    while (prefix[b + 1] <= f) ++b;
+    return f - prefix[b];
+  }
+};
 
 __global__ void __launch_bounds__(kResizeThreads, 1)
     fa_paged_resize_kernel(const __grid_constant__ ResizeParams p) {
   extern __shared__ __align__(16) int s_prefix[];   // [B + 1] releases, [B + 1] takes
-  __shared__ int s_warp[32], s_total;
+  __shared__ int s_warp[32], s_total, s_contest;
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -322,6 +351,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
   // the prefixes over the sequences, by every CTA for itself
   const int have = free_pages_of(p.pool);
   auto pages_of = [&](int tokens) { return (tokens + p.page_size - 1) / p.page_size; };
+  if (tid == 0) s_contest = 0;
   int releases = 0, takes = 0;
   for (int b0 = 0; b0 < p.B; b0 += kResizeThreads) {
     const int b = b0 + tid;
@@ -351,54 +381,100 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
     s_take[p.B] = takes;
   }
   __syncthreads();
-  // the sequence of item f: the last one whose first item is at or before it and which has any
-  auto sequence_of = [&](const int* prefix, int f) {
-    int lo = 0, hi = p.B;   // prefix[lo] <= f < prefix[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (prefix[mid] <= f)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    return lo;
+  // this warp's items of n
+  const int warps = ranks * (kResizeThreads / 32), w = rank * (kResizeThreads / 32) + warp;
+  auto first_item = [&](int n, int at) {
+    return static_cast<int>(static_cast<int64_t>(n) * at / warps);
   };
 
   int pushed = 0;
   if (releases > 0) {
-    // this warp's items, in order
-    const int warps = ranks * (kResizeThreads / 32), w = rank * (kResizeThreads / 32) + warp;
-    const int f0 = static_cast<int>(static_cast<int64_t>(releases) * w / warps);
-    const int f1 = static_cast<int>(static_cast<int64_t>(releases) * (w + 1) / warps);
-    auto entry = [&](int f) {
-      const int b = sequence_of(s_release, f);
-      return p.block_table + static_cast<int64_t>(b) * p.max_pages + pages_of(p.new_lens[b]) + f -
-             s_release[b];
+    const int f0 = first_item(releases, w), f1 = first_item(releases, w + 1);
+    // do(i, entry) for the lane's items f0 + lane + 32 i, kBatch entries at a time
+    auto for_items = [&](auto&& batch) {
+      if (f0 + lane >= f1) return;
+      ItemWalk walk(s_release, p.B, f0 + lane);
+      for (int i = 0; f0 + lane + 32 * i < f1; i += kBatch) {
+        int* at[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int f = f0 + lane + 32 * (i + u);
+          at[u] = nullptr;
+          if (f < f1) {
+            const int in = walk.to(f);
+            at[u] = p.block_table + static_cast<int64_t>(walk.b) * p.max_pages +
+                    pages_of(p.new_lens[walk.b]) + in;
+          }
+        }
+        batch(i, at);
+      }
     };
-    for (int f = f0 + lane; f < f1; f += 32) {
-      int* const at = entry(f);
-      const int page = *at;
-      bool ok = page >= 0 && page < p.pool.num_pages;
-      if (ok && atomicSub(p.pool.refs + page, 1) <= 0) {
-        atomicAdd(p.pool.refs + page, 1);   // no table should hold it
-        ok = false;
+    // Bit i: of the lane's item i. Past 64 items a lane there are no bits, and all bid.
+    const bool bits = f1 - f0 <= 2048;
+    uint64_t last = 0, other = 0;   // took the last reference; did not
+    bool contest = !bits;
+    for_items([&](int i, int* (&at)[kBatch]) {
+      int page[kBatch], old[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) page[u] = at[u] ? *at[u] : -1;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        old[u] = 0;
+        if (page[u] >= 0 && page[u] < p.pool.num_pages)
+          old[u] = atomicSub(p.pool.refs + page[u], 1);
+        else
+          page[u] = -1;
       }
-      if (!ok) {
-        record_page_error();
-        *at = -1;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (!at[u]) continue;
+        if (old[u] <= 0) {   // outside the pool, or held by no table
+          if (page[u] >= 0) atomicAdd(p.pool.refs + page[u], 1);
+          record_page_error();
+          *at[u] = -1;
+        } else if (bits) {
+          (old[u] == 1 ? last : other) |= 1ull << (i + u);
+        }
       }
-    }
+    });
     cluster.sync();
-    for (int f = f0 + lane; f < f1; f += 32) {
-      const int page = *entry(f);
-      if (page >= 0 && load_l2(p.pool.refs + page) <= 0) atomicMin(p.pool.refs + page, -1 - f);
-    }
+    // a page without references that this call gave up more than once
+    if (bits && other)
+      for_items([&](int i, int* (&at)[kBatch]) {
+        int left[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          left[u] = other >> (i + u) & 1 ? load_l2(p.pool.refs + *at[u]) : 1;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) contest |= left[u] == 0;
+      });
+    if (contest) *cluster.map_shared_rank(&s_contest, 0) = 1;
     cluster.sync();
+    const bool bid = *cluster.map_shared_rank(&s_contest, 0) != 0;
+    if (bid) {
+      for_items([&](int i, int* (&at)[kBatch]) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int page = at[u] ? *at[u] : -1;
+          if (page >= 0 && load_l2(p.pool.refs + page) <= 0)
+            atomicMin(p.pool.refs + page, -1 - (f0 + lane + 32 * (i + u)));
+        }
+      });
+      cluster.sync();
+    }
+    // whether item i is the one that pushes its page
+    auto pushes = [&](int i, int page) {
+      if (!bid) return (last >> i & 1) != 0;
+      return page >= 0 && load_l2(p.pool.refs + page) == -1 - (f0 + lane + 32 * i);
+    };
     int count = 0;
-    for (int f = f0 + lane; f < f1; f += 32) {
-      const int page = *entry(f);
-      count += page >= 0 && load_l2(p.pool.refs + page) == -1 - f;
-    }
+    if (!bid)
+      count = __popcll(last);
+    else
+      for_items([&](int i, int* (&at)[kBatch]) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) count += at[u] && pushes(i + u, *at[u]);
+      });
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) count += __shfl_xor_sync(0xffffffffu, count, off);
     int all;
@@ -411,34 +487,83 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
       pushed += n;
       if (r < rank) before += n;
     }
-    for (int f = f0; f < f1; f += 32) {
-      int* const at = f + lane < f1 ? entry(f + lane) : nullptr;
-      const int page = at ? *at : -1;
-      const bool mine = page >= 0 && load_l2(p.pool.refs + page) == -1 - (f + lane);
-      const unsigned all_mine = __ballot_sync(0xffffffffu, mine);
-      if (mine) {
-        const int place = have + before + __popc(all_mine & ((1u << lane) - 1));
-        if (place < p.pool.num_pages)
-          p.pool.free_pages[place] = page;
-        else
-          record_page_error();   // more free pages than the pool has
-        p.pool.refs[page] = 0;
+    // the warp's items in order: 32 of them for each i
+    {
+      ItemWalk walk(s_release, p.B, min(f0 + lane, releases - 1));
+      const int steps = (f1 - f0 + 31) / 32;
+      for (int i = 0; i < steps; i += kBatch) {
+        int* at[kBatch];
+        int page[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int f = f0 + lane + 32 * (i + u);
+          at[u] = nullptr;
+          page[u] = -1;
+          if (f < f1) {
+            const int in = walk.to(f);
+            at[u] = p.block_table + static_cast<int64_t>(walk.b) * p.max_pages +
+                    pages_of(p.new_lens[walk.b]) + in;
+            page[u] = *at[u];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const bool mine = at[u] && pushes(i + u, page[u]);
+          const unsigned all_mine = __ballot_sync(0xffffffffu, mine);
+          if (mine) {
+            const int place = have + before + __popc(all_mine & ((1u << lane) - 1));
+            if (place < p.pool.num_pages)
+              p.pool.free_pages[place] = page[u];
+            else
+              record_page_error();   // more free pages than the pool has
+            if (bid) p.pool.refs[page[u]] = 0;
+          }
+          if (at[u]) *at[u] = -1;
+          before += __popc(all_mine);
+        }
       }
-      if (at) *at = -1;
-      before += __popc(all_mine);
     }
     pushed = min(pushed, p.pool.num_pages - have);
     cluster.sync();   // the stack is whole; no CTA leaves while another reads its count
   }
 
+  // The takes. What fits is a prefix of them: up to the largest one within the stack, found by
+  // every CTA for itself.
   const int stack = have + pushed;
-  for (int f = rank * kResizeThreads + tid; f < takes; f += ranks * kResizeThreads) {
-    const int b = sequence_of(s_take, f);
-    if (s_take[b + 1] > stack) continue;   // does not fit
-    p.block_table[static_cast<int64_t>(b) * p.max_pages + pages_of(p.old_lens[b]) + f - s_take[b]] =
-        take_page(p.pool, stack - 1 - f);
+  int taken = 0;
+  for (int b = tid; b < p.B; b += kResizeThreads)
+    if (s_take[b + 1] <= stack) taken = max(taken, s_take[b + 1]);
+  taken = __reduce_max_sync(0xffffffffu, taken);
+  __syncthreads();
+  if (lane == 0) s_warp[warp] = taken;
+  __syncthreads();
+  taken = __reduce_max_sync(0xffffffffu, s_warp[lane]);
+  {
+    const int f0 = first_item(taken, w), f1 = first_item(taken, w + 1);
+    if (f0 + lane < f1) {
+      ItemWalk walk(s_take, p.B, f0 + lane);
+      for (int f = f0 + lane; f < f1; f += 32 * kBatch) {
+        int page[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          page[u] = f + 32 * u < f1 ? load_l2(p.pool.free_pages + stack - 1 - (f + 32 * u)) : -1;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (f + 32 * u >= f1) break;
+          const int in = walk.to(f + 32 * u);
+          if (page[u] >= 0 && page[u] < p.pool.num_pages) {
+            p.pool.refs[page[u]] = 1;
+          } else {
+            record_page_error();
+            page[u] = -1;
+          }
+          p.pool.free_pages[stack - 1 - (f + 32 * u)] = -1;
+          p.block_table[static_cast<int64_t>(walk.b) * p.max_pages + pages_of(p.old_lens[walk.b]) +
+                        in] = page[u];
+        }
+      }
+    }
   }
-  // what fits is a prefix of the takes
   for (int b = rank * kResizeThreads + tid; b < p.B; b += ranks * kResizeThreads) {
     const int from = p.old_lens[b], to = p.new_lens[b];
     const bool ok = from >= 0 && to >= 0 && from <= capacity && to <= capacity;
@@ -446,20 +571,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
     p.granted[b] = ok && fits ? to : from;
   }
   if (ranks > 1) cluster.sync();   // every CTA has read num_free
-  if (rank == 0) {
-    // takes of the sequences that fit: the largest prefix within the stack
-    int most = 0;
-    for (int b = tid; b < p.B; b += kResizeThreads)
-      if (s_take[b + 1] <= stack) most = max(most, s_take[b + 1]);
-    most = __reduce_max_sync(0xffffffffu, most);
-    __syncthreads();
-    if (lane == 0) s_warp[warp] = most;
-    __syncthreads();
-    if (tid < 32) {
-      most = __reduce_max_sync(0xffffffffu, s_warp[tid]);
-      if (tid == 0) *p.pool.num_free = stack - most;
-    }
-  }
+  if (rank == 0 && tid == 0) *p.pool.num_free = stack - taken;
 }
 
 int shift_of(int page_size) {
@@ -520,11 +632,16 @@ cudaError_t launch_paged_fork(const ForkParams& p, cudaStream_t stream) {
 
 cudaError_t launch_paged_resize(const ResizeParams& p, cudaStream_t stream) {
   constexpr int kMost = 2 * (kMaxPoolBatch + 1) * 4;
-  const cudaError_t err = cudaFuncSetAttribute(
+  cudaError_t err = cudaFuncSetAttribute(
       fa_paged_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   if (err != cudaSuccess) return err;
-  return launch_paged(fa_paged_resize_kernel, kResizeCluster, kResizeThreads, 2 * (p.B + 1) * 4,
-                      stream, kResizeCluster, p);
+  err = cudaFuncSetAttribute(fa_paged_resize_kernel,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err != cudaSuccess) return err;
+  // Small tables are one block's: two calls for 16 sequences of 258 pages XX us instead of 13.9.
+  const int ctas = static_cast<int64_t>(p.B) * p.max_pages <= kSmallTables ? 1 : kResizeCluster;
+  return launch_paged(fa_paged_resize_kernel, ctas, kResizeThreads, 2 * (p.B + 1) * 4, stream,
+                      ctas > 1 ? ctas : 0, p);
 }
 
 cudaError_t read_and_clear_pool_error(int* bits) { return read_and_clear_error(bits); }

@@ -36,6 +36,7 @@
 // P is rounded to the type once for the product with V, a rounding of the same size as the
 // output's. fp16 ends at 2^-24, so there P is taken 2^11 times as large, and up to 2^4 more until
 // a grown maximum moves the offset: what is lost are probabilities below 2^-36 of the largest.
+#include <cooperative_groups.h>
 #include <stddef.h>
 
 #include <algorithm>
@@ -48,6 +49,7 @@ namespace fa {
 namespace {
 
 using namespace paged;
+namespace cg = cooperative_groups;
 
 constexpr int kTile = 128;                     // tokens of a tile, and rows of a row tile
 constexpr int kSoftmaxThreads = 512;
@@ -366,7 +368,9 @@ __device__ __noinline__ void add_not_finite(const Args& a, const Segment& sg, in
   }
 }
 
-template <int D, bool FP16, int QT>
+// SHORT: a cluster of CTAs has one unit, each CTA an equal share of its tiles, and the parts are
+// joined through distributed shared memory. Otherwise: runs over all units.
+template <int D, bool FP16, int QT, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_paged_tree_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
@@ -429,6 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_p = 1;
     atomicOr(&g_error, kTimeoutBit);
   };
+  // SHORT: this CTA's part, where K and V were
+  float* const short_part = reinterpret_cast<float*>(smem_raw + L::kK);                 // [128][D]
+  float2* const short_ml = reinterpret_cast<float2*>(smem_raw + L::kK + kTile * D * 4);   // [128]
+  static_assert(!SHORT || L::kK + kTile * (D * 4 + 8) <= L::kMisc, "the part's place");
   // Segment s of the run for the warps that read them; false when a wait has run out.
   auto segment = [&](int s) {
     return ptx::wait_bounded(bar(BAR_SEG_FULL + s % kSegments), (s / kSegments) & 1, abort_p,
@@ -438,6 +446,58 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 3) {
     // ------------------------------------------------------------------ scheduler
+    int segs = 0;
+    bool ok = true;
+    auto publish = [&](int b, int hk, Draft dr, const Unit& u, int r0, int live, int tile, int count,
+                       int slot) {
+      const int s = segs % kSegments;
+      ok = ptx::wait_bounded_warp(bar(BAR_SEG_EMPTY + s), ((segs / kSegments) & 1) ^ 1, abort_p,
+                                  kWaitLimitNs);
+      if (ok && lane == 0) {
+        Segment& g = ms.seg[s];
+        g.b = b;
+        g.hk = hk;
+        g.base = dr.base;
+        g.drafted = dr.count;
+        g.r0 = r0;
+        g.live = live;
+        g.first_key = (u.first + tile) * kTile;
+        g.count = count;
+        g.lo = a.window_left < 0 ? 0 : max(0, dr.base - a.window_left);
+        g.hi = dr.base + u.i1;
+        g.full_lo = a.window_left < 0 ? 0 : dr.base + u.i1 - 1 - a.window_left;
+        g.full_hi = a.parents ? dr.base : dr.base + u.i0 + 1;
+        g.whole = !SHORT && count == u.count;
+        g.slot = slot;
+        ptx::mbar_arrive(bar(BAR_SEG_FULL + s));
+      }
+      ++segs;
+    };
+    // rows [max(live, 0), rows) of a unit, the padding's
+    auto clear = [&](int b, int hk, int r0, int live, int rows) {
+      constexpr int kChunks = D / 8;
+#pragma unroll 1
+      for (int w = max(live, 0) * kChunks + lane; w < rows * kChunks; w += 32) {
+        const int r = r0 + w / kChunks, token = r / a.G, head = hk * a.G + r % a.G;
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) +
+                                 ((static_cast<int64_t>(b) * a.T + token) * a.Hq + head) *
+                                     D)[w % kChunks] = make_uint4(0, 0, 0, 0);
+        if (w % kChunks == 0)
+          a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = -INFINITY;
+      }
+    };
+    if constexpr (SHORT) {
+      const int rank = static_cast<int>(cg::this_cluster().block_rank());
+      const int ranks = static_cast<int>(cg::this_cluster().num_blocks());
+      const int b = cta / ranks / a.Hkv, hk = cta / ranks % a.Hkv;
+      const Draft dr = draft(a, b);
+      const Unit u = unit_of<kRows>(a, dr, 0);
+      const int tile = u.count * rank / ranks, count = u.count * (rank + 1) / ranks - tile;
+      const int live = dr.count * a.G;
+      if (dr.count < 0 && lane == 0) record_page_error();
+      if (u.i1 > u.i0 && count > 0) publish(b, hk, dr, u, 0, live, tile, count, 0);
+      if (rank == 0) clear(b, hk, 0, live, a.T * a.G);
+    } else {
     // Where this CTA's run starts: the cost of the sequences summed up to it. The first 32
     // sequences' stays in registers.
     const int mine = lane < a.B ? head_cost<kRows>(a, lane) : 0;
@@ -468,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    int hk = at / per_head, rb = 0, segs = 0, taken = 0;
+    int hk = at / per_head, rb = 0, taken = 0;
     int pos = at % per_head;   // within the unit's cost, once rb is known
-    bool ok = true, found = false, first = true;
+    bool found = false, first = true;
 #pragma unroll 1
     while (left > 0) {
       const Draft dr = draft(a, b);
@@ -490,31 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = 2 * cta + (first ? 0 : 1);
       if (dr.count < 0 && lane == 0) record_page_error();
       if (u.i1 > u.i0 && count > 0) {
-        const int s = segs % kSegments;
-        if (!ptx::wait_bounded_warp(bar(BAR_SEG_EMPTY + s), ((segs / kSegments) & 1) ^ 1, abort_p,
-                                    kWaitLimitNs)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          Segment& g = ms.seg[s];
-          g.b = b;
-          g.hk = hk;
-          g.base = dr.base;
-          g.drafted = dr.count;
-          g.r0 = r0;
-          g.live = live;
-          g.first_key = (u.first + tile) * kTile;
-          g.count = count;
-          g.lo = a.window_left < 0 ? 0 : max(0, dr.base - a.window_left);
-          g.hi = dr.base + u.i1;
-          g.full_lo = a.window_left < 0 ? 0 : dr.base + u.i1 - 1 - a.window_left;
-          g.full_hi = a.parents ? dr.base : dr.base + u.i0 + 1;
-          g.whole = count == u.count;
-          g.slot = slot;
-          ptx::mbar_arrive(bar(BAR_SEG_FULL + s));
-        }
-        ++segs;
+        publish(b, hk, dr, u, r0, live, tile, count, slot);
+        if (!ok) break;
         first = false;
         // its Q and parents, which are read when the segment before ends
         if (segs > 1) {
@@ -526,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (tile == 0 && count > 0) {
-        if (lane == 0) {
+        if (a.units && lane == 0) {
           // This run holds the unit's first tile; its last is in the last run that starts before
           // the unit's end.
           const int end = start + taken - pos + cost;
@@ -540,18 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.units[(static_cast<int64_t>(b) * a.Hkv + hk) * a.blocks + rb] =
               make_int2(slot, count == u.count ? 0 : last - cta + 1);
         }
-        // the padding's rows
-        constexpr int kChunks = D / 8;
-#pragma unroll 1
-        for (int w = max(live, 0) * kChunks + lane; w < rows * kChunks; w += 32) {
-          const int r = r0 + w / kChunks, token = r / a.G, head = hk * a.G + r % a.G;
-          reinterpret_cast<uint4*>(
-              static_cast<uint16_t*>(a.o) +
-              ((static_cast<int64_t>(b) * a.T + token) * a.Hq + head) * D)[w % kChunks] =
-              make_uint4(0, 0, 0, 0);
-          if (w % kChunks == 0)
-            a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = -INFINITY;
-        }
+        clear(b, hk, r0, live, rows);
       }
       left -= share;
       taken += share;
@@ -566,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+    }
     }
     if (ok) {   // the end
       const int s = segs % kSegments;
@@ -840,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(bar(BAR_Q_FULL));
     };
-    bool go = next_segment(0);
+    bool go = next_segment(0), had = false;
     if (go) load_q(0);
 #pragma unroll 1
     for (int segs = 0; go; ++segs) {
@@ -1015,8 +1042,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Where this thread's row goes. Two row tiles: a row's 16-byte pieces are written by
         // consecutive lanes, by way of shared memory (from its own thread each store touches 32
         // lines: 11000 cycles for 256 rows, not 6000).
-        char* const own = whole ? reinterpret_cast<char*>(o_row)
-                                : reinterpret_cast<char*>(a.part_o + part * D);
+        float* const part_row = SHORT ? short_part + my * D : a.part_o + part * D;
+        char* const own = reinterpret_cast<char*>(whole ? static_cast<void*>(o_row) : part_row);
         const int wide = whole ? 2 : 4;                // bytes of a value
         const int live_rows = sn.live - (my - lane);   // of this warp's 32
         constexpr int kCols = QT == 2 ? D / 2 : D / 4, kChunk = L::kChunk;
@@ -1074,13 +1101,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (ms.not_finite[segs & 1] == segs + 1 && mine)
-          add_not_finite<FP16>(a, sn, token, D, c0, kCols, whole ? nullptr : a.part_o + part * D,
+          add_not_finite<FP16>(a, sn, token, D, c0, kCols, whole ? nullptr : part_row,
                                whole ? o_row : nullptr);
         if (mine && c0 == 0) {
           if (whole)
             a.lse[(static_cast<int64_t>(sn.b) * a.Hq + head) * a.T + token] = lse_of(m, l);
           else
-            a.part_ml[part] = make_float2(m, l);
+            (SHORT ? short_ml + my : a.part_ml + part)[0] = make_float2(m, l);
         }
       }
       n0 += ms.seg[segs % kSegments].count;
@@ -1088,7 +1115,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) segment_read(segs);
       ptx::tc_fence_before_sync();
       ptx::mbar_arrive(bar(BAR_O_FREE));
+      if constexpr (SHORT) had = true;
     }
+    // a share without tiles (nothing was loaded to where this goes)
+    if (SHORT && !had && tid < kTile) short_ml[tid] = make_float2(-INFINITY, 0.f);
+  }
+
+  if constexpr (SHORT) {
+    // ------------------------------------------------------------------ join
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank());
+    const int ranks = static_cast<int>(cluster.num_blocks());
+    __syncwarp();
+    cluster.sync();   // every CTA's part is in its shared memory
+    const int b = cta / ranks / a.Hkv, hk = cta / ranks % a.Hkv;
+    const int live = draft(a, b).count * a.G;
+    // four columns of a row a thread, the rows shared out over the cluster
+#pragma unroll 1
+    for (int at = rank * kThreads + threadIdx.x; at < live * (D / 4); at += ranks * kThreads) {
+      const int r = at / (D / 4), c = at % (D / 4);
+      float m = -INFINITY, l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int x = 0; x < ranks; ++x) {
+        const float2 ml = *cluster.map_shared_rank(short_ml + r, x);
+        if (ml.x == -INFINITY) continue;   // saw nothing, and may hold anything
+        const float4 v =
+            *reinterpret_cast<const float4*>(cluster.map_shared_rank(short_part + r * D + 4 * c, x));
+        const float top = fmaxf(m, ml.x);
+        const float f = ptx::exp2_approx(m - top), g = ptx::exp2_approx(ml.x - top);
+        m = top;
+        l = l * f + ml.y * g;
+        acc.x = acc.x * f + v.x * g;
+        acc.y = acc.y * f + v.y * g;
+        acc.z = acc.z * f + v.z * g;
+        acc.w = acc.w * f + v.w * g;
+      }
+      const float inv = inverse(l);
+      const int token = r / a.G, head = hk * a.G + r % a.G;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) +
+                                ((static_cast<int64_t>(b) * a.T + token) * a.Hq + head) * D + 4 * c) =
+          make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
+      if (c == 0) a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = lse_of(m, l);
+    }
+    __syncwarp();
+    cluster.sync();   // no CTA leaves while another reads its part
   }
 
   // ------------------------------------------------------------------ teardown
@@ -1149,9 +1220,27 @@ __global__ void __launch_bounds__(kJoinThreads)
 // Row tiles of a unit, and with it its rows: two where a key head has more than 128 rows.
 int row_tiles(int T, int Hq, int Hkv) { return static_cast<int64_t>(T) * (Hq / Hkv) > kTile ? 2 : 1; }
 
-// Workspace: the parts' O, their offsets and sums, the units' parts.
+// The smallest calls: 0, or the CTAs of a cluster that has one unit. A unit of up to kShortTiles
+// tiles for each CTA of a cluster, and few enough units that all clusters run at once, takes one
+// launch without a workspace. Units of one CTA may take a second turn.
+constexpr int kShortTiles = 4;
+int resident_clusters(int ctas) {   // of one CTA on each SM, as the runtime counts them on a GB300
+  return ctas == 8 ? 15 : ctas == 4 ? 36 : ctas == 2 ? 76 : 152;
+}
+int choose_short(int B, int T, int Hq, int Hkv, int64_t tiles) {
+  if (row_tiles(T, Hq, Hkv) > 1) return 0;
+  const int64_t units = static_cast<int64_t>(B) * Hkv;
+  for (int ctas = 8; ctas >= 2; ctas /= 2)
+    if (units <= resident_clusters(ctas) && ctas / 2 < tiles)
+      return tiles <= ctas * kShortTiles ? ctas : 0;
+  return units <= 2 * resident_clusters(1) && tiles <= kShortTiles ? 1 : 0;
+}
+
+// Workspace: the parts' O, their offsets and sums, the units' parts; nothing where a unit is one
+// tile, and never split.
 struct Layout {
   int64_t ctas, blocks, part_rows;
+  bool join;
   size_t part_ml, units, end;
 };
 Layout layout(int B, int T, int Hq, int Hkv, int d, int64_t capacity) {
@@ -1160,9 +1249,10 @@ Layout layout(int B, int T, int Hq, int Hkv, int d, int64_t capacity) {
   l.blocks = (rows + unit - 1) / unit;
   l.part_rows = std::min(rows, unit);
   l.ctas = std::min<int64_t>(kSms, B * Hkv * l.blocks * ((capacity + kTile - 1) / kTile));
+  l.join = capacity > kTile;
   l.part_ml = static_cast<size_t>(2 * l.ctas * l.part_rows * d) * 4;
   l.units = l.part_ml + static_cast<size_t>(2 * l.ctas * l.part_rows) * 8;
-  l.end = l.units + static_cast<size_t>(B * Hkv * l.blocks) * 8;
+  l.end = l.join ? l.units + static_cast<size_t>(B * Hkv * l.blocks) * 8 : 0;
   return l;
 }
 
@@ -1183,7 +1273,7 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t stream) {
   a.lse = p.lse;
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
-  a.units = reinterpret_cast<int2*>(ws + l.units);
+  a.units = l.join ? reinterpret_cast<int2*>(ws + l.units) : nullptr;
   a.B = c.B;
   a.T = p.T;
   a.Hq = p.Hq;
@@ -1202,14 +1292,23 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t stream) {
   if (!encode_pages(&tm_k, c.k_pages, c, a.box_rows, 1, FP16) ||
       !encode_pages(&tm_v, c.v_pages, c, a.box_rows, 1, FP16))
     return cudaErrorInvalidValue;
-  auto kernel = fa_paged_tree_kernel<D, FP16, QT>;
   const int smem = static_cast<int>(Smem<D, QT>::kDynamic);
+  if constexpr (QT == 1) {
+    if (const int cluster = choose_short(c.B, p.T, p.Hq, c.Hkv, (capacity + kTile - 1) / kTile)) {
+      auto kernel = fa_paged_tree_kernel<D, FP16, 1, true>;
+      const cudaError_t err =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (err != cudaSuccess) return err;
+      return launch_paged(kernel, static_cast<int64_t>(c.B) * c.Hkv * cluster, kThreads, smem,
+                          stream, cluster > 1 ? cluster : 0, tm_k, tm_v, a);
+    }
+  }
+  auto kernel = fa_paged_tree_kernel<D, FP16, QT, false>;
   cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   err = launch_paged(kernel, l.ctas, kThreads, smem, stream, 0, tm_k, tm_v, a);
-  // units of one tile are never split: nothing to join
-  if (err != cudaSuccess || capacity <= kTile) return err;
+  if (err != cudaSuccess || !l.join) return err;
   const int64_t rows = static_cast<int64_t>(c.B) * p.T * p.Hq;
   return launch_paged(fa_paged_tree_join_kernel<D, FP16, QT * kTile>,
                       (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), kJoinThreads, 0, stream, 0,
@@ -1225,7 +1324,9 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t stream) {
 }  // namespace
 
 size_t paged_tree_workspace(int B, int T, int Hq, int Hkv, int d, int page_size, int max_pages) {
-  return layout(B, T, Hq, Hkv, d, static_cast<int64_t>(max_pages) * page_size).end;
+  const int64_t capacity = static_cast<int64_t>(max_pages) * page_size;
+  if (choose_short(B, T, Hq, Hkv, (capacity + kTile - 1) / kTile)) return 0;
+  return layout(B, T, Hq, Hkv, d, capacity).end;
 }
 
 cudaError_t launch_paged_tree(const TreeParams& p, cudaStream_t stream) {

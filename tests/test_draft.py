@@ -58,6 +58,25 @@ def resize(lib, table=A[0], old=A[1], new=A[2], granted=A[3], refs=A[4], free=A[
                                None)
 
 
+def test_tree_workspace_sizes(lib):
+    size = lib.fa_paged_tree_workspace_size
+    # parts of two runs on each of 152 SMs: up to 128 rows (256 from 129 on), then the units
+    assert size(16, 16, 32, 8, 128, 16, 1024) == 304 * 64 * (128 * 4 + 8) + 16 * 8 * 8
+    assert size(8, 64, 32, 8, 128, 64, 512) == 304 * 256 * (128 * 4 + 8) + 8 * 8 * 8
+    assert size(8, 65, 32, 8, 128, 64, 512) == 304 * 256 * (128 * 4 + 8) + 8 * 8 * 2 * 8
+    assert size(1, 300, 1, 1, 64, 64, 4) == 2 * 4 * 256 * (64 * 4 + 8) + 2 * 8
+    assert size(1, 300, 1, 1, 64, 64, 2) == 0                 # one tile: never split
+    # clusters of 8, 4 and 2 CTAs, and one CTA, with up to four tiles of 128 tokens each
+    for units, tiles in ((1, 32), (15, 32), (16, 16), (36, 16), (37, 8), (76, 8), (77, 4), (304, 4)):
+        assert size(units, 8, 4, 1, 64, 128, tiles) == 0, units
+        assert size(units, 8, 4, 1, 64, 128, tiles + 1) > 0, units
+    assert size(305, 8, 4, 1, 64, 128, 4) > 0
+    assert size(1, 129, 1, 1, 64, 128, 4) > 0                 # two row tiles
+    assert size(2, 8, 8, 3, 64, 16, 10) == 0                  # 8 % 3
+    assert size(2, 8, 8, 2, 64, 17, 10) == 0                  # page size
+    assert size(2, 1025, 8, 2, 64, 16, 10) == 0
+
+
 def test_tree_refusals(lib):
     for name in ("q", "kp", "vp", "table", "lens", "o", "lse"):
         assert tree(lib, **{name: 0}) == NULL
@@ -69,6 +88,10 @@ def test_tree_refusals(lib):
     assert tree(lib, dtype=7) == DTYPE
     assert tree(lib, scale=math.nan) == SCALE
     assert tree(lib, scale=3e38) == SCALE                 # infinite in log2 units
+    assert tree(lib, ws=0) == NULL
+    assert tree(lib, ws_bytes=100) == WORKSPACE
+    assert tree(lib, ws=A[9] + 8) == ALIGN
+    assert tree(lib, ws=A[7]) == ALIAS
     assert tree(lib, o=A[7] + 2) == ALIGN
     assert tree(lib, parents=A[5] + 1) == ALIGN
     assert tree(lib, lse=A[8] + 2) == ALIGN

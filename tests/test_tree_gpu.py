@@ -69,6 +69,26 @@ def test_tokens_and_head_groups(T, Hq, Hkv, d, dtype, kind):
     check_tree(*run(c, q, parents), tree_ref(c, q, default_scale(d), parents), (T, Hq, kind))
 
 
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "bf16")])
+@pytest.mark.parametrize("B,tokens,T,Hq,Hkv,window", [
+    (1, 4096, 8, 4, 1, -1), (1, 4097, 8, 4, 1, -1), (5, 3000, 3, 12, 3, -1), (4, 2048, 16, 32, 4, -1),
+    (4, 2049, 16, 32, 4, -1), (9, 1024, 4, 16, 4, 300), (38, 1024, 2, 4, 2, -1), (38, 1025, 2, 4, 2, -1),
+    (77, 512, 5, 3, 1, -1), (77, 513, 5, 3, 1, 100), (152, 400, 1, 8, 2, -1), (153, 400, 1, 8, 2, -1),
+    (305, 128, 30, 4, 1, -1)])
+def test_short_and_long_tables(d, dtype, B, tokens, T, Hq, Hkv, window):
+    """Both sides of the rule that gives a unit to a cluster: few and many units, tables up to and
+    past its tiles, sequences that leave some CTAs of a cluster without any."""
+    r = torch.Generator().manual_seed(B * tokens)
+    total = [tokens] + torch.randint(T, min(tokens, 2500) + 1, (B - 1,), generator=r).tolist()
+    new = [T] + torch.randint(0, T + 1, (B - 1,), generator=r).tolist()
+    c = draft_cache([n - m for n, m in zip(total, new)], new, 16, Hkv, d, dtype, seed=B)
+    q, parents = queries(c, B, T, Hq), random_trees(c.g, B, T)
+    got = run(c, q, parents, new, window)
+    check_tree(*got, tree_ref(c, q, default_scale(d), parents, new, window), (B, tokens))
+    again = run(c, q, parents, new, window)
+    assert same_bits(got[0], again[0]) and same_bits(got[1], again[1])
+
+
 def test_most_tokens():
     """1024 drafted tokens, as a chain without parents, as the same chain with them, and as trees."""
     T = 1024
