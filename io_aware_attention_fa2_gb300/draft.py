@@ -27,7 +27,7 @@ import functools
 from typing import NamedTuple
 
 from .binding import FA_OK, FaError, _dtype_code, load_library
-from .paged import (_bound, _call, _check, _count, _default_scale, _first, _library, _ptr,
+from .paged import (_NO_CONTEXT, _bound, _call, _check, _count, _default_scale, _first, _library, _ptr,
                     _stream_of, _workspace)
 
 _INT_MAX = 2 ** 31 - 1
@@ -115,17 +115,20 @@ def _tree(q, k_pages, v_pages, block_table, seqlens, o, lse, scale, parents, new
         _fits("parents", parents, (B, T), int32, device)
     if new_lens is not None:
         _fits("new_lens", new_lens, (B,), int32, device)
+    if o is not None:
+        _fits("o", o, shape, dtype, device)
+    if lse is not None:
+        _fits("lse", lse, (B, Hq, T), float32, device)
     if o is None or lse is None:
-        with _stream_of(stream, q.device):
+        with _NO_CONTEXT if stream is None else _stream_of(stream, q.device):
             if o is None:
                 o = empty_like(q)
             if lse is None:
-                lse = q.new_empty((B, Hq, T), dtype=float32)
-    _fits("o", o, shape, dtype, device)
-    _fits("lse", lse, (B, Hq, T), float32, device)
+                lse = torch.empty((B, Hq, T), dtype=float32, device=q.device)
     need = 0 if workspace is not None else paged_tree_workspace_size(
         B, T, Hq, Hkv, d, page_size, max_pages)
-    keep, ws, ws_bytes = _workspace(need, workspace, q.device, stream)
+    keep, ws, ws_bytes = ((None, None, 0) if need == 0 and workspace is None else
+                          _workspace(need, workspace, q.device, stream))
     _enqueue("fa_paged_tree", _library().fa_paged_tree, device, stream, (
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         seqlens.data_ptr(), _ptr(parents), _ptr(new_lens), o.data_ptr(), lse.data_ptr(), B, T, Hq,
@@ -151,27 +154,39 @@ def fa_paged_accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seql
     """Enqueue the move of the drafted tokens that stay behind the context: leaf[b] (int32 [B];
     -1: none) and its ancestors. path int32 [B, T] gets them in their order (-1 behind the last),
     new_seqlens int32 [B] the new lengths; ``weights`` of a cache that keeps them move, too."""
-    _, int32, float32, _, _, _ = _torch()
-    device, dtype, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages)
-    B, max_pages = _sequences(block_table, device)
     if path.dim() != 2:
         raise ValueError("path must be [B, T]")
-    T = _count("T", path.shape[1])
-    _fits("path", path, (B, T), int32, device)
+    _accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seqlens, parents, new_lens,
+            weights, stream)
+
+
+def _accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seqlens, parents, new_lens,
+            weights, stream):
+    """fa_paged_accept; outputs that are None are allocated. Returns path, new_seqlens."""
+    _, int32, float32, empty_like, _, _ = _torch()
+    device, dtype, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages)
+    B, max_pages = _sequences(block_table, device)
+    T = _count("T", (parents if path is None else path).shape[1])
     _fits("seqlens", seqlens, (B,), int32, device)
     _fits("leaf", leaf, (B,), int32, device)
-    _fits("new_seqlens", new_seqlens, (B,), int32, device)
     if weights is not None:
         _fits("weights", weights, (num_pages, Hkv, page_size), float32, device)
     if parents is not None:
         _fits("parents", parents, (B, T), int32, device)
     if new_lens is not None:
         _fits("new_lens", new_lens, (B,), int32, device)
+    if path is None:
+        with _NO_CONTEXT if stream is None else _stream_of(stream, k_pages.device):
+            path, new_seqlens = empty_like(parents), empty_like(seqlens)
+    else:
+        _fits("path", path, (B, T), int32, device)
+        _fits("new_seqlens", new_seqlens, (B,), int32, device)
     _enqueue("fa_paged_accept", _library().fa_paged_accept, device, stream, (
         k_pages.data_ptr(), v_pages.data_ptr(), _ptr(weights), block_table.data_ptr(),
         seqlens.data_ptr(), _ptr(parents), leaf.data_ptr(), _ptr(new_lens), path.data_ptr(),
         new_seqlens.data_ptr(), B, T, Hkv, d, page_size, num_pages, max_pages,
         _dtype_code(k_pages)))
+    return path, new_seqlens
 
 
 def paged_accept(k_pages, v_pages, block_table, seqlens, leaf, parents, new_lens=None,
@@ -180,12 +195,8 @@ def paged_accept(k_pages, v_pages, block_table, seqlens, leaf, parents, new_lens
     ``fa_paged_accept``)."""
     if parents.dim() != 2:
         raise ValueError("parents must be [B, T]")
-    empty_like = _torch()[3]
-    with _stream_of(stream, k_pages.device):
-        path, new_seqlens = empty_like(parents), empty_like(seqlens)
-    fa_paged_accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seqlens, parents,
-                    new_lens, weights, stream)
-    return path, new_seqlens
+    return _accept(k_pages, v_pages, block_table, seqlens, leaf, None, None, parents, new_lens,
+                   weights, stream)
 
 
 def fa_paged_copy(k_pages, v_pages, src, dst, rows=None, weights=None, stream=None) -> None:
@@ -257,39 +268,43 @@ def fa_paged_fork(pool, block_table, seqlens, source, out: Forked, page_size: in
                   stream=None) -> None:
     """Enqueue a fork: sequence c of ``out`` continues sequence source[c] (int32 [C]; -1: empty),
     with its whole pages shared and its last one, where it is filled in part, from the pool."""
-    int32 = _torch()[1]
+    _fork(pool, block_table, seqlens, source, out, page_size, stream)
+
+
+def _fork(pool, block_table, seqlens, source, out, page_size, stream):
+    """fa_paged_fork; an `out` that is None is allocated. Returns it."""
+    torch, int32, _, _, _, _ = _torch()
     device, B, max_pages, num_pages = _tables(pool, block_table)
     refs, free_pages, num_free = pool
-    table, lens, src, dst, rows = out
     _fits("seqlens", seqlens, (B,), int32, device)
     if source.dim() != 1:
         raise ValueError("source must be [C]")
     shape = source.shape
     C = _count("C", shape[0])
     _fits("source", source, shape, int32, device)
-    _fits("out.block_table", table, (C, max_pages), int32, device)
-    _fits("out.seqlens", lens, shape, int32, device)
-    _fits("out.copy_src", src, shape, int32, device)
-    _fits("out.copy_dst", dst, shape, int32, device)
-    _fits("out.copy_rows", rows, shape, int32, device)
+    page_size = _count("page_size", page_size)
+    if out is None:
+        with _NO_CONTEXT if stream is None else _stream_of(stream, block_table.device):
+            out = Forked(torch.empty((C, max_pages), dtype=int32, device=source.device),
+                         *torch.empty((4, C), dtype=int32, device=source.device).unbind(0))
+        table, lens, src, dst, rows = out
+    else:
+        table, lens, src, dst, rows = out
+        _fits("out.block_table", table, (C, max_pages), int32, device)
+        _fits("out.seqlens", lens, shape, int32, device)
+        _fits("out.copy_src", src, shape, int32, device)
+        _fits("out.copy_dst", dst, shape, int32, device)
+        _fits("out.copy_rows", rows, shape, int32, device)
     _enqueue("fa_paged_fork", _library().fa_paged_fork, device, stream, (
         block_table.data_ptr(), seqlens.data_ptr(), source.data_ptr(), refs.data_ptr(),
         free_pages.data_ptr(), num_free.data_ptr(), table.data_ptr(), lens.data_ptr(),
-        src.data_ptr(), dst.data_ptr(), rows.data_ptr(), B, C, _count("page_size", page_size),
-        num_pages, max_pages))
+        src.data_ptr(), dst.data_ptr(), rows.data_ptr(), B, C, page_size, num_pages, max_pages))
+    return out
 
 
 def paged_fork(pool, block_table, seqlens, source, page_size: int, stream=None) -> Forked:
     """New sequences that continue others (see ``fa_paged_fork``), in tables of their own."""
-    if block_table.dim() != 2 or source.dim() != 1:
-        raise ValueError("block_table must be [B, max_pages] and source [C]")
-    torch, int32, _, empty_like, _, _ = _torch()
-    with _stream_of(stream, block_table.device):
-        out = Forked(block_table.new_empty((source.shape[0], block_table.shape[1])),
-                     empty_like(source), empty_like(source), empty_like(source),
-                     empty_like(source))
-    fa_paged_fork(pool, block_table, seqlens, source, out, page_size, stream)
-    return out
+    return _fork(pool, block_table, seqlens, source, None, page_size, stream)
 
 
 def fa_paged_resize(pool, block_table, old_lens, new_lens, granted, page_size: int,
@@ -297,22 +312,30 @@ def fa_paged_resize(pool, block_table, old_lens, new_lens, granted, page_size: i
     """Enqueue a change of lengths: sequence b has pages for old_lens[b] tokens and gets those for
     new_lens[b], given back to the pool or taken from it, in its row of block_table. granted
     int32 [B] gets new_lens[b], or old_lens[b] where the pool did not suffice."""
-    int32 = _torch()[1]
+    _resize(pool, block_table, old_lens, new_lens, granted, page_size, stream)
+
+
+def _resize(pool, block_table, old_lens, new_lens, granted, page_size, stream):
+    """fa_paged_resize; a `granted` that is None is allocated. Returns it."""
+    _, int32, _, empty_like, _, _ = _torch()
     device, B, max_pages, num_pages = _tables(pool, block_table)
     refs, free_pages, num_free = pool
     shape = (B,)
     _fits("old_lens", old_lens, shape, int32, device)
     _fits("new_lens", new_lens, shape, int32, device)
-    _fits("granted", granted, shape, int32, device)
+    page_size = _count("page_size", page_size)
+    if granted is None:
+        with _NO_CONTEXT if stream is None else _stream_of(stream, block_table.device):
+            granted = empty_like(old_lens)
+    else:
+        _fits("granted", granted, shape, int32, device)
     _enqueue("fa_paged_resize", _library().fa_paged_resize, device, stream, (
         block_table.data_ptr(), old_lens.data_ptr(), new_lens.data_ptr(), granted.data_ptr(),
-        refs.data_ptr(), free_pages.data_ptr(), num_free.data_ptr(), B,
-        _count("page_size", page_size), num_pages, max_pages))
+        refs.data_ptr(), free_pages.data_ptr(), num_free.data_ptr(), B, page_size, num_pages,
+        max_pages))
+    return granted
 
 
 def paged_resize(pool, block_table, old_lens, new_lens, page_size: int, stream=None):
     """granted int32 [B]: the lengths that the tables have pages for after ``fa_paged_resize``."""
-    with _stream_of(stream, block_table.device):
-        granted = _torch()[3](old_lens)
-    fa_paged_resize(pool, block_table, old_lens, new_lens, granted, page_size, stream)
-    return granted
+    return _resize(pool, block_table, old_lens, new_lens, None, page_size, stream)
