@@ -225,15 +225,14 @@ __device__ __forceinline__ int take_page(const PagePool& p, int i) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Fork, in two kernels: lengths, pages from the pool and the list of copies by one block; then the
-// tables' rows and the references of shared pages, a block for each 1024 entries.
+// Fork: lengths, pages from the pool and the list of copies by one block; then the tables' rows and
+// the references of shared pages, in a second launch with a block for each kForkThreads entries, or
+// by the same block where the tables are small. Bound by latency, or by the atomics (330000 shared
+// pages: XX us).
 constexpr int kForkThreads = 1024;
+constexpr int kSmallTables = 8192;   // entries of the tables of a call that one block has
 
-__global__ void __launch_bounds__(kForkThreads)
-    fa_paged_fork_plan_kernel(const __grid_constant__ ForkParams p) {
-  __shared__ int s_warp[32];
-  wait_prerequisites();
-  launch_dependents();
+__device__ __forceinline__ void fork_plan(const ForkParams& p, int* s_warp) {
   const int have = free_pages_of(p.pool);
   const int64_t capacity = static_cast<int64_t>(p.max_pages) * p.page_size;
   int taken = 0;
@@ -274,13 +273,8 @@ __global__ void __launch_bounds__(kForkThreads)
   if (threadIdx.x == 0) *p.pool.num_free = have - min(taken, have);
 }
 
-__global__ void __launch_bounds__(kForkThreads)
-    fa_paged_fork_kernel(const __grid_constant__ ForkParams p, int blocks_per_row) {
-  wait_prerequisites();
-  launch_dependents();
-  const int c = blockIdx.x / blocks_per_row;
-  const int col = (blockIdx.x % blocks_per_row) * kForkThreads + threadIdx.x;
-  if (col >= p.max_pages) return;
+// Entry `col` of new sequence c's row.
+__device__ __forceinline__ void fork_entry(const ForkParams& p, int c, int col) {
   const int len = load_l2(p.out_seqlens + c);
   const int full = len > 0 ? len / p.page_size : 0;
   int page = -1;
@@ -298,6 +292,27 @@ __global__ void __launch_bounds__(kForkThreads)
   p.out_table[static_cast<int64_t>(c) * p.max_pages + col] = page;
 }
 
+__global__ void __launch_bounds__(kForkThreads)
+    fa_paged_fork_plan_kernel(const __grid_constant__ ForkParams p, int small) {
+  __shared__ int s_warp[32];
+  wait_prerequisites();
+  launch_dependents();
+  fork_plan(p, s_warp);
+  if (!small) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.C * p.max_pages; i += kForkThreads)
+    fork_entry(p, i / p.max_pages, i % p.max_pages);
+}
+
+__global__ void __launch_bounds__(kForkThreads)
+    fa_paged_fork_kernel(const __grid_constant__ ForkParams p, int blocks_per_row) {
+  wait_prerequisites();
+  launch_dependents();
+  const int c = blockIdx.x / blocks_per_row;
+  const int col = (blockIdx.x % blocks_per_row) * kForkThreads + threadIdx.x;
+  if (col < p.max_pages) fork_entry(p, c, col);
+}
+
 // ---------------------------------------------------------------------------------------------
 // Resize, by one cluster: first the pages that shorter sequences give back, then those that
 // longer ones take. Bound by latency (a few pages), or by the atomics and scattered accesses of the
@@ -313,7 +328,6 @@ __global__ void __launch_bounds__(kForkThreads)
 // lane, so that as many accesses are on their way; item f belongs to the sequence whose prefix it
 // lies behind, which a lane finds by search once and then by steps.
 constexpr int kResizeThreads = 1024, kResizeCluster = 16, kBatch = 4;
-constexpr int kSmallTables = 8192;   // entries of the tables of a call that one block has
 
 struct ItemWalk {
   const int* prefix;   // [B + 1], shared memory
@@ -623,8 +637,9 @@ cudaError_t launch_paged_copy(const CopyParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged_fork(const ForkParams& p, cudaStream_t stream) {
-  cudaError_t err = launch_paged(fa_paged_fork_plan_kernel, 1, kForkThreads, 0, stream, 0, p);
-  if (err != cudaSuccess) return err;
+  const int small = static_cast<int64_t>(p.C) * p.max_pages <= kSmallTables;
+  cudaError_t err = launch_paged(fa_paged_fork_plan_kernel, 1, kForkThreads, 0, stream, 0, p, small);
+  if (err != cudaSuccess || small) return err;
   const int blocks = (p.max_pages + kForkThreads - 1) / kForkThreads;
   return launch_paged(fa_paged_fork_kernel, static_cast<int64_t>(p.C) * blocks, kForkThreads, 0,
                       stream, 0, p, blocks);
