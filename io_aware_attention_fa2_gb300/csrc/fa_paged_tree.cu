@@ -83,10 +83,18 @@ struct Args {
   int2* units;        // [B * Hkv * blocks]: slot of the unit's first part, number of parts (0: the
                       // unit was one run's, and is written)
   int B, T, Hq, Hkv, G, blocks;   // blocks of rows for each key head
+  uint32_t g_magic;               // ceil(2^32 / G), or 0: see token_of
   int part_rows;                  // rows of a unit, at most
   int page_shift, num_pages, max_pages, box_rows, window_left;
   float scale_log2;
 };
+
+// Drafted token of row r, r / G: by the product's upper half, which is exact while r * G < 2^32
+// (r < T * G, so for G up to 2047); g_magic is 0 for G = 1 and for more.
+__device__ __forceinline__ int token_of(const Args& a, int r) {
+  if (a.g_magic) return static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.g_magic));
+  return a.G == 1 ? r : r / a.G;
+}
 
 // A block of rows: tokens [i0, i1) (i1 <= i0: only rows of the padding) and tiles
 // [first, first + count), at least one.
@@ -96,8 +104,8 @@ struct Unit {
 template <int ROWS>
 __device__ __forceinline__ Unit unit_of(const Args& a, Draft dr, int rb) {
   Unit u;
-  u.i0 = rb * ROWS / a.G;
-  u.i1 = min(dr.count, ((rb + 1) * ROWS + a.G - 1) / a.G);
+  u.i0 = token_of(a, rb * ROWS);
+  u.i1 = min(dr.count, token_of(a, min((rb + 1) * ROWS, a.T * a.G) - 1) + 1);
   u.first = 0;
   u.count = 1;
   if (u.i1 > u.i0) {
@@ -138,6 +146,7 @@ struct Segment {
   int b, hk, base;          // sequence, key head, length of the context
   int drafted;              // drafted tokens
   int r0, live;             // the unit's first row, and its rows that are not padding
+  int rows;                 // rows with the padding's, which this segment writes; or 0
   int first_key, count;     // of the segment; its tiles (0: there is no further segment)
   int lo, hi;               // keys that some row sees are within [lo, hi)
   int full_lo, full_hi;     // every row sees all keys of a tile within these
@@ -448,11 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ scheduler
     int segs = 0;
     bool ok = true;
+    // a segment in front may take as long as the run's tiles do (some 2 us each)
+    uint64_t limit = kWaitLimitNs;
     auto publish = [&](int b, int hk, Draft dr, const Unit& u, int r0, int live, int tile, int count,
                        int slot) {
       const int s = segs % kSegments;
       ok = ptx::wait_bounded_warp(bar(BAR_SEG_EMPTY + s), ((segs / kSegments) & 1) ^ 1, abort_p,
-                                  kWaitLimitNs);
+                                  limit);
       if (ok && lane == 0) {
         Segment& g = ms.seg[s];
         g.b = b;
@@ -461,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         g.drafted = dr.count;
         g.r0 = r0;
         g.live = live;
+        g.rows = tile == 0 ? min(kRows, a.T * a.G - r0) : 0;
         g.first_key = (u.first + tile) * kTile;
         g.count = count;
         g.lo = a.window_left < 0 ? 0 : max(0, dr.base - a.window_left);
@@ -473,17 +485,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++segs;
     };
-    // rows [max(live, 0), rows) of a unit, the padding's
-    auto clear = [&](int b, int hk, int r0, int live, int rows) {
-      constexpr int kChunks = D / 8;
-#pragma unroll 1
-      for (int w = max(live, 0) * kChunks + lane; w < rows * kChunks; w += 32) {
-        const int r = r0 + w / kChunks, token = r / a.G, head = hk * a.G + r % a.G;
+    // a unit of padding alone: `rows` rows from r0 (12000 cycles for 256 of them, by one warp)
+    auto clear = [&](int b, int hk, int r0, int rows) {
+      constexpr int kChunks = D / 8, kStep = 32 / kChunks;
+      const int c = lane % kChunks, step_t = token_of(a, kStep), step_h = kStep - step_t * a.G;
+      int token = token_of(a, r0 + lane / kChunks), h = r0 + lane / kChunks - token * a.G;
+#pragma unroll 4
+      for (int r = lane / kChunks; r < rows; r += kStep) {
+        const int head = hk * a.G + h;
         reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) +
-                                 ((static_cast<int64_t>(b) * a.T + token) * a.Hq + head) *
-                                     D)[w % kChunks] = make_uint4(0, 0, 0, 0);
-        if (w % kChunks == 0)
-          a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = -INFINITY;
+                                 ((static_cast<int64_t>(b) * a.T + token) * a.Hq + head) * D)[c] =
+            make_uint4(0, 0, 0, 0);
+        if (c == 0) a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = -INFINITY;
+        token += step_t;
+        h += step_h;
+        if (h >= a.G) {
+          h -= a.G;
+          ++token;
+        }
       }
     };
     if constexpr (SHORT) {
@@ -496,7 +515,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int live = dr.count * a.G;
       if (dr.count < 0 && lane == 0) record_page_error();
       if (u.i1 > u.i0 && count > 0) publish(b, hk, dr, u, 0, live, tile, count, 0);
-      if (rank == 0) clear(b, hk, 0, live, a.T * a.G);
     } else {
     // Where this CTA's run starts: the cost of the sequences summed up to it. The first 32
     // sequences' stays in registers.
@@ -508,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ctas = min(total, static_cast<int>(gridDim.x));   // each gets at least one
     const int start = first_place(total, cta, ctas);
     int left = cta < ctas ? first_place(total, cta + 1, ctas) - start : 0;
+    limit += static_cast<uint64_t>(left) * 20000;
     int b = 0, at = 0, per_head = 1;
 #pragma unroll 1
     for (int b0 = 0, before = 0; b0 < a.B; b0 += 32) {
@@ -556,8 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // its Q and parents, which are read when the segment before ends
         if (segs > 1) {
           for (int r = lane; r < live; r += 32) {
-            const int64_t at = (static_cast<int64_t>(b) * a.T + (r0 + r) / a.G) * a.Hq + hk * a.G +
-                               (r0 + r) % a.G;
+            const int token = token_of(a, r0 + r);
+            const int64_t at = (static_cast<int64_t>(b) * a.T + token) * a.Hq + hk * a.G + r0 + r -
+                               token * a.G;
             for (int c = 0; c < D; c += 64) prefetch_l2(static_cast<const uint16_t*>(a.q) + at * D + c);
           }
         }
@@ -577,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.units[(static_cast<int64_t>(b) * a.Hkv + hk) * a.blocks + rb] =
               make_int2(slot, count == u.count ? 0 : last - cta + 1);
         }
-        clear(b, hk, r0, live, rows);
+        if (u.i1 <= u.i0 && !a.units) clear(b, hk, r0, rows);   // (else the join does)
       }
       left -= share;
       taken += share;
@@ -597,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {   // the end
       const int s = segs % kSegments;
       ok = ptx::wait_bounded_warp(bar(BAR_SEG_EMPTY + s), ((segs / kSegments) & 1) ^ 1, abort_p,
-                                  kWaitLimitNs);
+                                  limit);
       if (ok && lane == 0) {
         ms.seg[s].count = 0;
         ptx::mbar_arrive(bar(BAR_SEG_FULL + s));
@@ -839,16 +859,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Segment& sg = ms.seg[s % kSegments];
       const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u;
       const uint32_t q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-      const int c = tid % kChunks, step_t = kStep / a.G, step_h = kStep % a.G, live = sg.live;
-      int token = (sg.r0 + tid / kChunks) / a.G, h = (sg.r0 + tid / kChunks) % a.G;
-      const uint16_t* const q = static_cast<const uint16_t*>(a.q) +
-                                (static_cast<int64_t>(sg.b) * a.T * a.Hq + sg.hk * a.G) * D + c * 8;
+      const int c = tid % kChunks, step_t = token_of(a, kStep), step_h = kStep - step_t * a.G;
+      const int live = sg.live, rows = sg.rows;
+      int token = token_of(a, sg.r0 + tid / kChunks), h = sg.r0 + tid / kChunks - token * a.G;
+      const int64_t first = (static_cast<int64_t>(sg.b) * a.T * a.Hq + sg.hk * a.G) * D + c * 8;
       uint4 v[kEach];
 #pragma unroll
       for (int u = 0; u < kEach; ++u) {
+        const int r = u * kStep + tid / kChunks;
+        const int64_t at = first + (static_cast<int64_t>(token) * a.Hq + h) * D;
         v[u] = make_uint4(0, 0, 0, 0);
-        if (u * kStep + tid / kChunks < live)
-          v[u] = *reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(token) * a.Hq + h) * D);
+        if (r < live) {
+          v[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+        } else if (r < rows) {   // padding
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at) = v[u];
+          if (c == 0)
+            a.lse[(static_cast<int64_t>(sg.b) * a.Hq + sg.hk * a.G + h) * a.T + token] = -INFINITY;
+        }
         token += step_t;
         h += step_h;
         if (h >= a.G) {
@@ -889,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Segment& now = ms.seg[segs % kSegments];
           uint4 vis = make_uint4(0, 0, 0, 0);
           if (my < now.live)
-            vis = visible_bits(a, now.b, now.base, (now.r0 + my) / a.G, now.first_key + j * kTile,
+            vis = visible_bits(a, now.b, now.base, token_of(a, now.r0 + my), now.first_key + j * kTile,
                                ms.loaded[n % kInfoSlots]);
           vis0 = half ? vis.z : vis.x;
           vis1 = half ? vis.w : vis.y;
@@ -1032,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = sn.whole, two = QT == 1 && sn.count > 1;   // two: both streams have an O
         const bool mine = my < sn.live;
         // (rows behind the last get addresses, too, that nothing is written to)
-        const int token = (sn.r0 + my) / a.G, head = sn.hk * a.G + (sn.r0 + my) % a.G;
+        const int token = token_of(a, sn.r0 + my), head = sn.hk * a.G + sn.r0 + my - token * a.G;
         const float f = whole ? inverse(l) : 1.f;
         fa *= f;
         fb *= f;
@@ -1130,14 +1157,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster.sync();   // every CTA's part is in its shared memory
     const int b = cta / ranks / a.Hkv, hk = cta / ranks % a.Hkv;
     const int live = draft(a, b).count * a.G;
-    // four columns of a row a thread, the rows shared out over the cluster
+    // four columns of a row a thread, the rows shared out over the cluster (a sequence without
+    // drafted tokens has nothing but padding, which no segment wrote)
+    const int rows = live > 0 ? live : a.T * a.G;
 #pragma unroll 1
-    for (int at = rank * kThreads + threadIdx.x; at < live * (D / 4); at += ranks * kThreads) {
+    for (int at = rank * kThreads + threadIdx.x; at < rows * (D / 4); at += ranks * kThreads) {
       const int r = at / (D / 4), c = at % (D / 4);
       float m = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int x = 0; x < ranks; ++x) {
+      for (int x = 0; x < (live > 0 ? ranks : 0); ++x) {
         const float2 ml = *cluster.map_shared_rank(short_ml + r, x);
         if (ml.x == -INFINITY) continue;   // saw nothing, and may hold anything
         const float4 v =
@@ -1152,7 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc.w = acc.w * f + v.w * g;
       }
       const float inv = inverse(l);
-      const int token = r / a.G, head = hk * a.G + r % a.G;
+      const int token = token_of(a, r), head = hk * a.G + r - token * a.G;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) +
                                 ((static_cast<int64_t>(b) * a.T + token) * a.Hq + head) * D + 4 * c) =
           make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
@@ -1191,7 +1220,17 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int r = i * a.G + h % a.G, my = r % ROWS;
   const int2 u =
       a.units[(static_cast<int64_t>(b) * a.Hkv + h / a.G) * a.blocks + r / ROWS];
-  if (u.y == 0 || i >= draft(a, b).count) return;   // one run's, and written; padding
+  const int drafted = draft(a, b).count;
+  if (i >= drafted) {
+    // padding: of a unit without any token nobody else writes it
+    if (token_of(a, r - my) >= drafted) {
+      for (int e = 0; e < E; e += 2)
+        reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + id * D + lane * E)[e / 2] = 0;
+      if (lane == 0) a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.T + i] = -INFINITY;
+    }
+    return;
+  }
+  if (u.y == 0) return;   // one run's, and written
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -1279,6 +1318,7 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t stream) {
   a.Hq = p.Hq;
   a.Hkv = c.Hkv;
   a.G = p.Hq / c.Hkv;
+  a.g_magic = a.G > 1 && a.G < 2048 ? static_cast<uint32_t>(((1ull << 32) + a.G - 1) / a.G) : 0;
   a.blocks = static_cast<int>(l.blocks);
   a.part_rows = static_cast<int>(l.part_rows);
   a.page_shift = 0;
