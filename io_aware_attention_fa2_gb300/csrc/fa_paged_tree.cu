@@ -225,33 +225,34 @@ __device__ __forceinline__ int parent_of(const Args& a, int b, int i) {
   return -1;
 }
 
-// Keys k0 .. k0 + 127 that drafted token i of sequence b sees, as bits, of those in `loaded`.
-__device__ __noinline__ uint4 visible_bits(const Args& a, int b, int base, int i, int k0,
-                                           uint4 loaded) {
+// Keys k0 .. k0 + 63 that drafted token i of sequence b sees, as bits.
+__device__ __forceinline__ uint2 visible_bits(const Args& a, int b, int base, int i, int k0) {
   int lo = 0;
   if (a.window_left >= 0) {
     int depth = i;
     if (a.parents) {
       depth = 0;
+#pragma unroll 1
       for (int at = parent_of(a, b, i); at >= 0; at = parent_of(a, b, at)) ++depth;
     }
-    lo = max(0, base + depth - a.window_left);
+    lo = base + depth - a.window_left - k0;
   }
-  const int hi = a.parents ? base : base + i + 1;   // a chain's keys are a range, too
-  uint32_t vis[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) vis[w] = bit_range(lo - k0 - 32 * w, hi - k0 - 32 * w);
-  if (a.parents && k0 + kTile > base) {
-    int steps = 0;
-    for (int at = i; at >= 0 && base + at >= k0; at = parent_of(a, b, at), ++steps) {
-      if (a.window_left >= 0 && steps > a.window_left) break;
+  const int hi = (a.parents ? base : base + i + 1) - k0;   // a chain's keys are a range, too
+  uint32_t v0 = bit_range(lo, hi), v1 = bit_range(lo - 32, hi - 32);
+  if (a.parents && k0 + 64 > base) {
+    int steps = a.window_left >= 0 ? a.window_left : kMaxDraft;   // ancestors within the window
+#pragma unroll 1
+    for (int at = i; at >= 0 && base + at >= k0; at = parent_of(a, b, at)) {
+      if (steps-- < 0) break;
       const int t = base + at - k0;
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        if (t >> 5 == w) vis[w] |= 1u << (t & 31);
+      const uint32_t bit = 1u << (t & 31);
+      if (t < 32)
+        v0 |= bit;
+      else if (t < 64)
+        v1 |= bit;
     }
   }
-  return make_uint4(vis[0] & loaded.x, vis[1] & loaded.y, vis[2] & loaded.z, vis[3] & loaded.w);
+  return make_uint2(v0, v1);
 }
 
 // One lane of a converged warp: nonzero in it.
@@ -310,24 +311,27 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 // is not finite (then true).
 template <int D, bool FP16>
 __device__ __noinline__ bool clean_values(uint8_t* tile, uint4 loaded, int t) {
-  constexpr int kChunks = D / 8;
+  // thread t has the piece t % kChunks of every kStep-th row, at one place of the swizzle
+  constexpr int kChunks = D / 8, kStep = 256 / kChunks, kEach = kTile / kStep;
+  const int r0 = t / kChunks, c = t % kChunks;
+  uint4* const at = reinterpret_cast<uint4*>(tile + (c / 8) * kHalfBytes + r0 * 128 +
+                                             (((c % 8) ^ (r0 & 7)) << 4));
+  uint4 v[kEach];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) v[u] = at[u * kStep * 8];
   bool found = false;
-#pragma unroll 4
-  for (int u = t; u < kTile * kChunks; u += 256) {
-    const int r = u / kChunks, c = u % kChunks;
-    const uint32_t bits = r < 64 ? (r < 32 ? loaded.x : loaded.y) : (r < 96 ? loaded.z : loaded.w);
-    uint4* const at = reinterpret_cast<uint4*>(tile + (c / 8) * kHalfBytes + r * 128 +
-                                               (((c % 8) ^ (r & 7)) << 4));
-    if (!(bits >> (r % 32) & 1)) {
-      *at = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const uint32_t words[4] = {loaded.x, loaded.y, loaded.z, loaded.w};
+    if (!(words[u * kStep / 32] >> ((u * kStep + r0) % 32) & 1)) {
+      at[u * kStep * 8] = make_uint4(0, 0, 0, 0);
       continue;
     }
-    const uint4 v = *at;
-    const uint32_t x = not_finite2<FP16>(v.x), y = not_finite2<FP16>(v.y),
-                   z = not_finite2<FP16>(v.z), w = not_finite2<FP16>(v.w);
+    const uint32_t x = not_finite2<FP16>(v[u].x), y = not_finite2<FP16>(v[u].y),
+                   z = not_finite2<FP16>(v[u].z), w = not_finite2<FP16>(v[u].w);
     if (x | y | z | w) {
       found = true;
-      *at = make_uint4(v.x & ~x, v.y & ~y, v.z & ~z, v.w & ~w);
+      at[u * kStep * 8] = make_uint4(v[u].x & ~x, v[u].y & ~y, v[u].z & ~z, v[u].w & ~w);
     }
   }
   return found;
@@ -340,7 +344,6 @@ template <bool FP16>
 __device__ __noinline__ void add_not_finite(const Args& a, const Segment& sg, int i, int d, int c0,
                                             int cols, float* part, uint16_t* out) {
   const int* const tab = a.table + static_cast<int64_t>(sg.b) * a.max_pages;
-  const uint4 all = make_uint4(~0u, ~0u, ~0u, ~0u);
   for (int j = 0; j < sg.count; ++j) {
     const int k0 = sg.first_key + j * kTile;
     bool masked = k0 < sg.full_lo || k0 + kTile > sg.full_hi;
@@ -349,7 +352,9 @@ __device__ __noinline__ void add_not_finite(const Args& a, const Segment& sg, in
       masked = page < 0 || page >= a.num_pages;
     }
     if (!masked) continue;
-    const uint4 vis = visible_bits(a, sg.b, sg.base, i, k0, all);
+    const uint2 first = visible_bits(a, sg.b, sg.base, i, k0);
+    const uint2 second = visible_bits(a, sg.b, sg.base, i, k0 + 64);
+    const uint4 vis = make_uint4(first.x, first.y, second.x, second.y);
     for (int t = 0; t < kTile; ++t) {
       const uint32_t word = t < 64 ? (t < 32 ? vis.x : vis.y) : (t < 96 ? vis.z : vis.w);
       if (!(word >> (t % 32) & 1)) continue;
@@ -572,15 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         publish(b, hk, dr, u, r0, live, tile, count, slot);
         if (!ok) break;
         first = false;
-        // its Q and parents, which are read when the segment before ends
-        if (segs > 1) {
-          for (int r = lane; r < live; r += 32) {
-            const int token = token_of(a, r0 + r);
-            const int64_t at = (static_cast<int64_t>(b) * a.T + token) * a.Hq + hk * a.G + r0 + r -
-                               token * a.G;
-            for (int c = 0; c < D; c += 64) prefetch_l2(static_cast<const uint16_t*>(a.q) + at * D + c);
-          }
-        }
       }
       if (tile == 0 && count > 0) {
         if (a.units && lane == 0) {
@@ -651,6 +647,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto entry = [&](int j) { return needed(j) ? tab[(row0 + j * br) >> a.page_shift] : -1; };
       int cur = entry(lane), nxt = entry(32 + lane);
+      if (!is_v && segs > 0) {
+        // its Q, which is read when the segment before ends, in some 5 us (from HBM beside the
+        // other CTAs' loads that takes 5500 cycles, from L2 XX)
+#pragma unroll 1
+        for (int r = lane; r < sg.live; r += 32) {
+          const int token = token_of(a, sg.r0 + r);
+          const int64_t at = (static_cast<int64_t>(sg.b) * a.T + token) * a.Hq + hk * a.G + sg.r0 + r -
+                             token * a.G;
+          for (int c = 0; c < D; c += 64) prefetch_l2(static_cast<const uint16_t*>(a.q) + at * D + c);
+        }
+      }
 #pragma unroll 1
       for (int i = 0; i < count; ++i, ++n) {
         const int j0 = i * boxes;
@@ -860,28 +867,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_and = a.scale_log2 == 0.f ? 0u : ~0u;
       const uint32_t q_xor = a.scale_log2 < 0.f ? 0x80008000u : 0u;
       const int c = tid % kChunks, step_t = token_of(a, kStep), step_h = kStep - step_t * a.G;
-      const int live = sg.live, rows = sg.rows;
-      int token = token_of(a, sg.r0 + tid / kChunks), h = sg.r0 + tid / kChunks - token * a.G;
-      const int64_t first = (static_cast<int64_t>(sg.b) * a.T * a.Hq + sg.hk * a.G) * D + c * 8;
-      uint4 v[kEach];
-#pragma unroll
-      for (int u = 0; u < kEach; ++u) {
-        const int r = u * kStep + tid / kChunks;
-        const int64_t at = first + (static_cast<int64_t>(token) * a.Hq + h) * D;
-        v[u] = make_uint4(0, 0, 0, 0);
-        if (r < live) {
-          v[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
-        } else if (r < rows) {   // padding
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + at) = v[u];
-          if (c == 0)
-            a.lse[(static_cast<int64_t>(sg.b) * a.Hq + sg.hk * a.G + h) * a.T + token] = -INFINITY;
-        }
+      const int live = sg.live, r0 = tid / kChunks;
+      int token = token_of(a, sg.r0 + r0), h = sg.r0 + r0 - token * a.G;
+      auto next_row = [&] {
         token += step_t;
         h += step_h;
         if (h >= a.G) {
           h -= a.G;
           ++token;
         }
+      };
+      // the offset of a row's piece in q and o; rows behind the last load the first one's
+      const int64_t first = (static_cast<int64_t>(sg.b) * a.T * a.Hq + sg.hk * a.G) * D + c * 8;
+      auto place = [&] { return first + static_cast<int64_t>(token * a.Hq + h) * D; };
+      const int64_t safe = first + static_cast<int64_t>(token_of(a, sg.r0)) * a.Hq * D;
+      uint4 v[kEach];
+#pragma unroll
+      for (int u = 0; u < kEach; ++u) {
+        v[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                               (u * kStep + r0 < live ? place() : safe));
+        next_row();
       }
 #pragma unroll
       for (int u = 0; u < kEach; ++u) {
@@ -893,6 +898,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(bar(BAR_Q_FULL));
+      if (sg.rows > live) {   // the padding's rows
+        token = token_of(a, sg.r0 + r0);
+        h = sg.r0 + r0 - token * a.G;
+#pragma unroll 1
+        for (int r = r0; r < sg.rows; r += kStep, next_row()) {
+          if (r < live) continue;
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + place()) = make_uint4(0, 0, 0, 0);
+          if (c == 0)
+            a.lse[(static_cast<int64_t>(sg.b) * a.Hq + sg.hk * a.G + h) * a.T + token] = -INFINITY;
+        }
+      }
     };
     bool go = next_segment(0), had = false;
     if (go) load_q(0);
@@ -914,12 +930,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t vis0 = ~0u, vis1 = ~0u;
         if (masked && active) {
           const Segment& now = ms.seg[segs % kSegments];
-          uint4 vis = make_uint4(0, 0, 0, 0);
-          if (my < now.live)
-            vis = visible_bits(a, now.b, now.base, token_of(a, now.r0 + my), now.first_key + j * kTile,
-                               ms.loaded[n % kInfoSlots]);
-          vis0 = half ? vis.z : vis.x;
-          vis1 = half ? vis.w : vis.y;
+          const uint4 loaded = ms.loaded[n % kInfoSlots];
+          vis0 = vis1 = 0;
+          if (my < now.live) {
+            const uint2 vis = visible_bits(a, now.b, now.base, token_of(a, now.r0 + my),
+                                           now.first_key + j * kTile + half * 64);
+            vis0 = vis.x & (half ? loaded.z : loaded.x);
+            vis1 = vis.y & (half ? loaded.w : loaded.y);
+          }
           __syncwarp();
         }
         if (!wait(BAR_S_FULL + x, done)) {
