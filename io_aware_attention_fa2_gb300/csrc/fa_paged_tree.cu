@@ -6,36 +6,58 @@
 // What bounds it: K and V are read once, 4 d bytes a token and key head, for 4 d operations of
 // each row -- a drafted token and one of the G query heads that share the key head. Up to about
 // 250 rows HBM is the bound, from there the tensor cores; both products run on tcgen05 with 128 rows
-// to a tile, whatever their number, so that a tile of K and V costs the same time for 2 rows as for
-// 128 and less than its way from HBM.
+// to a tile, whatever their number: a tile of 128 keys takes 1100 cycles of the tensor pipe (d = 128)
+// for 2 rows as for 128, less than the 2800 that its 64 KiB take from HBM.
 //
 // Rows of a (sequence, key head) are taken in the order (token, query head), in blocks of 128 (one
-// row tile) or 256 (two). A block over its keys is a unit. The keys are cut into tiles of 128
-// tokens, and the tiles of all units, in order, into one equal run for each CTA (one on each SM),
-// whatever the lengths are. A run that covers a whole unit writes O and LSE; one that covers a part
-// leaves the part's maximum, sum and unnormalised O (fp32) in the workspace, and a second kernel
-// joins the parts of a unit in a fixed order.
+// row tile) or 256 (two, where there are more than 128 rows). A block over its keys is a unit. The
+// keys are cut into tiles of 128 tokens, and the tiles of all units, in order, into one equal run
+// for each CTA (one on each SM), whatever the lengths are; a unit's start and end count as some
+// tiles more. A run that covers a whole unit writes O and LSE; one that covers a part leaves the
+// part's offset, sum and unnormalised O (fp32) in the workspace, and a second kernel joins the
+// parts of a unit in a fixed order. Short caches take one launch and no workspace: a cluster of up to
+// eight CTAs has one unit, and the parts are joined through distributed shared memory.
 //
 // One CTA:
-//   warp 0       TMA producer: K and V tiles into two rings, box by box of a page's rows
-//   warp 1       TMEM allocator and MMA issuer (one thread)
-//   warps 4..11  two softmax groups, A and B, a row to a thread: S from TMEM, P back over it,
-//                O rescaled in TMEM when the maximum has grown; Q into shared memory at a unit's
-//                start, O out of TMEM at its end
-// Two row tiles: A has the first 128 rows, B the others; both see every tile. One row tile: A takes
-// the even tiles of a run's part of a unit and B the odd ones, each with a maximum, sum and O of its
-// own, joined at the end; so there, too, one group's softmax runs beside the other's products.
+//   warp 0, 2    TMA producers of K and V: boxes of a page's rows into two rings
+//   warp 1       TMEM allocator and MMA issuer
+//   warp 3       scheduler: the run's segments (a unit's part) from lengths that only the device
+//                knows, four of them ahead
+//   warps 4..19  softmax: S from TMEM, P back over it, O rescaled in TMEM when the maximum has
+//                grown; Q into shared memory at a segment's start, O out of TMEM at its end
+// Eight softmax warps have a stream, A or B. A thread has half a row, 64 keys of a tile, and
+// exchanges the row's maximum with the thread that has the others. Two row tiles: A has the first
+// 128 rows, B the others, and both see every tile. One row tile: A takes the even tiles of a
+// segment and B the odd ones, each with an offset, sums and O of its own, joined at the end; so
+// there, too, one stream's softmax runs beside the other's products.
 //
-// Masks. Tiles of the context that no window cuts need none. In the others a thread builds the
-// 128 bits of its row: a range of the context, and the ancestors by walking up the tree. Keys that
-// some row of the tile does not see have P = 0 there, but 0 times a NaN or an infinity would not
-// be 0: in such tiles group A (the tile's group) first replaces what is not finite in V by 0, and
-// rows of tokens that do not exist or were not loaded as well; where it found any, the unit's end
-// adds them to the rows that do see them.
+// Measured on the device (replays): B=8 Hkv=8 of 4 query heads d=128 bf16, 64 drafted tokens (256
+// rows) over up to 32K: 143 us, 1205 TFLOP/s, 4.8 TB/s; B=16, 16 drafted tokens (64 rows) over up to
+// 16K, pages of 16: 118 us, 5.5 TB/s (81 % of the measured copy rate); B=4 Hkv=4 of 8, up to 5 tokens
+// over up to 64K: 68 us, 4.3 TB/s. Of these 8 us are a CTA's start (lengths, table, first tile: three
+// dependent reads, and cold instructions), 5 the join. In the steady state a tile takes 1800 to 2600
+// cycles (one row tile; HBM) or 3200 (two; 2180 of them the tensor pipe's), and the step from one
+// unit to the next some 6000 or 14000 that nothing overlaps.
 //
-// P is rounded to the type once for the product with V, a rounding of the same size as the
-// output's. fp16 ends at 2^-24, so there P is taken 2^11 times as large, and up to 2^4 more until
-// a grown maximum moves the offset: what is lost are probabilities below 2^-36 of the largest.
+// Measured slower (the B=16 case where no other is named): eight softmax warps with a whole row each,
+// which spilled registers, and one producer for K and V, 151 us, when this form took 135; segments
+// worked out by every role for itself and S kept in registers between its maximum and P, 135 when
+// 129; products issued behind a branch on one lane, where operands move to uniform registers one
+// by one (85 cycles an instruction instead of 30), 180 us for the B=8 case when 150; equal runs
+// without the units' cost, 74 us for the B=4 case when 69; a third stage of K or of V for two row
+// tiles in the place that O passes through on its way out, 146 us for the B=8 case instead of 143.
+//
+// Masks. Tiles of the context that no window cuts need none. In the others a thread builds the 64
+// bits of its keys: a range of the context, and the ancestors by walking up the tree. Keys that some
+// row of the tile does not see have P = 0 there, but 0 times a NaN or an infinity would not be 0: in
+// such tiles stream A (the tile's stream) first replaces what is not finite in V by 0, and rows of
+// tokens that do not exist or were not loaded as well; where it found any, the segment's end adds
+// them to the rows that do see them.
+//
+// P is rounded to the type once for the product with V, a rounding of the same size as the output's
+// (relative error 0.0023 for both, bf16, instead of 0.0017 for the output's alone). fp16 ends at
+// 2^-24, so there P is taken 2^11 times as large, and up to 2^4 more until a grown maximum moves the
+// offset: what is lost are probabilities below 2^-36 of the largest.
 #include <cooperative_groups.h>
 #include <stddef.h>
 
@@ -648,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto entry = [&](int j) { return needed(j) ? tab[(row0 + j * br) >> a.page_shift] : -1; };
       int cur = entry(lane), nxt = entry(32 + lane);
       if (!is_v && segs > 0) {
-        // its Q, which is read when the segment before ends, in some 5 us (from HBM beside the
-        // other CTAs' loads that takes 5500 cycles, from L2 XX)
+        // its Q, which is read when the segment before ends, in some 5 us (146 -> 143 us for the
+        // B=8 case; fetched earlier, by the scheduler, it left L2 again)
 #pragma unroll 1
         for (int r = lane; r < sg.live; r += 32) {
           const int token = token_of(a, sg.r0 + r);
@@ -1279,7 +1301,8 @@ int row_tiles(int T, int Hq, int Hkv) { return static_cast<int64_t>(T) * (Hq / H
 
 // The smallest calls: 0, or the CTAs of a cluster that has one unit. A unit of up to kShortTiles
 // tiles for each CTA of a cluster, and few enough units that all clusters run at once, takes one
-// launch without a workspace. Units of one CTA may take a second turn.
+// launch without a workspace: 8 units of 1009 tokens (d=64) 10.7 us a replay instead of 14.2, and a
+// launch less for the caller. Units of one CTA may take a second turn.
 constexpr int kShortTiles = 4;
 int resident_clusters(int ctas) {   // of one CTA on each SM, as the runtime counts them on a GB300
   return ctas == 8 ? 15 : ctas == 4 ? 36 : ctas == 2 ? 76 : 152;
