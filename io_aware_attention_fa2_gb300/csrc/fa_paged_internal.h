@@ -133,7 +133,7 @@ struct ForkParams {
   int* copy_src;            // [C] each
   int* copy_dst;
   int* copy_rows;
-  int B, C, page_size, max_pages;
+  int B, C, page_shift, max_pages;   // 2^page_shift tokens
 };
 cudaError_t launch_paged_fork(const ForkParams& p, cudaStream_t stream);
 
@@ -143,7 +143,7 @@ struct ResizeParams {
   const int* old_lens;      // [B]
   const int* new_lens;      // [B]
   int* granted;             // [B]
-  int B, page_size, max_pages;
+  int B, page_shift, max_pages;
 };
 cudaError_t launch_paged_resize(const ResizeParams& p, cudaStream_t stream);
 

@@ -236,7 +236,7 @@ constexpr int kSmallTables = 8192;   // entries of the tables of a call that one
 
 __device__ __forceinline__ void fork_plan(const ForkParams& p, int* s_warp) {
   const int have = free_pages_of(p.pool);
-  const int64_t capacity = static_cast<int64_t>(p.max_pages) * p.page_size;
+  const int64_t capacity = static_cast<int64_t>(p.max_pages) << p.page_shift;
   int taken = 0;
   for (int c0 = 0; c0 < p.C; c0 += kForkThreads) {
     const int c = c0 + threadIdx.x;
@@ -251,14 +251,14 @@ __device__ __forceinline__ void fork_plan(const ForkParams& p, int* s_warp) {
       }
       if (len < 0) record_page_error();
     }
-    const int tail = len > 0 ? len % p.page_size : 0;
+    const int tail = len > 0 ? len & ((1 << p.page_shift) - 1) : 0;
     int all;
     const int place = taken + block_scan<kForkThreads>(tail > 0, s_warp, &all);
     if (c < p.C) {
       int src = -1, dst = -1, rows = 0;
       if (tail > 0) {
         if (place < have) {
-          src = p.block_table[static_cast<int64_t>(from) * p.max_pages + len / p.page_size];
+          src = p.block_table[static_cast<int64_t>(from) * p.max_pages + (len >> p.page_shift)];
           dst = take_page(p.pool, have - 1 - place);
           rows = tail;
         } else {
@@ -278,7 +278,7 @@ __device__ __forceinline__ void fork_plan(const ForkParams& p, int* s_warp) {
 // Entry `col` of new sequence c's row.
 __device__ __forceinline__ void fork_entry(const ForkParams& p, int c, int col) {
   const int len = load_l2(p.out_seqlens + c);
-  const int full = len > 0 ? len / p.page_size : 0;
+  const int full = len > 0 ? len >> p.page_shift : 0;
   int page = -1;
   if (col < full) {
     page = p.block_table[static_cast<int64_t>(p.source[c]) * p.max_pages + col];
@@ -288,7 +288,7 @@ __device__ __forceinline__ void fork_entry(const ForkParams& p, int c, int col) 
       record_page_error();
       page = -1;
     }
-  } else if (col == full && len > 0 && len % p.page_size) {
+  } else if (col == full && len > 0 && (len & ((1 << p.page_shift) - 1))) {
     page = load_l2(p.copy_dst + c);
   }
   p.out_table[static_cast<int64_t>(c) * p.max_pages + col] = page;
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t capacity = static_cast<int64_t>(p.max_pages) * p.page_size;
+  const int64_t capacity = static_cast<int64_t>(p.max_pages) << p.page_shift;
   int* const s_release = s_prefix;
   int* const s_take = s_prefix + p.B + 1;
   wait_prerequisites();
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
 
   // the prefixes over the sequences, by every CTA for itself
   const int have = free_pages_of(p.pool);
-  auto pages_of = [&](int tokens) { return (tokens + p.page_size - 1) / p.page_size; };
+  auto pages_of = [&](int tokens) { return (tokens + (1 << p.page_shift) - 1) >> p.page_shift; };
   if (tid == 0) s_contest = 0;
   int releases = 0, takes = 0;
   for (int b0 = 0; b0 < p.B; b0 += kResizeThreads) {
