@@ -309,7 +309,8 @@ int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* bloc
 
 size_t fa_paged_tree_workspace_size(int B, int T, int Hq, int Hkv, int d, int page_size,
                                     int max_pages) {
-  if (!cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) || !tree_shape_ok(B, T, Hq, Hkv, page_size, max_pages))
+  if (!cache_shape_ok(B, Hkv, d, page_size, 1, max_pages) ||
+      !tree_shape_ok(B, T, Hq, Hkv, page_size, max_pages))
     return 0;
   return fa::paged_tree_workspace(B, T, Hq, Hkv, d, page_size, max_pages);
 }

@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(kAcceptThreads)
 // ---------------------------------------------------------------------------------------------
 // Copy. Bound by HBM: 4096 pages of 64 tokens, Hkv=8 d=128 with weights (2.2 GB both ways) 311 us,
 // 7.0 TB/s, as fast as a plain copy; 16 pages of 16 tokens 1.7 us. The first rows of a page are
-// contiguous in K and in V: a block has 16 KiB of one of them, all its loads before its stores. Weights, [Hkv][page_size] of a page, go to the
-// blocks of K.
+// contiguous in K and in V: a block has 16 KiB of one of them, all its loads before its stores.
+// Weights, [Hkv][page_size] of a page, go to the blocks of K.
 constexpr int kCopyThreads = 256, kCopyLoads = 4;
 constexpr int kCopyChunks = kCopyThreads * kCopyLoads;   // 16 bytes each
 
@@ -318,8 +318,9 @@ __global__ void __launch_bounds__(kForkThreads)
 // ---------------------------------------------------------------------------------------------
 // Resize, by one cluster: first the pages that shorter sequences give back, then those that
 // longer ones take. Bound by latency (a few pages), or by the atomics and scattered accesses of the
-// cluster's SMs: 28 us for 330000 pages given back or taken, 57 where all of them are shared by five
-// tables (sixteen SMs; eight, with every page bid for, took 134).
+// cluster's SMs: 17 us for 330000 pages given back or taken, 27 to give back entries of pages that
+// other tables keep, 59 where five tables give up all of their pages at once and bid for them
+// (replays; eight SMs, with every page bid for, took 134).
 //
 // The order of the stack is the tables' order, whatever the number of threads and their timing: a
 // page that several tables give back at once goes by the last of them. Each gives up its
@@ -328,15 +329,26 @@ __global__ void __launch_bounds__(kForkThreads)
 // place in the order, by an atomic minimum on the references; the one whose bid stands pushes it.
 //
 // A warp has consecutive items (entries that are given back, or taken), kBatch at a time for each
-// lane, so that as many accesses are on their way; item f belongs to the sequence whose prefix it
-// lies behind, which a lane finds by search once and then by steps.
+// lane, so that as many accesses are on their way; a lane finds its first item's sequence by search
+// and the others' by steps.
 constexpr int kResizeThreads = 1024, kResizeCluster = 16, kBatch = 4;
 
-struct ItemWalk {
+// The table entry of item f, then of items 32 further on each. The items of sequence b are the
+// entries behind the page of its token lens[b] - 1.
+struct EntryWalk {
+  const ResizeParams& p;
   const int* prefix;   // [B + 1], shared memory
-  int b;               // the item's sequence
-  __device__ __forceinline__ ItemWalk(const int* p, int B, int f) : prefix(p) {
-    int lo = 0, hi = B;   // prefix[lo] <= f < prefix[hi]
+  const int* lens;
+  int b, f, end;       // sequence, item, the sequence's last item + 1
+  int* at;
+  __device__ __forceinline__ void find() {
+    const int64_t first = (static_cast<int64_t>(lens[b]) + (1 << p.page_shift) - 1) >> p.page_shift;
+    at = p.block_table + static_cast<int64_t>(b) * p.max_pages + first + f - prefix[b];
+    end = prefix[b + 1];
+  }
+  __device__ __forceinline__ EntryWalk(const ResizeParams& p, const int* prefix, const int* lens, int f)
+      : p(p), prefix(prefix), lens(lens), f(f) {
+    int lo = 0, hi = p.B;   // prefix[lo] <= f < prefix[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (prefix[mid] <= f)
@@ -345,10 +357,19 @@ struct ItemWalk {
         hi = mid;
     }
     b = lo;
+    find();
   }
-  __device__ __forceinline__ int to(int f) {   // f within the items, no smaller than before
-    while (prefix[b + 1] <= f) ++b;
-    return f - prefix[b];
+  // The entry, or null behind item `last` - 1; then on to the next.
+  __device__ __forceinline__ int* next(int last) {
+    if (f >= last) return nullptr;
+    if (f >= end) {
+      while (prefix[b + 1] <= f) ++b;
+      find();
+    }
+    int* const entry = at;
+    f += 32;
+    at += 32;
+    return entry;
   }
 };
 
@@ -407,22 +428,14 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
   int pushed = 0;
   if (releases > 0) {
     const int f0 = first_item(releases, w), f1 = first_item(releases, w + 1);
-    // do(i, entry) for the lane's items f0 + lane + 32 i, kBatch entries at a time
+    // batch(i, entries) for the lane's items f0 + lane + 32 i, kBatch entries at a time
     auto for_items = [&](auto&& batch) {
       if (f0 + lane >= f1) return;
-      ItemWalk walk(s_release, p.B, f0 + lane);
+      EntryWalk walk(p, s_release, p.new_lens, f0 + lane);
       for (int i = 0; f0 + lane + 32 * i < f1; i += kBatch) {
         int* at[kBatch];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int f = f0 + lane + 32 * (i + u);
-          at[u] = nullptr;
-          if (f < f1) {
-            const int in = walk.to(f);
-            at[u] = p.block_table + static_cast<int64_t>(walk.b) * p.max_pages +
-                    pages_of(p.new_lens[walk.b]) + in;
-          }
-        }
+        for (int u = 0; u < kBatch; ++u) at[u] = walk.next(f1);
         batch(i, at);
       }
     };
@@ -506,22 +519,16 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
     }
     // the warp's items in order: 32 of them for each i
     {
-      ItemWalk walk(s_release, p.B, min(f0 + lane, releases - 1));
+      EntryWalk walk(p, s_release, p.new_lens, min(f0 + lane, releases - 1));
+      walk.f = f0 + lane;   // (past the last item it is at none of them)
       const int steps = (f1 - f0 + 31) / 32;
       for (int i = 0; i < steps; i += kBatch) {
         int* at[kBatch];
         int page[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-          const int f = f0 + lane + 32 * (i + u);
-          at[u] = nullptr;
-          page[u] = -1;
-          if (f < f1) {
-            const int in = walk.to(f);
-            at[u] = p.block_table + static_cast<int64_t>(walk.b) * p.max_pages +
-                    pages_of(p.new_lens[walk.b]) + in;
-            page[u] = *at[u];
-          }
+          at[u] = walk.next(f1);
+          page[u] = at[u] ? *at[u] : -1;
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
   {
     const int f0 = first_item(taken, w), f1 = first_item(taken, w + 1);
     if (f0 + lane < f1) {
-      ItemWalk walk(s_take, p.B, f0 + lane);
+      EntryWalk walk(p, s_take, p.old_lens, f0 + lane);
       for (int f = f0 + lane; f < f1; f += 32 * kBatch) {
         int page[kBatch];
 #pragma unroll
@@ -566,8 +573,8 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
           page[u] = f + 32 * u < f1 ? load_l2(p.pool.free_pages + stack - 1 - (f + 32 * u)) : -1;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-          if (f + 32 * u >= f1) break;
-          const int in = walk.to(f + 32 * u);
+          int* const at = walk.next(f1);
+          if (!at) break;
           if (page[u] >= 0 && page[u] < p.pool.num_pages) {
             p.pool.refs[page[u]] = 1;
           } else {
@@ -575,8 +582,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
             page[u] = -1;
           }
           p.pool.free_pages[stack - 1 - (f + 32 * u)] = -1;
-          p.block_table[static_cast<int64_t>(walk.b) * p.max_pages + pages_of(p.old_lens[walk.b]) +
-                        in] = page[u];
+          *at = page[u];
         }
       }
     }
