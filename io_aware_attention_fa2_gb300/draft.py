@@ -5,11 +5,14 @@ fa_paged_tree, fa_paged_accept, fa_paged_copy, fa_paged_fork and fa_paged_resize
 A step of speculative decoding, for a batch whose drafted tokens form trees (``parents`` int32
 [B, T]: an earlier drafted token, or -1 for the context):
 
-    room = paged_resize(pool, block_table, seqlens, seqlens + T, page_size)  # == seqlens + T
-    fa_paged_append(k, v, k_pages, v_pages, block_table, room)
-    o, lse = paged_tree_attention(q, k_pages, v_pages, block_table, room, parents=parents)
-    # ... the model goes on; leaf int32 [B] is the last drafted token that it agrees with ...
-    path, seqlens = paged_accept(k_pages, v_pages, block_table, room, leaf, parents)
+    room = paged_resize(pool, block_table, seqlens, seqlens + T, page_size)
+    drafted = room - seqlens            # T, or 0 for a sequence that the pool had no pages for
+    fa_paged_append(k, v, k_pages, v_pages, block_table, room, new_lens=drafted)
+    o, lse = paged_tree_attention(q, k_pages, v_pages, block_table, room, parents=parents,
+                                  new_lens=drafted)
+    # ... the model goes on; leaf int32 [B] is the last drafted token that it agrees with, or -1 ...
+    path, seqlens = paged_accept(k_pages, v_pages, block_table, room, leaf, parents,
+                                 new_lens=drafted)
     paged_resize(pool, block_table, room, seqlens, page_size)
 
 A pool (``new_page_pool``) says which pages are free and how many tables hold each. Several
@@ -132,7 +135,7 @@ def _tree(q, k_pages, v_pages, block_table, seqlens, o, lse, scale, parents, new
     _enqueue("fa_paged_tree", _library().fa_paged_tree, device, stream, (
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         seqlens.data_ptr(), _ptr(parents), _ptr(new_lens), o.data_ptr(), lse.data_ptr(), B, T, Hq,
-        Hkv, d, page_size, num_pages, max_pages, _bound(window_left), scale, _dtype_code(q), ws,
+        Hkv, d, page_size, num_pages, max_pages, _bound(window_left), float(scale), _dtype_code(q), ws,
         ws_bytes))
     return o, lse
 

@@ -352,13 +352,14 @@ def test_same_bits_every_time_and_on_other_streams(T, Hq):
             run(c, q, parents, workspace=ws[:need - 16])
 
 
-def test_two_captured_graphs_and_an_eager_call():
+@pytest.mark.parametrize("ctx", [3000, 6000])
+def test_two_captured_graphs_and_an_eager_call(ctx):
     """Two graphs, each with a workspace of its own, replayed beside one another and beside eager
-    calls, on lengths and trees that change between the replays."""
+    calls, on lengths and trees that change between the replays; by one launch and by two."""
     T, Hq = 12, 8
     caches, graphs = [], []
     for s in (1, 2):
-        c = draft_cache([3000, 100], [T] * 2, 16, 2, 128, "bf16", seed=s)
+        c = draft_cache([ctx, 100], [T] * 2, 16, 2, 128, "bf16", seed=s)
         q, parents = queries(c, 2, T, Hq), random_trees(c.g, 2, T).cuda()
         run(c, q, parents)
         torch.cuda.synchronize()
@@ -439,3 +440,46 @@ def test_one_drafted_token_is_a_decoding_step():
     check_tree(o, lse, ref, "tree")
     o1, lse1 = fa.paged_attention(q[:, 0].contiguous(), c.k, c.v, c.table, c.seqlens)
     check_tree(o1[:, None], lse1[:, :, None], ref, "decode")
+
+
+def test_readme_example():
+    """The README's block as it stands: its attention, and its sequences after the fork."""
+    import os
+    import re
+
+    import io_aware_attention_fa2_gb300 as fa
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    blocks = [b for b in re.findall(r"```python\n(.*?)```", open(path).read(), flags=re.S)
+              if "paged_tree_attention" in b]
+    assert len(blocks) == 1
+    B, T, Hq, Hkv, d, page, width, num_pages = 3, 7, 4, 2, 64, 16, 12, 60
+    lens, leaves, source = [50, 16, 0], [6, 3, -1], [0, 0, 2, 1]
+    c = draft_cache(lens, [T] * B, page, Hkv, d, "bf16", seed=8)
+    pool = fa.new_page_pool(num_pages)
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    seqlens = fa.paged_resize(pool, table, int32([0] * B), int32(lens), page)
+    k_pages = torch.full((num_pages, page, Hkv, d), float("nan"), dtype=c.dtype, device="cuda")
+    v_pages = k_pages.clone()
+    parents = torch.tensor([[-1, 0, 0, 1, 2, 3, 5]] * B, dtype=torch.int32)
+    k, v = (torch.zeros((B, T, Hkv, d), dtype=c.dtype, device="cuda") for _ in "kv")
+    rows = []
+    for b, n in enumerate(lens):
+        pg, row = c.rows(c.table, b, n + T)
+        own = table[b].long().repeat_interleave(page)[:n]
+        k_pages[own, row[:n]], v_pages[own, row[:n]] = c.k[pg[:n], row[:n]], c.v[pg[:n], row[:n]]
+        k[b], v[b] = c.k[pg[n:], row[n:]], c.v[pg[n:], row[n:]]
+        keep = list(range(n)) + [n + i for i in (line(parents[b].tolist(), leaves[b]))]
+        rows.append((c.k[pg[keep], row[keep]], c.v[pg[keep], row[keep]]))
+    q = queries(c, B, T, Hq)
+    ns = dict(pool=pool, block_table=table, seqlens=seqlens, T=T, page_size=page, k=k, v=v, q=q,
+              k_pages=k_pages, v_pages=v_pages, parents=parents.cuda(), source=int32(source),
+              verify=lambda o: int32(leaves))
+    exec(blocks[0], ns)
+    check_tree(ns["o"], ns["lse"], tree_ref(c, q, default_scale(d), parents), "README")
+    forked = ns["forked"]
+    assert forked.seqlens.tolist() == [len(rows[s][0]) for s in source]
+    for i, s in enumerate(source):
+        n = len(rows[s][0])
+        pg = forked.block_table[i].long().repeat_interleave(page)[:n]
+        row = torch.arange(n, device="cuda") % page
+        assert same_bits(k_pages[pg, row], rows[s][0]) and same_bits(v_pages[pg, row], rows[s][1])
