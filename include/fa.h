@@ -466,8 +466,8 @@ int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* bloc
  * The cache's weights get nothing: which of the tokens will stay is not known yet. Rows at or
  * past n_b, and of tokens that see nothing, get O = 0 and LSE = -inf. What is in keys and values
  * that a token does not see (NaN included) does not matter to it; an infinite value of a token
- * that it sees makes its column of O infinite, values of both signs or a NaN make it NaN. A sequence
- * whose length is beyond the table or below n_b sees nothing, tokens in pages outside the pool are
+ * that it sees makes its column of O infinite (NaN where the token's probability is too small for
+ * the type), values of both signs or a NaN make it NaN. A sequence whose length is beyond the table or below n_b sees nothing, tokens in pages outside the pool are
  * left out, and a parent that is not an earlier token counts as -1 (each FA_ERR_PAGE in the
  * device error word). The same call gives the same bits.
  */
