@@ -358,7 +358,8 @@ int fa_paged_tree(const void* q, const void* k_pages, const void* v_pages, const
   p.workspace = workspace;
   p.T = T;
   p.Hq = Hq;
-  p.window_left = window_left < 0 ? -1 : window_left;
+  // (no token has more in front of it than the table holds)
+  p.window_left = window_left < 0 ? -1 : std::min(window_left, max_pages * page_size);
   p.fp16 = dtype == FA_FP16 ? 1 : 0;
   p.scale_log2 = scale * kLog2e;
   return fa::launch_paged_tree(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
