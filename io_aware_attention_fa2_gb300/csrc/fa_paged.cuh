@@ -116,6 +116,24 @@ cudaError_t launch_paged(void (*kernel)(Params...), int64_t grid, int block, siz
   return launch_chained(kernel, grid, block, smem, stream, cluster, args...);
 }
 
+// A kernel whose blocks, at most as many as run at once, wait for one another (cooperative launch;
+// it starts when what is in front of it on the stream has ended).
+template <typename... Params, typename... Args>
+cudaError_t launch_together(void (*kernel)(Params...), int grid, int block, size_t smem,
+                            cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {};
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // A run of equal length for each CTA, of tiles counted over all units of a call.

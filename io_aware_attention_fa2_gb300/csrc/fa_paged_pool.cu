@@ -332,6 +332,8 @@ __global__ void __launch_bounds__(kForkThreads)
 // lane, so that as many accesses are on their way; a lane finds its first item's sequence by search
 // and the others' by steps.
 constexpr int kResizeThreads = 1024, kResizeCluster = 16, kBatch = 4;
+constexpr int kLargeTables = 1 << 17, kLargeBatch = 64;
+constexpr int kFlag = 1 << 30;             // (a CTA of many has fewer items)
 
 // The table entry of item f, then of items 32 further on each. The items of sequence b are the
 // entries behind the page of its token lens[b] - 1.
@@ -373,12 +375,20 @@ struct EntryWalk {
   }
 };
 
+template <bool ALL>
 __global__ void __launch_bounds__(kResizeThreads, 1)
     fa_paged_resize_kernel(const __grid_constant__ ResizeParams p) {
   extern __shared__ __align__(16) int s_prefix[];   // [B + 1] releases, [B + 1] takes
-  __shared__ int s_warp[32], s_total, s_contest;
+  __shared__ int s_warp[32], s_total, s_before;
   const cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
+  const int rank = ALL ? blockIdx.x : static_cast<int>(cluster.block_rank());
+  const int ranks = ALL ? gridDim.x : static_cast<int>(cluster.num_blocks());
+  auto meet = [&] {   // all CTAs, with what they have written
+    if constexpr (ALL)
+      cg::this_grid().sync();
+    else
+      cluster.sync();
+  };
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t capacity = static_cast<int64_t>(p.max_pages) << p.page_shift;
   int* const s_release = s_prefix;
@@ -389,7 +399,6 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
   // the prefixes over the sequences, by every CTA for itself
   const int have = free_pages_of(p.pool);
   auto pages_of = [&](int tokens) { return (tokens + (1 << p.page_shift) - 1) >> p.page_shift; };
-  if (tid == 0) s_contest = 0;
   int releases = 0, takes = 0;
   for (int b0 = 0; b0 < p.B; b0 += kResizeThreads) {
     const int b = b0 + tid;
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
         }
       }
     });
-    cluster.sync();
+    meet();
     // a page without references that this call gave up more than once
     if (bits && other)
       for_items([&](int i, int* (&at)[kBatch]) {
@@ -478,9 +487,33 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) contest |= left[u] == 0;
       });
-    if (contest) *cluster.map_shared_rank(&s_contest, 0) = 1;
-    cluster.sync();
-    const bool bid = *cluster.map_shared_rank(&s_contest, 0) != 0;
+    // Pages to push by this warp's lanes, `count` each: by those of warps before this one, in
+    // `before`, and by all, in `pushed`; and whether `flag` is set in any thread.
+    int before = 0;
+    auto count_all = [&](int count, bool flag) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) count += __shfl_xor_sync(0xffffffffu, count, off);
+      int all;
+      before = block_scan<kResizeThreads>(lane == 0 ? count : 0, s_warp, &all);
+      before = __shfl_sync(0xffffffffu, before, 0);
+      const int mine = all | (__syncthreads_or(flag) ? kFlag : 0);
+      if (tid == 0) (ALL ? p.granted[rank] : s_total) = mine;
+      meet();
+      int of_rank = 0;
+      if (tid < ranks) of_rank = ALL ? load_l2(p.granted + tid) : *cluster.map_shared_rank(&s_total, tid);
+      const bool any = __syncthreads_or(of_rank & kFlag);
+      const int earlier = block_scan<kResizeThreads>(of_rank & (kFlag - 1), s_warp, &pushed);
+      if (tid == rank) s_before = earlier;
+      __syncthreads();
+      before += s_before;
+      return any;
+    };
+    const bool bid = count_all(__popcll(last), contest);
+    // whether item i is the one that pushes its page
+    auto pushes = [&](int i, int page) {
+      if (!bid) return (last >> i & 1) != 0;
+      return page >= 0 && load_l2(p.pool.refs + page) == -1 - (f0 + lane + 32 * i);
+    };
     if (bid) {
       for_items([&](int i, int* (&at)[kBatch]) {
 #pragma unroll
@@ -490,32 +523,13 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
             atomicMin(p.pool.refs + page, -1 - (f0 + lane + 32 * (i + u)));
         }
       });
-      cluster.sync();
-    }
-    // whether item i is the one that pushes its page
-    auto pushes = [&](int i, int page) {
-      if (!bid) return (last >> i & 1) != 0;
-      return page >= 0 && load_l2(p.pool.refs + page) == -1 - (f0 + lane + 32 * i);
-    };
-    int count = 0;
-    if (!bid)
-      count = __popcll(last);
-    else
+      meet();
+      int count = 0;
       for_items([&](int i, int* (&at)[kBatch]) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) count += at[u] && pushes(i + u, *at[u]);
       });
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) count += __shfl_xor_sync(0xffffffffu, count, off);
-    int all;
-    int before = block_scan<kResizeThreads>(lane == 0 ? count : 0, s_warp, &all);
-    before = __shfl_sync(0xffffffffu, before, 0);
-    if (tid == 0) s_total = all;
-    cluster.sync();
-    for (int r = 0; r < ranks; ++r) {
-      const int n = *cluster.map_shared_rank(&s_total, r);
-      pushed += n;
-      if (r < rank) before += n;
+      count_all(count, false);
     }
     // the warp's items in order: 32 of them for each i
     {
@@ -548,7 +562,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
       }
     }
     pushed = min(pushed, p.pool.num_pages - have);
-    cluster.sync();   // the stack is whole; no CTA leaves while another reads its count
+    meet();   // the stack is whole; every CTA has read the counts
   }
 
   // The takes. What fits is a prefix of them: up to the largest one within the stack, found by
@@ -593,7 +607,7 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
     const bool fits = s_take[b + 1] == s_take[b] || s_take[b + 1] <= stack;
     p.granted[b] = ok && fits ? to : from;
   }
-  if (ranks > 1) cluster.sync();   // every CTA has read num_free
+  if (ranks > 1 && releases == 0) meet();   // every CTA has read num_free
   if (rank == 0 && tid == 0) *p.pool.num_free = stack - taken;
 }
 
@@ -654,17 +668,34 @@ cudaError_t launch_paged_fork(const ForkParams& p, cudaStream_t stream) {
                       stream, 0, p, blocks);
 }
 
-cudaError_t launch_paged_resize(const ResizeParams& p, cudaStream_t stream) {
+template <bool ALL>
+cudaError_t prepare_resize() {
   constexpr int kMost = 2 * (kMaxPoolBatch + 1) * 4;
-  cudaError_t err = cudaFuncSetAttribute(
-      fa_paged_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  return cudaFuncSetAttribute(fa_paged_resize_kernel<ALL>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+}
+
+cudaError_t launch_paged_resize(const ResizeParams& p, cudaStream_t stream) {
+  const int64_t entries = static_cast<int64_t>(p.B) * p.max_pages;
+  const size_t smem = 2 * (p.B + 1) * 4;
+  cudaError_t err;
+  if (entries >= kLargeTables && p.B >= kLargeBatch) {
+    int device, sms;
+    if ((err = prepare_resize<true>()) != cudaSuccess ||
+        (err = cudaGetDevice(&device)) != cudaSuccess ||
+        (err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
+      return err;
+    return launch_together(fa_paged_resize_kernel<true>, std::min(p.B, sms), kResizeThreads, smem,
+                           stream, p);
+  }
+  err = prepare_resize<false>();
   if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(fa_paged_resize_kernel,
+  err = cudaFuncSetAttribute(fa_paged_resize_kernel<false>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (err != cudaSuccess) return err;
   // Small tables are one block's: two calls for 16 sequences of 258 pages 10.0 us instead of 13.9.
-  const int ctas = static_cast<int64_t>(p.B) * p.max_pages <= kSmallTables ? 1 : kResizeCluster;
-  return launch_paged(fa_paged_resize_kernel, ctas, kResizeThreads, 2 * (p.B + 1) * 4, stream,
+  const int ctas = entries <= kSmallTables ? 1 : kResizeCluster;
+  return launch_paged(fa_paged_resize_kernel<false>, ctas, kResizeThreads, smem, stream,
                       ctas > 1 ? ctas : 0, p);
 }
 

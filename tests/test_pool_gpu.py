@@ -253,6 +253,71 @@ def test_fork_and_the_end_of_all(page, B, C, longest):
     assert len(pool.free) == len(pool.refs) and not any(pool.refs)
 
 
+@pytest.mark.parametrize("B,width,page,spare", [(64, 2100, 16, 5), (152, 900, 64, 5),
+                                                (700, 200, 16, 5), (150, 1000, 16, -20000),
+                                                (8192, 16, 256, 5)])
+def test_large_tables(B, width, page, spare):
+    """Tables that all SMs work on: growth, changes both ways, a pool that runs out, forks and the
+    end of those that share pages, in one call."""
+    import io_aware_attention_fa2_gb300 as fa
+    r = random.Random(B)
+    longest = width * page
+    pool = shuffled_pool(r, B * width // 2 + spare)
+    table = [[-1] * width for _ in range(B)]
+    dev, dev_table = books(pool), int32(table)
+    lens = [0] * B
+    for step in range(3):
+        later = [r.randint(0, longest // (2 if step else 3)) if r.random() < 0.9 else n for n in lens]
+        later[r.randrange(B)] = longest
+        got = fa.paged_resize(dev, dev_table, int32(lens), int32(later), page)
+        lens = pool.resize(table, lens, later, page)
+        assert got.tolist() == lens, step
+        assert dev_table.tolist() == table, step
+        check_books(dev, pool, step)
+    source = [r.randrange(B // 3) for _ in range(B)]   # several of the same sequence
+    got = fa.paged_fork(dev, dev_table, int32(lens), int32(source), page)
+    new, new_lens = pool.fork(table, lens, source, page)[:2]
+    assert got.block_table.tolist() == new and got.seqlens.tolist() == new_lens
+    check_books(dev, pool, "fork")
+    new_lens = [max(n, 0) for n in new_lens]
+    for t, dev_t, n, to in ((table, dev_table, lens, 0), (new, got.block_table, new_lens, page),
+                            (new, got.block_table, [min(x, page) for x in new_lens], 0)):
+        later = [min(x, to) for x in n]
+        granted = fa.paged_resize(dev, dev_t, int32(n), int32(later), page)
+        assert granted.tolist() == pool.resize(t, n, later, page) == later
+        assert dev_t.tolist() == t
+        check_books(dev, pool, to)
+    assert len(pool.free) == len(pool.refs) and fa.device_error() == 0
+
+
+def test_large_tables_with_bad_entries():
+    """Of 200 sequences one names a page outside the pool, one a free page, two the same page once
+    referenced, and one has a length outside its table: recorded, the others are served."""
+    import io_aware_attention_fa2_gb300 as fa
+    B, width, page = 200, 700, 16
+    pool = Pool(1000)
+    table = [[-1] * width for _ in range(B)]
+    lens = [64] * B
+    pool.resize(table, [0] * B, lens, page)
+    dev, dev_table = books(pool), int32(table)
+    dev_table[3, 1], dev_table[7, 0] = 10 ** 6, pool.free[5]
+    dev_table[50, 2] = table[90][3]
+    lens[180] = width * page + 1
+    later = [0] * 150 + [64] * 30 + [0] + [64] * 19
+    got = fa.paged_resize(dev, dev_table, int32(lens), int32(later), page)
+    assert fa.device_error() == FA_ERR_PAGE
+    assert got.tolist() == later[:180] + [lens[180]] + later[181:]
+    assert (dev_table[:150] == -1).all() and dev_table[150:].tolist() == table[150:]
+    # which of the two entries counted is not told: the page returned once
+    back = {p for b in range(150) for p in table[b][:4]}
+    back -= {table[3][1], table[7][0], table[50][2]}
+    n = int(dev.num_free[0])
+    assert n == len(pool.free) + len(back)
+    assert dev.free_pages[:len(pool.free)].tolist() == pool.free
+    assert set(dev.free_pages[len(pool.free):n].tolist()) == back
+    assert all(dev.refs[p] == 0 for p in back)
+
+
 def test_an_empty_pool():
     """What the pool cannot give is refused from there on; pages given back in the same call count;
     sequences that need none are served."""
