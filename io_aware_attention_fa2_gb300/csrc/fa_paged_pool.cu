@@ -232,7 +232,7 @@ __device__ __forceinline__ int take_page(const PagePool& p, int i) {
 // by the same block where the tables are small. Bound by latency, or by the atomics: a plan of 256
 // sequences 4.7 us, their 330000 entries 8.2 (launches alone).
 constexpr int kForkThreads = 1024;
-constexpr int kSmallTables = 8192;   // entries of the tables of a call that one block has
+constexpr int kSmallTables = 8192;   // entries of a call's tables that one block has
 
 __device__ __forceinline__ void fork_plan(const ForkParams& p, int* s_warp) {
   const int have = free_pages_of(p.pool);
@@ -316,24 +316,33 @@ __global__ void __launch_bounds__(kForkThreads)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Resize, by one cluster: first the pages that shorter sequences give back, then those that
-// longer ones take. Bound by latency (a few pages), or by the atomics and scattered accesses of the
-// cluster's SMs: 17 us for 330000 pages given back or taken, 27 to give back entries of pages that
-// other tables keep, 59 where five tables give up all of their pages at once and bid for them
-// (replays; eight SMs, with every page bid for, took 134).
+// Resize: first the pages that shorter sequences give back, then those that longer ones take. Bound
+// by latency (a few pages), or by the atomics and scattered accesses of the SMs at work:
+//   - up to kSmallTables entries that change, one CTA: two calls for 16 sequences of 258 pages 10.0 us
+//     (replays; 13.9 by sixteen);
+//   - more, a cluster of sixteen: 65536 pages of 64 sequences taken and given back 19 us;
+//   - tables of kLargeTables entries of many sequences, all SMs by a cooperative launch: 524288
+//     pages of 152 sequences taken and given back 26.5 us, not 66.4; 131072 20.6, not 27.1; 65536
+//     19.9, not 20.1; of 32 sequences 524288 in 41.5, not 64.0, of 16 in 65.9, not 63.9 (a CTA for each
+//     sequence at most, see below). A few pages of such tables 14.1 us, not 12.1: a cooperative launch
+//     starts when what is in front of it has ended.
+// A fork of 64 sequences of up to 32K tokens into 256 and its end, where up to five tables give up
+// each page at once: 26 us, not 51.
 //
 // The order of the stack is the tables' order, whatever the number of threads and their timing: a
 // page that several tables give back at once goes by the last of them. Each gives up its
 // reference; the one that took the last reference pushes the page, unless the page was given up
 // by others of this call as well. Only if there is such a page do all bid for theirs: -1 - the
 // place in the order, by an atomic minimum on the references; the one whose bid stands pushes it.
+// What the CTAs count goes to the others through distributed shared memory, or through `granted`,
+// which has an element for each and gets its values at the end.
 //
 // A warp has consecutive items (entries that are given back, or taken), kBatch at a time for each
 // lane, so that as many accesses are on their way; a lane finds its first item's sequence by search
 // and the others' by steps.
 constexpr int kResizeThreads = 1024, kResizeCluster = 16, kBatch = 4;
-constexpr int kLargeTables = 1 << 17, kLargeBatch = 64;
-constexpr int kFlag = 1 << 30;             // (a CTA of many has fewer items)
+constexpr int kLargeTables = 1 << 17, kLargeBatch = 32;
+constexpr int kFlag = 1 << 30;             // beside a count (one CTA has fewer entries than that)
 
 // The table entry of item f, then of items 32 further on each. The items of sequence b are the
 // entries behind the page of its token lens[b] - 1.
@@ -382,9 +391,11 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
   __shared__ int s_warp[32], s_total, s_before;
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = ALL ? blockIdx.x : static_cast<int>(cluster.block_rank());
-  const int ranks = ALL ? gridDim.x : static_cast<int>(cluster.num_blocks());
+  int ranks = ALL ? gridDim.x : static_cast<int>(cluster.num_blocks());
   auto meet = [&] {   // all CTAs, with what they have written
-    if constexpr (ALL)
+    if (ranks == 1)
+      __syncthreads();
+    else if constexpr (ALL)
       cg::this_grid().sync();
     else
       cluster.sync();
@@ -428,6 +439,11 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
     s_take[p.B] = takes;
   }
   __syncthreads();
+  // A few entries of large tables are one CTA's (which waits for no other).
+  if (static_cast<int64_t>(releases) + takes <= kSmallTables) {
+    if (rank > 0) return;
+    ranks = 1;
+  }
   // this warp's items of n
   const int warps = ranks * (kResizeThreads / 32), w = rank * (kResizeThreads / 32) + warp;
   auto first_item = [&](int n, int at) {
@@ -693,7 +709,6 @@ cudaError_t launch_paged_resize(const ResizeParams& p, cudaStream_t stream) {
   err = cudaFuncSetAttribute(fa_paged_resize_kernel<false>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (err != cudaSuccess) return err;
-  // Small tables are one block's: two calls for 16 sequences of 258 pages 10.0 us instead of 13.9.
   const int ctas = entries <= kSmallTables ? 1 : kResizeCluster;
   return launch_paged(fa_paged_resize_kernel<false>, ctas, kResizeThreads, smem, stream,
                       ctas > 1 ? ctas : 0, p);
