@@ -276,7 +276,7 @@ def fa_paged_fork(pool, block_table, seqlens, source, out: Forked, page_size: in
 
 def _fork(pool, block_table, seqlens, source, out, page_size, stream):
     """fa_paged_fork; an `out` that is None is allocated. Returns it."""
-    torch, int32, _, _, _, _ = _torch()
+    torch, int32, _, empty_like, _, _ = _torch()
     device, B, max_pages, num_pages = _tables(pool, block_table)
     refs, free_pages, num_free = pool
     _fits("seqlens", seqlens, (B,), int32, device)
@@ -288,8 +288,10 @@ def _fork(pool, block_table, seqlens, source, out, page_size, stream):
     page_size = _count("page_size", page_size)
     if out is None:
         with _NO_CONTEXT if stream is None else _stream_of(stream, block_table.device):
+            # (four allocations cost less than views of one)
             out = Forked(torch.empty((C, max_pages), dtype=int32, device=source.device),
-                         *torch.empty((4, C), dtype=int32, device=source.device).unbind(0))
+                         empty_like(source), empty_like(source), empty_like(source),
+                         empty_like(source))
         table, lens, src, dst, rows = out
     else:
         table, lens, src, dst, rows = out
