@@ -116,8 +116,10 @@ cudaError_t launch_paged(void (*kernel)(Params...), int64_t grid, int block, siz
   return launch_chained(kernel, grid, block, smem, stream, cluster, args...);
 }
 
-// A kernel whose blocks, at most as many as run at once, wait for one another (cooperative launch;
-// it starts when what is in front of it on the stream has ended).
+// A kernel whose blocks, at most as many as run at once, wait for one another by the grid's barrier: a
+// cooperative launch, which has all of them resident together or fails, and whose barrier is its own,
+// so that calls on several streams and captured graphs do not meet. It starts when what is in front
+// of it on the stream has ended.
 template <typename... Params, typename... Args>
 cudaError_t launch_together(void (*kernel)(Params...), int grid, int block, size_t smem,
                             cudaStream_t stream, const Args&... args) {

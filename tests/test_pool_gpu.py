@@ -290,6 +290,62 @@ def test_large_tables(B, width, page, spare):
     assert len(pool.free) == len(pool.refs) and fa.device_error() == 0
 
 
+def test_large_tables_on_two_streams():
+    """Two captured graphs, each with a pool of its own, replayed beside one another, and eager calls
+    on a third pool meanwhile: the books of each as when it runs alone."""
+    import io_aware_attention_fa2_gb300 as fa
+    B, width, page = 160, 900, 16
+
+    def work(seed):
+        g = torch.Generator().manual_seed(seed)
+        pool = fa.new_page_pool(B * width)
+        pool.free_pages.copy_(torch.randperm(B * width, generator=g))
+        table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+        zero = int32([0] * B)
+        lens = [torch.randint(0, width * page, (B,), generator=g, dtype=torch.int32).cuda()
+                for _ in range(2)]
+        source = torch.randint(0, B // 2, (B,), generator=g, dtype=torch.int32).cuda()
+
+        def run():
+            a = fa.paged_resize(pool, table, zero, lens[0], page)
+            b = fa.paged_resize(pool, table, a, lens[1], page)
+            child = fa.paged_fork(pool, table, b, source, page)
+            kept = [x.clone() for x in (*pool, table, *child)]
+            c = fa.paged_resize(pool, table, b, zero, page)
+            fa.paged_resize(pool, child.block_table, child.seqlens.clamp(min=0), zero, page)
+            return [*pool, table, a, b, c, *child, *kept]
+        return run, pool
+
+    def state(pool):
+        return [x.clone() for x in pool]
+
+    jobs = [work(s) for s in (1, 2, 3)]
+    start = [state(pool) for _, pool in jobs]
+    # alone, twice: the second run finds the stack as the first one left it
+    alone = [[[x.clone() for x in run()] for _ in range(2)] for run, _ in jobs]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for (run, _), s in zip(jobs, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs.append(run())
+        graphs.append(graph)
+    for (_, pool), books_ in zip(jobs, start):
+        for x, y in zip(pool, books_):
+            x.copy_(y)
+    torch.cuda.synchronize()
+    for step in range(2):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        eager = jobs[2][0]()
+        torch.cuda.synchronize()
+        for got, want in zip((*outs, eager), alone):
+            for i, (x, y) in enumerate(zip(got, want[step])):
+                assert torch.equal(x, y), (step, i)
+    assert fa.device_error() == 0
+
+
 def test_large_tables_with_bad_entries():
     """Of 200 sequences one names a page outside the pool, one a free page, two the same page once
     referenced, and one has a length outside its table: recorded, the others are served."""
