@@ -142,12 +142,12 @@ __device__ __forceinline__ Unit unit_of(const Args& a, Draft dr, int rb) {
 __device__ __forceinline__ Draft draft(const Args& a, int b) {
   return draft_of(a.seqlens, a.new_lens, b, a.T, a.max_pages << a.page_shift);
 }
-// What a unit costs in a run, in tiles: its tiles and, for its start and end, kUnitCost.
-template <int ROWS>
-constexpr int kUnitCost = ROWS == 2 * kTile ? 8 : 6;
-template <int ROWS>
+// What a unit costs in a run, in tiles: its tiles and, for its start and end, kUnitCost (of 3 to 16
+// the best or within 2 % of it for 8 to 256 units, 64 of them by 118 us and 138; 512 units of up to
+// 4096 tokens take 133 us, with 4 131).
+constexpr int kUnitCost = 6;
 __device__ __forceinline__ int cost_of(const Unit& u) {
-  return u.i1 > u.i0 ? u.count + kUnitCost<ROWS> : 1;
+  return u.i1 > u.i0 ? u.count + kUnitCost : 1;
 }
 // That of all row blocks of a key head of sequence b.
 template <int ROWS>
@@ -155,7 +155,7 @@ __device__ __forceinline__ int head_cost(const Args& a, int b) {
   const Draft dr = draft(a, b);
   int n = 0;
 #pragma unroll 1
-  for (int rb = 0; rb < a.blocks; ++rb) n += cost_of<ROWS>(unit_of<ROWS>(a, dr, rb));
+  for (int rb = 0; rb < a.blocks; ++rb) n += cost_of(unit_of<ROWS>(a, dr, rb));
   return n;
 }
 // Where CTA c's run starts: a cost of `total` (within 31 bits) over `ctas` CTAs.
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (left > 0) {
       const Draft dr = draft(a, b);
       const Unit u = unit_of<kRows>(a, dr, rb);
-      const int cost = cost_of<kRows>(u), before = cost - u.count;
+      const int cost = cost_of(u), before = cost - u.count;
       if (!found && pos >= cost && rb + 1 < a.blocks) {
         pos -= cost;
         ++rb;
