@@ -149,19 +149,20 @@ constexpr int kUnitCost = 6;
 __device__ __forceinline__ int cost_of(const Unit& u) {
   return u.i1 > u.i0 ? u.count + kUnitCost : 1;
 }
-// That of all row blocks of a key head of sequence b.
+// That of all row blocks of a key head.
 template <int ROWS>
-__device__ __forceinline__ int head_cost(const Args& a, int b) {
-  const Draft dr = draft(a, b);
+__device__ __forceinline__ int head_cost(const Args& a, Draft dr) {
   int n = 0;
 #pragma unroll 1
   for (int rb = 0; rb < a.blocks; ++rb) n += cost_of(unit_of<ROWS>(a, dr, rb));
   return n;
 }
-// Where CTA c's run starts: a cost of `total` (within 31 bits) over `ctas` CTAs.
-__device__ __forceinline__ int first_place(int total, int c, int ctas) {
-  return total / ctas * c + total % ctas * c / ctas;
-}
+// Equal runs of a cost of `total` (within 31 bits) for `ctas` CTAs.
+struct Runs {
+  int each, more;   // the first `more` of them are longer by one
+  __device__ __forceinline__ Runs(int total, int ctas) : each(total / ctas), more(total - each * ctas) {}
+  __device__ __forceinline__ int start(int c) const { return each * c + min(c, more); }
+};
 
 // A part of a run: consecutive tiles of one unit.
 struct Segment {
@@ -545,19 +546,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
     // Where this CTA's run starts: the cost of the sequences summed up to it. The first 32
     // sequences' stays in registers.
-    const int mine = lane < a.B ? head_cost<kRows>(a, lane) : 0;
+    const Draft dr0 = lane < a.B ? draft(a, lane) : Draft{0, -1};
+    const int mine = lane < a.B ? head_cost<kRows>(a, dr0) : 0;
     int total = mine;
 #pragma unroll 1
-    for (int b = 32 + lane; b < a.B; b += 32) total += head_cost<kRows>(a, b);
+    for (int b = 32 + lane; b < a.B; b += 32) total += head_cost<kRows>(a, draft(a, b));
     total = __reduce_add_sync(0xffffffffu, total) * a.Hkv;
     const int ctas = min(total, static_cast<int>(gridDim.x));   // each gets at least one
-    const int start = first_place(total, cta, ctas);
-    int left = cta < ctas ? first_place(total, cta + 1, ctas) - start : 0;
+    const Runs runs(total, ctas);
+    const int start = runs.start(cta);
+    int left = cta < ctas ? runs.start(cta + 1) - start : 0;
     limit += static_cast<uint64_t>(left) * 20000;
     int b = 0, at = 0, per_head = 1;
 #pragma unroll 1
     for (int b0 = 0, before = 0; b0 < a.B; b0 += 32) {
-      const int head = b0 == 0 ? mine : b0 + lane < a.B ? head_cost<kRows>(a, b0 + lane) : 0;
+      const int head = b0 == 0 ? mine : b0 + lane < a.B ? head_cost<kRows>(a, draft(a, b0 + lane)) : 0;
       int inc = head * a.Hkv;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -579,7 +582,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool found = false, first = true;
 #pragma unroll 1
     while (left > 0) {
-      const Draft dr = draft(a, b);
+      Draft dr;   // (every lane is here)
+      if (b < 32) {
+        dr.base = __shfl_sync(0xffffffffu, dr0.base, b);
+        dr.count = __shfl_sync(0xffffffffu, dr0.count, b);
+      } else {
+        dr = draft(a, b);
+      }
       const Unit u = unit_of<kRows>(a, dr, rb);
       const int cost = cost_of(u), before = cost - u.count;
       if (!found && pos >= cost && rb + 1 < a.blocks) {
@@ -609,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (count < u.count) {
             last = static_cast<int>(static_cast<float>(end) / static_cast<float>(total) * ctas);
             last = min(max(last, cta), ctas - 1);
-            while (first_place(total, last, ctas) >= end) --last;
-            while (last + 1 < ctas && first_place(total, last + 1, ctas) < end) ++last;
+            while (runs.start(last) >= end) --last;
+            while (last + 1 < ctas && runs.start(last + 1) < end) ++last;
           }
           a.units[(static_cast<int64_t>(b) * a.Hkv + hk) * a.blocks + rb] =
               make_int2(slot, count == u.count ? 0 : last - cta + 1);
