@@ -32,10 +32,11 @@
 // there, too, one stream's softmax runs beside the other's products.
 //
 // Measured on the device (replays): B=8 Hkv=8 of 4 query heads d=128 bf16, 64 drafted tokens (256
-// rows) over up to 32K: 143 us, 1205 TFLOP/s, 4.8 TB/s; B=16, 16 drafted tokens (64 rows) over up to
-// 16K, pages of 16: 118 us, 5.5 TB/s (81 % of the measured copy rate); B=4 Hkv=4 of 8, up to 5 tokens
-// over up to 64K: 68 us, 4.3 TB/s. Of these 8 us are a CTA's start (lengths, table, first tile: three
-// dependent reads, and cold instructions), 5 the join. In the steady state a tile takes 1800 to 2600
+// rows) over up to 32K: 140 us, 1230 TFLOP/s, 4.9 TB/s; B=16, 16 drafted tokens (64 rows) over up to
+// 16K, pages of 16: 115 us, 5.6 TB/s (83 % of the measured copy rate); B=4 Hkv=4 of 8, up to 5 tokens
+// over up to 64K: 67 us, 4.4 TB/s. With one row tile HBM is busy at 97 % of the copy rate from the
+// first load to the last; before it are 3 us (lengths, table: dependent reads, and cold instructions),
+// behind it 4 for the last part and 4 for the join. In the steady state a tile takes 1800 to 2600
 // cycles (one row tile; HBM) or 3200 (two; 2180 of them the tensor pipe's), and the step from one
 // unit to the next some 6000 or 14000 that nothing overlaps.
 //
@@ -44,8 +45,10 @@
 // worked out by every role for itself and S kept in registers between its maximum and P, 135 when
 // 129; products issued behind a branch on one lane, where operands move to uniform registers one
 // by one (85 cycles an instruction instead of 30), 180 us for the B=8 case when 150; equal runs
-// without the units' cost, 74 us for the B=4 case when 69; a third stage of K or of V for two row
-// tiles in the place that O passes through on its way out, 146 us for the B=8 case instead of 143.
+// without the units' cost, 74 us for the B=4 case when 69; parts as rows of D columns, where 32
+// threads with a row each write 16 bytes to 32 lines, 117.0 us instead of 115.4, B=8 142.1 instead of
+// 139.8; a third stage of K or of V for two row tiles in the place that O passes through on its way
+// out, 146 us for the B=8 case when 143.
 //
 // Masks. Tiles of the context that no window cuts need none. In the others a thread builds the 64
 // bits of its keys: a range of the context, and the ancestors by walking up the tree. Keys that some
@@ -100,7 +103,9 @@ struct Args {
   const void* v_pages;
   void* o;
   float* lse;
-  float* part_o;      // [2 * CTAs][part_rows][D]: CTA c's first run at slot 2c, its last at 2c + 1
+  float* part_o;      // [2 * CTAs][D / 4][part_rows][4]: CTA c's first run at slot 2c, its last at
+                      // 2c + 1; four columns of all rows together, as 32 threads with a row each
+                      // write them
   float2* part_ml;    // [2 * CTAs][part_rows]: offset (log2 units) and sum of the part
   int2* units;        // [B * Hkv * blocks]: slot of the unit's first part, number of parts (0: the
                       // unit was one run's, and is written)
@@ -218,10 +223,10 @@ struct Smem {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + QT * kTileBytes;
   static constexpr uint32_t kV = kK + kStages * kTileBytes;
-  // two row tiles: for each softmax warp 32 rows of kChunk columns of O (fp32) on their way out
+  // two row tiles: for each softmax warp 32 rows of kChunk columns of O on their way out
   static constexpr int kChunk = 16;
   static constexpr uint32_t kOut = kV + kStages * kTileBytes;
-  static constexpr uint32_t kMisc = kOut + (QT == 2 ? kSoftmaxThreads * kChunk * 4 : 0);
+  static constexpr uint32_t kMisc = kOut + (QT == 2 ? kSoftmaxThreads * kChunk * 2 : 0);
   static constexpr uint32_t kDynamic = kMisc + sizeof(Misc);
 };
 static_assert(Smem<128, 1>::kDynamic <= 232448 && Smem<128, 2>::kDynamic <= 232448 &&
@@ -361,11 +366,11 @@ __device__ __noinline__ bool clean_values(uint8_t* tile, uint4 loaded, int t) {
 }
 
 // The rare end of a segment in whose masked tiles V was not finite: those values, which the
-// products have taken as 0, added to the row of token i (fp32 part or output, columns
-// [c0, c0 + cols)) for the keys that it sees.
+// products have taken as 0, added to the row of token i (its part, `step` floats from four columns
+// to the next four, or its output; columns [c0, c0 + cols)) for the keys that it sees.
 template <bool FP16>
 __device__ __noinline__ void add_not_finite(const Args& a, const Segment& sg, int i, int d, int c0,
-                                            int cols, float* part, uint16_t* out) {
+                                            int cols, float* part, int step, uint16_t* out) {
   const int* const tab = a.table + static_cast<int64_t>(sg.b) * a.max_pages;
   for (int j = 0; j < sg.count; ++j) {
     const int k0 = sg.first_key + j * kTile;
@@ -393,8 +398,9 @@ __device__ __noinline__ void add_not_finite(const Args& a, const Segment& sg, in
         const float2 f = unpack2<FP16>(w);
         const float fx = isfinite(f.x) ? 0.f : f.x, fy = isfinite(f.y) ? 0.f : f.y;
         if (part) {
-          part[c0 + c] += fx;
-          part[c0 + c + 1] += fy;
+          float* const to = part + (c0 + c) / 4 * step + (c0 + c) % 4;
+          to[0] += fx;
+          to[1] += fy;
         } else {
           uint32_t* const to = reinterpret_cast<uint32_t*>(out + c0 + c);
           const float2 o = unpack2<FP16>(*to);
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     atomicOr(&g_error, kTimeoutBit);
   };
   // SHORT: this CTA's part, where K and V were
-  float* const short_part = reinterpret_cast<float*>(smem_raw + L::kK);                 // [128][D]
+  float* const short_part = reinterpret_cast<float*>(smem_raw + L::kK);                 // [D / 4][128][4]
   float2* const short_ml = reinterpret_cast<float2*>(smem_raw + L::kK + kTile * D * 4);   // [128]
   static_assert(!SHORT || L::kK + kTile * (D * 4 + 8) <= L::kMisc, "the part's place");
   // Segment s of the run for the warps that read them; false when a wait has run out.
@@ -1112,23 +1118,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = whole ? inverse(l) : 1.f;
         fa *= f;
         fb *= f;
-        const int64_t part = static_cast<int64_t>(sn.slot) * a.part_rows + my;
         uint16_t* const o_row = static_cast<uint16_t*>(a.o) +
                                 ((static_cast<int64_t>(sn.b) * a.T + token) * a.Hq + head) * D;
-        // Where this thread's row goes. Two row tiles: a row's 16-byte pieces are written by
-        // consecutive lanes, by way of shared memory (from its own thread each store touches 32
-        // lines: 11000 cycles for 256 rows, not 6000).
-        float* const part_row = SHORT ? short_part + my * D : a.part_o + part * D;
-        char* const own = reinterpret_cast<char*>(whole ? static_cast<void*>(o_row) : part_row);
-        const int wide = whole ? 2 : 4;                // bytes of a value
+        // Where this thread's row of a part goes, and from four columns to the next four.
+        float* const part_row =
+            SHORT ? short_part + my * 4
+                  : a.part_o + (static_cast<int64_t>(sn.slot) * (D / 4) * a.part_rows + my) * 4;
+        const int step = (SHORT ? kTile : a.part_rows) * 4;
         const int live_rows = sn.live - (my - lane);   // of this warp's 32
         constexpr int kCols = QT == 2 ? D / 2 : D / 4, kChunk = L::kChunk;
         const int c0 = (QT == 2 ? half : 2 * x + half) * kCols;   // this thread's columns
-        const int shift = whole ? 1 : 2;               // 2^shift pieces of a row's chunk
-        uint8_t* const stage = smem_raw + L::kOut + (warp - 4) * (32 * kChunk * 4);
+        // The output of two row tiles: a row's 16-byte pieces are written by consecutive lanes, by
+        // way of shared memory (from its own thread each store touches 32 lines: 11000 cycles for
+        // 256 rows, not 6000).
+        constexpr int kPieces = kChunk / 8;            // of a row's chunk
+        uint8_t* const stage = smem_raw + L::kOut + (warp - 4) * (32 * kChunk * 2);
         auto piece = [&](int r, int c) {   // (those of eight rows in different banks)
-          return reinterpret_cast<uint4*>(
-              stage + (((r << shift) + (c ^ ((r >> 1) & ((1 << shift) - 1)))) << 4));
+          return reinterpret_cast<uint4*>(stage + ((r * kPieces + (c ^ ((r >> 2) & 1))) << 4));
         };
 #pragma unroll 1
         for (int col = c0; col < c0 + kCols; col += kChunk) {
@@ -1145,45 +1151,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[t] = __uint_as_float(oa[t]) * fa;
             if (two) v[t] += __uint_as_float(ob[t]) * fb;
           }
-          auto put = [&](int t, uint4 w) {
+          if (!whole) {
+            if (mine) {
+#pragma unroll
+              for (int t = 0; t < kChunk / 4; ++t)
+                *reinterpret_cast<float4*>(part_row + (col / 4 + t) * step) =
+                    make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+            }
+            continue;
+          }
+#pragma unroll
+          for (int t = 0; t < kPieces; ++t) {
+            const uint4 w = make_uint4(
+                pack2<FP16>(v[8 * t], v[8 * t + 1]), pack2<FP16>(v[8 * t + 2], v[8 * t + 3]),
+                pack2<FP16>(v[8 * t + 4], v[8 * t + 5]), pack2<FP16>(v[8 * t + 6], v[8 * t + 7]));
             if constexpr (QT == 2)
               *piece(lane, t) = w;
             else if (mine)
-              *reinterpret_cast<uint4*>(own + col * wide + t * 16) = w;
-          };
-          if (whole) {
-#pragma unroll
-            for (int t = 0; t < kChunk / 8; ++t)
-              put(t, make_uint4(pack2<FP16>(v[8 * t], v[8 * t + 1]),
-                                pack2<FP16>(v[8 * t + 2], v[8 * t + 3]),
-                                pack2<FP16>(v[8 * t + 4], v[8 * t + 5]),
-                                pack2<FP16>(v[8 * t + 6], v[8 * t + 7])));
-          } else {
-#pragma unroll
-            for (int t = 0; t < kChunk / 4; ++t)
-              put(t, make_uint4(__float_as_uint(v[4 * t]), __float_as_uint(v[4 * t + 1]),
-                                __float_as_uint(v[4 * t + 2]), __float_as_uint(v[4 * t + 3])));
+              *reinterpret_cast<uint4*>(o_row + col + t * 8) = w;
           }
           if constexpr (QT == 2) {
             __syncwarp();
-#pragma unroll 1
-            for (int i = lane; i < 32 << shift; i += 32) {
-              const int r = i >> shift, c = i & ((1 << shift) - 1);
-              char* const to = reinterpret_cast<char*>(__shfl_sync(
-                  0xffffffffu, reinterpret_cast<unsigned long long>(own), r));
-              if (r < live_rows) *reinterpret_cast<uint4*>(to + col * wide + c * 16) = *piece(r, c);
+#pragma unroll
+            for (int i = lane; i < 32 * kPieces; i += 32) {
+              const int r = i / kPieces, c = i % kPieces;
+              uint16_t* const to = reinterpret_cast<uint16_t*>(__shfl_sync(
+                  0xffffffffu, reinterpret_cast<unsigned long long>(o_row), r));
+              if (r < live_rows) *reinterpret_cast<uint4*>(to + col + c * 8) = *piece(r, c);
             }
           }
         }
         __syncwarp();
         if (ms.not_finite[segs & 1] == segs + 1 && mine)
-          add_not_finite<FP16>(a, sn, token, D, c0, kCols, whole ? nullptr : part_row,
+          add_not_finite<FP16>(a, sn, token, D, c0, kCols, whole ? nullptr : part_row, step,
                                whole ? o_row : nullptr);
         if (mine && c0 == 0) {
           if (whole)
             a.lse[(static_cast<int64_t>(sn.b) * a.Hq + head) * a.T + token] = lse_of(m, l);
           else
-            (SHORT ? short_ml + my : a.part_ml + part)[0] = make_float2(m, l);
+            (SHORT ? short_ml + my
+                   : a.part_ml + static_cast<int64_t>(sn.slot) * a.part_rows + my)[0] =
+                make_float2(m, l);
         }
       }
       n0 += ms.seg[segs % kSegments].count;
@@ -1210,8 +1218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // drafted tokens has nothing but padding, which no segment wrote)
     const int rows = live > 0 ? live : a.T * a.G;
 #pragma unroll 1
-    for (int at = rank * kThreads + threadIdx.x; at < rows * (D / 4); at += ranks * kThreads) {
-      const int r = at / (D / 4), c = at % (D / 4);
+    for (int at = rank * kThreads + threadIdx.x; at < (rows + 7) / 8 * 8 * (D / 4);
+         at += ranks * kThreads) {
+      // (a part's rows are next to one another, an output's columns)
+      const int r = at / (8 * (D / 4)) * 8 + at % 8, c = at / 8 % (D / 4);
+      if (r >= rows) continue;
       float m = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -1219,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 ml = *cluster.map_shared_rank(short_ml + r, x);
         if (ml.x == -INFINITY) continue;   // saw nothing, and may hold anything
         const float4 v =
-            *reinterpret_cast<const float4*>(cluster.map_shared_rank(short_part + r * D + 4 * c, x));
+            *reinterpret_cast<const float4*>(cluster.map_shared_rank(short_part + (c * kTile + r) * 4, x));
         const float top = fmaxf(m, ml.x);
         const float f = ptx::exp2_approx(m - top), g = ptx::exp2_approx(ml.x - top);
         m = top;
@@ -1249,60 +1260,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The parts of a unit that more than one run covers, joined: a warp for each row, D / 32 columns
-// a lane. The part in the first run's slot is followed by those of the next CTAs, each in its
-// CTA's first slot.
+// The parts of a unit that more than one run covers, joined: a thread for four columns of a row, a
+// block for 1024 / D consecutive rows of a key head. The part in the first run's slot is followed by
+// those of the next CTAs, each in its CTA's first slot.
 constexpr int kJoinThreads = 256;
+template <int D>
+constexpr int kJoinRows = kJoinThreads / (D / 4);
 
 template <int D, bool FP16, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads)
-    fa_paged_tree_join_kernel(const __grid_constant__ Args a) {
-  constexpr int E = D / 32;
-  using Vec = typename std::conditional<E == 4, float4, float2>::type;
+    fa_paged_tree_join_kernel(const __grid_constant__ Args a, int blocks_per_head) {
   wait_prerequisites();
   launch_dependents();
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
-  if (id >= static_cast<int64_t>(a.B) * a.T * a.Hq) return;
-  const int lane = threadIdx.x % 32;
-  const int h = static_cast<int>(id % a.Hq), i = static_cast<int>(id / a.Hq % a.T);
-  const int b = static_cast<int>(id / a.Hq / a.T);
-  const int r = i * a.G + h % a.G, my = r % ROWS;
-  const int2 u =
-      a.units[(static_cast<int64_t>(b) * a.Hkv + h / a.G) * a.blocks + r / ROWS];
+  const int head = blockIdx.x / blocks_per_head;   // sequence and key head
+  const int r = blockIdx.x % blocks_per_head * kJoinRows<D> + threadIdx.x % kJoinRows<D>;
+  if (r >= a.T * a.G) return;
+  const int b = head / a.Hkv, hk = head % a.Hkv, col = threadIdx.x / kJoinRows<D>, my = r % ROWS;
+  const int i = token_of(a, r), h = hk * a.G + r - i * a.G;
+  const int2 u = a.units[static_cast<int64_t>(head) * a.blocks + r / ROWS];
   const int drafted = draft(a, b).count;
+  uint2* const dst = reinterpret_cast<uint2*>(
+      static_cast<uint16_t*>(a.o) + ((static_cast<int64_t>(b) * a.T + i) * a.Hq + h) * D + 4 * col);
+  float* const lse = a.lse + (static_cast<int64_t>(b) * a.Hq + h) * a.T + i;
   if (i >= drafted) {
     // padding: of a unit without any token nobody else writes it
     if (token_of(a, r - my) >= drafted) {
-      for (int e = 0; e < E; e += 2)
-        reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + id * D + lane * E)[e / 2] = 0;
-      if (lane == 0) a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.T + i] = -INFINITY;
+      *dst = make_uint2(0, 0);
+      if (col == 0) *lse = -INFINITY;
     }
     return;
   }
   if (u.y == 0) return;   // one run's, and written
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
 #pragma unroll 4
   for (int p = 0; p < u.y; ++p) {
     const int64_t slot = p == 0 ? u.x : 2 * (u.x / 2 + p);
-    const int64_t at = slot * a.part_rows + my;
-    const float2 ml = a.part_ml[at];
-    const Vec v = *reinterpret_cast<const Vec*>(a.part_o + at * D + lane * E);
-    const float* const f = reinterpret_cast<const float*>(&v);
+    const float2 ml = a.part_ml[slot * a.part_rows + my];
+    const float4 f = *reinterpret_cast<const float4*>(
+        a.part_o + ((slot * (D / 4) + col) * a.part_rows + my) * 4);
     const float n = fmaxf(m, ml.x), top = n == -INFINITY ? 0.f : n;
     const float old = ptx::exp2_approx(m - top), now = ptx::exp2_approx(ml.x - top);
     m = n;
     l = l * old + ml.y * now;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * old + f[e] * now;
+    acc.x = acc.x * old + f.x * now;
+    acc.y = acc.y * old + f.y * now;
+    acc.z = acc.z * old + f.z * now;
+    acc.w = acc.w * old + f.w * now;
   }
   const float inv = inverse(l);
-  uint32_t* const dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + id * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.T + i] = lse_of(m, l);
+  *dst = make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
+  if (col == 0) *lse = lse_of(m, l);
 }
 
 // Row tiles of a unit, and with it its rows: two where a key head has more than 128 rows.
@@ -1399,10 +1407,10 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   err = launch_paged(kernel, l.ctas, kThreads, smem, stream, 0, tm_k, tm_v, a);
   if (err != cudaSuccess || !l.join) return err;
-  const int64_t rows = static_cast<int64_t>(c.B) * p.T * p.Hq;
+  const int per_head = (p.T * a.G + kJoinRows<D> - 1) / kJoinRows<D>;
   return launch_paged(fa_paged_tree_join_kernel<D, FP16, QT * kTile>,
-                      (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), kJoinThreads, 0, stream, 0,
-                      a);
+                      static_cast<int64_t>(c.B) * c.Hkv * per_head, kJoinThreads, 0, stream, 0, a,
+                      per_head);
 }
 
 template <int D, bool FP16>
