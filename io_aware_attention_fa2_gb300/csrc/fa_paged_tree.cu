@@ -34,7 +34,7 @@
 // Measured on the device (replays): B=8 Hkv=8 of 4 query heads d=128 bf16, 64 drafted tokens (256
 // rows) over up to 32K: 140 us, 1230 TFLOP/s, 4.9 TB/s; B=16, 16 drafted tokens (64 rows) over up to
 // 16K, pages of 16: 115 us, 5.6 TB/s (83 % of the measured copy rate); B=4 Hkv=4 of 8, up to 5 tokens
-// over up to 64K: 67 us, 4.4 TB/s. With one row tile HBM is busy at 97 % of the copy rate from the
+// over up to 64K: 65 us, 4.5 TB/s. With one row tile HBM is busy at 97 % of the copy rate from the
 // first load to the last; before it are 3 us (lengths, table: dependent reads, and cold instructions),
 // behind it 4 for the last part and 4 for the join. In the steady state a tile takes 1800 to 2600
 // cycles (one row tile; HBM) or 3200 (two; 2180 of them the tensor pipe's), and the step from one
@@ -113,6 +113,7 @@ struct Args {
   uint32_t g_magic;               // ceil(2^32 / G), or 0: see token_of
   int part_rows;                  // rows of a unit, at most
   int page_shift, num_pages, max_pages, box_rows, window_left;
+  int unit_cost;                  // of a unit's start and end, in tiles
   float scale_log2;
 };
 
@@ -147,19 +148,16 @@ __device__ __forceinline__ Unit unit_of(const Args& a, Draft dr, int rb) {
 __device__ __forceinline__ Draft draft(const Args& a, int b) {
   return draft_of(a.seqlens, a.new_lens, b, a.T, a.max_pages << a.page_shift);
 }
-// What a unit costs in a run, in tiles: its tiles and, for its start and end, kUnitCost (of 3 to 16
-// the best or within 2 % of it for 8 to 256 units, 64 of them by 118 us and 138; 512 units of up to
-// 4096 tokens take 133 us, with 4 131).
-constexpr int kUnitCost = 6;
-__device__ __forceinline__ int cost_of(const Unit& u) {
-  return u.i1 > u.i0 ? u.count + kUnitCost : 1;
+// What a unit costs in a run, in tiles: its tiles and, for its start and end, unit_cost.
+__device__ __forceinline__ int cost_of(const Args& a, const Unit& u) {
+  return u.i1 > u.i0 ? u.count + a.unit_cost : 1;
 }
 // That of all row blocks of a key head.
 template <int ROWS>
 __device__ __forceinline__ int head_cost(const Args& a, Draft dr) {
   int n = 0;
 #pragma unroll 1
-  for (int rb = 0; rb < a.blocks; ++rb) n += cost_of(unit_of<ROWS>(a, dr, rb));
+  for (int rb = 0; rb < a.blocks; ++rb) n += cost_of(a, unit_of<ROWS>(a, dr, rb));
   return n;
 }
 // Equal runs of a cost of `total` (within 31 bits) for `ctas` CTAs.
@@ -596,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         dr = draft(a, b);
       }
       const Unit u = unit_of<kRows>(a, dr, rb);
-      const int cost = cost_of(u), before = cost - u.count;
+      const int cost = cost_of(a, u), before = cost - u.count;
       if (!found && pos >= cost && rb + 1 < a.blocks) {
         pos -= cost;
         ++rb;
@@ -1333,6 +1331,13 @@ int choose_short(int B, int T, int Hq, int Hkv, int64_t tiles) {
   return units <= 2 * resident_clusters(1) && tiles <= kShortTiles ? 1 : 0;
 }
 
+// What a unit's start and end cost in a run, in tiles: of 3 to 16 the best, or within 1 % of it, for 32
+// to 256 units is 6 (64 units of up to 32K tokens 117.6 us and, with two row tiles, 138.4; with 8 118.8
+// and 138.8). Where few CTAs have such a step, the bandwidth that it leaves goes to the others and is
+// missing at the end: 16 units of up to 64K tokens 67.4 us, with 8 65.0; 8 units 60.7 and 60.3. (512
+// units of up to 4096 tokens 133 us, with 4 130.5.)
+int unit_cost(int64_t units) { return units <= 16 ? 8 : 6; }
+
 // Workspace: the parts' O, their offsets and sums, the units' parts; nothing where a unit is one
 // tile, and never split.
 struct Layout {
@@ -1385,6 +1390,7 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t stream) {
   a.max_pages = c.max_pages;
   a.box_rows = std::min(c.page_size, kTile);
   a.window_left = p.window_left;
+  a.unit_cost = unit_cost(static_cast<int64_t>(c.B) * c.Hkv * l.blocks);
   a.scale_log2 = p.scale_log2;
   CUtensorMap tm_k, tm_v;
   if (!encode_pages(&tm_k, c.k_pages, c, a.box_rows, 1, FP16) ||
