@@ -290,6 +290,33 @@ def test_large_tables(B, width, page, spare):
     assert len(pool.free) == len(pool.refs) and fa.device_error() == 0
 
 
+@pytest.mark.parametrize("B,width,page", [(40, 5000, 16), (300, 500, 16)])
+def test_few_pages_of_large_tables(B, width, page):
+    """Steps of a few tokens, both ways, over tables that are large and mostly empty; children that
+    give up the same few pages in one call."""
+    import io_aware_attention_fa2_gb300 as fa
+    r = random.Random(B)
+    pool = shuffled_pool(r, 8 * B)
+    table = [[-1] * width for _ in range(B)]
+    dev, dev_table = books(pool), int32(table)
+    lens = [0] * B
+    for step in range(6):
+        later = [max(0, n + r.randint(-20, 40)) for n in lens]
+        got = fa.paged_resize(dev, dev_table, int32(lens), int32(later), page)
+        lens = pool.resize(table, lens, later, page)
+        assert got.tolist() == lens and dev_table.tolist() == table, step
+        check_books(dev, pool, step)
+    source = [r.randrange(B // 4) for _ in range(B)]
+    got = fa.paged_fork(dev, dev_table, int32(lens), int32(source), page)
+    new, new_lens = pool.fork(table, lens, source, page)[:2]
+    for dev_t, t, n in ((dev_table, table, lens), (got.block_table, new, new_lens)):
+        fa.paged_resize(dev, dev_t, int32(n), int32([0] * B), page)
+        pool.resize(t, n, [0] * B, page)
+        assert dev_t.tolist() == t
+        check_books(dev, pool, "end")
+    assert len(pool.free) == 8 * B and fa.device_error() == 0
+
+
 def test_large_tables_on_two_streams():
     """Two captured graphs, each with a pool of its own, replayed beside one another, and eager calls
     on a third pool meanwhile: the books of each as when it runs alone."""
