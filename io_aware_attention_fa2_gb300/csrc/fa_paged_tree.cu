@@ -945,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    bool go = next_segment(0), had = false;
+    bool go = next_segment(0);
     if (go) load_q(0);
 #pragma unroll 1
     for (int segs = 0; go; ++segs) {
@@ -1197,10 +1197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) segment_read(segs);
       ptx::tc_fence_before_sync();
       ptx::mbar_arrive(bar(BAR_O_FREE));
-      if constexpr (SHORT) had = true;
     }
-    // a share without tiles (nothing was loaded to where this goes)
-    if (SHORT && !had && tid < kTile) short_ml[tid] = make_float2(-INFINITY, 0.f);
   }
 
   if constexpr (SHORT) {
@@ -1208,10 +1205,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
     const int ranks = static_cast<int>(cluster.num_blocks());
+    const int b = cta / ranks / a.Hkv, hk = cta / ranks % a.Hkv;
+    const Draft dr = draft(a, b);
+    const int live = dr.count * a.G, tiles = unit_of<kRows>(a, dr, 0).count;
+    // The CTAs with tiles, as bits. Each of them counts, one whose scores are all NaN (its maximum is
+    // -inf, its sum is not 0) and one with infinite values as well; the others wrote nothing.
+    unsigned parts = 0;
+    if (live > 0)
+      for (int x = 0; x < ranks; ++x)
+        if (tiles * x / ranks < tiles * (x + 1) / ranks) parts |= 1u << x;
     __syncwarp();
     cluster.sync();   // every CTA's part is in its shared memory
-    const int b = cta / ranks / a.Hkv, hk = cta / ranks % a.Hkv;
-    const int live = draft(a, b).count * a.G;
     // four columns of a row a thread, the rows shared out over the cluster (a sequence without
     // drafted tokens has nothing but padding, which no segment wrote)
     const int rows = live > 0 ? live : a.T * a.G;
@@ -1224,14 +1228,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int x = 0; x < (live > 0 ? ranks : 0); ++x) {
+      for (int x = 0; x < ranks; ++x) {
+        if (!(parts >> x & 1)) continue;
         const float2 ml = *cluster.map_shared_rank(short_ml + r, x);
-        if (ml.x == -INFINITY) continue;   // saw nothing, and may hold anything
         const float4 v =
             *reinterpret_cast<const float4*>(cluster.map_shared_rank(short_part + (c * kTile + r) * 4, x));
-        const float top = fmaxf(m, ml.x);
+        const float most = fmaxf(m, ml.x), top = most == -INFINITY ? 0.f : most;
         const float f = ptx::exp2_approx(m - top), g = ptx::exp2_approx(ml.x - top);
-        m = top;
+        m = most;
         l = l * f + ml.y * g;
         acc.x = acc.x * f + v.x * g;
         acc.y = acc.y * f + v.y * g;
