@@ -87,8 +87,11 @@ constexpr int kMaxStages = 6;
 // softmax of the tile kMaxStages + 2 before it is over by then.
 constexpr int kInfoSlots = kMaxStages + 2;
 
-// The offset of a row's exponents is its maximum less kShift, and moves when the maximum has
-// grown by more than kLag (log2 units).
+// P = 2^((s - m) scale + kShift): m is the row's maximum of the products s as they are, and moves
+// when that has grown by more than kLag (log2 units). The difference comes first, and is 0 for the
+// maximum itself: scaled, a large maximum would be rounded by more than the type holds beside the
+// shift (from 2^24 on by 1 and more). The packed addition that this takes costs nothing measurable
+// (B=8 140.1 and 140.3 us).
 template <bool FP16>
 constexpr float kShift = FP16 ? 11.f : 0.f;
 template <bool FP16>
@@ -106,7 +109,7 @@ struct Args {
   float* part_o;      // [2 * CTAs][D / 4][part_rows][4]: CTA c's first run at slot 2c, its last at
                       // 2c + 1; four columns of all rows together, as 32 threads with a row each
                       // write them
-  float2* part_ml;    // [2 * CTAs][part_rows]: offset (log2 units) and sum of the part
+  float2* part_ml;    // [2 * CTAs][part_rows]: offset (a product, not scaled) and sum of the part
   int2* units;        // [B * Hkv * blocks]: slot of the unit's first part, number of parts (0: the
                       // unit was one run's, and is written)
   int B, T, Hq, Hkv, G, blocks;   // blocks of rows for each key head
@@ -122,6 +125,17 @@ struct Args {
 __device__ __forceinline__ int token_of(const Args& a, int r) {
   if (a.g_magic) return static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.g_magic));
   return a.G == 1 ? r : r / a.G;
+}
+
+// Factor of a difference of products in an exponent (log2 units). Q takes the scale's sign, and a
+// scale of 0, so that it is positive.
+__device__ __forceinline__ float factor_of(const Args& a) {
+  return a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+}
+// LSE in natural units of a row from its offset and its sum.
+template <bool FP16>
+__device__ __forceinline__ float lse_at(float m, float l, float scale) {
+  return l == 0.f ? -INFINITY : fmaf(m, scale, log2f(l) - kShift<FP16>) * kLn2;
 }
 
 // A block of rows: tokens [i0, i1) (i1 <= i0: only rows of the padding) and tiles
@@ -872,8 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + x * kTile + half * 64;   // this thread's keys of S, then P
     const uint32_t tO = tmem + lane_off + kTmemO;  // O_A; O_B is D columns on
-    // Q takes the scale's sign, and a scale of 0: the exponents' factor is positive
-    const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+    const float scale = factor_of(a);
     int n0 = 0;               // tiles so far
     int done = 0, ends = 0;   // this stream's tiles and segments with tiles
     bool ok = true;
@@ -953,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool active = (QT == 2 ? x * kTile : 0) + quarter * 32 < live;   // rows of this warp
       const int j_first = QT == 2 ? 0 : x, j_step = QT == 2 ? 1 : 2;
       const int j_end = QT == 2 && x == 1 && live <= kTile ? 0 : count;
-      // offset of the exponents (log2 units), sum over this thread's keys
+      // offset of the exponents, sum over this thread's keys
       float m = -INFINITY, l = 0.f;
 
 #pragma unroll 1
@@ -1013,18 +1026,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           ms.red[x][half][row] = mt;
           ptx::named_barrier_sync(2 + x * 4 + quarter, 64);
           mt = fmaxf(mt, ms.red[x][half ^ 1][row]);
-          const float m_tile = mt * scale - kShift<FP16>;
           float alpha = 1.f;
-          const bool rescale = __any_sync(0xffffffffu, m_tile > m + kLag<FP16>);
+          const bool rescale = __any_sync(0xffffffffu, (mt - m) * scale > kLag<FP16>);
           if (rescale) {
             // every row of this warp to its running maximum; l now, O below
-            const float m_new = fmaxf(m, m_tile);
-            alpha = ptx::exp2_approx(m - (m_new == -INFINITY ? 0.f : m_new));
+            const float m_new = fmaxf(m, mt);
+            alpha = ptx::exp2_approx((m - (m_new == -INFINITY ? 0.f : m_new)) * scale);
             l *= alpha;
             m = m_new;
           }
           const float m_use = m == -INFINITY ? 0.f : m;
-          // P = 2^(scaled score - offset) over the S of these keys, two of them to a column
+          // P over the S of these keys, two of them to a column
           float rs0 = 0.f, rs1 = 0.f;
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -1041,8 +1053,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int t = 0; t < 16; ++t) {
               float e0, e1;
-              ptx::fma2(e0, e1, __uint_as_float(s[2 * t]), __uint_as_float(s[2 * t + 1]), scale,
-                        scale, -m_use, -m_use);
+              ptx::add2(e0, e1, __uint_as_float(s[2 * t]), __uint_as_float(s[2 * t + 1]), -m_use,
+                        -m_use);
+              ptx::fma2(e0, e1, e0, e1, scale, scale, kShift<FP16>, kShift<FP16>);
               const float p0 = ptx::exp2_approx(e0), p1 = ptx::exp2_approx(e1);
               ptx::add2(rs0, rs1, rs0, rs1, p0, p1);
               pr[t] = pack2<FP16>(p0, p1);
@@ -1101,8 +1114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_a = ms.red[0][0][row], m_b = ms.red[1][0][row];
           m = fmaxf(m_a, m_b);
           const float u = m == -INFINITY ? 0.f : m;
-          fa = ptx::exp2_approx(m_a - u);
-          fb = ptx::exp2_approx(m_b - u);
+          fa = ptx::exp2_approx((m_a - u) * scale);
+          fb = ptx::exp2_approx((m_b - u) * scale);
           l = ms.red[0][1][row] * fa + ms.red[1][1][row] * fb;
           ptx::named_barrier_sync(10 + quarter, 128);
         }
@@ -1185,7 +1198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                whole ? o_row : nullptr);
         if (mine && c0 == 0) {
           if (whole)
-            a.lse[(static_cast<int64_t>(sn.b) * a.Hq + head) * a.T + token] = lse_of(m, l);
+            a.lse[(static_cast<int64_t>(sn.b) * a.Hq + head) * a.T + token] =
+                lse_at<FP16>(m, l, scale);
           else
             (SHORT ? short_ml + my
                    : a.part_ml + static_cast<int64_t>(sn.slot) * a.part_rows + my)[0] =
@@ -1219,6 +1233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // four columns of a row a thread, the rows shared out over the cluster (a sequence without
     // drafted tokens has nothing but padding, which no segment wrote)
     const int rows = live > 0 ? live : a.T * a.G;
+    const float scale = factor_of(a);
 #pragma unroll 1
     for (int at = rank * kThreads + threadIdx.x; at < (rows + 7) / 8 * 8 * (D / 4);
          at += ranks * kThreads) {
@@ -1234,7 +1249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float4 v =
             *reinterpret_cast<const float4*>(cluster.map_shared_rank(short_part + (c * kTile + r) * 4, x));
         const float most = fmaxf(m, ml.x), top = most == -INFINITY ? 0.f : most;
-        const float f = ptx::exp2_approx(m - top), g = ptx::exp2_approx(ml.x - top);
+        const float f = ptx::exp2_approx((m - top) * scale);
+        const float g = ptx::exp2_approx((ml.x - top) * scale);
         m = most;
         l = l * f + ml.y * g;
         acc.x = acc.x * f + v.x * g;
@@ -1247,7 +1263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) +
                                 ((static_cast<int64_t>(b) * a.T + token) * a.Hq + head) * D + 4 * c) =
           make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
-      if (c == 0) a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = lse_of(m, l);
+      if (c == 0)
+        a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.T + token] = lse_at<FP16>(m, l, scale);
     }
     __syncwarp();
     cluster.sync();   // no CTA leaves while another reads its part
@@ -1295,6 +1312,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (u.y == 0) return;   // one run's, and written
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
+  const float scale = factor_of(a);
 #pragma unroll 4
   for (int p = 0; p < u.y; ++p) {
     const int64_t slot = p == 0 ? u.x : 2 * (u.x / 2 + p);
@@ -1302,7 +1320,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     const float4 f = *reinterpret_cast<const float4*>(
         a.part_o + ((slot * (D / 4) + col) * a.part_rows + my) * 4);
     const float n = fmaxf(m, ml.x), top = n == -INFINITY ? 0.f : n;
-    const float old = ptx::exp2_approx(m - top), now = ptx::exp2_approx(ml.x - top);
+    const float old = ptx::exp2_approx((m - top) * scale);
+    const float now = ptx::exp2_approx((ml.x - top) * scale);
     m = n;
     l = l * old + ml.y * now;
     acc.x = acc.x * old + f.x * now;
@@ -1312,7 +1331,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
   const float inv = inverse(l);
   *dst = make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
-  if (col == 0) *lse = lse_of(m, l);
+  if (col == 0) *lse = lse_at<FP16>(m, l, scale);
 }
 
 // Row tiles of a unit, and with it its rows: two where a key head has more than 128 rows.
