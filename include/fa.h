@@ -538,7 +538,8 @@ int fa_paged_copy(void* k_pages, void* v_pages, float* weights, const int* src, 
  *   copy_src, copy_dst, copy_rows  device int32 [C], written: fa_paged_copy's src, dst and rows;
  *                -1, -1 and 0 without a copy
  * Pages come from the pool in the order of c. A page outside the pool in the source's table is
- * passed on as -1 (FA_ERR_PAGE).
+ * passed on as -1 (FA_ERR_PAGE), and if it is the one that is filled in part, no page is taken for
+ * it and none copied; nor where the pool's entry is none of its pages (FA_ERR_PAGE).
  */
 int fa_paged_fork(const int* block_table, const int* seqlens, const int* source, int* refs,
                   int* free_pages, int* num_free, int* out_table, int* out_seqlens, int* copy_src,

@@ -251,24 +251,27 @@ __device__ __forceinline__ void fork_plan(const ForkParams& p, int* s_warp) {
       }
       if (len < 0) record_page_error();
     }
-    const int tail = len > 0 ? len & ((1 << p.page_shift) - 1) : 0;
+    int tail = len > 0 ? len & ((1 << p.page_shift) - 1) : 0, src = -1, dst = -1;
+    if (tail > 0) {
+      src = p.block_table[static_cast<int64_t>(from) * p.max_pages + (len >> p.page_shift)];
+      if (src < 0 || src >= p.pool.num_pages) {   // nothing to copy: its entry is -1, too
+        record_page_error();
+        tail = 0;
+      }
+    }
     int all;
     const int place = taken + block_scan<kForkThreads>(tail > 0, s_warp, &all);
     if (c < p.C) {
-      int src = -1, dst = -1, rows = 0;
       if (tail > 0) {
-        if (place < have) {
-          src = p.block_table[static_cast<int64_t>(from) * p.max_pages + (len >> p.page_shift)];
+        if (place < have)
           dst = take_page(p.pool, have - 1 - place);
-          rows = tail;
-        } else {
+        else
           len = -1;   // the pool is empty
-        }
       }
       p.out_seqlens[c] = len;
-      p.copy_src[c] = src;
+      p.copy_src[c] = dst < 0 ? -1 : src;
       p.copy_dst[c] = dst;
-      p.copy_rows[c] = rows;
+      p.copy_rows[c] = dst < 0 ? 0 : tail;
     }
     taken += all;
   }
