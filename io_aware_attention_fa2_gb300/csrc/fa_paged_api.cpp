@@ -72,6 +72,8 @@ bool decode_shape_ok(int B, int Hq, int Hkv, int page_size, int max_pages) {
 // tiles of 128 keys of all blocks of 128 rows (places in an order of them are ints).
 bool tree_shape_ok(int B, int T, int Hq, int Hkv, int page_size, int max_pages) {
   if (T < 1 || T > fa::kMaxDraft || Hq < Hkv || Hq % Hkv) return false;
+  // (heads first: each product below stays within 64 bits)
+  if ((uint64_t)B * (uint64_t)Hq >= (1ull << 31)) return false;
   const uint64_t rows = (uint64_t)B * (uint64_t)T * (uint64_t)Hq;
   const uint64_t blocks = ((uint64_t)T * (uint64_t)(Hq / Hkv) + 127) / 128;
   const uint64_t tiles = ((uint64_t)max_pages * page_size + 127) / 128 + 16;
