@@ -65,7 +65,8 @@ bool scale_ok(float scale) { return isfinite(scale) && isfinite(scale * kLog2e);
 bool decode_shape_ok(int B, int Hq, int Hkv, int page_size, int max_pages) {
   if (Hq < Hkv || Hq % Hkv) return false;
   const uint64_t tokens = (uint64_t)max_pages * page_size;
-  return (uint64_t)B * (uint64_t)Hq * (tokens / 1024 + 2) < (1ull << 31);
+  const uint64_t heads = (uint64_t)B * (uint64_t)Hq;
+  return heads < (1ull << 31) && heads * (tokens / 1024 + 2) < (1ull << 31);
 }
 
 // Drafted tokens: up to kMaxDraft of each sequence, rows (b, t, h) within 2^31 - 1, and as many
