@@ -492,10 +492,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* const short_part = reinterpret_cast<float*>(smem_raw + L::kK);                 // [D / 4][128][4]
   float2* const short_ml = reinterpret_cast<float2*>(smem_raw + L::kK + kTile * D * 4);   // [128]
   static_assert(!SHORT || L::kK + kTile * (D * 4 + 8) <= L::kMisc, "the part's place");
-  // Segment s of the run for the warps that read them; false when a wait has run out.
+  // Segment s of the run for the warps that read them; false when a wait has run out. What is in front
+  // of it may be all lengths of the batch, or units of nothing but padding: 41 ns a sequence.
+  const uint64_t segment_limit = kWaitLimitNs + static_cast<uint64_t>(a.B) * 200;
   auto segment = [&](int s) {
     return ptx::wait_bounded(bar(BAR_SEG_FULL + s % kSegments), (s / kSegments) & 1, abort_p,
-                             kWaitLimitNs);
+                             segment_limit);
   };
   auto segment_read = [&](int s) { ptx::mbar_arrive(bar(BAR_SEG_EMPTY + s % kSegments)); };
 
@@ -892,8 +894,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // after a wait has run out the loop goes on without data, so that every warp reaches the
     // barriers below
-    auto wait = [&](int slot, uint32_t parity) {
-      if (ok && !ptx::wait_bounded_warp(bar(slot), parity & 1, abort_p, kWaitLimitNs)) {
+    auto wait = [&](int slot, uint32_t parity, uint64_t limit = kWaitLimitNs) {
+      if (ok && !ptx::wait_bounded_warp(bar(slot), parity & 1, abort_p, limit)) {
         ok = false;
         if (lane == 0) give_up();
       }
@@ -902,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Whether there is a segment s is decided by one warp for all of them, which meet here.
     auto next_segment = [&](int s) {
       if (tid < 32) {
-        const bool there = wait(BAR_SEG_FULL + s % kSegments, s / kSegments);
+        const bool there = wait(BAR_SEG_FULL + s % kSegments, s / kSegments, segment_limit);
         if (lane == 0) ms.go = there && ms.seg[s % kSegments].count > 0;
       }
       ptx::named_barrier_sync(1, kSoftmaxThreads);
