@@ -164,12 +164,14 @@ def fa_paged_accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seql
 
 
 def _accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seqlens, parents, new_lens,
-            weights, stream):
+            weights, stream, T=None):
     """fa_paged_accept; outputs that are None are allocated. Returns path, new_seqlens."""
-    _, int32, float32, empty_like, _, _ = _torch()
+    torch, int32, float32, empty_like, _, _ = _torch()
+    if T is None:
+        T = (parents if path is None else path).shape[1]
+    T = _count("T", T)
     device, dtype, num_pages, page_size, Hkv, d = _pages(k_pages, v_pages)
     B, max_pages = _sequences(block_table, device)
-    T = _count("T", (parents if path is None else path).shape[1])
     _fits("seqlens", seqlens, (B,), int32, device)
     _fits("leaf", leaf, (B,), int32, device)
     if weights is not None:
@@ -180,7 +182,9 @@ def _accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seqlens, par
         _fits("new_lens", new_lens, (B,), int32, device)
     if path is None:
         with _NO_CONTEXT if stream is None else _stream_of(stream, k_pages.device):
-            path, new_seqlens = empty_like(parents), empty_like(seqlens)
+            path = (torch.empty((B, max(T, 0)), dtype=int32, device=k_pages.device)
+                    if parents is None else empty_like(parents))
+            new_seqlens = empty_like(seqlens)
     else:
         _fits("path", path, (B, T), int32, device)
         _fits("new_seqlens", new_seqlens, (B,), int32, device)
@@ -192,14 +196,17 @@ def _accept(k_pages, v_pages, block_table, seqlens, leaf, path, new_seqlens, par
     return path, new_seqlens
 
 
-def paged_accept(k_pages, v_pages, block_table, seqlens, leaf, parents, new_lens=None,
-                 weights=None, stream=None):
+def paged_accept(k_pages, v_pages, block_table, seqlens, leaf, parents=None, new_lens=None,
+                 weights=None, stream=None, T: int | None = None):
     """path, new_seqlens = the drafted tokens that stay, moved behind the context (see
-    ``fa_paged_accept``)."""
-    if parents.dim() != 2:
+    ``fa_paged_accept``). ``T``: the width of the draft, for chains without ``parents``."""
+    if parents is None:
+        if T is None:
+            raise ValueError("T has to be given where parents are not")
+    elif parents.dim() != 2 or (T is not None and parents.shape[1] != T):
         raise ValueError("parents must be [B, T]")
     return _accept(k_pages, v_pages, block_table, seqlens, leaf, None, None, parents, new_lens,
-                   weights, stream)
+                   weights, stream, T)
 
 
 def fa_paged_copy(k_pages, v_pages, src, dst, rows=None, weights=None, stream=None) -> None:
