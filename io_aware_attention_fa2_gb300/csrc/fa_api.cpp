@@ -23,16 +23,21 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// A function of the driver as of that version, or null.
+void* driver_entry(const char* name, unsigned version) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  return cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) ==
+                     cudaSuccess &&
+                 q == cudaDriverEntryPointSuccess
+             ? p : nullptr;
+}
+
 EncodeTiledFn encode_tiled_fn() {
   static std::once_flag once;
   static EncodeTiledFn fn = nullptr;
   std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
+    fn = reinterpret_cast<EncodeTiledFn>(driver_entry("cuTensorMapEncodeTiled", 12000));
   });
   return fn;
 }
@@ -45,6 +50,26 @@ std::atomic<int> g_arch_ok[kMaxDevices];   // 0 unknown, 1 sm_103, -1 other
 namespace fa {
 
 void* encode_tiled_entry() { return reinterpret_cast<void*>(encode_tiled_fn()); }
+
+int stream_sms(cudaStream_t stream, int all) {
+  using StreamContextFn = CUresult (*)(CUstream, CUcontext*, CUgreenCtx*);
+  using ResourceFn = CUresult (*)(CUgreenCtx, CUdevResource*, CUdevResourceType);
+  static std::once_flag once;
+  static StreamContextFn context_of = nullptr;
+  static ResourceFn resource_of = nullptr;
+  std::call_once(once, [] {
+    context_of = reinterpret_cast<StreamContextFn>(driver_entry("cuStreamGetCtx", 12050));
+    resource_of = reinterpret_cast<ResourceFn>(driver_entry("cuGreenCtxGetDevResource", 12040));
+  });
+  if (!context_of || !resource_of) return all;
+  CUcontext context = nullptr;
+  CUgreenCtx green = nullptr;
+  CUdevResource r = {};
+  if (context_of(stream, &context, &green) != CUDA_SUCCESS || !green ||
+      resource_of(green, &r, CU_DEV_RESOURCE_TYPE_SM) != CUDA_SUCCESS)
+    return all;
+  return std::max(1, std::min(all, static_cast<int>(r.sm.smCount)));
+}
 
 int check_arch(int* device) {
   if (cudaGetDevice(device) != cudaSuccess) return FA_ERR_CUDA;

@@ -18,6 +18,8 @@ int check_device_ptrs(int device, std::initializer_list<const void*> ptrs);
 bool overlaps(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes);
 // The driver's cuTensorMapEncodeTiled, or null.
 void* encode_tiled_entry();
+// SMs that work on `stream` has: those of its green context, or all of the device's.
+int stream_sms(cudaStream_t stream, int all);
 // [B, N, H, d] 16-bit tensor as a 4-D TMA map (d, H, N, B) with box (64, 1, 128, 1).
 bool encode_bnhd(CUtensorMap* map, const void* base, int B, int H, int N, int d, bool fp16);
 

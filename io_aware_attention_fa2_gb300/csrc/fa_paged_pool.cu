@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kForkThreads)
 //     pages of 152 sequences taken and given back 26.5 us, not 66.4; 131072 20.6, not 27.1; 65536
 //     19.9, not 20.1; of 32 sequences 524288 in 41.5, not 64.0, of 16 in 65.9, not 63.9 (a CTA for each
 //     sequence at most, see below). A few pages of such tables 14.1 us, not 12.1: a cooperative launch
-//     starts when what is in front of it has ended.
+//     starts when what is in front of it has ended. So are all tables past kSmallTables on a stream
+//     that has only some of the SMs: a CTA on each of those.
 // A fork of 64 sequences of up to 32K tokens into 256 and its end, where up to five tables give up
 // each page at once: 26 us, not 51.
 //
@@ -698,14 +699,18 @@ cudaError_t launch_paged_resize(const ResizeParams& p, cudaStream_t stream) {
   const int64_t entries = static_cast<int64_t>(p.B) * p.max_pages;
   const size_t smem = 2 * (p.B + 1) * 4;
   cudaError_t err;
-  if (entries >= kLargeTables && p.B >= kLargeBatch) {
-    int device, sms;
-    if ((err = prepare_resize<true>()) != cudaSuccess ||
-        (err = cudaGetDevice(&device)) != cudaSuccess ||
-        (err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
+  if (entries > kSmallTables) {
+    int device, all;
+    if ((err = cudaGetDevice(&device)) != cudaSuccess ||
+        (err = cudaDeviceGetAttribute(&all, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
       return err;
-    return launch_together(fa_paged_resize_kernel<true>, std::min(p.B, sms), kResizeThreads, smem,
-                           stream, p);
+    // (where a stream has only some of the SMs, a cluster of sixteen need not fit)
+    const int sms = stream_sms(stream, all);
+    if (sms < all || (entries >= kLargeTables && p.B >= kLargeBatch)) {
+      if ((err = prepare_resize<true>()) != cudaSuccess) return err;
+      return launch_together(fa_paged_resize_kernel<true>, std::min(p.B, sms), kResizeThreads, smem,
+                             stream, p);
+    }
   }
   err = prepare_resize<false>();
   if (err != cudaSuccess) return err;
