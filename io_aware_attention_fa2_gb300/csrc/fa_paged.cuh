@@ -109,7 +109,8 @@ cudaError_t launch_chained(void (*kernel)(Params...), int64_t grid, int block, s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The same without a cluster, or with one, for the files of drafted and forked sequences.
+// launch_chained, under the name by which the files of drafted and forked sequences call it (the
+// rules that hold for the callers of either are tested by these names).
 template <typename... Params, typename... Args>
 cudaError_t launch_paged(void (*kernel)(Params...), int64_t grid, int block, size_t smem,
                          cudaStream_t stream, int cluster, const Args&... args) {
@@ -138,22 +139,8 @@ cudaError_t launch_together(void (*kernel)(Params...), int grid, int block, size
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// A run of equal length for each CTA, of tiles counted over all units of a call.
-// CTAs that get a run: every one of them at least a tile, so that no part of a unit is empty.
-__device__ __forceinline__ int running(int64_t total, int ctas) {
-  return static_cast<int>(min(total, static_cast<int64_t>(ctas)));
-}
-// First tile of CTA c's run, of `total` tiles over `ctas` running CTAs: floor(total * c / ctas).
-__device__ __forceinline__ int64_t run_start(int64_t total, int c, int ctas) {
-  return total / ctas * c + total % ctas * c / ctas;
-}
-
 // 1 / sum of a row's probabilities: 0 for a row without any, NaN for a NaN.
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
-// LSE in natural units from the maximum (log2 units) and the sum.
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
 
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {

@@ -89,13 +89,6 @@ bool pool_shape_ok(int B, int page_size, int num_pages, int max_pages) {
   return (uint64_t)B * (uint64_t)max_pages < (1ull << 31) - 1;
 }
 
-// page_size, a power of two, as a shift.
-int shift_of(int page_size) {
-  int shift = 0;
-  while (1 << shift < page_size) ++shift;
-  return shift;
-}
-
 uint64_t pool_bytes(int Hkv, int d, int page_size, int num_pages) {
   return (uint64_t)num_pages * page_size * Hkv * d * 2;
 }
@@ -473,7 +466,7 @@ int fa_paged_fork(const int* block_table, const int* seqlens, const int* source,
   p.copy_rows = copy_rows;
   p.B = B;
   p.C = C;
-  p.page_shift = shift_of(page_size);
+  p.page_shift = fa::shift_of(page_size);
   p.max_pages = max_pages;
   return fa::launch_paged_fork(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK : FA_ERR_LAUNCH;
@@ -502,7 +495,7 @@ int fa_paged_resize(int* block_table, const int* old_lens, const int* new_lens, 
   p.new_lens = new_lens;
   p.granted = granted;
   p.B = B;
-  p.page_shift = shift_of(page_size);
+  p.page_shift = fa::shift_of(page_size);
   p.max_pages = max_pages;
   return fa::launch_paged_resize(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK : FA_ERR_LAUNCH;

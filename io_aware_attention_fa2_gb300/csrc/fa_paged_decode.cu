@@ -136,6 +136,20 @@ __device__ __forceinline__ int64_t count_tiles(const Args& a) {
   return x;
 }
 
+// CTAs that get a run: every one of them at least a tile, so that no part of a unit is empty.
+__device__ __forceinline__ int running(int64_t total, int ctas) {
+  return static_cast<int>(min(total, static_cast<int64_t>(ctas)));
+}
+// First tile of CTA c's run, of `total` tiles over `ctas` running CTAs: floor(total * c / ctas).
+__device__ __forceinline__ int64_t run_start(int64_t total, int c, int ctas) {
+  return total / ctas * c + total % ctas * c / ctas;
+}
+
+// LSE in natural units from the maximum (log2 units) and the sum.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 // A run as its segments: consecutive tiles of one unit.
 struct Segment {
   int b, unit, tile, count;   // unit of the sequence, first tile of it, tiles

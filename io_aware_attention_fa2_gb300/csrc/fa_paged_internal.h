@@ -78,6 +78,13 @@ struct EvictParams {
 };
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t stream);
 
+// page_size, a power of two, as a shift.
+inline int shift_of(int page_size) {
+  int shift = 0;
+  while (1 << shift < page_size) ++shift;
+  return shift;
+}
+
 // ---- drafted and forked sequences
 struct TreeParams {
   PagedCache c;

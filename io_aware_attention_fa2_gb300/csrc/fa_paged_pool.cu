@@ -631,12 +631,6 @@ __global__ void __launch_bounds__(kResizeThreads, 1)
   if (rank == 0 && tid == 0) *p.pool.num_free = stack - taken;
 }
 
-int shift_of(int page_size) {
-  int shift = 0;
-  while (1 << shift < page_size) ++shift;
-  return shift;
-}
-
 }  // namespace
 
 cudaError_t launch_paged_accept(const AcceptParams& p, cudaStream_t stream) {

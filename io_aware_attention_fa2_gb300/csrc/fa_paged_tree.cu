@@ -184,7 +184,6 @@ struct Runs {
 // A part of a run: consecutive tiles of one unit.
 struct Segment {
   int b, hk, base;          // sequence, key head, length of the context
-  int drafted;              // drafted tokens
   int r0, live;             // the unit's first row, and its rows that are not padding
   int rows;                 // rows with the padding's, which this segment writes; or 0
   int first_key, count;     // of the segment; its tiles (0: there is no further segment)
@@ -517,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         g.b = b;
         g.hk = hk;
         g.base = dr.base;
-        g.drafted = dr.count;
         g.r0 = r0;
         g.live = live;
         g.rows = tile == 0 ? min(kRows, a.T * a.G - r0) : 0;
@@ -1359,8 +1357,8 @@ int choose_short(int B, int T, int Hq, int Hkv, int64_t tiles) {
 // What a unit's start and end cost in a run, in tiles: of 3 to 16 the best, or within 1 % of it, for 32
 // to 256 units is 6 (64 units of up to 32K tokens 117.6 us and, with two row tiles, 138.4; with 8 118.8
 // and 138.8). Where few CTAs have such a step, the bandwidth that it leaves goes to the others and is
-// missing at the end: 16 units of up to 64K tokens 67.4 us, with 8 65.0; 8 units 60.7 and 60.3. (512
-// units of up to 4096 tokens 133 us, with 4 130.5.)
+// missing at the end: 16 units of up to 64K tokens 67.4 us, with 8 65.0; 8 units 60.7 and 60.3.
+// 512 units of up to 4096 tokens would take 130.5 us with 4 instead of 133: a third value for 2 %.
 int unit_cost(int64_t units) { return units <= 16 ? 8 : 6; }
 
 // Workspace: the parts' O, their offsets and sums, the units' parts; nothing where a unit is one
@@ -1409,8 +1407,7 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t stream) {
   a.g_magic = a.G > 1 && a.G < 2048 ? static_cast<uint32_t>(((1ull << 32) + a.G - 1) / a.G) : 0;
   a.blocks = static_cast<int>(l.blocks);
   a.part_rows = static_cast<int>(l.part_rows);
-  a.page_shift = 0;
-  while (1 << a.page_shift < c.page_size) ++a.page_shift;
+  a.page_shift = shift_of(c.page_size);
   a.num_pages = c.num_pages;
   a.max_pages = c.max_pages;
   a.box_rows = std::min(c.page_size, kTile);
