@@ -463,13 +463,21 @@ int fa_paged_evict(void* k_pages, void* v_pages, float* weights, const int* bloc
  *   workspace    device memory of at least fa_paged_tree_workspace_size(...) bytes, 16-byte
  *                aligned, not overlapping any other argument; NULL where that is 0. Calls
  *                sharing a workspace must not overlap. Its contents need no initialisation.
- * The cache's weights get nothing: which of the tokens will stay is not known yet. Rows at or
- * past n_b, and of tokens that see nothing, get O = 0 and LSE = -inf. What is in keys and values
- * that a token does not see (NaN included) does not matter to it; an infinite value of a token
- * that it sees makes its column of O infinite (NaN where the token's probability is too small for
- * the type), values of both signs or a NaN make it NaN. A sequence whose length is beyond the table or below n_b sees nothing, tokens in pages outside the pool are
- * left out, and a parent that is not an earlier token counts as -1 (each FA_ERR_PAGE in the
- * device error word). The same call gives the same bits.
+ * The cache's weights get nothing: which of the tokens will stay is not known yet. Nor does
+ * fa_paged_accept add anything to them: weights by which fa_paged_evict ranks count the queries of
+ * prompts and of decoding steps, not those of accepted drafts.
+ * Rows at or past n_b, and of tokens that see nothing, get O = 0 and LSE = -inf. What is in keys
+ * and values that a token does not see (NaN included) does not matter to it. A NaN in a query, or
+ * in a key that it sees, makes its O and LSE NaN. An infinite value of a token that it sees makes
+ * its column of O infinite (NaN where the token's probability is too small for the type), values
+ * of both signs or a NaN make it NaN. A sequence whose length is beyond the table or below n_b
+ * sees nothing, tokens in pages outside the pool are left out, and a parent that is not an earlier
+ * token counts as -1 (each FA_ERR_PAGE in the device error word).
+ * Probabilities are rounded to dtype once for the product with V, where fa_paged_decode keeps each
+ * in two such numbers: O of drafted tokens is off by 0.0019 to 0.0023 (bf16) or 0.00024 to 0.00028
+ * (fp16) of its size, that of the same tokens decoded one by one by its own rounding alone (0.0016,
+ * 0.0002).
+ * The same call gives the same bits.
  */
 int fa_paged_tree(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
                   const int* seqlens, const int* parents, const int* new_lens, void* o, float* lse,
@@ -521,7 +529,10 @@ int fa_paged_copy(void* k_pages, void* v_pages, float* weights, const int* src, 
  *                stack whose last entry is taken first; a place that is taken becomes -1
  *   num_free     device int32 [1]
  * All three are updated; calls on one pool must not overlap. A caller starts with refs all 0 and
- * every page in free_pages. Batches of at most 8192 sequences; B * max_pages below 2^31 - 1. */
+ * every page in free_pages. Batches of at most 8192 sequences; B * max_pages below 2^31 - 1.
+ * A page that several tables hold is written by none of them. fa_paged_fork arranges that for a
+ * sequence that grows; one that is cut back to a length inside a shared page, and grows again or
+ * is evicted within its own pages, would write to what the others see. */
 
 /*
  * fa_paged_fork -- new sequences that continue others: sequence c of the new tables has the tokens
@@ -558,7 +569,8 @@ int fa_paged_fork(const int* block_table, const int* seqlens, const int* source,
  *                suffice or a length is negative or beyond the table (FA_ERR_PAGE)
  * Pages return to the pool in the order of the tables (a page that several give up at once by the
  * last of them). An entry outside the pool, or of a page without references, is not returned
- * (FA_ERR_PAGE). The same call gives the same result whatever the timing.
+ * (FA_ERR_PAGE). The same call gives the same result whatever the timing; only where more entries
+ * give a page up than have references to it, which of them returns it is not told.
  */
 int fa_paged_resize(int* block_table, const int* old_lens, const int* new_lens, int* granted,
                     int* refs, int* free_pages, int* num_free, int B, int page_size, int num_pages,

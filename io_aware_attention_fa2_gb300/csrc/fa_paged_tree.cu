@@ -32,9 +32,9 @@
 // there, too, one stream's softmax runs beside the other's products.
 //
 // Measured on the device (replays): B=8 Hkv=8 of 4 query heads d=128 bf16, 64 drafted tokens (256
-// rows) over up to 32K: 140 us, 1230 TFLOP/s, 4.9 TB/s; B=16, 16 drafted tokens (64 rows) over up to
-// 16K, pages of 16: 115 us, 5.6 TB/s (83 % of the measured copy rate); B=4 Hkv=4 of 8, up to 5 tokens
-// over up to 64K: 65 us, 4.5 TB/s. With one row tile HBM is busy at 97 % of the copy rate from the
+// rows) over up to 32K: 140-142 us, 1210-1230 TFLOP/s, 4.8-4.9 TB/s; B=16, 16 drafted tokens (64 rows)
+// over up to 16K, pages of 16: 116-118 us, 5.5-5.6 TB/s (82-83 % of the measured copy rate); B=4 Hkv=4
+// of 8, up to 5 tokens over up to 64K: 65-66 us, 4.4-4.5 TB/s. With one row tile HBM is busy at 97 % of the copy rate from the
 // first load to the last; before it are 3 us (lengths, table: dependent reads, and cold instructions),
 // behind it 4 for the last part and 4 for the join. In the steady state a tile takes 1800 to 2600
 // cycles (one row tile; HBM) or 3200 (two; 2180 of them the tensor pipe's), and the step from one
@@ -58,9 +58,10 @@
 // them to the rows that do see them.
 //
 // P is rounded to the type once for the product with V, a rounding of the same size as the output's
-// (relative error 0.0023 for both, bf16, instead of 0.0017 for the output's alone). fp16 ends at
-// 2^-24, so there P is taken 2^11 times as large, and up to 2^4 more until a grown maximum moves the
-// offset: what is lost are probabilities below 2^-36 of the largest.
+// (relative error 0.0019 to 0.0023 for both, bf16, instead of 0.0016 for the output's alone, at which
+// the decoding kernel stays, which keeps two numbers for P). fp16 ends at 2^-24, so there P is taken
+// 2^11 times as large, and up to 2^4 more until a grown maximum moves the offset: what is lost are
+// probabilities below 2^-36 of the largest.
 #include <cooperative_groups.h>
 #include <stddef.h>
 
@@ -1339,7 +1340,7 @@ int row_tiles(int T, int Hq, int Hkv) { return static_cast<int64_t>(T) * (Hq / H
 
 // The smallest calls: 0, or the CTAs of a cluster that has one unit. A unit of up to kShortTiles
 // tiles for each CTA of a cluster, and few enough units that all clusters run at once, takes one
-// launch without a workspace: 8 units of 1009 tokens (d=64) 10.7 us a replay instead of 14.2, and a
+// launch without a workspace: 8 units of 1009 tokens (d=64) 10.3 us a replay instead of 14.2, and a
 // launch less for the caller. Units of one CTA may take a second turn.
 constexpr int kShortTiles = 4;
 int resident_clusters(int ctas) {   // of one CTA on each SM, as the runtime counts them on a GB300

@@ -15,6 +15,10 @@ A step of speculative decoding, for a batch whose drafted tokens form trees (``p
                                  new_lens=drafted)
     paged_resize(pool, block_table, room, seqlens, page_size)
 
+Drafts that are chains need no ``parents`` (``paged_accept`` then takes their width as ``T``), and
+their masks cost less. Nothing here adds to the weights of a cache that keeps them: accepted tokens
+bring theirs along, their queries' attention to the others is not counted.
+
 A pool (``new_page_pool``) says which pages are free and how many tables hold each. Several
 continuations of a sequence share its whole pages:
 
