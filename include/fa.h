@@ -545,7 +545,7 @@ int fa_paged_copy(void* k_pages, void* v_pages, float* weights, const int* src, 
  *   out_table    device int32 [C, max_pages], written (every element; -1 behind the last page)
  *   out_seqlens  device int32 [C], written: the lengths; -1 for a sequence that got no page
  *                because the pool was empty, or whose source or length is bad (FA_ERR_PAGE in the
- *                device error word): it holds nothing
+ *                device error word): it holds nothing (-1 is no length for the other calls; 0 is)
  *   copy_src, copy_dst, copy_rows  device int32 [C], written: fa_paged_copy's src, dst and rows;
  *                -1, -1 and 0 without a copy
  * Pages come from the pool in the order of c. A page outside the pool in the source's table is

@@ -28,6 +28,8 @@ def partition(sms):
 
     def call(fn, *args):
         rc = fn(*args)
+        if rc == 801:                                  # CUDA_ERROR_NOT_SUPPORTED
+            pytest.skip("green contexts are not supported here")
         assert rc == 0, (fn.__name__, rc)
 
     class Resource(ctypes.Structure):                  # CUdevResource
